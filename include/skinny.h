@@ -74,7 +74,8 @@ typedef enum {
     SKINNY_ERR_CAPTURE = 7,  /* first call on a device made during stream capture */
     SKINNY_ERR_ALLOC = 8,    /* the one-time scratch allocation failed */
     SKINNY_ERR_TIMEOUT = 9,  /* a kernel's bounded internal wait ran out */
-    SKINNY_ERR_ARG = 10      /* a scalar argument is invalid (eps, timeout, ...) */
+    SKINNY_ERR_ARG = 10,     /* a scalar argument is invalid (eps, timeout, ...) */
+    SKINNY_ERR_INDEX = 11    /* a kernel met an index out of range in device memory */
 } skinny_status;
 
 /* Row width of every reduce + RMSNorm row: 7168 ("drafter/comm", ArNorm
@@ -163,6 +164,40 @@ SKINNY_API int decode_gemm_bf16_ex(const void *x, const void *W, void *out, int 
 SKINNY_API int decode_gemm_bf16_logits(const void *x, const void *W, void *out, int M,
                                        int N, int K, int n_out, float soft_cap, float scale,
                                        void *stream);
+
+/* Activations of decode_gemm_bf16_epilogue. */
+typedef enum {
+    SKINNY_ACT_NONE = 0,
+    SKINNY_ACT_RELU = 1,      /* max(v, 0); NaN stays */
+    SKINNY_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
+    SKINNY_ACT_GELU = 3,      /* v/2 (1 + erf(v / sqrt 2)) */
+    SKINNY_ACT_GELU_TANH = 4  /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+} skinny_activation;
+
+/*
+ * decode_gemm_bf16_epilogue -- out = act(x @ W^T + bias) + residual
+ *   The drafter pages have no counterpart; the linears of a decoder layer around
+ *   them do: a QKV projection with a bias, a feed-forward input with its
+ *   activation, a feed-forward output added to the residual stream.
+ *
+ *   x [M, K], W [N, K], out [M, N] as for decode_gemm_bf16.
+ *   bias      [N] BF16 or NULL, 2-byte aligned.
+ *   residual  [M, N] BF16 row-major or NULL, 2-byte aligned. May be the same
+ *             pointer as out (in place); no other overlap of out with an input.
+ *   activation  a skinny_activation.
+ *   opts      host pointer, or NULL for the process-wide settings (see
+ *             decode_gemm_bf16_ex).
+ *   out[m][n] = BF16(act(s + bias[n]) + residual[m][n]), s the FP32 sum over k of
+ *   x[m,k] W[n,k]: every step in FP32, one rounding. With neither bias nor residual
+ *   and SKINNY_ACT_NONE the bits are decode_gemm_bf16's. With programmatic dependent
+ *   launch bias and residual are read after the wait for the previous kernel.
+ *   Other rules (sizes, the device's scratch) and errors as decode_gemm_bf16_ex;
+ *   SKINNY_ERR_ARG for an unknown activation.
+ */
+SKINNY_API int decode_gemm_bf16_epilogue(const void *x, const void *W, const void *bias,
+                                         const void *residual, void *out, int M, int N, int K,
+                                         int activation, const skinny_launch_opts *opts,
+                                         void *stream);
 
 /*
  * decode_gemm_bf16_noalloc -- decode_gemm_bf16 that allocates no device memory
@@ -296,6 +331,145 @@ SKINNY_API int decode_gemm_bf16_reduce_rmsnorm_ex(const void *x, const void *W, 
 SKINNY_API int gather_shards_bf16(const void *shards, int TP, int M, int S, void *out,
                                   void *stream);
 
+/* ---- attention of single tokens over a paged key-value cache ------------------ */
+
+/* A paged key-value cache: `num_pages` pages of `page_size` tokens, each with
+ * kv_heads keys and values of head_dim BF16. Element (page, token, head, i) of the
+ * keys is k[page * page_stride + token * token_stride + head * head_stride + i], of
+ * the values the same with v: any order of the three outer axes, padded or not
+ * (keys and values interleaved in one buffer: two base pointers, the same strides).
+ * k, v 16-byte aligned; strides in elements, >= 0, multiples of 8. */
+typedef struct {
+    void *k, *v;
+    int num_pages, page_size, kv_heads, head_dim;
+    long long page_stride, token_stride, head_stride;
+} skinny_kv_cache;
+
+/*
+ * qk_norm_rope_bf16 -- RMSNorm of every query and key head, position rotation, and
+ *   the append of keys and values to a paged cache, in one pass over the rows of a
+ *   QKV projection. The drafter pages have no counterpart.
+ *
+ *   qkv        rows of (q_heads + 2 kv_heads) * head_dim BF16: query heads, key heads,
+ *              value heads; qkv_stride elements from row to row.
+ *   q_gamma, k_gamma  [head_dim] BF16 norm weights, or NULL: no norm of the query
+ *              (key) heads. Weights: with programmatic dependent launch they are
+ *              read before the wait for the previous kernel (see skinny_set_pdl).
+ *   rope       [max_pos, rot_dim] FP32: rot_dim / 2 cosines, then rot_dim / 2 sines
+ *              of the row's position. rot_dim = 0: no rotation, rope and positions
+ *              unused (may be NULL).
+ *   interleaved  0: value i turns with value i + rot_dim / 2; 1: value 2i with 2i + 1.
+ *              Values from rot_dim on are not rotated.
+ *   positions  [M] int32.
+ *   q_out      rows of q_heads * head_dim, q_stride elements apart. May be qkv itself
+ *              with q_stride == qkv_stride (in place).
+ *   k_out      rows of kv_heads * head_dim, k_stride apart, or NULL. May be the key
+ *              heads of qkv in place (qkv + q_heads * head_dim, k_stride == qkv_stride).
+ *   cache      host pointer, or NULL: nothing is appended. kv_heads and head_dim as
+ *              in the call; along an axis longer than one, its elements must not
+ *              overlap (stride >= head_dim).
+ *   slots      [M] int64, with a cache: row m's key and value heads go to token
+ *              slots[m] % page_size of page slots[m] / page_size. A negative slot is
+ *              not stored (padding rows). Two rows with the same slot leave either
+ *              row's values, possibly some of each.
+ *   Per head, FP32: y = x * rsqrt(sum(x^2) / head_dim + eps) * gamma; the pairs (a, b)
+ *   of the first rot_dim values become (a cos - b sin, b cos + a sin); one rounding.
+ *   Value heads are copied. k_out and the cache get the same bits.
+ *   1 <= M; 1 <= q_heads, kv_heads <= 1024; head_dim a multiple of 8 in [8, 256];
+ *   rot_dim a multiple of 16 in [0, head_dim]; strides multiples of 8 and at least the
+ *   row; data pointers 16-byte aligned, positions 4, slots 8; eps > 0, finite.
+ *   Outputs must not overlap inputs or each other but as said (address ranges count,
+ *   rows' padding included).
+ *   A position outside [0, max_pos) or a slot past the last page: nothing of that row
+ *   is written and skinny_device_error() reports bit 256.
+ *   Errors: SKINNY_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARG, _DEVICE, _LAUNCH.
+ */
+typedef struct {
+    const void *qkv;
+    long long qkv_stride;
+    int M, q_heads, kv_heads, head_dim;
+    const void *q_gamma, *k_gamma;
+    float eps;
+    const void *rope;
+    int max_pos, rot_dim, interleaved;
+    const void *positions;
+    void *q_out;
+    long long q_stride;
+    void *k_out;
+    long long k_stride;
+    const skinny_kv_cache *cache;
+    const void *slots;
+} skinny_qk_norm_rope_args;
+SKINNY_API int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *args,
+                                 const skinny_launch_opts *opts, void *stream);
+
+/* Most rows of decode_attention_bf16. */
+#define SKINNY_ATTENTION_MAX_ROWS 1024
+
+/*
+ * decode_attention_bf16 -- attention of one new token per row over a paged cache,
+ *   split over the cache's length and joined. The drafter pages have no counterpart.
+ *
+ *   q            rows of q_heads * head_dim BF16, q_stride elements apart (the query
+ *                heads of qk_norm_rope_bf16, in place in the QKV rows or not). Query
+ *                head h reads key head h / (q_heads / cache->kv_heads).
+ *   cache        host pointer: the keys and values (the new token's among them).
+ *   block_table  [rows, table_width] int32, table_stride entries from row to row:
+ *                token j of row r is token j % page_size of page
+ *                block_table[r][j / page_size]. Rows may share pages: the drafted
+ *                tokens of one sequence are rows with the same pages and growing
+ *                lengths.
+ *   lengths      [rows] int32: tokens in the row's cache. A row of length 0 (padding)
+ *                gets zeros and a log-sum of -inf.
+ *   window, sinks  window = 0: a row sees tokens 0 .. length - 1. window > 0: its last
+ *                `window` tokens and its first `sinks`. Table entries of pages that a
+ *                row sees nothing of are not read.
+ *   scale        factor of the scores (1 / sqrt(head_dim) as a rule), finite.
+ *   out          [rows, q_heads, head_dim] BF16.
+ *   lse          [rows, q_heads] FP32 or NULL: the natural logarithm of the sum of
+ *                exp(scale q.k), for joining with attention over other tokens.
+ *   workspace    device memory of skinny_attention_workspace_bytes(SM count) bytes,
+ *                16-byte aligned, all zeros before its first use; every call leaves it
+ *                ready for the next. Calls that may run at the same time (other
+ *                streams, graphs replayed side by side) need one each.
+ *   Scores, maxima, sums and the output are FP32, weights are rounded to 15 bits of
+ *   precision (two BF16 terms) for the product with the values, and the output is
+ *   rounded once. Deterministic: the same inputs on the same device give the same bits.
+ *   A score of NaN or +inf makes the head's output NaN; if every score is -inf the
+ *   output is zero.
+ *   1 <= rows <= 1024; q_heads a multiple of kv_heads, kv_heads >= 1, q_heads <= 1024;
+ *   head_dim 64, 96, 128, 192 or 256; page_size, num_pages, table_width >= 1;
+ *   table_width * page_size < 2^30; rows * key heads * head blocks * tiles of 64 tokens
+ *   < 2^31; window, sinks >= 0; q_stride a multiple of 8, at least the row; q, k, v, out
+ *   and workspace 16-byte aligned, tables, lengths and lse 4. out, lse and the workspace
+ *   must not overlap anything.
+ *   On the device, a length outside [0, table_width * page_size] is taken as the
+ *   nearest, a token on a page outside [0, num_pages) as not seen, and
+ *   skinny_device_error() reports bit 256.
+ *   Errors: SKINNY_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARG, _DEVICE, _LAUNCH.
+ */
+typedef struct {
+    const void *q;
+    long long q_stride;
+    int rows, q_heads;
+    const skinny_kv_cache *cache;
+    const void *block_table;
+    long long table_stride;
+    int table_width;
+    const void *lengths;
+    int window, sinks;
+    float scale;
+    void *out;
+    void *lse;
+    void *workspace;
+    size_t workspace_bytes;
+} skinny_decode_attention_args;
+SKINNY_API int decode_attention_bf16(const skinny_decode_attention_args *args,
+                                     const skinny_launch_opts *opts, void *stream);
+
+/* Bytes of the workspace on a device with num_sms SMs (0 for num_sms < 1). */
+SKINNY_API size_t skinny_attention_workspace_bytes(int num_sms);
+
 /* Human-readable text of a skinny_status code (static storage). */
 SKINNY_API const char *skinny_status_string(int status);
 
@@ -305,7 +479,9 @@ SKINNY_API const char *skinny_status_string(int status);
  *   recorded a problem since the last read, else SKINNY_ERR_TIMEOUT, and writes
  *   the raw word (a bit set per waiting role that gave up; 64 if only the
  *   host-mapped word was set; 128 if a reduce_residual_rmsnorm cluster's
- *   exchange of its sums of squares ran out) to *word if word is not NULL. Clearing also
+ *   exchange of its sums of squares ran out; 256 if qk_norm_rope_bf16 or
+ *   decode_attention_bf16 met an index out of range, and if that is the only bit the
+ *   status is SKINNY_ERR_INDEX) to *word if word is not NULL. Clearing also
  *   re-arms the decode GEMM's scratch flags, so the next call starts clean and
  *   calls stop returning SKINNY_ERR_TIMEOUT. Host pointer: word.
  */

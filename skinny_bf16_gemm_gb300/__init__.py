@@ -9,6 +9,10 @@ operations raises.
     decode_gemm_bf16(x, W, out)                      out = x @ W^T (BF16)
     reduce_residual_rmsnorm(partials, residual, gamma, out, residual_out, eps)
     gather_shards_bf16(shards, out)                  TP shards side by side
+    decode_gemm_bf16_epilogue(x, W, out, bias, activation, residual)
+                                                     out = act(x @ W^T + bias) + residual
+    qk_norm_rope_bf16(qkv, ...)                      per-head norm, rotation, cache append
+    decode_attention_bf16(q, k_cache, v_cache, ...)  one token per row over a paged cache
 """
 import ctypes
 import os
@@ -24,7 +28,7 @@ STATUS = {
     0: "SKINNY_OK", 1: "SKINNY_ERR_NULL", 2: "SKINNY_ERR_SHAPE", 3: "SKINNY_ERR_ALIGN",
     4: "SKINNY_ERR_DEVICE", 5: "SKINNY_ERR_LAUNCH", 6: "SKINNY_ERR_ALIAS",
     7: "SKINNY_ERR_CAPTURE", 8: "SKINNY_ERR_ALLOC", 9: "SKINNY_ERR_TIMEOUT",
-    10: "SKINNY_ERR_ARG",
+    10: "SKINNY_ERR_ARG", 11: "SKINNY_ERR_INDEX",
 }
 
 
@@ -58,6 +62,38 @@ class GemmPlan(ctypes.Structure):
                 ("smem_bytes", ctypes.c_int), ("split_tiles", ctypes.c_int)]
 
 
+class KVCacheArgs(ctypes.Structure):
+    """skinny_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    """skinny_qk_norm_rope_args."""
+    _fields_ = [("qkv", ctypes.c_void_p), ("qkv_stride", ctypes.c_longlong), ("M", ctypes.c_int),
+                ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("q_gamma", ctypes.c_void_p), ("k_gamma", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rope", ctypes.c_void_p), ("max_pos", ctypes.c_int),
+                ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_longlong), ("k_out", ctypes.c_void_p),
+                ("k_stride", ctypes.c_longlong), ("cache", ctypes.POINTER(KVCacheArgs)),
+                ("slots", ctypes.c_void_p)]
+
+
+class DecodeAttentionArgs(ctypes.Structure):
+    """skinny_decode_attention_args."""
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("rows", ctypes.c_int),
+                ("q_heads", ctypes.c_int), ("cache", ctypes.POINTER(KVCacheArgs)),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
+                ("table_width", ctypes.c_int), ("lengths", ctypes.c_void_p),
+                ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 
 
@@ -82,12 +118,20 @@ def load_library(path: str = LIBRARY):
     lib.reduce_residual_rmsnorm_ex.restype = i32
     lib.decode_gemm_bf16_logits.argtypes = [vp, vp, vp, i32, i32, i32, i32, f32, f32, vp]
     lib.decode_gemm_bf16_logits.restype = i32
+    lib.decode_gemm_bf16_epilogue.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, op, vp]
+    lib.decode_gemm_bf16_epilogue.restype = i32
     lib.decode_gemm_bf16_reduce_rmsnorm.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32,
                                                     f32, vp]
     lib.decode_gemm_bf16_reduce_rmsnorm.restype = i32
     lib.decode_gemm_bf16_reduce_rmsnorm_ex.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32,
                                                        f32, op, vp]
     lib.decode_gemm_bf16_reduce_rmsnorm_ex.restype = i32
+    lib.qk_norm_rope_bf16.argtypes = [ctypes.POINTER(QkNormRopeArgs), op, vp]
+    lib.qk_norm_rope_bf16.restype = i32
+    lib.decode_attention_bf16.argtypes = [ctypes.POINTER(DecodeAttentionArgs), op, vp]
+    lib.decode_attention_bf16.restype = i32
+    lib.skinny_attention_workspace_bytes.argtypes = [i32]
+    lib.skinny_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.gather_shards_bf16.argtypes = [vp, i32, i32, i32, vp, vp]
     lib.gather_shards_bf16.restype = i32
     lib.skinny_status_string.argtypes = [i32]
@@ -184,6 +228,40 @@ def decode_gemm_bf16_logits(x, W, out, soft_cap=0.0, scale=1.0, stream=None):
     return out
 
 
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def decode_gemm_bf16_epilogue(x, W, out, bias=None, activation="none", residual=None, stream=None,
+                              pdl=None, l2_prefetch=None):
+    """out[M, N] = act(x[M, K] @ W[N, K]^T + bias[N]) + residual[M, N].
+
+    bias and residual may be None; residual may be out itself. activation: one of
+    ACTIVATIONS. FP32 throughout, one BF16 rounding. x, W, out, pdl and l2_prefetch
+    as for decode_gemm_bf16. Returns ``out``.
+    """
+    _bf16_cuda(x, "x")
+    _bf16_cuda(W, "W")
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} and W {tuple(W.shape)} must be [M,K] and [N,K]")
+    M, K = x.shape
+    N = W.shape[0]
+    _bf16_cuda(out, "out", (M, N))
+    if bias is not None:
+        _bf16_cuda(bias, "bias", (N,))
+    if residual is not None:
+        _bf16_cuda(residual, "residual", (M, N))
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    o = _opts(pdl, l2_prefetch)
+    st = load_library().decode_gemm_bf16_epilogue(
+        x.data_ptr(), W.data_ptr(), None if bias is None else bias.data_ptr(),
+        None if residual is None else residual.data_ptr(), out.data_ptr(), M, N, K, act,
+        None if o is None else ctypes.byref(o), _stream_handle(stream))
+    _check(st, "decode_gemm_bf16_epilogue")
+    return out
+
+
 def reduce_residual_rmsnorm(partials, residual, gamma, out, residual_out, eps=1e-6,
                             stream=None, pdl=None):
     """(out, residual_out) of the rank-order reduce + residual + RMSNorm.
@@ -263,6 +341,174 @@ def gather_shards_bf16(shards, out, stream=None):
     st = load_library().gather_shards_bf16(shards.data_ptr(), TP, M, S, out.data_ptr(),
                                            _stream_handle(stream))
     _check(st, "gather_shards_bf16")
+    return out
+
+
+def _rows(t, name, width=None):
+    """A CUDA bfloat16 tensor whose trailing dimensions are contiguous within a row: the
+    stride between rows, in elements (the row's width for a single row)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
+    n = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != n:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        n *= size
+    if width is not None and n != width:
+        raise ValueError(f"{name} has rows of {n}, expected {width}")
+    return t.stride(0) if t.shape[0] > 1 else n
+
+
+def _plain_cuda(t, name, dtype, shape):
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor (got {t.dtype} on {t.device})")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _cache_args(k_cache, v_cache):
+    """The KVCacheArgs of two [pages, page_size, kv_heads, head_dim] views."""
+    import torch
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != torch.bfloat16 or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must be "
+                         "[pages, page_size, kv_heads, head_dim]")
+    # The stride of an axis of one element says nothing.
+    ks, vs = ([0 if n == 1 else st for n, st in zip(shape, t.stride())] for t in (k_cache, v_cache))
+    if ks != vs or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        raise ValueError("k_cache and v_cache must have the same strides, 1 along head_dim")
+    return KVCacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), *shape, *ks[:3])
+
+
+def qk_norm_rope_bf16(qkv, q_heads, kv_heads, q_gamma, k_gamma, rope, positions, q_out, k_out=None,
+                      k_cache=None, v_cache=None, slots=None, eps=1e-6, interleaved=False,
+                      stream=None, pdl=None):
+    """Per-head RMSNorm and position rotation of QKV rows, and the append to a paged cache.
+
+    qkv [M, (q_heads + 2 kv_heads) * head_dim], rows contiguous, any row stride;
+    q_gamma, k_gamma [head_dim] or None (no norm); rope [max_pos, rot_dim] FP32
+    (cosines, then sines) or None (no rotation); positions [M] int32. q_out [M, q_heads,
+    head_dim] (or flat rows; may be qkv's own query heads, in place); k_out [M, kv_heads,
+    head_dim] or None. k_cache, v_cache: [pages, page_size, kv_heads, head_dim] views of
+    equal strides, or None; slots [M] int64 (page * page_size + token; negative: not
+    stored). Returns ``q_out``.
+    """
+    import torch
+    qkv_stride = _rows(qkv, "qkv")
+    if qkv.dim() != 2 or q_heads < 1 or kv_heads < 1 or qkv.shape[1] % (q_heads + 2 * kv_heads):
+        raise ValueError(f"qkv {tuple(qkv.shape)} must be [M, ({q_heads} + 2 * {kv_heads}) * head_dim]")
+    M = qkv.shape[0]
+    D = qkv.shape[1] // (q_heads + 2 * kv_heads)
+    if q_out.shape[0] != M or (k_out is not None and k_out.shape[0] != M):
+        raise ValueError(f"q_out and k_out must have {M} rows")
+    for g, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
+        if g is not None:
+            _bf16_cuda(g, name, (D,))
+    a = QkNormRopeArgs(qkv=qkv.data_ptr(), qkv_stride=qkv_stride, M=M, q_heads=q_heads,
+                       kv_heads=kv_heads, head_dim=D, eps=eps, interleaved=bool(interleaved),
+                       q_out=q_out.data_ptr(), q_stride=_rows(q_out, "q_out", q_heads * D))
+    if q_gamma is not None:
+        a.q_gamma = q_gamma.data_ptr()
+    if k_gamma is not None:
+        a.k_gamma = k_gamma.data_ptr()
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError(f"rope must be [max_pos, rot_dim], got {tuple(rope.shape)}")
+        _plain_cuda(rope, "rope", torch.float32, rope.shape)
+        _plain_cuda(positions, "positions", torch.int32, (M,))
+        a.rope, a.max_pos, a.rot_dim = rope.data_ptr(), rope.shape[0], rope.shape[1]
+        a.positions = positions.data_ptr()
+    if k_out is not None:
+        a.k_out, a.k_stride = k_out.data_ptr(), _rows(k_out, "k_out", kv_heads * D)
+    if k_cache is not None or v_cache is not None:
+        if k_cache is None or v_cache is None or slots is None:
+            raise ValueError("k_cache, v_cache and slots go together")
+        cache = _cache_args(k_cache, v_cache)
+        _plain_cuda(slots, "slots", torch.int64, (M,))
+        a.cache, a.slots = ctypes.pointer(cache), slots.data_ptr()
+    o = _opts(pdl, None)
+    st = load_library().qk_norm_rope_bf16(ctypes.byref(a), None if o is None else ctypes.byref(o),
+                                          _stream_handle(stream))
+    _check(st, "qk_norm_rope_bf16")
+    return q_out
+
+
+def attention_workspace(device=None):
+    """A workspace for decode_attention_bf16 on a device: zeros, left ready by every call.
+    Calls that may run at the same time need one each."""
+    import torch
+    dev = torch.cuda.current_device() if device is None else device
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    return torch.zeros(load_library().skinny_attention_workspace_bytes(sms), dtype=torch.uint8,
+                       device=torch.device("cuda", dev) if isinstance(dev, int) else dev)
+
+
+_workspaces = {}  # (device, stream) -> the workspace of calls that bring none
+
+
+def _own_workspace(device, stream):
+    """The workspace of a call that brings none: calls on one stream run one after
+    another and share one; a call being captured gets its own, zeroed in the graph, so
+    that graphs replayed side by side do not meet."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return attention_workspace(device)
+    key = (device, stream.value)
+    ws = _workspaces.get(key)
+    if ws is None:
+        ws = _workspaces[key] = attention_workspace(device)
+        torch.cuda.current_stream(device).synchronize()  # zeroed before another stream's first use
+    return ws
+
+
+def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=None, window=0,
+                          sinks=0, lse=None, workspace=None, stream=None, pdl=None):
+    """Attention of one new token per row over a paged key-value cache.
+
+    q [rows, q_heads, head_dim], each row contiguous, any row stride; k_cache, v_cache
+    [pages, page_size, kv_heads, head_dim] views of equal strides; block_table [rows,
+    table_width] int32; lengths [rows] int32; out like q, contiguous; lse [rows, q_heads]
+    FP32 or None. scale: 1 / sqrt(head_dim) if None. window > 0: a row sees its last
+    ``window`` tokens and its first ``sinks``. workspace: attention_workspace(), or None
+    for one kept per stream (a call under graph capture gets its own). Returns ``out``.
+    """
+    import torch
+    q_stride = _rows(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [rows, q_heads, head_dim], got {tuple(q.shape)}")
+    rows, q_heads, D = q.shape
+    cache = _cache_args(k_cache, v_cache)
+    if cache.head_dim != D:
+        raise ValueError(f"q has heads of {D}, the cache of {cache.head_dim}")
+    _bf16_cuda(out, "out", (rows, q_heads, D))
+    if block_table.dtype != torch.int32 or not block_table.is_cuda:
+        raise TypeError("block_table must be a CUDA int32 tensor")
+    if block_table.dim() != 2 or block_table.shape[0] != rows or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be [{rows}, table_width] with contiguous rows")
+    _plain_cuda(lengths, "lengths", torch.int32, (rows,))
+    if lse is not None:
+        _plain_cuda(lse, "lse", torch.float32, (rows, q_heads))
+    handle = _stream_handle(stream)
+    if workspace is None:
+        workspace = _own_workspace(q.device.index, handle)
+    width = block_table.shape[1]
+    a = DecodeAttentionArgs(
+        q.data_ptr(), q_stride, rows, q_heads, ctypes.pointer(cache), block_table.data_ptr(),
+        block_table.stride(0) if rows > 1 else width, width, lengths.data_ptr(), window, sinks,
+        D ** -0.5 if scale is None else scale, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size())
+    o = _opts(pdl, None)
+    st = load_library().decode_attention_bf16(ctypes.byref(a), None if o is None else ctypes.byref(o),
+                                              handle)
+    _check(st, "decode_attention_bf16")
     return out
 
 

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "attention_plan.cuh"
 #include "kernels.h"
 #include "plan.cuh"
 #include "skinny.h"
@@ -17,6 +18,8 @@ namespace skinny {
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxHeads = 1024;
+constexpr int kMaxHeadDim = 256;
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // 1 s per internal wait
 
 struct DeviceState {
@@ -235,20 +238,30 @@ int resolve_settings(const skinny_launch_opts *opts, LaunchSettings *out) {
 
 int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, void *stream,
                 const skinny_launch_opts *opts, int selftest, unsigned long long limit_ns,
-                int logits = 0, float soft_cap = 0.0f, float scale = 1.0f) {
+                int logits = 0, float soft_cap = 0.0f, float scale = 1.0f,
+                const Epilogue *epi = nullptr) {
     if (!x || !W || !out) return SKINNY_ERR_NULL;
     int st = gemm_shape_ok(M, N, K);
     if (st) return st;
-    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(out, 2)) return SKINNY_ERR_ALIGN;
+    const void *bias = epi ? epi->bias : nullptr, *residual = epi ? epi->residual : nullptr;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(out, 2) || !aligned(bias, 2) ||
+        !aligned(residual, 2))
+        return SKINNY_ERR_ALIGN;
     const size_t xb = static_cast<size_t>(M) * K * 2, wb = static_cast<size_t>(N) * K * 2,
                  ob = static_cast<size_t>(M) * N * 2;
-    if (overlaps(out, ob, x, xb) || overlaps(out, ob, W, wb)) return SKINNY_ERR_ALIAS;
+    // out may be the residual itself (element-wise in place), nothing else.
+    if (overlaps(out, ob, x, xb) || overlaps(out, ob, W, wb) ||
+        (bias && overlaps(out, ob, bias, static_cast<size_t>(N) * 2)) ||
+        (residual && residual != out && overlaps(out, ob, residual, ob)))
+        return SKINNY_ERR_ALIAS;
     LaunchSettings ls;
     if ((st = resolve_settings(opts, &ls))) return st;
     int dev;
     if ((st = current_device(&dev))) return st;
     if ((st = check_device_pointer(x, dev)) || (st = check_device_pointer(W, dev)) ||
-        (st = check_device_pointer(out, dev)))
+        (st = check_device_pointer(out, dev)) ||
+        (bias && (st = check_device_pointer(bias, dev))) ||
+        (residual && residual != out && (st = check_device_pointer(residual, dev))))
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DeviceState *d = nullptr;
@@ -276,6 +289,10 @@ int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, vo
     a.logits = logits;
     a.soft_cap = soft_cap;
     a.scale = scale;
+    if (epi) {
+        a.epilogue = 1;
+        a.epi = *epi;
+    }
     const bool pdl = ls.pdl;
     a.l2_lead = ls.l2_lead;
     a.gemm_done = d->gemm_done;
@@ -305,7 +322,7 @@ int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, vo
             fix.N = N;
             fix.K = K;
             fix.ctas = g.ctas;
-            e = launch_splitk_finish(fix, static_cast<uint16_t *>(out), s, pdl);
+            e = launch_splitk_finish(fix, static_cast<uint16_t *>(out), epi, s, pdl);
         }
         if (e != cudaSuccess) {
             cudaGetLastError();
@@ -439,6 +456,34 @@ int reduce_device_checks(const void *partials, const void *residual, const void 
     return SKINNY_OK;
 }
 
+// Bytes from a row's first element to past the last row's last.
+size_t row_span(int rows, long long stride, long long width) {
+    return (static_cast<size_t>(rows - 1) * stride + width) * 2;
+}
+
+// A cache's own rules, and the bytes its keys (or values) span.
+int check_cache(const skinny_kv_cache *c, bool write, size_t *span) {
+    if (!c->k || !c->v) return SKINNY_ERR_NULL;
+    if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->kv_heads > kMaxHeads ||
+        c->head_dim < 8 || c->head_dim > kMaxHeadDim || c->head_dim % 8 != 0)
+        return SKINNY_ERR_SHAPE;
+    const long long strides[3] = {c->page_stride, c->token_stride, c->head_stride};
+    const int sizes[3] = {c->num_pages, c->page_size, c->kv_heads};
+    unsigned long long last = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (strides[i] < 0 || strides[i] > (1ll << 40)) return SKINNY_ERR_SHAPE;
+        if (strides[i] % 8 != 0) return SKINNY_ERR_ALIGN;
+        if (write && sizes[i] > 1 && strides[i] < c->head_dim) return SKINNY_ERR_ALIAS;
+        // At most 3 * 2^31 * 2^40: no overflow of the unsigned 128-bit sum.
+        const unsigned __int128 more = static_cast<unsigned __int128>(sizes[i] - 1) * strides[i];
+        if (more > (1ull << 44)) return SKINNY_ERR_SHAPE;
+        last += static_cast<unsigned long long>(more);
+    }
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return SKINNY_ERR_ALIGN;
+    *span = static_cast<size_t>(last + c->head_dim) * 2;
+    return SKINNY_OK;
+}
+
 }  // namespace
 }  // namespace skinny
 
@@ -567,6 +612,17 @@ int decode_gemm_bf16_logits(const void *x, const void *W, void *out, int M, int 
                        soft_cap > 0.0f ? soft_cap : 0.0f, scale);
 }
 
+int decode_gemm_bf16_epilogue(const void *x, const void *W, const void *bias,
+                              const void *residual, void *out, int M, int N, int K,
+                              int activation, const skinny_launch_opts *opts, void *stream) {
+    if (activation < SKINNY_ACT_NONE || activation > SKINNY_ACT_GELU_TANH) return SKINNY_ERR_ARG;
+    Epilogue epi = {};
+    epi.bias = static_cast<const uint16_t *>(bias);
+    epi.residual = static_cast<const uint16_t *>(residual);
+    epi.activation = activation;
+    return gemm_launch(x, W, out, M, N, K, stream, opts, 0, kWaitLimitNs, 0, 0.0f, 1.0f, &epi);
+}
+
 int skinny_watchdog_selftest(const void *x, const void *W, void *out, int M, int N, int K,
                              long long timeout_ns, void *stream) {
     if (timeout_ns < 1000 || timeout_ns > 2000000000LL) return SKINNY_ERR_ARG;
@@ -644,6 +700,203 @@ int gather_shards_bf16(const void *shards, int TP, int M, int S, void *out, void
     return SKINNY_OK;
 }
 
+int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opts *opts,
+                      void *stream) {
+    if (!p || !p->qkv || !p->q_out || (p->rot_dim != 0 && (!p->rope || !p->positions)) ||
+        (p->cache && !p->slots))
+        return SKINNY_ERR_NULL;
+    const int D = p->head_dim;
+    if (p->M < 1 || p->q_heads < 1 || p->q_heads > kMaxHeads || p->kv_heads < 1 ||
+        p->kv_heads > kMaxHeads || D < 8 || D > kMaxHeadDim || D % 8 != 0 || p->rot_dim < 0 ||
+        p->rot_dim > D || p->rot_dim % 16 != 0 || (p->rot_dim > 0 && p->max_pos < 1))
+        return SKINNY_ERR_SHAPE;
+    const long long q_width = static_cast<long long>(p->q_heads) * D;
+    const long long kv_width = static_cast<long long>(p->kv_heads) * D;
+    const long long width = q_width + 2 * kv_width;
+    constexpr long long kMaxStride = 1ll << 30;  // rows * stride stays far below 2^63 bytes
+    if (p->qkv_stride < width || p->qkv_stride > kMaxStride || p->q_stride < q_width ||
+        p->q_stride > kMaxStride || (p->k_out && (p->k_stride < kv_width || p->k_stride > kMaxStride)))
+        return SKINNY_ERR_SHAPE;
+    if (!(p->eps > 0.0f) || !std::isfinite(p->eps) || p->interleaved < 0 || p->interleaved > 1)
+        return SKINNY_ERR_ARG;
+    if (!aligned(p->qkv, 16) || !aligned(p->q_out, 16) || !aligned(p->k_out, 16) ||
+        !aligned(p->q_gamma, 16) || !aligned(p->k_gamma, 16) || !aligned(p->rope, 16) ||
+        !aligned(p->positions, 4) || !aligned(p->slots, 8) || p->qkv_stride % 8 != 0 ||
+        p->q_stride % 8 != 0 || (p->k_out && p->k_stride % 8 != 0))
+        return SKINNY_ERR_ALIGN;
+    int st;
+    size_t pool = 0;
+    if (p->cache) {
+        if (p->cache->kv_heads != p->kv_heads || p->cache->head_dim != D) return SKINNY_ERR_SHAPE;
+        if ((st = check_cache(p->cache, true, &pool))) return st;
+        if (p->cache->k == p->cache->v) return SKINNY_ERR_ALIAS;
+    }
+    // Every output against every input and the other outputs; q_out and k_out may be
+    // their own heads of qkv in place.
+    const struct { const void *p; size_t n; } in[] = {
+        {p->qkv, row_span(p->M, p->qkv_stride, width)},
+        {p->q_gamma, static_cast<size_t>(D) * 2},
+        {p->k_gamma, static_cast<size_t>(D) * 2},
+        {p->rot_dim ? p->rope : nullptr, static_cast<size_t>(p->max_pos) * p->rot_dim * 4},
+        {p->rot_dim ? p->positions : nullptr, static_cast<size_t>(p->M) * 4},
+        {p->cache ? p->slots : nullptr, static_cast<size_t>(p->M) * 8}};
+    const bool q_in_place = p->q_out == p->qkv && p->q_stride == p->qkv_stride;
+    const bool k_in_place = p->k_out == static_cast<const uint16_t *>(p->qkv) + q_width &&
+                            p->k_stride == p->qkv_stride;
+    const struct { const void *p; size_t n; bool in_place; } outs[] = {
+        {p->q_out, row_span(p->M, p->q_stride, q_width), q_in_place},
+        {p->k_out, p->k_out ? row_span(p->M, p->k_stride, kv_width) : 0, k_in_place},
+        {p->cache ? p->cache->k : nullptr, pool, false},
+        {p->cache ? p->cache->v : nullptr, pool, false}};
+    for (int i = 0; i < 4; ++i) {
+        if (!outs[i].p) continue;
+        for (int j = 0; j < 6; ++j)
+            if (in[j].p && !(j == 0 && outs[i].in_place) && overlaps(outs[i].p, outs[i].n, in[j].p, in[j].n))
+                return SKINNY_ERR_ALIAS;
+        for (int j = i + 1; j < 4; ++j)
+            if (outs[j].p && !(outs[i].in_place && outs[j].in_place) && !(i == 2 && j == 3) &&
+                overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+                return SKINNY_ERR_ALIAS;
+    }
+    LaunchSettings ls;
+    if ((st = resolve_settings(opts, &ls))) return st;
+    int dev;
+    if ((st = current_device(&dev))) return st;
+    DeviceState *d = nullptr;
+    if ((st = device_state(dev, &d))) return st;
+    for (const auto &b : in)
+        if (b.p && (st = check_device_pointer(b.p, dev))) return st;
+    for (const auto &b : outs)
+        if (b.p && !b.in_place && (st = check_device_pointer(b.p, dev))) return st;
+    RopeArgs a = {};
+    a.qkv = static_cast<const uint16_t *>(p->qkv);
+    a.qkv_stride = p->qkv_stride;
+    a.rows = p->M;
+    a.q_heads = p->q_heads;
+    a.kv_heads = p->kv_heads;
+    a.head_dim = D;
+    a.q_gamma = static_cast<const uint16_t *>(p->q_gamma);
+    a.k_gamma = static_cast<const uint16_t *>(p->k_gamma);
+    a.eps = p->eps;
+    a.rope = static_cast<const float *>(p->rope);
+    a.max_pos = p->max_pos;
+    a.rot_dim = p->rot_dim;
+    a.interleaved = p->interleaved;
+    a.positions = static_cast<const int *>(p->positions);
+    a.q_out = static_cast<uint16_t *>(p->q_out);
+    a.q_stride = p->q_stride;
+    a.k_out = static_cast<uint16_t *>(p->k_out);
+    a.k_stride = p->k_stride;
+    if (p->cache) {
+        a.k_cache = static_cast<uint16_t *>(p->cache->k);
+        a.v_cache = static_cast<uint16_t *>(p->cache->v);
+        a.num_pages = p->cache->num_pages;
+        a.page_size = p->cache->page_size;
+        a.page_stride = p->cache->page_stride;
+        a.token_stride = p->cache->token_stride;
+        a.head_stride = p->cache->head_stride;
+        a.slots = static_cast<const long long *>(p->slots);
+    }
+    if (launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream), ls.pdl) != cudaSuccess) {
+        cudaGetLastError();
+        return SKINNY_ERR_LAUNCH;
+    }
+    return SKINNY_OK;
+}
+
+size_t skinny_attention_workspace_bytes(int num_sms) {
+    return num_sms < 1 ? 0 : attn_workspace_bytes(attn_sms(num_sms));
+}
+
+int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_launch_opts *opts,
+                          void *stream) {
+    if (!p || !p->q || !p->cache || !p->block_table || !p->lengths || !p->out || !p->workspace)
+        return SKINNY_ERR_NULL;
+    const skinny_kv_cache *c = p->cache;
+    size_t pool = 0;
+    int st = check_cache(c, false, &pool);
+    if (st) return st;
+    const int D = c->head_dim;
+    if (D != 64 && D != 96 && D != 128 && D != 192 && D != 256) return SKINNY_ERR_SHAPE;
+    if (p->rows < 1 || p->rows > SKINNY_ATTENTION_MAX_ROWS || p->q_heads < 1 ||
+        p->q_heads > kMaxHeads || p->q_heads % c->kv_heads != 0 || p->table_width < 1 ||
+        p->table_stride < p->table_width || p->table_stride > (1ll << 40))
+        return SKINNY_ERR_SHAPE;
+    const long long capacity = static_cast<long long>(p->table_width) * c->page_size;
+    if (capacity >= (1ll << 30)) return SKINNY_ERR_SHAPE;
+    const int group = p->q_heads / c->kv_heads, most = 8 * attn_max_nb(D);
+    const int head_blocks = (group + most - 1) / most;
+    const long long tiles = (capacity + kAttnTile - 1) / kAttnTile;
+    if (tiles * p->rows * c->kv_heads * head_blocks >= (1ll << 31)) return SKINNY_ERR_SHAPE;
+    const long long q_width = static_cast<long long>(p->q_heads) * D;
+    if (p->q_stride < q_width || p->q_stride > (1ll << 30)) return SKINNY_ERR_SHAPE;
+    if (p->window < 0 || p->sinks < 0 || !std::isfinite(p->scale)) return SKINNY_ERR_ARG;
+    if (!aligned(p->q, 16) || !aligned(p->out, 16) || !aligned(p->workspace, 16) ||
+        !aligned(p->block_table, 4) || !aligned(p->lengths, 4) || !aligned(p->lse, 4) ||
+        p->q_stride % 8 != 0)
+        return SKINNY_ERR_ALIGN;
+    const size_t heads = static_cast<size_t>(p->rows) * p->q_heads;
+    const struct { const void *p; size_t n; } in[] = {
+        {p->q, row_span(p->rows, p->q_stride, q_width)}, {c->k, pool}, {c->v, pool},
+        {p->block_table, (static_cast<size_t>(p->rows - 1) * p->table_stride + p->table_width) * 4},
+        {p->lengths, static_cast<size_t>(p->rows) * 4}};
+    const struct { const void *p; size_t n; } outs[] = {
+        {p->out, heads * D * 2}, {p->lse, heads * 4}, {p->workspace, p->workspace_bytes}};
+    for (int i = 0; i < 3; ++i) {
+        if (!outs[i].p) continue;
+        for (const auto &b : in)
+            if (overlaps(outs[i].p, outs[i].n, b.p, b.n)) return SKINNY_ERR_ALIAS;
+        for (int j = i + 1; j < 3; ++j)
+            if (outs[j].p && overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return SKINNY_ERR_ALIAS;
+    }
+    LaunchSettings ls;
+    if ((st = resolve_settings(opts, &ls))) return st;
+    int dev;
+    if ((st = current_device(&dev))) return st;
+    DeviceState *d = nullptr;
+    if ((st = device_state(dev, &d))) return st;
+    const int sms = attn_sms(d->sms);
+    if (p->workspace_bytes < attn_workspace_bytes(sms)) return SKINNY_ERR_SHAPE;
+    for (const auto &b : in)
+        if ((st = check_device_pointer(b.p, dev))) return st;
+    for (const auto &b : outs)
+        if (b.p && (st = check_device_pointer(b.p, dev))) return st;
+    AttentionArgs a = {};
+    a.q = static_cast<const uint16_t *>(p->q);
+    a.q_stride = p->q_stride;
+    a.k = static_cast<const uint16_t *>(c->k);
+    a.v = static_cast<const uint16_t *>(c->v);
+    a.num_pages = c->num_pages;
+    a.page_size = c->page_size;
+    a.page_stride = c->page_stride;
+    a.token_stride = c->token_stride;
+    a.head_stride = c->head_stride;
+    a.block_table = static_cast<const int *>(p->block_table);
+    a.table_stride = p->table_stride;
+    a.lengths = static_cast<const int *>(p->lengths);
+    a.rows = p->rows;
+    a.q_heads = p->q_heads;
+    a.kv_heads = c->kv_heads;
+    a.group = group;
+    a.head_blocks = head_blocks;
+    a.block_heads = (group + head_blocks - 1) / head_blocks;
+    a.capacity = static_cast<int>(capacity);
+    a.window = p->window;
+    a.sinks = p->sinks;
+    a.scale_log2 = p->scale * 1.44269504088896341f;
+    a.out = static_cast<uint16_t *>(p->out);
+    a.lse = static_cast<float *>(p->lse);
+    a.counters = static_cast<unsigned *>(p->workspace);
+    a.partials = reinterpret_cast<float *>(static_cast<char *>(p->workspace) +
+                                           attn_counter_bytes(attn_max_ctas(sms)));
+    if (launch_decode_attention(a, D, sms, dev, static_cast<cudaStream_t>(stream), ls.pdl) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return SKINNY_ERR_LAUNCH;
+    }
+    return SKINNY_OK;
+}
+
 const char *skinny_status_string(int status) {
     switch (status) {
         case SKINNY_OK: return "ok";
@@ -657,6 +910,7 @@ const char *skinny_status_string(int status) {
         case SKINNY_ERR_ALLOC: return "scratch allocation failed";
         case SKINNY_ERR_TIMEOUT: return "a kernel's bounded internal wait ran out";
         case SKINNY_ERR_ARG: return "a scalar argument is invalid";
+        case SKINNY_ERR_INDEX: return "a kernel met an index out of range in device memory";
         default: return "unknown status";
     }
 }
@@ -704,9 +958,18 @@ int skinny_device_error(int device, int *word) {
         st = SKINNY_ERR_DEVICE;
     }
     if (reduce_word) value |= kErrReduceExchange;
+    // The words of the kernels that read indices from device memory.
+    int rope_word = 0, attention_word = 0;
+    if (st == SKINNY_OK && (rope_error_word(&rope_word, true) != cudaSuccess ||
+                            attention_error_word(&attention_word, true) != cudaSuccess)) {
+        cudaGetLastError();
+        st = SKINNY_ERR_DEVICE;
+    }
+    if (rope_word || attention_word) value |= kErrIndex;
     cudaSetDevice(prev);
     if (word) *word = value;
     if (st != SKINNY_OK) return st;
+    if (value == kErrIndex) return SKINNY_ERR_INDEX;
     return value ? SKINNY_ERR_TIMEOUT : SKINNY_OK;
 }
 

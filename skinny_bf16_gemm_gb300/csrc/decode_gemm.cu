@@ -37,6 +37,7 @@
 
 #include <mutex>
 
+#include "epilogue.cuh"
 #include "kernels.h"
 #include "plan.cuh"
 #include "ptx.cuh"
@@ -174,7 +175,10 @@ __device__ __forceinline__ void store_tile_staged(const float (&v)[MP], uint16_t
     }
 }
 
-template <int MP, int STAGES>
+// EPI: the epilogue of epilogue.cuh. A template so that the plain kernel keeps its
+// registers; the bias and residual of a tile's column are loaded before the wait
+// for its accumulator, so their latency hides behind the weight stream.
+template <int MP, int STAGES, bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_gemm_kernel(const __grid_constant__ CUtensorMap w_map,
                        const __grid_constant__ CUtensorMap x_map, const GemmArgs args) {
@@ -403,6 +407,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool staged = kStagedOut && (reinterpret_cast<uintptr_t>(args.out) & 15) == 0 &&
                             (g.N & 7) == 0;
 
+        // EPI: this thread's column of the current tile: the bias, and the residual's
+        // rows two to a register.
+        [[maybe_unused]] uint32_t res[EPI ? MP / 2 : 1];
+        [[maybe_unused]] float bias = 0.0f;
+        auto load_epilogue = [&](int n) {
+            if constexpr (EPI) {
+                if (n >= g.N) return;
+                if (args.epi.bias != nullptr) bias = bf16_value(args.epi.bias[n]);
+                if (args.epi.residual != nullptr) {
+#pragma unroll
+                    for (int m = 0; m < MP; m += 2) {
+                        const uint16_t *src = args.epi.residual + static_cast<size_t>(m) * g.N + n;
+                        const uint32_t lo = m < g.M ? src[0] : 0u;
+                        const uint32_t hi = m + 1 < g.M ? src[g.N] : 0u;
+                        res[m / 2] = lo | (hi << 16);
+                    }
+                }
+            }
+        };
+        // The value output element (m, this thread's column) is rounded from.
+        auto value = [&](float v, int m) -> float {
+            if constexpr (EPI) {
+                if (args.epi.bias != nullptr) v = __fadd_rn(v, bias);
+                v = activate(v, args.epi.activation);
+                if (args.epi.residual != nullptr)
+                    v = __fadd_rn(v, bf16_value((m & 1) ? res[m / 2] >> 16 : res[m / 2] & 0xFFFFu));
+                return v;
+            } else {
+                return output_value(v, args);
+            }
+        };
+
         // Finish split tile t. This CTA holds the tile's first K blocks, so the
         // tile is its last piece: its own partial is in registers and the ring
         // is free. Wait until the other contributors have published their
@@ -468,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int m = 0; m < MP; ++m)
                     if (m < g.M)
-                        args.out[static_cast<size_t>(m) * g.N + n] = to_bf16_bits(output_value(sum[m], args));
+                        args.out[static_cast<size_t>(m) * g.N + n] = to_bf16_bits(value(sum[m], m));
             }
             return true;
         };
@@ -482,6 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int my_slot = 2 * cta + (p.tile == start.t ? 0 : 1);  // plan.cuh partial_slot
             const int first_peer_slot =
                 first + 1 + etid <= last ? partial_slot(g, first + 1 + etid, p.tile) : 0;
+            // A piece from the tile's first K block on is the one that stores the tile.
+            if (EPI && p.kb0 == 0 && !args.publish_only) load_epilogue(p.tile * kBlockN + row);
             const int b = q & 1;
             const uint32_t aph = (q >> 1) & 1;
             const int r = bounded_wait(bar_acc_full + 8 * b, aph, abort_flag, limit);
@@ -509,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Whole tile in this CTA: round once and store.
                 if (kStagedOut && staged && q == pieces - 1) {
 #pragma unroll
-                    for (int m = 0; m < MP; ++m) acc[m] = output_value(acc[m], args);
+                    for (int m = 0; m < MP; ++m) acc[m] = value(acc[m], m);
                     store_tile_staged<MP>(acc, args.out, g.M, g.N, p.tile, row, etid, sbase);
                     continue;
                 }
@@ -518,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int m = 0; m < MP; ++m)
                         if (m < g.M)
                             args.out[static_cast<size_t>(m) * g.N + n] =
-                                to_bf16_bits(output_value(acc[m], args));
+                                to_bf16_bits(value(acc[m], m));
                 }
                 continue;
             }
@@ -589,15 +627,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int MP, int STAGES>
-cudaError_t launch_variant(const CUtensorMap &w_map, const CUtensorMap &x_map,
+template <int MP, int STAGES, bool EPI>
+cudaError_t launch_kernel(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            const GemmArgs &args, int ctas, cudaStream_t stream, bool pdl,
                            int device) {
     using L = Layout<MP, STAGES>;
     static bool configured[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (!configured[device]) {
-        cudaError_t e = cudaFuncSetAttribute(decode_gemm_kernel<MP, STAGES>,
+        cudaError_t e = cudaFuncSetAttribute(decode_gemm_kernel<MP, STAGES, EPI>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              L::kDynamicBytes);
         if (e != cudaSuccess) return e;
@@ -613,7 +651,16 @@ cudaError_t launch_variant(const CUtensorMap &w_map, const CUtensorMap &x_map,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_gemm_kernel<MP, STAGES>, w_map, x_map, args);
+    return cudaLaunchKernelEx(&cfg, decode_gemm_kernel<MP, STAGES, EPI>, w_map, x_map, args);
+}
+
+template <int MP, int STAGES>
+cudaError_t launch_variant(const CUtensorMap &w_map, const CUtensorMap &x_map,
+                           const GemmArgs &args, int ctas, cudaStream_t stream, bool pdl,
+                           int device) {
+    if (args.epilogue)
+        return launch_kernel<MP, STAGES, true>(w_map, x_map, args, ctas, stream, pdl, device);
+    return launch_kernel<MP, STAGES, false>(w_map, x_map, args, ctas, stream, pdl, device);
 }
 
 // Deep rings: about 185 KB for 16 rows, near the 227 KB a CTA may use for 32 and

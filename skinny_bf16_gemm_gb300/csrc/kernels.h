@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "epilogue.cuh"
+
 namespace skinny {
 
 // Bits of the device error word (one per waiting role that gave up).
@@ -17,6 +19,7 @@ enum ErrorBits : int {
     kErrSelftest = 32,      // the watchdog self-test's deliberate wait ran out
     kErrUnknown = 64,       // the host-mapped word was set but the device word was not
     kErrReduceExchange = 128,  // reduce: a cluster exchange wait ran out
+    kErrIndex = 256,  // a position, slot, length or page index on the device was out of range
 };
 
 struct GemmArgs {
@@ -47,6 +50,9 @@ struct GemmArgs {
     unsigned *gemm_done;
     int l2_after_reduce;
     int clear_gemm_done;  // 1: clear the word once the previous kernel is complete
+    // epilogue = 1: bias, activation and residual (epilogue.cuh) on the FP32 sum.
+    int epilogue;
+    Epilogue epi;
 };
 
 // Default and largest l2_lead. Measured on GB300: 6 suits back-to-back GEMMs
@@ -99,9 +105,9 @@ cudaError_t launch_reduce_rmsnorm(const void *partials, int TP, const void *resi
                                   float eps, int ctas_per_row, cudaStream_t stream, bool pdl);
 
 // Finish a publish-only decode GEMM: out[M, N] = the partials added in K order,
-// rounded once to BF16.
-cudaError_t launch_splitk_finish(const SplitKPartials &fix, uint16_t *out, cudaStream_t stream,
-                                 bool pdl);
+// rounded once to BF16, after the epilogue's steps if epi is given.
+cudaError_t launch_splitk_finish(const SplitKPartials &fix, uint16_t *out, const Epilogue *epi,
+                                 cudaStream_t stream, bool pdl);
 
 // The same with slot 0 made from a publish-only GEMM's FP32 partials (added in
 // K order, rounded once, and written to slot 0 of `partials`).
@@ -126,5 +132,53 @@ cudaError_t reduce_error_word(int *value, bool clear);
 // Gather TP shards [TP, M, S] into rows [M, TP * S] (S a multiple of 8).
 cudaError_t launch_gather(const void *shards, int TP, int M, int S, void *out,
                           cudaStream_t stream, bool pdl);
+
+// Per-head norm, rotation and cache append (qk_norm_rope_bf16). Strides in elements.
+struct RopeArgs {
+    const uint16_t *qkv;  // rows of q heads, key heads, value heads
+    long long qkv_stride;
+    int rows, q_heads, kv_heads, head_dim;
+    const uint16_t *q_gamma, *k_gamma;  // [head_dim] or nullptr: no norm
+    float eps;
+    const float *rope;  // [max_pos][rot_dim]: rot_dim / 2 cosines, then sines
+    int max_pos, rot_dim, interleaved;
+    const int *positions;
+    uint16_t *q_out;
+    long long q_stride;
+    uint16_t *k_out;  // or nullptr
+    long long k_stride;
+    uint16_t *k_cache, *v_cache;  // both or neither
+    int num_pages, page_size;
+    long long page_stride, token_stride, head_stride;
+    const long long *slots;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs &a, cudaStream_t stream, bool pdl);
+cudaError_t rope_error_word(int *value, bool clear);
+
+// Decode attention over a paged cache (decode_attention_bf16). Strides in elements.
+struct AttentionArgs {
+    const uint16_t *q;  // rows of q_heads * head_dim
+    long long q_stride;
+    const uint16_t *k, *v;
+    int num_pages, page_size;
+    long long page_stride, token_stride, head_stride;
+    const int *block_table;  // [rows][capacity / page_size]
+    long long table_stride;
+    const int *lengths;
+    int rows, q_heads, kv_heads;
+    int group;        // query heads per key head
+    int head_blocks;  // blocks the group is cut into, of block_heads heads at most
+    int block_heads;
+    int capacity;     // tokens a row's table holds
+    int window, sinks;
+    float scale_log2;  // scale * log2(e)
+    uint16_t *out;     // [rows][q_heads][head_dim]
+    float *lse;        // [rows][q_heads] or nullptr
+    unsigned *counters;  // workspace: two per slot, zero between calls
+    float *partials;     // workspace: kAttnSlotFloats per slot, two slots per CTA
+};
+cudaError_t launch_decode_attention(const AttentionArgs &a, int head_dim, int num_sms, int device,
+                                    cudaStream_t stream, bool pdl);
+cudaError_t attention_error_word(int *value, bool clear);
 
 }  // namespace skinny

@@ -5,10 +5,13 @@
 //
 // One thread per 8 consecutive output columns of one row (all in one 128-column
 // tile): two 16-byte loads per contributor, up to 4 contributors in flight, one
-// 16-byte store (scalar stores at a ragged right edge or an unaligned out).
+// 16-byte store (scalar stores at a ragged right edge or an unaligned out). EPI: the
+// epilogue of epilogue.cuh on each sum; out may be the residual itself (each element
+// is read by the thread that writes it, before it does), so neither is restrict.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "epilogue.cuh"
 #include "kernels.h"
 #include "plan.cuh"
 #include "ptx.cuh"
@@ -18,8 +21,9 @@ namespace {
 
 constexpr int kThreads = 128;
 
+template <bool EPI>
 __global__ void __launch_bounds__(kThreads)
-    splitk_finish_kernel(SplitKPartials fix, uint16_t *__restrict__ out, int vector_out) {
+    splitk_finish_kernel(SplitKPartials fix, uint16_t *out, int vector_out, Epilogue epi) {
     ptx::pdl_launch_dependents();
     const int frag = blockIdx.x * kThreads + threadIdx.x;
     const int m = blockIdx.y;
@@ -52,6 +56,16 @@ __global__ void __launch_bounds__(kThreads)
             for (int j = 0; j < 8; ++j) a[j] = c0 + q == first ? u[j] : __fadd_rn(a[j], u[j]);
         }
     }
+    if constexpr (EPI) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (col + j >= fix.N) break;
+            if (epi.bias != nullptr) a[j] = __fadd_rn(a[j], bf16_value(epi.bias[col + j]));
+            a[j] = activate(a[j], epi.activation);
+            if (epi.residual != nullptr)
+                a[j] = __fadd_rn(a[j], bf16_value(epi.residual[static_cast<size_t>(m) * fix.N + col + j]));
+        }
+    }
     uint16_t b[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) b[j] = __bfloat16_as_ushort(__float2bfloat16_rn(a[j]));
@@ -69,8 +83,8 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-cudaError_t launch_splitk_finish(const SplitKPartials &fix, uint16_t *out, cudaStream_t stream,
-                                 bool pdl) {
+cudaError_t launch_splitk_finish(const SplitKPartials &fix, uint16_t *out, const Epilogue *epi,
+                                 cudaStream_t stream, bool pdl) {
     const int frags = (fix.N + 7) / 8;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((frags + kThreads - 1) / kThreads, fix.M, 1);
@@ -82,7 +96,9 @@ cudaError_t launch_splitk_finish(const SplitKPartials &fix, uint16_t *out, cudaS
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     const int vector_out = (fix.N % 8 == 0 && (reinterpret_cast<uintptr_t>(out) % 16) == 0) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, splitk_finish_kernel, fix, out, vector_out);
+    if (epi != nullptr)
+        return cudaLaunchKernelEx(&cfg, splitk_finish_kernel<true>, fix, out, vector_out, *epi);
+    return cudaLaunchKernelEx(&cfg, splitk_finish_kernel<false>, fix, out, vector_out, Epilogue{});
 }
 
 }  // namespace skinny
