@@ -365,7 +365,7 @@ typedef struct {
  *              with q_stride == qkv_stride (in place).
  *   k_out      rows of kv_heads * head_dim, k_stride apart, or NULL. May be the key
  *              heads of qkv in place (qkv + q_heads * head_dim, k_stride == qkv_stride).
- *   cache      host pointer, or NULL: nothing is appended. kv_heads and head_dim as
+ *   cache      cache.k and cache.v NULL: nothing is appended. kv_heads and head_dim as
  *              in the call; along an axis longer than one, its elements must not
  *              overlap (stride >= head_dim).
  *   slots      [M] int64, with a cache: row m's key and value heads go to token
@@ -397,7 +397,7 @@ typedef struct {
     long long q_stride;
     void *k_out;
     long long k_stride;
-    const skinny_kv_cache *cache;
+    skinny_kv_cache cache;
     const void *slots;
 } skinny_qk_norm_rope_args;
 SKINNY_API int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *args,
@@ -412,8 +412,8 @@ SKINNY_API int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *args,
  *
  *   q            rows of q_heads * head_dim BF16, q_stride elements apart (the query
  *                heads of qk_norm_rope_bf16, in place in the QKV rows or not). Query
- *                head h reads key head h / (q_heads / cache->kv_heads).
- *   cache        host pointer: the keys and values (the new token's among them).
+ *                head h reads key head h / (q_heads / cache.kv_heads).
+ *   cache        the keys and values (the new token's among them).
  *   block_table  [rows, table_width] int32, table_stride entries from row to row:
  *                token j of row r is token j % page_size of page
  *                block_table[r][j / page_size]. Rows may share pages: the drafted
@@ -452,7 +452,7 @@ typedef struct {
     const void *q;
     long long q_stride;
     int rows, q_heads;
-    const skinny_kv_cache *cache;
+    skinny_kv_cache cache;
     const void *block_table;
     long long table_stride;
     int table_width;

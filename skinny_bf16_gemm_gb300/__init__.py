@@ -16,6 +16,7 @@ operations raises.
 """
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(PKG, "libskinny.so")
@@ -79,19 +80,27 @@ class QkNormRopeArgs(ctypes.Structure):
                 ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
                 ("positions", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
                 ("q_stride", ctypes.c_longlong), ("k_out", ctypes.c_void_p),
-                ("k_stride", ctypes.c_longlong), ("cache", ctypes.POINTER(KVCacheArgs)),
+                ("k_stride", ctypes.c_longlong), ("cache", KVCacheArgs),
                 ("slots", ctypes.c_void_p)]
 
 
 class DecodeAttentionArgs(ctypes.Structure):
     """skinny_decode_attention_args."""
     _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("rows", ctypes.c_int),
-                ("q_heads", ctypes.c_int), ("cache", ctypes.POINTER(KVCacheArgs)),
+                ("q_heads", ctypes.c_int), ("cache", KVCacheArgs),
                 ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
                 ("table_width", ctypes.c_int), ("lengths", ctypes.c_void_p),
                 ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float),
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+# The same two structures as one packed string each: a third of the host time of
+# filling a ctypes.Structure field by field.
+_CACHE = "PPiiiiqqq"
+_pack_rope = struct.Struct("@PqiiiiPPfPiiiPPqPq" + _CACHE + "P").pack
+_pack_attention = struct.Struct("@Pqii" + _CACHE + "PqiPiifPPPN").pack
+_NO_CACHE = (0,) * 9
 
 
 _lib = None
@@ -126,9 +135,9 @@ def load_library(path: str = LIBRARY):
     lib.decode_gemm_bf16_reduce_rmsnorm_ex.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32,
                                                        f32, op, vp]
     lib.decode_gemm_bf16_reduce_rmsnorm_ex.restype = i32
-    lib.qk_norm_rope_bf16.argtypes = [ctypes.POINTER(QkNormRopeArgs), op, vp]
+    lib.qk_norm_rope_bf16.argtypes = [vp, op, vp]
     lib.qk_norm_rope_bf16.restype = i32
-    lib.decode_attention_bf16.argtypes = [ctypes.POINTER(DecodeAttentionArgs), op, vp]
+    lib.decode_attention_bf16.argtypes = [vp, op, vp]
     lib.decode_attention_bf16.restype = i32
     lib.skinny_attention_workspace_bytes.argtypes = [i32]
     lib.skinny_attention_workspace_bytes.restype = ctypes.c_size_t
@@ -162,7 +171,8 @@ def status_string(status: int) -> str:
 def _stream_handle(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # torch.cuda.current_stream() without the Stream object it makes (3 us a call).
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -179,7 +189,7 @@ def _bf16_cuda(t, name, shape=None):
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -345,45 +355,48 @@ def gather_shards_bf16(shards, out, stream=None):
 
 
 def _rows(t, name, width=None):
-    """A CUDA bfloat16 tensor whose trailing dimensions are contiguous within a row: the
+    """A CUDA bfloat16 tensor whose rows (all but its first axis) are contiguous: the
     stride between rows, in elements (the row's width for a single row)."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
+    shape, stride = t.shape, t.stride()
     n = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != n:
+    for i in range(len(shape) - 1, 0, -1):
+        if stride[i] != n and shape[i] != 1:
             raise ValueError(f"{name}'s rows must be contiguous")
-        n *= size
+        n *= shape[i]
     if width is not None and n != width:
         raise ValueError(f"{name} has rows of {n}, expected {width}")
-    return t.stride(0) if t.shape[0] > 1 else n
+    return stride[0] if shape[0] > 1 else n
 
 
 def _plain_cuda(t, name, dtype, shape):
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor (got {t.dtype} on {t.device})")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _cache_args(k_cache, v_cache):
-    """The KVCacheArgs of two [pages, page_size, kv_heads, head_dim] views."""
+def _cache_fields(k_cache, v_cache):
+    """The fields of skinny_kv_cache for two [pages, page_size, kv_heads, head_dim] views."""
     import torch
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != torch.bfloat16 or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
+    bf16 = torch.bfloat16
+    if k_cache.dtype != bf16 or v_cache.dtype != bf16 or not (k_cache.is_cuda and v_cache.is_cuda):
+        raise TypeError("k_cache and v_cache must be CUDA bfloat16 tensors")
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must be "
                          "[pages, page_size, kv_heads, head_dim]")
-    # The stride of an axis of one element says nothing.
-    ks, vs = ([0 if n == 1 else st for n, st in zip(shape, t.stride())] for t in (k_cache, v_cache))
-    if ks != vs or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
-        raise ValueError("k_cache and v_cache must have the same strides, 1 along head_dim")
-    return KVCacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), *shape, *ks[:3])
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if ks != vs or ks[3] != 1 or (ks[0] | ks[1] | ks[2]) & 7:
+        # The stride of an axis of one element says nothing.
+        ks, vs = ([0 if n == 1 else st for n, st in zip(shape, t)] for t in (ks, vs))
+        if ks != vs or (ks[3] != 1 and shape[3] != 1):
+            raise ValueError("k_cache and v_cache must have the same strides, 1 along head_dim")
+    return k_cache.data_ptr(), v_cache.data_ptr(), *shape, ks[0], ks[1], ks[2]
 
 
 def qk_norm_rope_bf16(qkv, q_heads, kv_heads, q_gamma, k_gamma, rope, positions, q_out, k_out=None,
@@ -407,33 +420,33 @@ def qk_norm_rope_bf16(qkv, q_heads, kv_heads, q_gamma, k_gamma, rope, positions,
     D = qkv.shape[1] // (q_heads + 2 * kv_heads)
     if q_out.shape[0] != M or (k_out is not None and k_out.shape[0] != M):
         raise ValueError(f"q_out and k_out must have {M} rows")
-    for g, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
-        if g is not None:
-            _bf16_cuda(g, name, (D,))
-    a = QkNormRopeArgs(qkv=qkv.data_ptr(), qkv_stride=qkv_stride, M=M, q_heads=q_heads,
-                       kv_heads=kv_heads, head_dim=D, eps=eps, interleaved=bool(interleaved),
-                       q_out=q_out.data_ptr(), q_stride=_rows(q_out, "q_out", q_heads * D))
     if q_gamma is not None:
-        a.q_gamma = q_gamma.data_ptr()
+        _bf16_cuda(q_gamma, "q_gamma", (D,))
     if k_gamma is not None:
-        a.k_gamma = k_gamma.data_ptr()
+        _bf16_cuda(k_gamma, "k_gamma", (D,))
+    max_pos = rot_dim = 0
     if rope is not None:
         if rope.dim() != 2:
             raise ValueError(f"rope must be [max_pos, rot_dim], got {tuple(rope.shape)}")
         _plain_cuda(rope, "rope", torch.float32, rope.shape)
         _plain_cuda(positions, "positions", torch.int32, (M,))
-        a.rope, a.max_pos, a.rot_dim = rope.data_ptr(), rope.shape[0], rope.shape[1]
-        a.positions = positions.data_ptr()
-    if k_out is not None:
-        a.k_out, a.k_stride = k_out.data_ptr(), _rows(k_out, "k_out", kv_heads * D)
+        max_pos, rot_dim = rope.shape
+    cache = _NO_CACHE
     if k_cache is not None or v_cache is not None:
         if k_cache is None or v_cache is None or slots is None:
             raise ValueError("k_cache, v_cache and slots go together")
-        cache = _cache_args(k_cache, v_cache)
+        cache = _cache_fields(k_cache, v_cache)
         _plain_cuda(slots, "slots", torch.int64, (M,))
-        a.cache, a.slots = ctypes.pointer(cache), slots.data_ptr()
+    a = _pack_rope(
+        qkv.data_ptr(), qkv_stride, M, q_heads, kv_heads, D,
+        0 if q_gamma is None else q_gamma.data_ptr(), 0 if k_gamma is None else k_gamma.data_ptr(),
+        eps, 0 if rope is None else rope.data_ptr(), max_pos, rot_dim, bool(interleaved),
+        0 if rope is None else positions.data_ptr(), q_out.data_ptr(),
+        _rows(q_out, "q_out", q_heads * D), 0 if k_out is None else k_out.data_ptr(),
+        0 if k_out is None else _rows(k_out, "k_out", kv_heads * D), *cache,
+        0 if cache is _NO_CACHE else slots.data_ptr())
     o = _opts(pdl, None)
-    st = load_library().qk_norm_rope_bf16(ctypes.byref(a), None if o is None else ctypes.byref(o),
+    st = load_library().qk_norm_rope_bf16(a, None if o is None else ctypes.byref(o),
                                           _stream_handle(stream))
     _check(st, "qk_norm_rope_bf16")
     return q_out
@@ -480,17 +493,18 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
     """
     import torch
     q_stride = _rows(q, "q")
-    if q.dim() != 3:
-        raise ValueError(f"q must be [rows, q_heads, head_dim], got {tuple(q.shape)}")
-    rows, q_heads, D = q.shape
-    cache = _cache_args(k_cache, v_cache)
-    if cache.head_dim != D:
-        raise ValueError(f"q has heads of {D}, the cache of {cache.head_dim}")
-    _bf16_cuda(out, "out", (rows, q_heads, D))
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must be [rows, q_heads, head_dim], got {tuple(shape)}")
+    rows, q_heads, D = shape
+    cache = _cache_fields(k_cache, v_cache)
+    if cache[5] != D:
+        raise ValueError(f"q has heads of {D}, the cache of {cache[5]}")
+    _bf16_cuda(out, "out", shape)
     if block_table.dtype != torch.int32 or not block_table.is_cuda:
         raise TypeError("block_table must be a CUDA int32 tensor")
     if block_table.dim() != 2 or block_table.shape[0] != rows or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            (block_table.stride(1) != 1 and block_table.shape[1] > 1):
         raise ValueError(f"block_table must be [{rows}, table_width] with contiguous rows")
     _plain_cuda(lengths, "lengths", torch.int32, (rows,))
     if lse is not None:
@@ -499,15 +513,13 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
     if workspace is None:
         workspace = _own_workspace(q.device.index, handle)
     width = block_table.shape[1]
-    a = DecodeAttentionArgs(
-        q.data_ptr(), q_stride, rows, q_heads, ctypes.pointer(cache), block_table.data_ptr(),
+    a = _pack_attention(
+        q.data_ptr(), q_stride, rows, q_heads, *cache, block_table.data_ptr(),
         block_table.stride(0) if rows > 1 else width, width, lengths.data_ptr(), window, sinks,
-        D ** -0.5 if scale is None else scale, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size())
+        D ** -0.5 if scale is None else scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes)
     o = _opts(pdl, None)
-    st = load_library().decode_attention_bf16(ctypes.byref(a), None if o is None else ctypes.byref(o),
-                                              handle)
+    st = load_library().decode_attention_bf16(a, None if o is None else ctypes.byref(o), handle)
     _check(st, "decode_attention_bf16")
     return out
 

@@ -702,8 +702,11 @@ int gather_shards_bf16(const void *shards, int TP, int M, int S, void *out, void
 
 int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opts *opts,
                       void *stream) {
-    if (!p || !p->qkv || !p->q_out || (p->rot_dim != 0 && (!p->rope || !p->positions)) ||
-        (p->cache && !p->slots))
+    if (!p) return SKINNY_ERR_NULL;
+    const skinny_kv_cache *cache = &p->cache;
+    const bool has_cache = cache->k || cache->v;
+    if (!p->qkv || !p->q_out || (p->rot_dim != 0 && (!p->rope || !p->positions)) ||
+        (has_cache && !p->slots))
         return SKINNY_ERR_NULL;
     const int D = p->head_dim;
     if (p->M < 1 || p->q_heads < 1 || p->q_heads > kMaxHeads || p->kv_heads < 1 ||
@@ -726,10 +729,10 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
         return SKINNY_ERR_ALIGN;
     int st;
     size_t pool = 0;
-    if (p->cache) {
-        if (p->cache->kv_heads != p->kv_heads || p->cache->head_dim != D) return SKINNY_ERR_SHAPE;
-        if ((st = check_cache(p->cache, true, &pool))) return st;
-        if (p->cache->k == p->cache->v) return SKINNY_ERR_ALIAS;
+    if (has_cache) {
+        if (cache->kv_heads != p->kv_heads || cache->head_dim != D) return SKINNY_ERR_SHAPE;
+        if ((st = check_cache(cache, true, &pool))) return st;
+        if (cache->k == cache->v) return SKINNY_ERR_ALIAS;
     }
     // Every output against every input and the other outputs; q_out and k_out may be
     // their own heads of qkv in place.
@@ -739,15 +742,15 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
         {p->k_gamma, static_cast<size_t>(D) * 2},
         {p->rot_dim ? p->rope : nullptr, static_cast<size_t>(p->max_pos) * p->rot_dim * 4},
         {p->rot_dim ? p->positions : nullptr, static_cast<size_t>(p->M) * 4},
-        {p->cache ? p->slots : nullptr, static_cast<size_t>(p->M) * 8}};
+        {has_cache ? p->slots : nullptr, static_cast<size_t>(p->M) * 8}};
     const bool q_in_place = p->q_out == p->qkv && p->q_stride == p->qkv_stride;
     const bool k_in_place = p->k_out == static_cast<const uint16_t *>(p->qkv) + q_width &&
                             p->k_stride == p->qkv_stride;
     const struct { const void *p; size_t n; bool in_place; } outs[] = {
         {p->q_out, row_span(p->M, p->q_stride, q_width), q_in_place},
         {p->k_out, p->k_out ? row_span(p->M, p->k_stride, kv_width) : 0, k_in_place},
-        {p->cache ? p->cache->k : nullptr, pool, false},
-        {p->cache ? p->cache->v : nullptr, pool, false}};
+        {has_cache ? cache->k : nullptr, pool, false},
+        {has_cache ? cache->v : nullptr, pool, false}};
     for (int i = 0; i < 4; ++i) {
         if (!outs[i].p) continue;
         for (int j = 0; j < 6; ++j)
@@ -787,14 +790,14 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
     a.q_stride = p->q_stride;
     a.k_out = static_cast<uint16_t *>(p->k_out);
     a.k_stride = p->k_stride;
-    if (p->cache) {
-        a.k_cache = static_cast<uint16_t *>(p->cache->k);
-        a.v_cache = static_cast<uint16_t *>(p->cache->v);
-        a.num_pages = p->cache->num_pages;
-        a.page_size = p->cache->page_size;
-        a.page_stride = p->cache->page_stride;
-        a.token_stride = p->cache->token_stride;
-        a.head_stride = p->cache->head_stride;
+    if (has_cache) {
+        a.k_cache = static_cast<uint16_t *>(cache->k);
+        a.v_cache = static_cast<uint16_t *>(cache->v);
+        a.num_pages = cache->num_pages;
+        a.page_size = cache->page_size;
+        a.page_stride = cache->page_stride;
+        a.token_stride = cache->token_stride;
+        a.head_stride = cache->head_stride;
         a.slots = static_cast<const long long *>(p->slots);
     }
     if (launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream), ls.pdl) != cudaSuccess) {
@@ -810,9 +813,9 @@ size_t skinny_attention_workspace_bytes(int num_sms) {
 
 int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_launch_opts *opts,
                           void *stream) {
-    if (!p || !p->q || !p->cache || !p->block_table || !p->lengths || !p->out || !p->workspace)
+    if (!p || !p->q || !p->block_table || !p->lengths || !p->out || !p->workspace)
         return SKINNY_ERR_NULL;
-    const skinny_kv_cache *c = p->cache;
+    const skinny_kv_cache *c = &p->cache;
     size_t pool = 0;
     int st = check_cache(c, false, &pool);
     if (st) return st;
@@ -826,7 +829,7 @@ int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_la
     if (capacity >= (1ll << 30)) return SKINNY_ERR_SHAPE;
     const int group = p->q_heads / c->kv_heads, most = 8 * attn_max_nb(D);
     const int head_blocks = (group + most - 1) / most;
-    const long long tiles = (capacity + kAttnTile - 1) / kAttnTile;
+    const long long tiles = (capacity + kAttnMinTile - 1) / kAttnMinTile;
     if (tiles * p->rows * c->kv_heads * head_blocks >= (1ll << 31)) return SKINNY_ERR_SHAPE;
     const long long q_width = static_cast<long long>(p->q_heads) * D;
     if (p->q_stride < q_width || p->q_stride > (1ll << 30)) return SKINNY_ERR_SHAPE;
@@ -868,6 +871,7 @@ int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_la
     a.v = static_cast<const uint16_t *>(c->v);
     a.num_pages = c->num_pages;
     a.page_size = c->page_size;
+    a.page_shift = (c->page_size & (c->page_size - 1)) == 0 ? __builtin_ctz(c->page_size) : -1;
     a.page_stride = c->page_stride;
     a.token_stride = c->token_stride;
     a.head_stride = c->head_stride;
@@ -881,6 +885,7 @@ int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_la
     a.head_blocks = head_blocks;
     a.block_heads = (group + head_blocks - 1) / head_blocks;
     a.capacity = static_cast<int>(capacity);
+    a.wide = pool > (1ull << 36);
     a.window = p->window;
     a.sinks = p->sinks;
     a.scale_log2 = p->scale * 1.44269504088896341f;
@@ -888,7 +893,7 @@ int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_la
     a.lse = static_cast<float *>(p->lse);
     a.counters = static_cast<unsigned *>(p->workspace);
     a.partials = reinterpret_cast<float *>(static_cast<char *>(p->workspace) +
-                                           attn_counter_bytes(attn_max_ctas(sms)));
+                                           attn_counter_bytes(sms));
     if (launch_decode_attention(a, D, sms, dev, static_cast<cudaStream_t>(stream), ls.pdl) !=
         cudaSuccess) {
         cudaGetLastError();

@@ -7,14 +7,13 @@
 // so every key and value is read once. Bound by HBM: 4 D bytes a token and key head
 // against 4 G D flops (G heads sharing) -- 8 flops a byte for G = 8.
 //
-// CTAs of 4 warps, two to an SM (one for heads over 128), take equal ranges of
-// 64-token tiles (attention_plan.cuh). A warp streams its own 16 tokens of every
-// tile through a private ring of cp.async stages and keeps its own maximum, sum and
-// accumulator, so nothing in the main loop waits for another warp; the four are
-// joined when the piece of an item ends. The ring is filled by 16-byte copies with
+// CTAs of 4 warps take equal ranges of tiles (attention_plan.cuh). A warp streams its
+// own 16 or 32 tokens of every tile through a private ring of cp.async stages and keeps
+// its own maximum, sum and accumulator, so nothing in the main loop waits for another
+// warp; the four are joined when the piece of an item ends, while the copies of the
+// next piece go on. The ring is filled by 16-byte copies with
 // each token's address from the block table, so pages of any size, tokens at any
-// 16-byte-aligned strides and ranges that end inside a page are all the same to it;
-// rows are padded by 16 bytes, which spreads ldmatrix over the banks.
+// 16-byte-aligned strides and ranges that end inside a page are all the same to it.
 // The products run on the tensor cores with tokens (scores) and head dimension
 // (output) as the MMA's 16 rows and the query heads as its 8 columns: HBM feeds an
 // SM about 23 bytes a clock, a fraction of what these small MMAs need to be fast.
@@ -39,27 +38,41 @@
 namespace skinny {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kSub = 16;  // tokens of a warp's stage
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kAttnMaxJoin = 24;  // partials of one join: kAttnGroup, or the groups of the largest grid
+constexpr int kWarps = kAttnWarps;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxGroups = 32;   // groups of the second level of a join
+constexpr int kSnapChunk = 8;    // items of so many tiles are not cut by chunks,
+constexpr int kSnapShare = 2;    // and of so many by warps' shares
 __device__ int g_attn_err;  // nonzero: a length or page index was out of range
 
 template <int D, int NB>
 struct Shape {
-    static constexpr int kCtasPerSm = D <= 128 ? 2 : 1;
-    static constexpr int kRowBytes = D * 2 + 16;
+    // A tile is a warp's step: 16 tokens, or two such sets side by side where the
+    // registers allow (their chains of dependent instructions overlap).
+    static constexpr int kSets = NB == 1 && D <= 192 ? 2 : 1;
+    static constexpr int kSub = 16 * kSets;
+    static constexpr int kRowBytes = D * 2;
     static constexpr int kStageBytes = 2 * kSub * kRowBytes;  // keys, then values
-    static constexpr int kStages = D <= 64 ? 5 : D <= 96 ? 4 : D <= 128 ? 3 : D <= 192 ? 4 : 3;
+    static constexpr int kStages = D > 192 ? 3 : (D <= 64 ? 3 : D <= 96 ? 4 : D <= 128 ? 3 : 2) * 2 / kSets;
+    static constexpr int kSlots = kStages + 1;  // lookups on their way
     static constexpr int kHeads = 8 * NB;
-    static constexpr int kMergeStride = D + 4;  // floats: spreads the fragment stores over the banks
-    static constexpr int kRingBytes = kStages * kStageBytes;
-    static constexpr int kMlOffset = kWarps * kRingBytes;           // [kWarps][kHeads] m, then l
-    static constexpr int kScaleOffset = kMlOffset + 2 * kWarps * kHeads * 4;  // [kAttnMaxJoin][kHeads]
-    static constexpr int kPrefixOffset = kScaleOffset + kAttnMaxJoin * kHeads * 4;
-    static_assert(kHeads * kMergeStride * 4 <= kRingBytes, "a warp's accumulator reuses its ring");
-    static int bytes(int rows) { return kPrefixOffset + (rows + 1 + 8) * 4; }
+    static constexpr int kRingBytes = kStages * kStageBytes;  // per warp
+    static constexpr int kSlotFloats = attn_slot_floats(D, NB);
+    static constexpr int kMaximaAt = kHeads * D;  // in a partial: the maxima, then the sums
+    // A warp's last partial is kept in its ring, which is empty by then; one of an item
+    // that ends earlier in its share here, if there is room, else in the workspace.
+    static constexpr bool kEarlyShared = kWarps * (kRingBytes + kSlotFloats * 4) <= 216 * 1024 / attn_ctas_per_sm(D);
+    static constexpr int kEarlyOffset = kWarps * kRingBytes;
+    static constexpr int kFactorOffset = kEarlyOffset + (kEarlyShared ? kWarps * kSlotFloats * 4 : 0);
+    static constexpr int kMlOffset = kFactorOffset + kMaxGroups * kHeads * 4;  // factors [kMaxGroups][kHeads]
+    static constexpr int kLookOffset = kMlOffset + 2 * kHeads * 4;             // m, l of a join
+    static constexpr int kRowsOffset = kLookOffset + kWarps * kSlots * (kSub + 1) * 8;  // prefix, lengths
+    static_assert(kSlotFloats * 4 <= kRingBytes, "a partial fits the ring");
+    static_assert(kSub >= kAttnMinTile, "the host counts tiles of kAttnMinTile");
+    static_assert(kLookOffset % 8 == 0, "64-bit places");
+    static_assert(kRowsOffset + (2 * kAttnMaxRows + 1) * 4 + 1024 <= 232448, "a block's shared memory");
+    static int bytes(int rows) { return kRowsOffset + (2 * rows + 1) * 4; }
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -68,12 +81,18 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool full) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zeros(uint32_t dst, const void *src, bool full) {
     const int bytes = full ? 16 : 0;  // 0: the 16 bytes are zero-filled, nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -130,50 +149,71 @@ __device__ __forceinline__ Seen seen_of(int n, int window, int sinks) {
     return s;
 }
 
-// Ranges of the tile sequence: the first `extra` of `ctas` CTAs take base + 1 tiles.
-struct Ranges {
-    int ctas, base, extra;
+// x / d for 0 <= x < 2^31, d > 0 and a quotient below 2^20: the float quotient is off by
+// less than one, which the remainder's sign shows. A third of an integer division's time.
+__device__ __forceinline__ int quotient(int x, int d) {
+    const int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(d)));
+    const int r = x - q * d;
+    return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+}
+
+// An even cut of `tiles` tiles into `parts` (at most 2^20): the first `extra` parts have
+// base + 1.
+struct Cut {
+    int base, extra;
+    __device__ Cut(int tiles, int parts) {
+        base = tiles / parts;
+        extra = tiles - base * parts;
+    }
     __device__ int begin(int c) const { return c * base + min(c, extra); }
     __device__ int owner(int x) const {
-        const int cut = extra * (base + 1);
-        return x < cut ? x / (base + 1) : extra + (x - cut) / base;
+        const int at = extra * (base + 1);
+        const bool low = x < at;
+        return (low ? 0 : extra) + quotient(low ? x : x - at, low ? base + 1 : base);
     }
 };
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtasPerSm)
-    decode_attention_kernel(const AttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attention_kernel(const AttentionArgs a) {
     using S = Shape<D, NB>;
+    constexpr int kSub = S::kSub, kSets = S::kSets, kSlots = S::kSlots;
+    constexpr uint32_t kAllSeen = kSub == 32 ? 0xFFFFFFFFu : (1u << (kSub & 31)) - 1u;
     constexpr int kChunks = D / 8;            // 16-byte chunks of a token's row
     constexpr int kCopies = kSub * kChunks / 32;
     constexpr int kSteps = D / 16;
+    // Chunk c of token row r is kept at chunk c ^ swizzle(r): eight rows of one chunk
+    // then cover all banks. Rows of 96 values alternate between the two halves of the
+    // banks by themselves, so two bits are enough (and all that 12 chunks allow).
+    constexpr bool kWide = kChunks % 8 == 0;
+    auto swizzle = [](int r) { return kWide ? r & 7 : (r >> 1) & 3; };
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t sm_valid[kWarps][S::kStages];
+    __shared__ uint32_t sm_places[kWarps][kSub];
+    __shared__ int sm_scan[kWarps];
+    __shared__ int sm_key[2 * kWarps];  // items of the warps' partials, -1: none
+    __shared__ int sm_last;
     const uint32_t sbase = ptx::smem_addr(smem);
-    float *sm_m = reinterpret_cast<float *>(smem + S::kMlOffset);
-    float *sm_l = sm_m + kWarps * S::kHeads;
-    float *sm_scale = reinterpret_cast<float *>(smem + S::kScaleOffset);
-    int *prefix = reinterpret_cast<int *>(smem + S::kPrefixOffset);
-    int *sm_tmp = prefix + a.rows + 1;
+    int *prefix = reinterpret_cast<int *>(smem + S::kRowsOffset);
+    int *lengths = prefix + a.rows + 1;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int cta = blockIdx.x;
 
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
 
+    // ---- the split ----
     // Prefix sums of the rows' tiles. A length is taken within [0, capacity].
     const int per = (a.rows + kThreads - 1) / kThreads;
     const int r_lo = min(tid * per, a.rows), r_hi = min(r_lo + per, a.rows);
-    auto row_length = [&](int r) {
-        int n = __ldcg(a.lengths + r);
-        if (n < 0 || n > a.capacity) {
-            if (blockIdx.x == 0) atomicOr(&g_attn_err, 1);
-            n = n < 0 ? 0 : a.capacity;
-        }
-        return n;
-    };
     int mine = 0;
     for (int r = r_lo; r < r_hi; ++r) {
-        const int n = seen_of(row_length(r), a.window, a.sinks).count;
-        mine += (n + kAttnTile - 1) / kAttnTile;
+        int n = __ldcg(a.lengths + r);
+        if (n < 0 || n > a.capacity) {
+            if (cta == 0) atomicOr(&g_attn_err, 1);
+            n = n < 0 ? 0 : a.capacity;
+        }
+        lengths[r] = n;
+        mine += (seen_of(n, a.window, a.sinks).count + kSub - 1) / kSub;
         prefix[r + 1] = mine;
     }
     int scan = mine;
@@ -182,18 +222,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtasPerSm)
         const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
         if (lane >= o) scan += v;
     }
-    if (lane == 31) sm_tmp[warp] = scan;
+    if (lane == 31) sm_scan[warp] = scan;
+    if (tid < 2 * kWarps) sm_key[tid] = -1;
     __syncthreads();
     int before = scan - mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-        if (w < warp) before += sm_tmp[w];
+        if (w < warp) before += sm_scan[w];
     for (int r = r_lo; r < r_hi; ++r) prefix[r + 1] += before;
     if (tid == 0) prefix[0] = 0;
     __syncthreads();
 
     // Rows that see nothing: zeros, and a log-sum of -inf.
-    for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    for (int r = cta; r < a.rows; r += gridDim.x) {
         if (prefix[r + 1] != prefix[r]) continue;
         uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<size_t>(r) * a.q_heads * D);
         for (int i = tid; i < a.q_heads * kChunks; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
@@ -205,89 +246,229 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtasPerSm)
     const int items_per_row = a.kv_heads * a.head_blocks;
     const int total = prefix[a.rows] * items_per_row;  // below 2^31 (host check)
     if (total == 0) return;
-    Ranges rg;
-    rg.ctas = min(static_cast<int>(gridDim.x), total);
-    if (static_cast<int>(blockIdx.x) >= rg.ctas) return;
-    rg.base = total / rg.ctas;
-    rg.extra = total - rg.base * rg.ctas;
-    const int cta = blockIdx.x;
-    int x = rg.begin(cta);
-    const int x_end = rg.begin(cta + 1);
+    // Fewer CTAs where each would have less than kMinTiles a warp: a step costs less than
+    // a join.
+    constexpr int kMinTiles = 2;
+    const int chunks = min(static_cast<int>(gridDim.x), (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles));
+    if (cta >= chunks) return;
+    const Cut cut(total, chunks);
 
-    int row = 0;  // the row of tile x: the last one whose first tile is at or before it
-    for (int lo = 0, hi = a.rows; lo < hi;) {
-        const int mid = (lo + hi) / 2;
-        if (prefix[mid + 1] * items_per_row <= x) lo = mid + 1; else hi = mid;
-        row = lo;
-    }
-
-    const uint32_t ring = sbase + warp * S::kRingBytes;
-    float *merge = reinterpret_cast<float *>(smem + warp * S::kRingBytes);
-    __shared__ uint32_t sm_valid[kWarps][S::kStages];
-    __shared__ int sm_last;
-
-    while (x < x_end) {
-        while (prefix[row + 1] * items_per_row <= x) ++row;
-        const int row_tiles = prefix[row + 1] - prefix[row];
-        const int in_row = x - prefix[row] * items_per_row;
-        const int item = in_row / row_tiles;
-        const int tile0 = in_row - item * row_tiles;
-        const int tile1 = min(row_tiles, tile0 + x_end - x);
-        const int kv_head = item / a.head_blocks;
-        const int g0 = (item - kv_head * a.head_blocks) * a.block_heads;  // first head of the group
-        const int n_heads = min(a.block_heads, a.group - g0);
-        const int head0 = kv_head * a.group + g0;
-        const int length = min(max(__ldcg(a.lengths + row), 0), a.capacity);
-        const Seen seen = seen_of(length, a.window, a.sinks);
-        const int *table = a.block_table + static_cast<size_t>(row) * a.table_stride;
-        const uint16_t *kbase = a.k + kv_head * a.head_stride;
-        const uint16_t *vbase = a.v + kv_head * a.head_stride;
-
-        // This warp's stages: tokens [t0, t0 + 16) of every tile of the piece.
-        const int n_stages = tile1 - tile0;
-        auto issue = [&](int i) {  // stage i of the piece into the ring
-            if (i < n_stages) {
-                const int t = (tile0 + i) * kAttnTile + warp * kSub + (lane & 15);
-                long long off = -1;
-                if (t < seen.count) {
-                    const int j = t < seen.sinks ? t : t + seen.gap;
-                    const int entry = j / a.page_size;
-                    const int page = __ldcg(table + entry);
-                    if (page >= 0 && page < a.num_pages)
-                        off = page * a.page_stride + static_cast<long long>(j - entry * a.page_size) * a.token_stride;
-                    else
-                        atomicOr(&g_attn_err, 1);
-                }
-                const uint32_t valid = __ballot_sync(0xFFFFFFFFu, off >= 0);
-                if (lane == 0) sm_valid[warp][i % S::kStages] = valid;
-                const uint32_t st = ring + (i % S::kStages) * S::kStageBytes;
-#pragma unroll
-                for (int it = 0; it < kCopies; ++it) {
-                    const int id = it * 32 + lane, tok = id / kChunks, ch = id % kChunks;
-                    const long long o = __shfl_sync(0xFFFFFFFFu, off, tok);
-                    const uint32_t dst = st + tok * S::kRowBytes + ch * 16;
-                    const long long e = (o < 0 ? 0 : o) + ch * 8;
-                    cp_async16(dst, kbase + e, o >= 0);
-                    cp_async16(dst + kSub * S::kRowBytes, vbase + e, o >= 0);
-                }
+    // A place in the tile sequence: tile `tile` of item `item` (key head and head block)
+    // of row `row`.
+    struct Place {
+        int row, item, tile;
+    };
+    auto find = [&](int x) -> Place {  // x: the same in the whole warp
+        int row = 0;  // the first row that ends after tile x
+        for (;; row += 32) {
+            const int r = row + lane;
+            const unsigned over = __ballot_sync(0xFFFFFFFFu, r < a.rows && prefix[r + 1] * items_per_row > x);
+            if (over != 0) {
+                row += __ffs(over) - 1;
+                break;
             }
-            cp_async_commit();  // an empty group past the end keeps the count
-        };
-#pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+        }
+        const int tiles = prefix[row + 1] - prefix[row];
+        const int in_row = x - prefix[row] * items_per_row;
+        const int item = quotient(in_row, tiles);
+        return {row, item, in_row - item * tiles};
+    };
+    // The end of a chunk or share that would be at tile x: not within an item of at most
+    // `most` tiles (a few tiles more or less cost less than a join).
+    auto snap = [&](int x, int most) -> int {
+        if (x <= 0 || x >= total) return x;
+        const Place p = find(x);
+        const int tiles = prefix[p.row + 1] - prefix[p.row];
+        if (p.tile == 0 || tiles > most) return x;
+        return x - p.tile + (2 * p.tile < tiles ? 0 : tiles);
+    };
+    // This warp's share [x, x_end).
+    int x, x_end;
+    {
+        const int b = snap(cut.begin(cta), kSnapChunk), n = snap(cut.begin(cta + 1), kSnapChunk) - b;
+        x = snap(b + n * warp / kWarps, kSnapShare);
+        x_end = snap(b + n * (warp + 1) / kWarps, kSnapShare);
+        if (warp == 0) x = b;
+        if (warp == kWarps - 1) x_end = b + n;
+    }
+    auto next_item = [&](Place &p) {  // only where a further tile exists
+        p.tile = 0;
+        if (++p.item == items_per_row) {
+            p.item = 0;
+            do ++p.row; while (prefix[p.row + 1] == prefix[p.row]);
+        }
+    };
+    Place here = x < x_end ? find(x) : Place{0, 0, 0};
 
-        // Queries as the MMA's B: head lane / 4 of each block of 8, values 2 (lane % 4) on.
-        uint32_t qf[kSteps][NB][2];
+    // ---- the copies: one stage a tile ----
+    // A stage is refilled as soon as it is read, so that while a warp waits its whole ring
+    // is in flight. Lane t < kSub finds token t's address. Its page index comes by cp.async
+    // too, kStages steps before the copy that needs it and in the group that is waited for
+    // by then, so the block table's latency is hidden as the data's is (a lookup one step
+    // ahead, which waited a full L2 trip every step, cost up to a third of the bandwidth).
+    const uint32_t ring = sbase + warp * S::kRingBytes;
+    long long *look_head = reinterpret_cast<long long *>(smem + S::kLookOffset) + warp * kSlots;
+    int2 *look = reinterpret_cast<int2 *>(smem + S::kLookOffset + kWarps * kSlots * 8) + warp * kSlots * kSub;
+    Place ahead = here;
+    int ahead_x = x, ahead_tiles = 0;
+    Seen ahead_seen = {};
+    const int *ahead_table = nullptr;
+    long long ahead_head = 0;
+    auto enter = [&]() {  // `ahead` is at a new item
+        ahead_tiles = prefix[ahead.row + 1] - prefix[ahead.row];
+        ahead_seen = seen_of(lengths[ahead.row], a.window, a.sinks);
+        ahead_table = a.block_table + ahead.row * a.table_stride;
+        ahead_head = quotient(ahead.item, a.head_blocks) * a.head_stride;
+    };
+    if (x < x_end) enter();
+    // Look the next tile up: this lane's token's place within its page (-1: none), and on
+    // its way the page.
+    auto look_up = [&](int slot) {
+        int2 *to = look + slot * kSub + lane;
+        int in_page = -1;
+        if (ahead_x < x_end) {
+            const int t = ahead.tile * kSub + lane;
+            if (lane < kSub && t < ahead_seen.count) {
+                const int j = t < ahead_seen.sinks ? t : t + ahead_seen.gap;
+                const int e = a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size;
+                in_page = j - e * a.page_size;
+                cp_async4(ptx::smem_addr(&to->y), ahead_table + e);
+            }
+            if (lane == 0) look_head[slot] = ahead_head;
+            if (++ahead.tile == ahead_tiles && ahead_x + 1 < x_end) {
+                next_item(ahead);
+                enter();
+            }
+            ++ahead_x;
+        }
+        if (lane < kSub) to->x = in_page;
+    };
+    // Fill a stage with the tile of a lookup slot. With every token there and 16-byte chunk
+    // numbers of 32 bits, a row's place is one multiply-add away (the places go through
+    // shared memory rather than shuffles, and rows are named by the few swizzles that occur,
+    // so that the addresses need few registers); rows that are not there are zero-filled.
+    uint32_t *places = sm_places[warp];
+    auto fill = [&](int stage, int slot) {
+        const int2 at = look[slot * kSub + (lane & (kSub - 1))];
+        long long off = -1;
+        if (lane < kSub && at.x >= 0) {
+            if (at.y >= 0 && at.y < a.num_pages)
+                off = at.y * a.page_stride + at.x * a.token_stride + look_head[slot];
+            else
+                atomicOr(&g_attn_err, 1);
+        }
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, off >= 0);
+        if (lane == 0) sm_valid[warp][stage] = valid;
+        const uint32_t to = ring + stage * S::kStageBytes;
+        if (valid == kAllSeen && !a.wide) {
+            if (lane < kSub) places[lane] = static_cast<uint32_t>(off >> 3);
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < kCopies; ++it) {
+                int tok, ch, swz;
+                if constexpr (32 % kChunks == 0) {
+                    constexpr int kRows = 32 / kChunks;  // rows of one copy
+                    tok = it * kRows + lane / kChunks;
+                    ch = lane % kChunks;
+                    swz = (lane / kChunks + it % (8 / kRows) * kRows) & 7;
+                } else {
+                    tok = (it * 32 + lane) / kChunks;
+                    ch = (it * 32 + lane) % kChunks;
+                    swz = swizzle(tok);
+                }
+                const size_t e = static_cast<size_t>(places[tok]) * 16;
+                const uint32_t dst = to + (ch ^ swz) * 16 + tok * S::kRowBytes;
+                cp_async16(dst, reinterpret_cast<const uint8_t *>(a.k + ch * 8) + e);
+                cp_async16(dst + kSub * S::kRowBytes, reinterpret_cast<const uint8_t *>(a.v + ch * 8) + e);
+            }
+        } else if (valid != 0) {
+#pragma unroll 1
+            for (int it = 0; it < kCopies; ++it) {
+                const int id = it * 32 + lane, tok = id / kChunks, ch = id % kChunks;
+                const long long o = __shfl_sync(0xFFFFFFFFu, off, tok);
+                const uint32_t dst = to + tok * S::kRowBytes + (ch ^ swizzle(tok)) * 16;
+                const long long e = (o < 0 ? 0 : o) + ch * 8;
+                cp_async16_or_zeros(dst, a.k + e, o >= 0);
+                cp_async16_or_zeros(dst + kSub * S::kRowBytes, a.v + e, o >= 0);
+            }
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) look_up(i);
+    cp_async_commit();
+
+    // Queries as the MMA's B: head lane / 4 of each block of 8, values 2 (lane % 4) on.
+    uint32_t qf[kSteps][NB][2];
+    auto load_queries = [&](const Place &p) {
+        const int kv_head = quotient(p.item, a.head_blocks);
+        const int g0 = (p.item - kv_head * a.head_blocks) * a.block_heads;
+        const int n = min(a.block_heads, a.group - g0);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int h = b * 8 + lane / 4;
-            const uint16_t *q = a.q + row * a.q_stride + static_cast<long long>(head0 + h) * D + (lane & 3) * 2;
+            const unsigned *q = reinterpret_cast<const unsigned *>(
+                a.q + p.row * a.q_stride + static_cast<long long>(kv_head * a.group + g0 + h) * D + (lane & 3) * 2);
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
-                qf[ks][b][0] = h < n_heads ? __ldcg(reinterpret_cast<const unsigned *>(q + ks * 16)) : 0u;
-                qf[ks][b][1] = h < n_heads ? __ldcg(reinterpret_cast<const unsigned *>(q + ks * 16 + 8)) : 0u;
+                qf[ks][b][0] = h < n ? __ldcg(q + ks * 8) : 0u;
+                qf[ks][b][1] = h < n ? __ldcg(q + ks * 8 + 4) : 0u;
             }
         }
+    };
+    if (x < x_end) load_queries(here);
+    cp_async_wait<0>();
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) {  // tile i is in lookup slot i mod kSlots
+        fill(i, i);
+        look_up(i == 0 ? S::kStages : i - 1);
+        cp_async_commit();
+        __syncwarp();
+    }
+
+    // An item's first output head, and how many it has.
+    struct Heads {
+        size_t first;
+        int count;
+    };
+    auto heads_of = [&](int row, int item) -> Heads {
+        const int kv_head = quotient(item, a.head_blocks);
+        const int g0 = (item - kv_head * a.head_blocks) * a.block_heads;
+        return {static_cast<size_t>(row) * a.q_heads + kv_head * a.group + g0, min(a.block_heads, a.group - g0)};
+    };
+    // A fragment of the output (16 values of 8 heads) from sums and the heads' 1 / l. The
+    // transpose puts a head's values side by side in a lane.
+    auto store_out = [&](const Heads &h, int s, int b, float v0, float v1, float v2, float v3, float inv0, float inv1) {
+        const uint32_t w0 = movmatrix_trans(pack_bf16(v0 * inv0, v1 * inv1));
+        const uint32_t w1 = movmatrix_trans(pack_bf16(v2 * inv0, v3 * inv1));
+        if (b * 8 + lane / 4 < h.count) {
+            uint32_t *o = reinterpret_cast<uint32_t *>(a.out + (h.first + b * 8 + lane / 4) * D + s * 16 + (lane & 3) * 2);
+            o[0] = w0;
+            o[4] = w1;
+        }
+    };
+    auto store_lse = [&](const Heads &h, int at, float m, float l) {
+        if (a.lse != nullptr && at < h.count)
+            a.lse[h.first + at] = l > 0.0f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
+    };
+    auto inverse = [](float l) { return l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l); };
+    auto slot_at = [&](int slot) { return a.partials + static_cast<size_t>(slot) * S::kSlotFloats; };
+    // Partial e of this CTA's warps: 2 w of an item that ends within warp w's share, 2 w + 1
+    // the last of the share.
+    auto entry_at = [&](int e) -> float * {
+        if (e & 1) return reinterpret_cast<float *>(smem + (e >> 1) * S::kRingBytes);
+        if constexpr (S::kEarlyShared) return reinterpret_cast<float *>(smem + S::kEarlyOffset) + (e >> 1) * S::kSlotFloats;
+        return slot_at(2 * chunks + cta * kWarps + (e >> 1));
+    };
+
+    // ---- this warp's share ----
+    int stage = 0, step = 0;  // step: the lookup slot of this step's tile
+    while (x < x_end) {       // one item's tiles
+        const int row_tiles = prefix[here.row + 1] - prefix[here.row];
+        const int n_tiles = min(row_tiles - here.tile, x_end - x);
+        const bool whole = n_tiles == row_tiles;
+        const int row = here.row, item = here.item;
+        const bool more = x + n_tiles < x_end;
 
         float o[kSteps][NB][4];
         float m[NB][2], l[NB][2];
@@ -301,35 +482,63 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtasPerSm)
                 for (int i = 0; i < 4; ++i) o[s][b][i] = 0.0f;
         }
 
-        for (int i = 0; i < n_stages; ++i) {
-            cp_async_wait<S::kStages - 2>();
+#pragma unroll 1
+        for (int i = 0; i < n_tiles; ++i) {
+            cp_async_wait<S::kStages - 1>();
             __syncwarp();
-            issue(i + S::kStages - 1);  // into the stage read last time round
-            const uint32_t st = ring + (i % S::kStages) * S::kStageBytes;
-            const uint32_t valid = sm_valid[warp][i % S::kStages];
+            const uint32_t st = ring + stage * S::kStageBytes;
+            const uint32_t valid = sm_valid[warp][stage];
+            // Chunk 2 s + e of a row whose swizzle is in `at` already.
+            auto chunk_pair = [](uint32_t at, int s) {
+                return kWide ? (at ^ ((s & 3) << 5)) + (s >> 2) * 128 : (at ^ ((s & 1) << 5)) + (s >> 1) * 64;
+            };
 
-            // Scores: rows = tokens lane / 4 and + 8, columns = heads 2 (lane % 4) and + 1.
-            float c[NB][4] = {};
+            // Scores: rows = tokens lane / 4 and + 8 of each set, columns = heads
+            // 2 (lane % 4) and + 1.
+            constexpr int kChains = NB == 1 ? 2 : 1;  // shorter chains of dependent MMAs
+            float sc[kSets][NB][4] = {}, sd[kSets][NB][4] = {};
             {
-                const uint32_t at = st + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kRowBytes + (lane >> 4) * 16;
+                const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+                const uint32_t at = st + r * S::kRowBytes + (((lane >> 4) ^ swizzle(r)) << 4);
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) {
-                    uint32_t kf[4];
-                    ldmatrix4(kf, at + ks * 32);
+                for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) mma16816(c[b], kf, qf[ks][b][0], qf[ks][b][1]);
-                }
+                    for (int t = 0; t < kSets; ++t) {
+                        uint32_t kf[4];
+                        ldmatrix4(kf, chunk_pair(at, ks) + t * 16 * S::kRowBytes);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+                            mma16816(ks % kChains == 0 ? sc[t][b] : sd[t][b], kf, qf[ks][b][0], qf[ks][b][1]);
+                    }
             }
-            const bool v0 = (valid >> (lane / 4)) & 1, v1 = (valid >> (lane / 4 + 8)) & 1;
+            if (more && i == n_tiles - 1) {  // the next item's queries are on their way
+                next_item(here);
+                load_queries(here);
+            }
+#pragma unroll
+            for (int t = 0; t < kSets; ++t)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc[t][b][e] = (kChains == 2 ? sc[t][b][e] + sd[t][b][e] : sc[t][b][e]) * a.scale_log2;
+            if (valid != kAllSeen) {
+#pragma unroll
+                for (int t = 0; t < kSets; ++t)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!((valid >> (t * 16 + (e >> 1) * 8 + lane / 4)) & 1)) sc[t][b][e] = -INFINITY;
+            }
             float top[NB][2];
             bool grew = false;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    c[b][e] = v0 ? c[b][e] * a.scale_log2 : -INFINITY;
-                    c[b][e + 2] = v1 ? c[b][e + 2] * a.scale_log2 : -INFINITY;
-                    float t = fmaxf(c[b][e], c[b][e + 2]);
+                    float t = fmaxf(sc[0][b][e], sc[0][b][e + 2]);
+                    if constexpr (kSets == 2) t = fmaxf(t, fmaxf(sc[kSets - 1][b][e], sc[kSets - 1][b][e + 2]));
                     t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
                     t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
                     t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
@@ -353,45 +562,55 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtasPerSm)
                         }
                     }
             }
-            uint32_t hi[NB][2], lo[NB][2];
+            uint32_t hi[kSets][NB][2], lo[kSets][NB][2];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float p[4];
+                const float ref[2] = {m[b][0] == -INFINITY ? 0.0f : m[b][0], m[b][1] == -INFINITY ? 0.0f : m[b][1]};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float ref = m[b][e & 1] == -INFINITY ? 0.0f : m[b][e & 1];
-                    p[e] = exp2_approx(c[b][e] - ref);
-                    l[b][e & 1] += p[e];
-                }
-                // Tokens by heads -> heads by tokens, the B operand of the product with V.
+                for (int t = 0; t < kSets; ++t) {
+                    float p[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t h = __byte_perm(__float_as_uint(p[2 * e]), __float_as_uint(p[2 * e + 1]), 0x7632);
-                    const uint32_t r = pack_bf16(rest_of(p[2 * e]), rest_of(p[2 * e + 1]));
-                    hi[b][e] = movmatrix_trans(h);
-                    lo[b][e] = movmatrix_trans(r);
-                }
-            }
-            {
-                const uint32_t at = st + kSub * S::kRowBytes +
-                                    ((lane & 7) + ((lane >> 4) & 1) * 8) * S::kRowBytes + ((lane >> 3) & 1) * 16;
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = exp2_approx(sc[t][b][e] - ref[e & 1]);
+                        l[b][e & 1] += p[e];
+                    }
+                    // Tokens by heads -> heads by tokens, the B operand of the product with V.
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    uint32_t vf[4];
-                    ldmatrix4_trans(vf, at + s * 32);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        mma16816(o[s][b], vf, hi[b][0], hi[b][1]);
-                        mma16816(o[s][b], vf, lo[b][0], lo[b][1]);
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t h = __byte_perm(__float_as_uint(p[2 * e]), __float_as_uint(p[2 * e + 1]), 0x7632);
+                        const uint32_t r = pack_bf16(rest_of(p[2 * e]), rest_of(p[2 * e + 1]));
+                        hi[t][b][e] = movmatrix_trans(h);
+                        lo[t][b][e] = movmatrix_trans(r);
                     }
                 }
             }
-            __syncwarp();  // every lane is done with the stage before it is refilled
+            if (valid != 0) {  // a tile with nothing in it was not copied
+                const int r = (lane & 7) + ((lane >> 4) & 1) * 8;
+                const uint32_t at = st + (kSub + r) * S::kRowBytes + ((((lane >> 3) & 1) ^ swizzle(r)) << 4);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int t = 0; t < kSets; ++t) {
+                        uint32_t vf[4];
+                        ldmatrix4_trans(vf, chunk_pair(at, s) + t * 16 * S::kRowBytes);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            mma16816(o[s][b], vf, hi[t][b][0], hi[t][b][1]);
+                            mma16816(o[s][b], vf, lo[t][b][0], lo[t][b][1]);
+                        }
+                    }
+            }
+            __syncwarp();  // the stage is read: it takes the tile kStages on
+            // That tile's lookup slot is one before this step's, mod kSlots; the one kStages
+            // further is looked up now. (Keys refilled right after the scores, before the
+            // softmax, came out slower: the copies' issue waits for the memory system.)
+            fill(stage, step == 0 ? kSlots - 1 : step - 1);
+            look_up(step < 2 ? step + kSlots - 2 : step - 2);
+            cp_async_commit();  // a group a step, empty or not
+            stage = stage + 1 == S::kStages ? 0 : stage + 1;
+            step = step + 1 == kSlots ? 0 : step + 1;
         }
-        cp_async_wait<0>();
-        __syncwarp();
 
-        // ---- join the four warps ----
         // Sums over the lanes that share a column; the maxima are equal there already.
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -400,159 +619,242 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtasPerSm)
                 l[b][e] += __shfl_xor_sync(0xFFFFFFFFu, l[b][e], 4);
                 l[b][e] += __shfl_xor_sync(0xFFFFFFFFu, l[b][e], 8);
                 l[b][e] += __shfl_xor_sync(0xFFFFFFFFu, l[b][e], 16);
+            }
+        x += n_tiles;
+        if (whole) {  // nobody else has tiles of this item
+            const Heads heads = heads_of(row, item);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float inv0 = inverse(l[b][0]), inv1 = inverse(l[b][1]);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+                    store_out(heads, s, b, o[s][b][0], o[s][b][1], o[s][b][2], o[s][b][3], inv0, inv1);
                 if (lane < 4) {
-                    sm_m[warp * S::kHeads + b * 8 + lane * 2 + e] = m[b][e];
-                    sm_l[warp * S::kHeads + b * 8 + lane * 2 + e] = l[b][e];
+                    store_lse(heads, b * 8 + lane * 2, m[b][0], l[b][0]);
+                    store_lse(heads, b * 8 + lane * 2 + 1, m[b][1], l[b][1]);
                 }
             }
+        } else {
+            const int entry = warp * 2 + (x == x_end ? 1 : 0);
+            if (x == x_end) {  // into the ring: nothing but empty groups is on its way
+                cp_async_wait<0>();
+                __syncwarp();
+            }
+            float *to = entry_at(entry);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+            for (int b = 0; b < NB; ++b) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    merge[(b * 8 + (lane & 3) * 2 + (i & 1)) * S::kMergeStride + s * 16 + lane / 4 + (i >> 1) * 8] =
-                        o[s][b][i];
-        __syncthreads();
+                for (int s = 0; s < kSteps; ++s)
+                    reinterpret_cast<float4 *>(to)[(s * NB + b) * 32 + lane] =
+                        make_float4(o[s][b][0], o[s][b][1], o[s][b][2], o[s][b][3]);
+                if (lane < 4) {
+                    float2 *ml = reinterpret_cast<float2 *>(to + S::kMaximaAt + b * 8) + lane;
+                    ml[0] = make_float2(m[b][0], m[b][1]);
+                    ml[S::kHeads / 2] = make_float2(l[b][0], l[b][1]);
+                }
+            }
+            if (lane == 0) sm_key[entry] = row * items_per_row + item;
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
 
-        // Piece q of n of this item: CTAs first .. first + n - 1 hold one each.
-        const int item_x0 = prefix[row] * items_per_row + item * row_tiles;
-        const int first = rg.owner(item_x0);
-        const int pieces = rg.owner(item_x0 + row_tiles - 1) - first + 1;
-        const int slot = 2 * cta + (tile0 > 0 ? 0 : 1);
-
-        // Head h's values over n sources: combined maximum and sum, and each source's
-        // factor in sm_scale.
-        auto store_out = [&](int h, int d4, float4 v, float inv) {
-            const uint2 w = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-            *reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(row) * a.q_heads + head0 + h) * D + d4 * 4) = w;
-        };
-        auto store_lse = [&](int h, float mm, float ll) {
-            if (a.lse != nullptr)
-                a.lse[static_cast<size_t>(row) * a.q_heads + head0 + h] =
-                    ll > 0.0f || ll != ll ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-        };
-
-        constexpr int kQuads = D / 4;
-        float *ws_slot = a.partials + static_cast<size_t>(slot) * kAttnSlotFloats;
-        for (int i = tid; i < n_heads * kQuads; i += kThreads) {
-            const int h = i / kQuads, d4 = i % kQuads;
-            float mm = -INFINITY;
+    // ---- join what the warps have left, item by item ----
+    // Each warp takes its share of the fragments (16 values of 8 heads).
+    constexpr int kJobs = (kSteps + kWarps - 1) / kWarps * NB;
+    auto frag_of = [&](int job) { return (warp * (kJobs / NB) + job / NB) * NB + job % NB; };
+    auto slot_of = [&](int first, int q) { return 2 * (first + q) + (q == 0 ? 1 : 0); };  // piece q of an item
+    const int my_key = lane < 2 * kWarps ? sm_key[lane] : -1;
+    unsigned alike = 0;  // entries of the same item
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w * S::kHeads + h]);
-            const float ref = mm == -INFINITY ? 0.0f : mm;
-            float ll = 0.0f;
+    for (int e = 0; e < 2 * kWarps; ++e)
+        alike |= static_cast<unsigned>(__shfl_sync(0xFFFFFFFFu, my_key, e) == my_key) << e;
+    unsigned items = __ballot_sync(0xFFFFFFFFu, my_key >= 0 && lane == __ffs(alike) - 1);
+    for (; items != 0; items &= items - 1) {
+        const int key = __shfl_sync(0xFFFFFFFFu, my_key, __ffs(items) - 1);
+        const unsigned entries = __shfl_sync(0xFFFFFFFFu, alike, __ffs(items) - 1);
+        const int row = quotient(key, items_per_row), item = key - row * items_per_row;
+        const int row_tiles = prefix[row + 1] - prefix[row];
+        const int item_x = prefix[row] * items_per_row + item * row_tiles;
+        // Chunks first .. first + pieces - 1 hold a piece of this item each (a short one is in
+        // one chunk, wherever the even cut would be).
+        const bool within = row_tiles <= kSnapChunk;
+        const int first = within ? cta : cut.owner(item_x);
+        const int pieces = within ? 1 : cut.owner(item_x + row_tiles - 1) - first + 1;
+        const Heads heads = heads_of(row, item);
+        int dst = pieces == 1 ? -1 : slot_of(first, cta - first);
+#pragma unroll 1
+        for (int job = 0; job < kJobs; ++job) {
+            const int frag = frag_of(job), h = frag % NB * 8 + (lane & 3) * 2;
+            if (frag >= kSteps * NB) break;
+            float2 mk[2 * kWarps], mm = make_float2(-INFINITY, -INFINITY), ll = make_float2(0.0f, 0.0f);
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2_approx(sm_m[w * S::kHeads + h] - ref);
-                const float4 u = *reinterpret_cast<const float4 *>(
-                    reinterpret_cast<const float *>(smem + w * S::kRingBytes) + h * S::kMergeStride + d4 * 4);
-                ll += f * sm_l[w * S::kHeads + h];
-                v.x += f * u.x; v.y += f * u.y; v.z += f * u.z; v.w += f * u.w;
-            }
-            if (pieces == 1) {
-                store_out(h, d4, v, ll == 0.0f ? 0.0f : __fdiv_rn(1.0f, ll));
-                if (d4 == 0) store_lse(h, mm, ll);
+            for (int e = 0; e < 2 * kWarps; ++e)
+                if (entries >> e & 1) {
+                    mk[e] = *reinterpret_cast<const float2 *>(entry_at(e) + S::kMaximaAt + h);
+                    mm.x = fmaxf(mm.x, mk[e].x);
+                    mm.y = fmaxf(mm.y, mk[e].y);
+                }
+#pragma unroll
+            for (int e = 0; e < 2 * kWarps; ++e)
+                if (entries >> e & 1) {
+                    const float2 lk = *reinterpret_cast<const float2 *>(entry_at(e) + S::kMaximaAt + S::kHeads + h);
+                    const float4 u = reinterpret_cast<const float4 *>(entry_at(e))[frag * 32 + lane];
+                    // A maximum of -inf goes with sums of zero, or of NaN.
+                    const float f0 = mk[e].x == -INFINITY ? 1.0f : exp2_approx(mk[e].x - mm.x);
+                    const float f1 = mk[e].y == -INFINITY ? 1.0f : exp2_approx(mk[e].y - mm.y);
+                    ll.x += f0 * lk.x;
+                    ll.y += f1 * lk.y;
+                    v.x += f0 * u.x; v.y += f1 * u.y; v.z += f0 * u.z; v.w += f1 * u.w;
+                }
+            const bool tell = frag < NB && lane < 4;  // the first fragment of a block of heads
+            if (dst < 0) {
+                store_out(heads, frag / NB, frag % NB, v.x, v.y, v.z, v.w, inverse(ll.x), inverse(ll.y));
+                if (tell) {
+                    store_lse(heads, h, mm.x, ll.x);
+                    store_lse(heads, h + 1, mm.y, ll.y);
+                }
             } else {
-                __stcg(reinterpret_cast<float4 *>(ws_slot + h * D + d4 * 4), v);
-                if (d4 == 0) {
-                    __stcg(ws_slot + 4096 + h, mm);
-                    __stcg(ws_slot + 4096 + kAttnMaxHeads + h, ll);
+                float *to = slot_at(dst);
+                __stcg(reinterpret_cast<float4 *>(to) + frag * 32 + lane, v);
+                if (tell) {
+                    __stcg(reinterpret_cast<float2 *>(to + S::kMaximaAt + h), mm);
+                    __stcg(reinterpret_cast<float2 *>(to + S::kMaximaAt + S::kHeads + h), ll);
                 }
             }
         }
+        if (dst < 0) continue;
 
-        if (pieces > 1) {
-            // Arrive; the last of the group joins it, and the last group's joiner the
-            // groups. Counters go back to zero for the next call.
-            const int me = cta - first;
-            const int group = me / kAttnGroup;
-            const int groups = (pieces + kAttnGroup - 1) / kAttnGroup;
-            auto slot_of = [&](int q) { return 2 * (first + q) + (q == 0 ? 1 : 0); };
-            auto arrive = [&](unsigned *counter, int expected) -> bool {
-                __syncthreads();  // every thread's partial is stored
-                if (tid == 0) {
-                    __threadfence();
-                    const unsigned old = atomicAdd(counter, 1u);
-                    sm_last = old + 1 == static_cast<unsigned>(expected);
-                    if (sm_last) *counter = 0u;
-                    __threadfence();
-                }
-                __syncthreads();
-                return sm_last != 0;
+        // The chunks' partials: arrive, and the last of a group joins it; arrive, and the
+        // last group's joiner joins the groups. Sources are added in order.
+        float *factor = reinterpret_cast<float *>(smem + S::kFactorOffset);
+        float *sm_m = reinterpret_cast<float *>(smem + S::kMlOffset), *sm_l = sm_m + S::kHeads;
+        const int groups = (pieces + kAttnGroup - 1) / kAttnGroup;
+        int q0 = (cta - first) / kAttnGroup * kAttnGroup, q_step = 1, n = min(kAttnGroup, pieces - q0);
+        for (int level = 0; level < 2; ++level) {
+            __syncthreads();  // every thread's stores are done
+            if (tid == 0) {
+                // Releases all threads' stores (the barrier orders them before it), acquires
+                // the other CTAs'.
+                unsigned *counter = a.counters + 2 * slot_of(first, q0) + level;
+                sm_last = ptx::atom_add_acq_rel_gpu(counter, 1u) + 1 == static_cast<unsigned>(n);
+                if (sm_last) *counter = 0u;  // ready for the next call
+            }
+            __syncthreads();
+            if (!sm_last) break;
+            dst = level == 1 || groups == 1 ? -1 : slot_of(first, q0);
+            auto source = [&](int k) { return slot_at(slot_of(first, q0 + k * q_step)); };
+
+            // The first loads are in flight while the factors are worked out: a lane is a
+            // source there.
+            constexpr int kPair = kJobs > 1 ? 2 : 1, kBatch = 12;
+            float4 u[kPair][kBatch];
+            auto load = [&](int job, int k0) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                    for (int j = 0; j < kPair; ++j)
+                        if (k0 + k < n && job + j < kJobs && frag_of(job + j) < kSteps * NB)
+                            u[j][k] = __ldcg(reinterpret_cast<const float4 *>(source(k0 + k)) + frag_of(job + j) * 32 + lane);
             };
-            // Join sources q0, q0 + step, .. (n of them) into `dst` slot, or the output.
-            auto join = [&](int q0, int step, int n, int dst) {
-                float mm = -INFINITY, ll = 0.0f;
-                if (tid < n_heads) {
-                    for (int k = 0; k < n; ++k)
-                        mm = fmaxf(mm, __ldcg(a.partials + static_cast<size_t>(slot_of(q0 + k * step)) * kAttnSlotFloats +
-                                              4096 + tid));
-                    const float ref = mm == -INFINITY ? 0.0f : mm;
-                    for (int k = 0; k < n; ++k) {
-                        const float *src = a.partials + static_cast<size_t>(slot_of(q0 + k * step)) * kAttnSlotFloats + 4096;
-                        const float f = exp2_approx(__ldcg(src + tid) - ref);
-                        ll += f * __ldcg(src + kAttnMaxHeads + tid);
-                        sm_scale[k * S::kHeads + tid] = f;
-                    }
-                    sm_m[tid] = mm;
-                    sm_l[tid] = ll;
+            load(0, 0);
+            {
+                constexpr int kMine = S::kHeads / kWarps;  // heads of a warp
+                float mk[kMine], lk[kMine], mm[kMine];
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const float *src = source(min(lane, n - 1)) + S::kMaximaAt + warp * kMine + i;
+                    mm[i] = mk[i] = lane < n ? __ldcg(src) : -INFINITY;
+                    lk[i] = lane < n ? __ldcg(src + S::kHeads) : 0.0f;
                 }
-                __syncthreads();
-                float *to = a.partials + static_cast<size_t>(dst < 0 ? 0 : dst) * kAttnSlotFloats;
-                for (int i = tid; i < n_heads * kQuads; i += kThreads) {
-                    const int h = i / kQuads, d4 = i % kQuads;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = 0; k < n; ++k) {
-                        const float f = sm_scale[k * S::kHeads + h];
-                        const float4 u = __ldcg(reinterpret_cast<const float4 *>(
-                            a.partials + static_cast<size_t>(slot_of(q0 + k * step)) * kAttnSlotFloats + h * D + d4 * 4));
-                        v.x += f * u.x; v.y += f * u.y; v.z += f * u.z; v.w += f * u.w;
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) mm[i] = fmaxf(mm[i], __shfl_xor_sync(0xFFFFFFFFu, mm[i], s));
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const float f = mk[i] == -INFINITY ? 1.0f : exp2_approx(mk[i] - mm[i]);
+                    if (lane < n) factor[lane * S::kHeads + warp * kMine + i] = f;
+                    lk[i] *= f;
+                }
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) lk[i] += __shfl_xor_sync(0xFFFFFFFFu, lk[i], s);
+                if (lane == 0)
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        sm_m[warp * kMine + i] = mm[i];
+                        sm_l[warp * kMine + i] = lk[i];
                     }
-                    if (dst < 0) {
-                        const float sum = sm_l[h];
-                        store_out(h, d4, v, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum));
-                        if (d4 == 0) store_lse(h, sm_m[h], sum);
-                    } else {
-                        __stcg(reinterpret_cast<float4 *>(to + h * D + d4 * 4), v);
-                        if (d4 == 0) {
-                            __stcg(to + 4096 + h, sm_m[h]);
-                            __stcg(to + 4096 + kAttnMaxHeads + h, sm_l[h]);
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int job = 0; job < kJobs; job += kPair) {
+                float v[kPair][4] = {};
+#pragma unroll 1
+                for (int k0 = 0; k0 < n; k0 += kBatch) {
+                    if (job + k0 > 0) load(job, k0);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        if (k0 + k >= n) break;
+#pragma unroll
+                        for (int j = 0; j < kPair; ++j) {
+                            const int h = frag_of(job + j) % NB * 8 + (lane & 3) * 2;
+                            const float2 f = *reinterpret_cast<const float2 *>(factor + (k0 + k) * S::kHeads + h);
+                            v[j][0] += f.x * u[j][k].x;
+                            v[j][1] += f.y * u[j][k].y;
+                            v[j][2] += f.x * u[j][k].z;
+                            v[j][3] += f.y * u[j][k].w;
                         }
                     }
                 }
-            };
-            const int q0 = group * kAttnGroup;
-            const int in_group = min(kAttnGroup, pieces - q0);
-            const bool one_level = groups == 1;
-            if (arrive(a.counters + 2 * slot_of(q0), in_group)) {
-                join(q0, 1, in_group, one_level ? -1 : slot_of(q0));
-                if (!one_level && arrive(a.counters + 2 * slot_of(0) + 1, groups)) join(0, kAttnGroup, groups, -1);
+#pragma unroll
+                for (int j = 0; j < kPair; ++j) {
+                    const int frag = frag_of(job + j), h = frag % NB * 8 + (lane & 3) * 2;
+                    if (job + j >= kJobs || frag >= kSteps * NB) continue;
+                    if (dst >= 0)
+                        __stcg(reinterpret_cast<float4 *>(slot_at(dst)) + frag * 32 + lane,
+                               make_float4(v[j][0], v[j][1], v[j][2], v[j][3]));
+                    else
+                        store_out(heads, frag / NB, frag % NB, v[j][0], v[j][1], v[j][2], v[j][3], inverse(sm_l[h]),
+                                  inverse(sm_l[h + 1]));
+                }
             }
+            if (tid < S::kHeads) {
+                if (dst >= 0) {
+                    __stcg(slot_at(dst) + S::kMaximaAt + tid, sm_m[tid]);
+                    __stcg(slot_at(dst) + S::kMaximaAt + S::kHeads + tid, sm_l[tid]);
+                } else {
+                    store_lse(heads, tid, sm_m[tid], sm_l[tid]);
+                }
+            }
+            if (dst < 0) break;
+            q0 = 0;
+            q_step = kAttnGroup;
+            n = groups;
         }
-        __syncthreads();  // the ring and the joins' arrays are reused
-        x += tile1 - tile0;
+        __syncthreads();  // the factors are used again
     }
 }
 
 template <int D, int NB>
 cudaError_t launch(const AttentionArgs &a, int num_sms, int device, cudaStream_t stream, bool pdl) {
     using S = Shape<D, NB>;
-    static int configured[64] = {};
+    static bool configured[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-    const int most = S::bytes(kAttnMaxRows);
     if (!configured[device]) {
         cudaError_t e = cudaFuncSetAttribute(decode_attention_kernel<D, NB>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes(kAttnMaxRows));
         if (e != cudaSuccess) return e;
-        configured[device] = 1;
+        configured[device] = true;
     }
-    // No more CTAs than the tables could ever hold tiles.
+    // No more CTAs than the tables could ever hold tiles for their warps.
     const long long tiles = static_cast<long long>(a.rows) * a.kv_heads * a.head_blocks *
-                            ((a.capacity + kAttnTile - 1ll) / kAttnTile);
+                            ((a.capacity + S::kSub - 1ll) / S::kSub);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, std::min<long long>(num_sms * S::kCtasPerSm, tiles))), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(num_sms * attn_ctas_per_sm(D), (tiles + kWarps - 1) / kWarps)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = S::bytes(a.rows);
     cfg.stream = stream;

@@ -161,6 +161,7 @@ struct AttentionArgs {
     long long q_stride;
     const uint16_t *k, *v;
     int num_pages, page_size;
+    int page_shift;  // log2(page_size), or -1
     long long page_stride, token_stride, head_stride;
     const int *block_table;  // [rows][capacity / page_size]
     long long table_stride;
@@ -170,12 +171,13 @@ struct AttentionArgs {
     int head_blocks;  // blocks the group is cut into, of block_heads heads at most
     int block_heads;
     int capacity;     // tokens a row's table holds
+    int wide;         // the keys (or values) span more than 2^32 chunks of 16 bytes
     int window, sinks;
     float scale_log2;  // scale * log2(e)
     uint16_t *out;     // [rows][q_heads][head_dim]
     float *lse;        // [rows][q_heads] or nullptr
-    unsigned *counters;  // workspace: two per slot, zero between calls
-    float *partials;     // workspace: kAttnSlotFloats per slot, two slots per CTA
+    unsigned *counters;  // workspace (attention_plan.cuh): zero between calls
+    float *partials;     // workspace: the slots
 };
 cudaError_t launch_decode_attention(const AttentionArgs &a, int head_dim, int num_sms, int device,
                                     cudaStream_t stream, bool pdl);

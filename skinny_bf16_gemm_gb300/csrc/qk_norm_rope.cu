@@ -10,10 +10,9 @@
 //
 // Layout: a group of L lanes (8, 16 or 32: the smallest that covers D / 8) holds a
 // head, 16 bytes to a lane, so the norm is a butterfly within the group and the
-// half-split partner one shuffle away; a block's groups take heads of one row, so
-// the table row is read once into registers for the U heads a group does. U = 4
-// keeps four loads in flight per lane for long inputs, U = 1 spreads few rows over
-// the most SMs.
+// half-split partner one shuffle away; a block has one row's heads, U to a group, so
+// the table row is read once into registers for them. U = 4 keeps four loads in flight
+// per lane for long inputs, U = 1 spreads few rows over the most threads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,7 +22,7 @@
 namespace skinny {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxThreads = 512;
 __device__ int g_rope_err;  // nonzero: a position or slot was out of range
 
 __device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8]) {
@@ -47,14 +46,14 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
 }
 
 template <int L, int U>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
-    constexpr int kGroups = kThreads / L;
+__global__ void __launch_bounds__(kMaxThreads, 2) qk_norm_rope_kernel(const RopeArgs a) {
+    const int groups = blockDim.x / L;
     const int lane = threadIdx.x % L;
     const int group = threadIdx.x / L;
     const int row = blockIdx.x;
     const bool active = lane * 8 < a.head_dim;
     const int heads = a.q_heads + 2 * a.kv_heads;
-    const int head0 = blockIdx.y * (kGroups * U) + group;
+    const int head0 = blockIdx.y * (groups * U) + group;
 
     // The gammas are weights: read before waiting for the previous kernel.
     uint4 gq = make_uint4(0, 0, 0, 0), gk = gq;
@@ -66,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
     uint4 raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int h = head0 + u * kGroups;
+        const int h = head0 + u * groups;
         raw[u] = make_uint4(0, 0, 0, 0);
         if (active && h < heads)
             raw[u] = __ldcs(reinterpret_cast<const uint4 *>(a.qkv + row * a.qkv_stride +
@@ -119,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int h = head0 + u * kGroups;
+        const int h = head0 + u * groups;
         if (h - group >= heads) break;  // past the last head for every group of the block
         const bool is_v = h >= a.q_heads + a.kv_heads, is_q = h < a.q_heads;
         uint4 w = raw[u];
@@ -176,10 +175,13 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
 
 template <int L, int U>
 cudaError_t launch(const RopeArgs &a, cudaStream_t stream, bool pdl) {
-    const int heads = a.q_heads + 2 * a.kv_heads, per_block = kThreads / L * U;
+    // Blocks of a row just large enough for their share of its heads.
+    const int heads = a.q_heads + 2 * a.kv_heads, most = kMaxThreads / L * U;
+    const int blocks = (heads + most - 1) / most, share = (heads + blocks - 1) / blocks;
+    const int threads = ((share + U - 1) / U * L + 31) / 32 * 32, per_block = threads / L * U;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.rows, (heads + per_block - 1) / per_block, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -67,7 +67,7 @@ def rope_args(p, cache=None, **kw):
     a.update(kw)
     args = sk.QkNormRopeArgs(**a)
     if cache is not None:
-        args.cache = ctypes.pointer(cache)
+        args.cache = cache
     return args
 
 
@@ -123,11 +123,10 @@ def test_decode_attention_refusals(lib, mem):
 
     def call(cache=None, opts=None, **kw):
         a = sk.DecodeAttentionArgs(**dict(ok, **kw))
-        if cache is not False:
-            a.cache = ctypes.pointer(cache if cache is not None else cache_at(p + 6 * MB, v=p + 7 * MB))
+        a.cache = cache if cache is not None else cache_at(p + 6 * MB, v=p + 7 * MB)
         return lib.decode_attention_bf16(ctypes.byref(a), opts, None)
     assert lib.decode_attention_bf16(None, None, None) == NULL
-    assert call(cache=False) == NULL
+    assert call(cache=cache_at(p, k=None)) == NULL and call(cache=cache_at(p, v=None)) == NULL
     for n in ("q", "block_table", "lengths", "out", "workspace"):
         assert call(**{n: None}) == NULL, n
     for kw in (dict(rows=0), dict(rows=1025), dict(q_heads=3), dict(q_heads=0), dict(q_heads=1026),
@@ -160,7 +159,7 @@ def test_table_too_wide_for_32_bit_tiles_is_refused(lib, mem):
     a = sk.DecodeAttentionArgs(q=p, q_stride=65536, rows=1024, q_heads=1024, block_table=p, table_stride=1 << 20,
                                table_width=1 << 20, lengths=p, scale=1.0, out=p, workspace=p,
                                workspace_bytes=1 << 30)
-    a.cache = ctypes.pointer(c)
+    a.cache = c
     assert lib.decode_attention_bf16(ctypes.byref(a), None, None) == SHAPE
 
 
@@ -177,6 +176,19 @@ def test_python_checks_name_the_tensor(lib):
         x = torch.zeros(1, 8, dtype=torch.bfloat16).as_subclass(Fake)
         sk.decode_gemm_bf16_epilogue(x, x, torch.zeros(1, 1, dtype=torch.bfloat16).as_subclass(Fake),
                                      activation="tanh")
+
+
+def test_packed_strings_match_the_structures(lib):
+    """The wrappers fill the two argument structures as packed strings: the same bytes."""
+    n = iter(range(1, 100))
+    cache = [next(n) for _ in range(9)]
+    rope = [next(n) for _ in range(18)]
+    packed = sk._pack_rope(*rope, *cache, 98)
+    a = sk.QkNormRopeArgs(*rope, sk.KVCacheArgs(*cache), 98)
+    assert bytes(a) == packed
+    first, last = [next(n) for _ in range(4)], [next(n) for _ in range(11)]
+    assert bytes(sk.DecodeAttentionArgs(*first, sk.KVCacheArgs(*cache), *last)) == \
+        sk._pack_attention(*first, *cache, *last)
 
 
 def test_new_status_has_a_text(lib):
