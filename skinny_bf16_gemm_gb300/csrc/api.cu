@@ -456,6 +456,8 @@ int reduce_device_checks(const void *partials, const void *residual, const void 
     return SKINNY_OK;
 }
 
+int log2_or_minus_one(int n) { return (n & (n - 1)) == 0 ? __builtin_ctz(n) : -1; }
+
 // Bytes from a row's first element to past the last row's last.
 size_t row_span(int rows, long long stride, long long width) {
     return (static_cast<size_t>(rows - 1) * stride + width) * 2;
@@ -781,6 +783,7 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
     a.q_gamma = static_cast<const uint16_t *>(p->q_gamma);
     a.k_gamma = static_cast<const uint16_t *>(p->k_gamma);
     a.eps = p->eps;
+    a.inv_dim = 1.0f / static_cast<float>(D);
     a.rope = static_cast<const float *>(p->rope);
     a.max_pos = p->max_pos;
     a.rot_dim = p->rot_dim;
@@ -793,14 +796,15 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
     if (has_cache) {
         a.k_cache = static_cast<uint16_t *>(cache->k);
         a.v_cache = static_cast<uint16_t *>(cache->v);
-        a.num_pages = cache->num_pages;
         a.page_size = cache->page_size;
+        a.page_shift = log2_or_minus_one(cache->page_size);
+        a.num_slots = static_cast<long long>(cache->num_pages) * cache->page_size;
         a.page_stride = cache->page_stride;
         a.token_stride = cache->token_stride;
         a.head_stride = cache->head_stride;
         a.slots = static_cast<const long long *>(p->slots);
     }
-    if (launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream), ls.pdl) != cudaSuccess) {
+    if (launch_qk_norm_rope(a, d->sms, static_cast<cudaStream_t>(stream), ls.pdl) != cudaSuccess) {
         cudaGetLastError();
         return SKINNY_ERR_LAUNCH;
     }
@@ -871,7 +875,7 @@ int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_la
     a.v = static_cast<const uint16_t *>(c->v);
     a.num_pages = c->num_pages;
     a.page_size = c->page_size;
-    a.page_shift = (c->page_size & (c->page_size - 1)) == 0 ? __builtin_ctz(c->page_size) : -1;
+    a.page_shift = log2_or_minus_one(c->page_size);
     a.page_stride = c->page_stride;
     a.token_stride = c->token_stride;
     a.head_stride = c->head_stride;

@@ -139,7 +139,7 @@ struct RopeArgs {
     long long qkv_stride;
     int rows, q_heads, kv_heads, head_dim;
     const uint16_t *q_gamma, *k_gamma;  // [head_dim] or nullptr: no norm
-    float eps;
+    float eps, inv_dim;  // inv_dim: 1 / head_dim
     const float *rope;  // [max_pos][rot_dim]: rot_dim / 2 cosines, then sines
     int max_pos, rot_dim, interleaved;
     const int *positions;
@@ -148,11 +148,12 @@ struct RopeArgs {
     uint16_t *k_out;  // or nullptr
     long long k_stride;
     uint16_t *k_cache, *v_cache;  // both or neither
-    int num_pages, page_size;
+    int page_size, page_shift;  // page_shift: log2(page_size), or -1
+    long long num_slots;        // pages * page_size
     long long page_stride, token_stride, head_stride;
     const long long *slots;
 };
-cudaError_t launch_qk_norm_rope(const RopeArgs &a, cudaStream_t stream, bool pdl);
+cudaError_t launch_qk_norm_rope(const RopeArgs &a, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t rope_error_word(int *value, bool clear);
 
 // Decode attention over a paged cache (decode_attention_bf16). Strides in elements.
