@@ -176,8 +176,7 @@ __device__ __forceinline__ void store_tile_staged(const float (&v)[MP], uint16_t
 }
 
 // EPI: the epilogue of epilogue.cuh. A template so that the plain kernel keeps its
-// registers; the bias and residual of a tile's column are loaded before the wait
-// for its accumulator, so their latency hides behind the weight stream.
+// registers.
 template <int MP, int STAGES, bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_gemm_kernel(const __grid_constant__ CUtensorMap w_map,
@@ -407,35 +406,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool staged = kStagedOut && (reinterpret_cast<uintptr_t>(args.out) & 15) == 0 &&
                             (g.N & 7) == 0;
 
-        // EPI: this thread's column of the current tile: the bias, and the residual's
-        // rows two to a register.
-        [[maybe_unused]] uint32_t res[EPI ? MP / 2 : 1];
+        // EPI: the output of this thread's column n of a tile from its FP32 sums, kRows rows at
+        // a time (the activations unrolled over all rows would be code that is fetched
+        // longer than it runs: 64 rows with a tanh cost 12 us more than without): from
+        // tensor memory, or from this thread's column of the idle ring. Rows' residuals are
+        // loaded kRows ahead, two to a register, the first before the wait for the accumulator.
+        constexpr int kRows = MP == 16 ? 4 : 16;
+        [[maybe_unused]] uint32_t ahead[kRows / 2];
         [[maybe_unused]] float bias = 0.0f;
-        auto load_epilogue = [&](int n) {
-            if constexpr (EPI) {
-                if (n >= g.N) return;
-                if (args.epi.bias != nullptr) bias = bf16_value(args.epi.bias[n]);
-                if (args.epi.residual != nullptr) {
+        auto load_residual = [&](int n, int m0) {
+            if (args.epi.residual == nullptr || n >= g.N) return;
+            const uint16_t *src = args.epi.residual + static_cast<size_t>(m0) * g.N + n;
 #pragma unroll
-                    for (int m = 0; m < MP; m += 2) {
-                        const uint16_t *src = args.epi.residual + static_cast<size_t>(m) * g.N + n;
-                        const uint32_t lo = m < g.M ? src[0] : 0u;
-                        const uint32_t hi = m + 1 < g.M ? src[g.N] : 0u;
-                        res[m / 2] = lo | (hi << 16);
-                    }
-                }
+            for (int i = 0; i < kRows / 2; ++i) {
+                const uint32_t lo = m0 + 2 * i < g.M ? src[static_cast<size_t>(2 * i) * g.N] : 0u;
+                const uint32_t hi = m0 + 2 * i + 1 < g.M ? src[static_cast<size_t>(2 * i + 1) * g.N] : 0u;
+                ahead[i] = lo | (hi << 16);
             }
         };
-        // The value output element (m, this thread's column) is rounded from.
-        auto value = [&](float v, int m) -> float {
-            if constexpr (EPI) {
-                if (args.epi.bias != nullptr) v = __fadd_rn(v, bias);
-                v = activate(v, args.epi.activation);
-                if (args.epi.residual != nullptr)
-                    v = __fadd_rn(v, bf16_value((m & 1) ? res[m / 2] >> 16 : res[m / 2] & 0xFFFFu));
-                return v;
-            } else {
-                return output_value(v, args);
+        auto emit = [&](int n, bool from_tmem, uint32_t taddr) {
+#pragma unroll 1
+            for (int m0 = 0; m0 < g.M; m0 += kRows) {
+                uint32_t res[kRows / 2], w[kRows];
+#pragma unroll
+                for (int i = 0; i < kRows / 2; ++i) res[i] = ahead[i];
+                if (m0 + kRows < g.M) load_residual(n, m0 + kRows);
+                if (from_tmem) {
+                    ptx::tmem_ld_now(taddr + m0, w);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+                        w[i] = reinterpret_cast<const uint32_t *>(smem)[(m0 + i) * kBlockN + row];
+                }
+                float v[kRows];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    v[i] = __uint_as_float(w[i]);
+                    if (args.epi.bias != nullptr) v[i] = __fadd_rn(v[i], bias);
+                }
+                activate(v, args.epi.activation);
+                if (n >= g.N) continue;
+                uint16_t *dst = args.out + static_cast<size_t>(m0) * g.N + n;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    if (args.epi.residual != nullptr)
+                        v[i] = __fadd_rn(v[i], bf16_value((i & 1) ? res[i / 2] >> 16 : res[i / 2] & 0xFFFFu));
+                    if (m0 + i < g.M) dst[static_cast<size_t>(i) * g.N] = to_bf16_bits(v[i]);
+                }
             }
         };
 
@@ -500,11 +517,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 c0 = c1;
             }
             const int n = t * kBlockN + row;
+            if constexpr (EPI) {
+#pragma unroll
+                for (int m = 0; m < MP; ++m)
+                    if (m < g.M) reinterpret_cast<float *>(smem)[m * kBlockN + row] = sum[m];
+                emit(n, false, 0u);
+                return true;
+            }
             if (n < g.N) {
 #pragma unroll
                 for (int m = 0; m < MP; ++m)
                     if (m < g.M)
-                        args.out[static_cast<size_t>(m) * g.N + n] = to_bf16_bits(value(sum[m], m));
+                        args.out[static_cast<size_t>(m) * g.N + n] = to_bf16_bits(output_value(sum[m], args));
             }
             return true;
         };
@@ -519,13 +543,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int first_peer_slot =
                 first + 1 + etid <= last ? partial_slot(g, first + 1 + etid, p.tile) : 0;
             // A piece from the tile's first K block on is the one that stores the tile.
-            if (EPI && p.kb0 == 0 && !args.publish_only) load_epilogue(p.tile * kBlockN + row);
+            if (EPI && p.kb0 == 0 && !args.publish_only) {
+                const int n = p.tile * kBlockN + row;
+                if (args.epi.bias != nullptr && n < g.N) bias = bf16_value(args.epi.bias[n]);
+                load_residual(n, 0);
+            }
             const int b = q & 1;
             const uint32_t aph = (q >> 1) & 1;
             const int r = bounded_wait(bar_acc_full + 8 * b, aph, abort_flag, limit);
             if (r == kWaitTimeout) raise_error(args, abort_flag, kErrEpilogueWait);
             if (epilogue_any(r != kWaitDone)) break;
             ptx::tc_fence_after_sync();
+            if constexpr (EPI) {
+                if (p.kb0 == 0 && p.kb1 == g.kblocks && !args.publish_only) {
+                    emit(p.tile * kBlockN + row, true,
+                         tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * L::kAccCols);
+                    ptx::tc_fence_before_sync();
+                    ptx::mbar_arrive(bar_acc_empty + 8 * b);  // the MMA may reuse this buffer
+                    continue;
+                }
+            }
             float acc[MP];
             {
                 const uint32_t taddr =
@@ -547,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Whole tile in this CTA: round once and store.
                 if (kStagedOut && staged && q == pieces - 1) {
 #pragma unroll
-                    for (int m = 0; m < MP; ++m) acc[m] = value(acc[m], m);
+                    for (int m = 0; m < MP; ++m) acc[m] = output_value(acc[m], args);
                     store_tile_staged<MP>(acc, args.out, g.M, g.N, p.tile, row, etid, sbase);
                     continue;
                 }
@@ -556,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int m = 0; m < MP; ++m)
                         if (m < g.M)
                             args.out[static_cast<size_t>(m) * g.N + n] =
-                                to_bf16_bits(value(acc[m], m));
+                                to_bf16_bits(output_value(acc[m], args));
                 }
                 continue;
             }

@@ -19,14 +19,28 @@ struct Epilogue {
 
 __device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
 
-__device__ __forceinline__ float activate(float v, int activation) {
+// The activation of n values; one branch, not one a value.
+template <int n>
+__device__ __forceinline__ void activate(float (&v)[n], int activation) {
     switch (activation) {
-        case kActRelu: return v < 0.0f ? 0.0f : v;  // NaN stays
-        case kActSilu: return __fdiv_rn(v, 1.0f + expf(-v));
-        case kActGelu: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+        case kActRelu:
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];  // NaN stays
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[i] = __fdiv_rn(v[i], 1.0f + expf(-v[i]));
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
+            break;
         case kActGeluTanh:
-            return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
-        default: return v;
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                v[i] = 0.5f * v[i] * (1.0f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+            break;
+        default: break;
     }
 }
 

@@ -23,7 +23,7 @@ constexpr int kThreads = 128;
 
 template <bool EPI>
 __global__ void __launch_bounds__(kThreads)
-    splitk_finish_kernel(SplitKPartials fix, uint16_t *out, int vector_out, Epilogue epi) {
+    splitk_finish_kernel(SplitKPartials fix, uint16_t *out, int vector, Epilogue epi) {
     ptx::pdl_launch_dependents();
     const int frag = blockIdx.x * kThreads + threadIdx.x;
     const int m = blockIdx.y;
@@ -34,6 +34,23 @@ __global__ void __launch_bounds__(kThreads)
     const int t = col / kBlockN;
     int first, last;
     tile_contributors(g, t, first, last);
+    // The bias and residual are on their way while the partials are.
+    [[maybe_unused]] uint16_t bias[8], res[8];
+    if constexpr (EPI) {
+        auto load8 = [&](const uint16_t *src, bool vector, uint16_t (&to)[8]) {
+            if (vector && col + 8 <= fix.N) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) to[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) to[j] = col + j < fix.N ? src[j] : 0;
+            }
+        };
+        if (epi.bias != nullptr) load8(epi.bias + col, (vector & 2) != 0, bias);
+        if (epi.residual != nullptr) load8(epi.residual + static_cast<size_t>(m) * fix.N + col, (vector & 4) != 0, res);
+    }
     float a[8];
     for (int c0 = first; c0 <= last; c0 += 4) {
         float4 v[4][2];
@@ -57,20 +74,21 @@ __global__ void __launch_bounds__(kThreads)
         }
     }
     if constexpr (EPI) {
+        if (epi.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (col + j >= fix.N) break;
-            if (epi.bias != nullptr) a[j] = __fadd_rn(a[j], bf16_value(epi.bias[col + j]));
-            a[j] = activate(a[j], epi.activation);
-            if (epi.residual != nullptr)
-                a[j] = __fadd_rn(a[j], bf16_value(epi.residual[static_cast<size_t>(m) * fix.N + col + j]));
+            for (int j = 0; j < 8; ++j) a[j] = __fadd_rn(a[j], bf16_value(bias[j]));
+        }
+        activate(a, epi.activation);
+        if (epi.residual != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = __fadd_rn(a[j], bf16_value(res[j]));
         }
     }
     uint16_t b[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) b[j] = __bfloat16_as_ushort(__float2bfloat16_rn(a[j]));
     uint16_t *dst = out + static_cast<size_t>(m) * fix.N + col;
-    if (vector_out && col + 8 <= fix.N) {
+    if ((vector & 1) && col + 8 <= fix.N) {
         *reinterpret_cast<uint4 *>(dst) =
             make_uint4(b[0] | (static_cast<uint32_t>(b[1]) << 16), b[2] | (static_cast<uint32_t>(b[3]) << 16),
                        b[4] | (static_cast<uint32_t>(b[5]) << 16), b[6] | (static_cast<uint32_t>(b[7]) << 16));
@@ -95,10 +113,15 @@ cudaError_t launch_splitk_finish(const SplitKPartials &fix, uint16_t *out, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    const int vector_out = (fix.N % 8 == 0 && (reinterpret_cast<uintptr_t>(out) % 16) == 0) ? 1 : 0;
-    if (epi != nullptr)
-        return cudaLaunchKernelEx(&cfg, splitk_finish_kernel<true>, fix, out, vector_out, *epi);
-    return cudaLaunchKernelEx(&cfg, splitk_finish_kernel<false>, fix, out, vector_out, Epilogue{});
+    // Which of out, bias and residual have 16-byte aligned pieces.
+    auto aligned = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    const bool rows = fix.N % 8 == 0;
+    int vector = rows && aligned(out) ? 1 : 0;
+    if (epi != nullptr) {
+        vector |= (aligned(epi->bias) ? 2 : 0) | (rows && aligned(epi->residual) ? 4 : 0);
+        return cudaLaunchKernelEx(&cfg, splitk_finish_kernel<true>, fix, out, vector, *epi);
+    }
+    return cudaLaunchKernelEx(&cfg, splitk_finish_kernel<false>, fix, out, vector, Epilogue{});
 }
 
 }  // namespace skinny
