@@ -172,7 +172,7 @@ def _stream_handle(stream):
     import torch
     if stream is None:
         # torch.cuda.current_stream() without the Stream object it makes (3 us a call).
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -363,6 +363,8 @@ def _rows(t, name, width=None):
     if t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
     shape, stride = t.shape, t.stride()
+    if len(shape) == 2 and stride[1] == 1 and shape[0] > 1 and (width is None or width == shape[1]):
+        return stride[0]
     n = 1
     for i in range(len(shape) - 1, 0, -1):
         if stride[i] != n and shape[i] != 1:
@@ -470,7 +472,7 @@ def _own_workspace(device, stream):
     another and share one; a call being captured gets its own, zeroed in the graph, so
     that graphs replayed side by side do not meet."""
     import torch
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         return attention_workspace(device)
     key = (device, stream.value)
     ws = _workspaces.get(key)

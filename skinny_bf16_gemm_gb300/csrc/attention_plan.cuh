@@ -25,7 +25,9 @@ inline int attn_sms(int num_sms) { return num_sms < kAttnMaxSms ? num_sms : kAtt
 // accumulators (NB * D / 4 registers a thread) go.
 __host__ __device__ inline int attn_max_nb(int head_dim) { return head_dim <= 128 ? 4 : 2; }
 
-constexpr int attn_ctas_per_sm(int head_dim) { return head_dim <= 64 ? 2 : 1; }
+// Two CTAs an SM where the rings fit and a warp's step leaves gaps: small heads, and many
+// query heads to a key head.
+constexpr int attn_ctas_per_sm(int head_dim, int nb) { return head_dim <= 64 || (nb > 1 && head_dim <= 128) ? 2 : 1; }
 
 // A partial: heads * head_dim sums, then the heads' maxima and sums of weights. Every
 // CTA has two slots for its chunk's (of an item that began before it, and of one that
@@ -43,7 +45,7 @@ inline size_t attn_workspace_bytes(int sms) {
     size_t most = 0;
     for (int d : dims)
         for (int nb = 1; nb <= attn_max_nb(d); nb *= 2) {
-            const size_t n = static_cast<size_t>(attn_ctas_per_sm(d)) * attn_slots_per_cta() * attn_slot_floats(d, nb);
+            const size_t n = static_cast<size_t>(attn_ctas_per_sm(d, nb)) * attn_slots_per_cta() * attn_slot_floats(d, nb);
             if (n > most) most = n;
         }
     return attn_counter_bytes(sms) + most * sms * sizeof(float);

@@ -54,7 +54,7 @@ struct Shape {
     static constexpr int kSub = 16 * kSets;
     static constexpr int kRowBytes = D * 2;
     static constexpr int kStageBytes = 2 * kSub * kRowBytes;  // keys, then values
-    static constexpr int kStages = D > 192 ? 3 : (D <= 64 ? 3 : D <= 96 ? 4 : D <= 128 ? 3 : 2) * 2 / kSets;
+    static constexpr int kStages = D > 192 ? 3 : D > 128 ? 4 / kSets : D > 96 ? 3 : D > 64 ? 4 : NB > 1 ? 4 : 3;
     static constexpr int kSlots = kStages + 1;  // lookups on their way
     static constexpr int kHeads = 8 * NB;
     static constexpr int kRingBytes = kStages * kStageBytes;  // per warp
@@ -62,7 +62,7 @@ struct Shape {
     static constexpr int kMaximaAt = kHeads * D;  // in a partial: the maxima, then the sums
     // A warp's last partial is kept in its ring, which is empty by then; one of an item
     // that ends earlier in its share here, if there is room, else in the workspace.
-    static constexpr bool kEarlyShared = kWarps * (kRingBytes + kSlotFloats * 4) <= 216 * 1024 / attn_ctas_per_sm(D);
+    static constexpr bool kEarlyShared = kWarps * (kRingBytes + kSlotFloats * 4) <= 216 * 1024 / attn_ctas_per_sm(D, NB);
     static constexpr int kEarlyOffset = kWarps * kRingBytes;
     static constexpr int kFactorOffset = kEarlyOffset + (kEarlyShared ? kWarps * kSlotFloats * 4 : 0);
     static constexpr int kMlOffset = kFactorOffset + kMaxGroups * kHeads * 4;  // factors [kMaxGroups][kHeads]
@@ -174,7 +174,7 @@ struct Cut {
 };
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attention_kernel(const AttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_attention_kernel(const AttentionArgs a) {
     using S = Shape<D, NB>;
     constexpr int kSub = S::kSub, kSets = S::kSets, kSlots = S::kSlots;
     constexpr uint32_t kAllSeen = kSub == 32 ? 0xFFFFFFFFu : (1u << (kSub & 31)) - 1u;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attentio
     __shared__ uint32_t sm_places[kWarps][kSub];
     __shared__ int sm_scan[kWarps];
     __shared__ int sm_key[2 * kWarps];  // items of the warps' partials, -1: none
-    __shared__ int sm_last;
+    __shared__ int sm_last[3];  // arrivals that were the last: two items' chunks, a group
     const uint32_t sbase = ptx::smem_addr(smem);
     int *prefix = reinterpret_cast<int *>(smem + S::kRowsOffset);
     int *lengths = prefix + a.rows + 1;
@@ -258,39 +258,6 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attentio
     struct Place {
         int row, item, tile;
     };
-    auto find = [&](int x) -> Place {  // x: the same in the whole warp
-        int row = 0;  // the first row that ends after tile x
-        for (;; row += 32) {
-            const int r = row + lane;
-            const unsigned over = __ballot_sync(0xFFFFFFFFu, r < a.rows && prefix[r + 1] * items_per_row > x);
-            if (over != 0) {
-                row += __ffs(over) - 1;
-                break;
-            }
-        }
-        const int tiles = prefix[row + 1] - prefix[row];
-        const int in_row = x - prefix[row] * items_per_row;
-        const int item = quotient(in_row, tiles);
-        return {row, item, in_row - item * tiles};
-    };
-    // The end of a chunk or share that would be at tile x: not within an item of at most
-    // `most` tiles (a few tiles more or less cost less than a join).
-    auto snap = [&](int x, int most) -> int {
-        if (x <= 0 || x >= total) return x;
-        const Place p = find(x);
-        const int tiles = prefix[p.row + 1] - prefix[p.row];
-        if (p.tile == 0 || tiles > most) return x;
-        return x - p.tile + (2 * p.tile < tiles ? 0 : tiles);
-    };
-    // This warp's share [x, x_end).
-    int x, x_end;
-    {
-        const int b = snap(cut.begin(cta), kSnapChunk), n = snap(cut.begin(cta + 1), kSnapChunk) - b;
-        x = snap(b + n * warp / kWarps, kSnapShare);
-        x_end = snap(b + n * (warp + 1) / kWarps, kSnapShare);
-        if (warp == 0) x = b;
-        if (warp == kWarps - 1) x_end = b + n;
-    }
     auto next_item = [&](Place &p) {  // only where a further tile exists
         p.tile = 0;
         if (++p.item == items_per_row) {
@@ -298,7 +265,55 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attentio
             do ++p.row; while (prefix[p.row + 1] == prefix[p.row]);
         }
     };
-    Place here = x < x_end ? find(x) : Place{0, 0, 0};
+    // The places of two tiles (the same two in the whole warp).
+    auto find = [&](int x0, int x1, Place (&p)[2]) {
+        const int xs[2] = {x0, x1};
+        int at[2] = {-1, -1};  // rows: the first that ends after the tile
+        for (int r0 = 0; at[0] < 0 || at[1] < 0; r0 += 32) {
+            const int end = r0 + lane < a.rows ? prefix[r0 + lane + 1] * items_per_row : 0x7FFFFFFF;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const unsigned over = __ballot_sync(0xFFFFFFFFu, end > xs[i]);
+                if (at[i] < 0 && over != 0) at[i] = r0 + __ffs(over) - 1;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int begin = prefix[at[i]], tiles = prefix[at[i] + 1] - begin;
+            const int in_row = xs[i] - begin * items_per_row;
+            const int item = quotient(in_row, tiles);
+            p[i] = {at[i], item, in_row - item * tiles};
+        }
+    };
+    // The end of a chunk or share that would be at tile x, at place p: not within an item of
+    // at most `most` tiles (a few tiles more or less cost less than a join).
+    auto snap = [&](int x, Place &p, int most) -> int {
+        const int tiles = prefix[p.row + 1] - prefix[p.row];
+        if (p.tile == 0 || tiles > most) return x;
+        const bool up = 2 * p.tile >= tiles;
+        x += up ? tiles - p.tile : -p.tile;
+        p.tile = 0;
+        if (up && x < total) next_item(p);
+        return x;
+    };
+    // This warp's share [x, x_end), and the place it begins at. The end of the sequence,
+    // where there is no tile, stands for itself.
+    int x, x_end;
+    Place here;
+    {
+        const int last = total - 1;
+        Place p[2];
+        int b = cut.begin(cta), e = cut.begin(cta + 1);
+        find(b, min(e, last), p);
+        b = snap(b, p[0], kSnapChunk);
+        if (e < total) e = snap(e, p[1], kSnapChunk);
+        x = b + (e - b) * warp / kWarps;
+        x_end = b + (e - b) * (warp + 1) / kWarps;
+        find(min(x, last), min(x_end, last), p);
+        if (x < total && warp > 0) x = snap(x, p[0], kSnapShare);
+        if (x_end < total && warp < kWarps - 1) x_end = snap(x_end, p[1], kSnapShare);
+        here = p[0];
+    }
 
     // ---- the copies: one stage a tile ----
     // A stage is refilled as soon as it is read, so that while a warp waits its whole ring
@@ -670,6 +685,12 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attentio
     for (int e = 0; e < 2 * kWarps; ++e)
         alike |= static_cast<unsigned>(__shfl_sync(0xFFFFFFFFu, my_key, e) == my_key) << e;
     unsigned items = __ballot_sync(0xFFFFFFFFu, my_key >= 0 && lane == __ffs(alike) - 1);
+    // Items that other CTAs have pieces of too: at most the first and the last.
+    struct Crossing {
+        int key, first, pieces;
+    };
+    Crossing crossing[2] = {};
+    int crossings = 0;
     for (; items != 0; items &= items - 1) {
         const int key = __shfl_sync(0xFFFFFFFFu, my_key, __ffs(items) - 1);
         const unsigned entries = __shfl_sync(0xFFFFFFFFu, alike, __ffs(items) - 1);
@@ -724,30 +745,55 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attentio
                 }
             }
         }
-        if (dst < 0) continue;
+        if (dst >= 0) crossing[crossings++ > 0 ? 1 : 0] = {key, first, pieces};
+    }
+    if (crossings == 0) return;
 
-        // The chunks' partials: arrive, and the last of a group joins it; arrive, and the
-        // last group's joiner joins the groups. Sources are added in order.
+    // ---- join the chunks ----
+    // Arrive, and the last of a group of chunks joins it; arrive, and the last group's
+    // joiner joins the groups. Sources are added in order.
+    auto arrive = [&](int first, int q, int level, int n) -> int {
+        // Releases all threads' stores (a barrier orders them before it), acquires the other
+        // CTAs'. The counter is zero again for the next call.
+        unsigned *counter = a.counters + 2 * slot_of(first, q) + level;
+        const bool last = ptx::atom_add_acq_rel_gpu(counter, 1u) + 1 == static_cast<unsigned>(n);
+        if (last) *counter = 0u;
+        return last;
+    };
+    auto group_of = [&](int first) { return quotient(cta - first, kAttnGroup) * kAttnGroup; };
+    __syncthreads();  // every thread's stores are done
+    if (tid % 32 == 0 && warp < crossings) {
+        const Crossing &c = warp == 0 ? crossing[0] : crossing[1];
+        const int q0 = group_of(c.first);
+        sm_last[warp] = arrive(c.first, q0, 0, min(kAttnGroup, c.pieces - q0));
+    }
+    __syncthreads();
+    for (int i = 0; i < crossings; ++i) {
+        if (!sm_last[i]) continue;
+        const int key = i == 0 ? crossing[0].key : crossing[1].key;
+        const int first = i == 0 ? crossing[0].first : crossing[1].first;
+        const int pieces = i == 0 ? crossing[0].pieces : crossing[1].pieces;
+        const int row = quotient(key, items_per_row);
+        const Heads heads = heads_of(row, key - row * items_per_row);
         float *factor = reinterpret_cast<float *>(smem + S::kFactorOffset);
         float *sm_m = reinterpret_cast<float *>(smem + S::kMlOffset), *sm_l = sm_m + S::kHeads;
         const int groups = (pieces + kAttnGroup - 1) / kAttnGroup;
-        int q0 = (cta - first) / kAttnGroup * kAttnGroup, q_step = 1, n = min(kAttnGroup, pieces - q0);
+        int q0 = group_of(first), q_step = 1, n = min(kAttnGroup, pieces - q0);
         for (int level = 0; level < 2; ++level) {
-            __syncthreads();  // every thread's stores are done
-            if (tid == 0) {
-                // Releases all threads' stores (the barrier orders them before it), acquires
-                // the other CTAs'.
-                unsigned *counter = a.counters + 2 * slot_of(first, q0) + level;
-                sm_last = ptx::atom_add_acq_rel_gpu(counter, 1u) + 1 == static_cast<unsigned>(n);
-                if (sm_last) *counter = 0u;  // ready for the next call
+            if (level == 1) {
+                __syncthreads();  // every thread's stores are done
+                if (tid == 0) sm_last[2] = arrive(first, 0, 1, groups);
+                __syncthreads();
+                if (!sm_last[2]) break;
+                q0 = 0;
+                q_step = kAttnGroup;
+                n = groups;
             }
-            __syncthreads();
-            if (!sm_last) break;
-            dst = level == 1 || groups == 1 ? -1 : slot_of(first, q0);
+            const int dst = level == 1 || groups == 1 ? -1 : slot_of(first, q0);
             auto source = [&](int k) { return slot_at(slot_of(first, q0 + k * q_step)); };
 
-            // The first loads are in flight while the factors are worked out: a lane is a
-            // source there.
+            // A lane is a source for the factors; the first fragments are on their way
+            // meanwhile.
             constexpr int kPair = kJobs > 1 ? 2 : 1, kBatch = 12;
             float4 u[kPair][kBatch];
             auto load = [&](int job, int k0) {
@@ -758,7 +804,6 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attentio
                         if (k0 + k < n && job + j < kJobs && frag_of(job + j) < kSteps * NB)
                             u[j][k] = __ldcg(reinterpret_cast<const float4 *>(source(k0 + k)) + frag_of(job + j) * 32 + lane);
             };
-            load(0, 0);
             {
                 constexpr int kMine = S::kHeads / kWarps;  // heads of a warp
                 float mk[kMine], lk[kMine], mm[kMine];
@@ -768,6 +813,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attentio
                     mm[i] = mk[i] = lane < n ? __ldcg(src) : -INFINITY;
                     lk[i] = lane < n ? __ldcg(src + S::kHeads) : 0.0f;
                 }
+                load(0, 0);
 #pragma unroll
                 for (int s = 16; s > 0; s >>= 1)
 #pragma unroll
@@ -831,9 +877,6 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D)) decode_attentio
                 }
             }
             if (dst < 0) break;
-            q0 = 0;
-            q_step = kAttnGroup;
-            n = groups;
         }
         __syncthreads();  // the factors are used again
     }
@@ -854,7 +897,7 @@ cudaError_t launch(const AttentionArgs &a, int num_sms, int device, cudaStream_t
     const long long tiles = static_cast<long long>(a.rows) * a.kv_heads * a.head_blocks *
                             ((a.capacity + S::kSub - 1ll) / S::kSub);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(num_sms * attn_ctas_per_sm(D), (tiles + kWarps - 1) / kWarps)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(num_sms * attn_ctas_per_sm(D, NB), (tiles + kWarps - 1) / kWarps)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = S::bytes(a.rows);
     cfg.stream = stream;
