@@ -38,6 +38,8 @@
 namespace skinny {
 namespace {
 
+// The maximum of no scores: finite, so that exp2(-inf - m) is 0 and exp2(m - m) is 1.
+constexpr float kNoMaximum = -3.402823466e+38f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kWarps = kAttnWarps;
 constexpr int kThreads = kWarps * 32;
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         float m[NB][2], l[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            m[b][0] = m[b][1] = -INFINITY;
+            m[b][0] = m[b][1] = kNoMaximum;
             l[b][0] = l[b][1] = 0.0f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
@@ -546,29 +548,30 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
                         for (int e = 0; e < 4; ++e)
                             if (!((valid >> (t * 16 + (e >> 1) * 8 + lane / 4)) & 1)) sc[t][b][e] = -INFINITY;
             }
+            // The maximum m is kept until a score is 2^8 past it (weights up to 2^8 cost
+            // nothing in FP32): most steps then need no maximum over the lanes, and no rescaling.
             float top[NB][2];
-            bool grew = false;
+            bool past = false;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float t = fmaxf(sc[0][b][e], sc[0][b][e + 2]);
                     if constexpr (kSets == 2) t = fmaxf(t, fmaxf(sc[kSets - 1][b][e], sc[kSets - 1][b][e + 2]));
-                    t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
-                    t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
-                    t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-                    top[b][e] = fmaxf(t, m[b][e]);
-                    grew |= top[b][e] > m[b][e];
+                    top[b][e] = t;
+                    past |= top[b][e] > m[b][e] + 8.0f;
                 }
-            }
-            if (__any_sync(0xFFFFFFFFu, grew)) {
+            if (__any_sync(0xFFFFFFFFu, past)) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        // A maximum that is still -inf leaves zeros: any factor will do.
-                        const float f = m[b][e] == -INFINITY ? 0.0f : exp2_approx(m[b][e] - top[b][e]);
-                        m[b][e] = top[b][e];
+                        float t = fmaxf(top[b][e], m[b][e]);
+                        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
+                        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
+                        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
+                        const float f = exp2_approx(m[b][e] - t);
+                        m[b][e] = t;
                         l[b][e] *= f;
 #pragma unroll
                         for (int s = 0; s < kSteps; ++s) {
@@ -580,13 +583,12 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
             uint32_t hi[kSets][NB][2], lo[kSets][NB][2];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const float ref[2] = {m[b][0] == -INFINITY ? 0.0f : m[b][0], m[b][1] == -INFINITY ? 0.0f : m[b][1]};
 #pragma unroll
                 for (int t = 0; t < kSets; ++t) {
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[e] = exp2_approx(sc[t][b][e] - ref[e & 1]);
+                        p[e] = exp2_approx(sc[t][b][e] - m[b][e & 1]);
                         l[b][e & 1] += p[e];
                     }
                     // Tokens by heads -> heads by tokens, the B operand of the product with V.
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         for (int job = 0; job < kJobs; ++job) {
             const int frag = frag_of(job), h = frag % NB * 8 + (lane & 3) * 2;
             if (frag >= kSteps * NB) break;
-            float2 mk[2 * kWarps], mm = make_float2(-INFINITY, -INFINITY), ll = make_float2(0.0f, 0.0f);
+            float2 mk[2 * kWarps], mm = make_float2(kNoMaximum, kNoMaximum), ll = make_float2(0.0f, 0.0f);
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 2 * kWarps; ++e)
@@ -722,9 +724,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
                 if (entries >> e & 1) {
                     const float2 lk = *reinterpret_cast<const float2 *>(entry_at(e) + S::kMaximaAt + S::kHeads + h);
                     const float4 u = reinterpret_cast<const float4 *>(entry_at(e))[frag * 32 + lane];
-                    // A maximum of -inf goes with sums of zero, or of NaN.
-                    const float f0 = mk[e].x == -INFINITY ? 1.0f : exp2_approx(mk[e].x - mm.x);
-                    const float f1 = mk[e].y == -INFINITY ? 1.0f : exp2_approx(mk[e].y - mm.y);
+                    const float f0 = exp2_approx(mk[e].x - mm.x), f1 = exp2_approx(mk[e].y - mm.y);
                     ll.x += f0 * lk.x;
                     ll.y += f1 * lk.y;
                     v.x += f0 * u.x; v.y += f1 * u.y; v.z += f0 * u.z; v.w += f1 * u.w;
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
                     const float *src = source(min(lane, n - 1)) + S::kMaximaAt + warp * kMine + i;
-                    mm[i] = mk[i] = lane < n ? __ldcg(src) : -INFINITY;
+                    mm[i] = mk[i] = lane < n ? __ldcg(src) : kNoMaximum;
                     lk[i] = lane < n ? __ldcg(src + S::kHeads) : 0.0f;
                 }
                 load(0, 0);
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
                     for (int i = 0; i < kMine; ++i) mm[i] = fmaxf(mm[i], __shfl_xor_sync(0xFFFFFFFFu, mm[i], s));
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
-                    const float f = mk[i] == -INFINITY ? 1.0f : exp2_approx(mk[i] - mm[i]);
+                    const float f = exp2_approx(mk[i] - mm[i]);
                     if (lane < n) factor[lane * S::kHeads + warp * kMine + i] = f;
                     lk[i] *= f;
                 }
