@@ -403,8 +403,10 @@ typedef struct {
 SKINNY_API int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *args,
                                  const skinny_launch_opts *opts, void *stream);
 
-/* Most rows of decode_attention_bf16. */
+/* Most rows of decode_attention_bf16, and the bytes at the start of its workspace that
+ * must be zero before the workspace's first use. */
 #define SKINNY_ATTENTION_MAX_ROWS 1024
+#define SKINNY_ATTENTION_COUNTER_BYTES 8192
 
 /*
  * decode_attention_bf16 -- attention of one new token per row over a paged cache,
@@ -429,9 +431,10 @@ SKINNY_API int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *args,
  *   lse          [rows, q_heads] FP32 or NULL: the natural logarithm of the sum of
  *                exp(scale q.k), for joining with attention over other tokens.
  *   workspace    device memory of skinny_attention_workspace_bytes(SM count) bytes,
- *                16-byte aligned, all zeros before its first use; every call leaves it
- *                ready for the next. Calls that may run at the same time (other
- *                streams, graphs replayed side by side) need one each.
+ *                16-byte aligned, its first SKINNY_ATTENTION_COUNTER_BYTES zero before
+ *                its first use; every call leaves it ready for the next. Calls that may
+ *                run at the same time (other streams, graphs replayed side by side)
+ *                need one each.
  *   Scores, maxima, sums and the output are FP32, weights are rounded to 15 bits of
  *   precision (two BF16 terms) for the product with the values, and the output is
  *   rounded once. Deterministic: the same inputs on the same device give the same bits.

@@ -454,14 +454,19 @@ def qk_norm_rope_bf16(qkv, q_heads, kv_heads, q_gamma, k_gamma, rope, positions,
     return q_out
 
 
+ATTENTION_COUNTER_BYTES = 8192
+
+
 def attention_workspace(device=None):
-    """A workspace for decode_attention_bf16 on a device: zeros, left ready by every call.
-    Calls that may run at the same time need one each."""
+    """A workspace for decode_attention_bf16 on a device; every call leaves it ready for the
+    next. Calls that may run at the same time need one each."""
     import torch
     dev = torch.cuda.current_device() if device is None else device
     sms = torch.cuda.get_device_properties(dev).multi_processor_count
-    return torch.zeros(load_library().skinny_attention_workspace_bytes(sms), dtype=torch.uint8,
-                       device=torch.device("cuda", dev) if isinstance(dev, int) else dev)
+    ws = torch.empty(load_library().skinny_attention_workspace_bytes(sms), dtype=torch.uint8,
+                     device=torch.device("cuda", dev) if isinstance(dev, int) else dev)
+    ws[:ATTENTION_COUNTER_BYTES].zero_()
+    return ws
 
 
 _workspaces = {}  # (device, stream) -> the workspace of calls that bring none

@@ -896,8 +896,8 @@ int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_la
     a.out = static_cast<uint16_t *>(p->out);
     a.lse = static_cast<float *>(p->lse);
     a.counters = static_cast<unsigned *>(p->workspace);
-    a.partials = reinterpret_cast<float *>(static_cast<char *>(p->workspace) +
-                                           attn_counter_bytes(sms));
+    static_assert(kAttnCounterBytes == SKINNY_ATTENTION_COUNTER_BYTES, "the header's number");
+    a.partials = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + kAttnCounterBytes);
     if (launch_decode_attention(a, D, sms, dev, static_cast<cudaStream_t>(stream), ls.pdl) !=
         cudaSuccess) {
         cudaGetLastError();

@@ -35,11 +35,9 @@ constexpr int attn_ctas_per_sm(int head_dim, int nb) { return head_dim <= 64 || 
 constexpr int attn_slot_floats(int head_dim, int nb) { return 8 * nb * (head_dim + 2); }
 constexpr int attn_slots_per_cta() { return 2 + kAttnWarps; }
 
-// The workspace: two counters for each of the chunks' slots (all zero between calls),
-// then the slots.
-inline size_t attn_counter_bytes(int sms) {
-    return (static_cast<size_t>(2 * 2) * 2 * sms * sizeof(unsigned) + 255) / 256 * 256;
-}
+// The workspace: two counters for each of the chunks' slots (all zero between calls), in
+// a space that does for the largest grid, then the slots.
+constexpr size_t kAttnCounterBytes = static_cast<size_t>(2 * 2 * 2) * kAttnMaxSms * sizeof(unsigned);
 inline size_t attn_workspace_bytes(int sms) {
     constexpr int dims[] = {64, 96, 128, 192, 256};
     size_t most = 0;
@@ -48,7 +46,7 @@ inline size_t attn_workspace_bytes(int sms) {
             const size_t n = static_cast<size_t>(attn_ctas_per_sm(d, nb)) * attn_slots_per_cta() * attn_slot_floats(d, nb);
             if (n > most) most = n;
         }
-    return attn_counter_bytes(sms) + most * sms * sizeof(float);
+    return kAttnCounterBytes + most * sms * sizeof(float);
 }
 
 }  // namespace skinny

@@ -7,25 +7,42 @@
 // so every key and value is read once. Bound by HBM: 4 D bytes a token and key head
 // against 4 G D flops (G heads sharing) -- 8 flops a byte for G = 8.
 //
-// CTAs of 4 warps take equal ranges of tiles (attention_plan.cuh). A warp streams its
-// own 16 or 32 tokens of every tile through a private ring of cp.async stages and keeps
+// CTAs of 4 warps, one or two to an SM; every warp has an equal share of the tiles
+// (attention_plan.cuh), streams it through a private ring of cp.async stages and keeps
 // its own maximum, sum and accumulator, so nothing in the main loop waits for another
-// warp; the four are joined when the piece of an item ends, while the copies of the
-// next piece go on. The ring is filled by 16-byte copies with
-// each token's address from the block table, so pages of any size, tokens at any
-// 16-byte-aligned strides and ranges that end inside a page are all the same to it.
-// The products run on the tensor cores with tokens (scores) and head dimension
-// (output) as the MMA's 16 rows and the query heads as its 8 columns: HBM feeds an
-// SM about 23 bytes a clock, a fraction of what these small MMAs need to be fast.
+// warp. The ring runs across items. It is filled by 16-byte copies with each token's
+// address from the block table, so pages of any size, tokens at any 16-byte-aligned
+// strides and ranges that end inside a page are all the same to it. A copy engine's
+// tensor loads would want pages of a multiple of the tile; one bulk copy per row was not
+// tried.
+// The products run on the tensor cores with tokens (scores) and head dimension (output)
+// as the 16 rows of mma.sync and the query heads as its 8 columns. HBM feeds an SM 23
+// bytes a clock, 8 KB (16 tokens of 128) in 356 clocks; the 24 MMAs of those tokens take
+// 48 clocks of its four tensor cores (1024 multiply-adds a clock, measured), so a larger
+// MMA's set-up through tensor memory would buy nothing for one block of 8 heads. With 32
+// heads to a key head the instructions around the MMAs are the bound (see below).
 // Weights p are split into two BF16 terms (p truncated, and the rest rounded: within
 // 2^-15 of p), so the product with V loses nothing that the BF16 output shows; maxima
 // and sums are FP32.
 //
-// An item whose tiles span several CTAs is joined by whichever of them is last to
-// publish its partial (a counter in the workspace): it adds the partials in range
-// order, so the bits do not depend on who was last. More than 16 partials are joined
-// in two such levels, 16 at a time, to keep the last reader's share short. No CTA
-// waits for another.
+// An item that is one warp's alone is stored from its registers. Other warps' partials
+// are joined by the CTA through shared memory, and an item whose tiles span several CTAs
+// by whichever of them is last to publish its part (a counter in the workspace): it adds
+// the parts in order, so the bits do not depend on who was last. More than 20 parts are
+// joined in two such levels, to keep the last reader's share short. No CTA waits for
+// another.
+//
+// Measured on GB300 (graph of calls; bytes of keys and values over the time): 131071
+// tokens of 8 key heads of 128, 56 query heads, 95 us, 5.7 TB/s; 64 ragged rows to 16384
+// of 8 x 64 170-195 us (the two layouts), 5.4-6.2 TB/s; a window of 4096 in 32 rows 86 us,
+// 5.5 TB/s; 64 ragged rows to 4000 of one key head 20 us; one row of 129 tokens 7.2 us.
+// What is left over the floor: about 1.5 us until the lengths' prefix sums and shares are
+// known and 1.5 us to the first tile; SMs that get up to 15 % less of the memory's
+// bandwidth than the average (their CTAs end last); the joins, 3 us for one level and
+// 3 us more for a second. Tried and not faster: keys refilled before the softmax (the
+// copies' issue waits for the memory system, and the softmax with it), 8 warps a CTA,
+// two CTAs an SM with half the ring for 128-wide heads, L2 prefetch sizes on the copies,
+// chunks dealt out as CTAs come free (each costs a join).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
