@@ -394,9 +394,12 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         const uint32_t valid = __ballot_sync(0xFFFFFFFFu, off >= 0);
         if (lane == 0) sm_valid[warp][stage] = valid;
         const uint32_t to = ring + stage * S::kStageBytes;
-        if (valid == kAllSeen && !a.wide) {
-            if (lane < kSub) places[lane] = static_cast<uint32_t>(off >> 3);
+        auto share = [&]() {
+            if (lane < kSub) places[lane] = off < 0 ? 0u : static_cast<uint32_t>(off >> 3);
             __syncwarp();
+        };
+        if (valid == kAllSeen && !a.wide) {
+            share();
 #pragma unroll
             for (int it = 0; it < kCopies; ++it) {
                 int tok, ch, swz;
@@ -415,15 +418,20 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
                 cp_async16(dst, reinterpret_cast<const uint8_t *>(a.k + ch * 8) + e);
                 cp_async16(dst + kSub * S::kRowBytes, reinterpret_cast<const uint8_t *>(a.v + ch * 8) + e);
             }
-        } else if (valid != 0) {
-#pragma unroll 1
+        } else if (valid != 0) {  // the last tile of an item, as a rule
+            if (kSets == 2) share();
+#pragma unroll(kSets == 2 ? 4 : 1)
             for (int it = 0; it < kCopies; ++it) {
                 const int id = it * 32 + lane, tok = id / kChunks, ch = id % kChunks;
-                const long long o = __shfl_sync(0xFFFFFFFFu, off, tok);
+                const bool there = valid >> tok & 1;
+                size_t e = kSets == 2 ? static_cast<size_t>(places[tok]) * 16 : 0;
+                if (kSets == 1 || a.wide) {
+                    const long long o = __shfl_sync(0xFFFFFFFFu, off, tok);
+                    e = o < 0 ? 0 : static_cast<size_t>(o) * 2;
+                }
                 const uint32_t dst = to + tok * S::kRowBytes + (ch ^ swizzle(tok)) * 16;
-                const long long e = (o < 0 ? 0 : o) + ch * 8;
-                cp_async16_or_zeros(dst, a.k + e, o >= 0);
-                cp_async16_or_zeros(dst + kSub * S::kRowBytes, a.v + e, o >= 0);
+                cp_async16_or_zeros(dst, reinterpret_cast<const uint8_t *>(a.k + ch * 8) + e, there);
+                cp_async16_or_zeros(dst + kSub * S::kRowBytes, reinterpret_cast<const uint8_t *>(a.v + ch * 8) + e, there);
             }
         }
     };
