@@ -354,17 +354,19 @@ def gather_shards_bf16(shards, out, stream=None):
     return out
 
 
-def _rows(t, name, width=None):
+def _rows(t, name, bf16, width=None, rows=None):
     """A CUDA bfloat16 tensor whose rows (all but its first axis) are contiguous: the
     stride between rows, in elements (the row's width for a single row)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+    try:
+        good = t.dtype == bf16 and t.is_cuda
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if not good:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2 and stride[1] == 1 and shape[0] > 1 and (width is None or width == shape[1]):
-        return stride[0]
+    shape = t.shape
+    if rows is not None and shape[0] != rows:
+        raise ValueError(f"{name} has {shape[0]} rows, expected {rows}")
+    stride = t.stride()
     n = 1
     for i in range(len(shape) - 1, 0, -1):
         if stride[i] != n and shape[i] != 1:
@@ -376,16 +378,16 @@ def _rows(t, name, width=None):
 
 
 def _plain_cuda(t, name, dtype, shape):
+    """The address of a contiguous CUDA tensor of a dtype and shape."""
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor (got {t.dtype} on {t.device})")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _cache_fields(k_cache, v_cache):
+def _cache_fields(k_cache, v_cache, bf16):
     """The fields of skinny_kv_cache for two [pages, page_size, kv_heads, head_dim] views."""
-    import torch
-    bf16 = torch.bfloat16
     if k_cache.dtype != bf16 or v_cache.dtype != bf16 or not (k_cache.is_cuda and v_cache.is_cuda):
         raise TypeError("k_cache and v_cache must be CUDA bfloat16 tensors")
     shape = k_cache.shape
@@ -415,38 +417,36 @@ def qk_norm_rope_bf16(qkv, q_heads, kv_heads, q_gamma, k_gamma, rope, positions,
     stored). Returns ``q_out``.
     """
     import torch
-    qkv_stride = _rows(qkv, "qkv")
-    if qkv.dim() != 2 or q_heads < 1 or kv_heads < 1 or qkv.shape[1] % (q_heads + 2 * kv_heads):
-        raise ValueError(f"qkv {tuple(qkv.shape)} must be [M, ({q_heads} + 2 * {kv_heads}) * head_dim]")
-    M = qkv.shape[0]
-    D = qkv.shape[1] // (q_heads + 2 * kv_heads)
-    if q_out.shape[0] != M or (k_out is not None and k_out.shape[0] != M):
-        raise ValueError(f"q_out and k_out must have {M} rows")
-    if q_gamma is not None:
-        _bf16_cuda(q_gamma, "q_gamma", (D,))
-    if k_gamma is not None:
-        _bf16_cuda(k_gamma, "k_gamma", (D,))
+    bf16 = torch.bfloat16
+    qkv_stride = _rows(qkv, "qkv", bf16)
+    shape = qkv.shape
+    heads = q_heads + 2 * kv_heads
+    if len(shape) != 2 or q_heads < 1 or kv_heads < 1 or shape[1] % heads:
+        raise ValueError(f"qkv {tuple(shape)} must be [M, ({q_heads} + 2 * {kv_heads}) * head_dim]")
+    M = shape[0]
+    D = shape[1] // heads
+    q_stride = _rows(q_out, "q_out", bf16, q_heads * D, M)
+    k_ptr = k_stride = q_gamma_ptr = k_gamma_ptr = rope_ptr = positions_ptr = slots_ptr = 0
     max_pos = rot_dim = 0
-    if rope is not None:
-        if rope.dim() != 2:
-            raise ValueError(f"rope must be [max_pos, rot_dim], got {tuple(rope.shape)}")
-        _plain_cuda(rope, "rope", torch.float32, rope.shape)
-        _plain_cuda(positions, "positions", torch.int32, (M,))
-        max_pos, rot_dim = rope.shape
     cache = _NO_CACHE
+    if k_out is not None:
+        k_ptr, k_stride = k_out.data_ptr(), _rows(k_out, "k_out", bf16, kv_heads * D, M)
+    if q_gamma is not None:
+        q_gamma_ptr = _plain_cuda(q_gamma, "q_gamma", bf16, (D,))
+    if k_gamma is not None:
+        k_gamma_ptr = _plain_cuda(k_gamma, "k_gamma", bf16, (D,))
+    if rope is not None:
+        max_pos, rot_dim = rope.shape if rope.dim() == 2 else (0, 0)
+        rope_ptr = _plain_cuda(rope, "rope", torch.float32, (max_pos, rot_dim))
+        positions_ptr = _plain_cuda(positions, "positions", torch.int32, (M,))
     if k_cache is not None or v_cache is not None:
         if k_cache is None or v_cache is None or slots is None:
             raise ValueError("k_cache, v_cache and slots go together")
-        cache = _cache_fields(k_cache, v_cache)
-        _plain_cuda(slots, "slots", torch.int64, (M,))
-    a = _pack_rope(
-        qkv.data_ptr(), qkv_stride, M, q_heads, kv_heads, D,
-        0 if q_gamma is None else q_gamma.data_ptr(), 0 if k_gamma is None else k_gamma.data_ptr(),
-        eps, 0 if rope is None else rope.data_ptr(), max_pos, rot_dim, bool(interleaved),
-        0 if rope is None else positions.data_ptr(), q_out.data_ptr(),
-        _rows(q_out, "q_out", q_heads * D), 0 if k_out is None else k_out.data_ptr(),
-        0 if k_out is None else _rows(k_out, "k_out", kv_heads * D), *cache,
-        0 if cache is _NO_CACHE else slots.data_ptr())
+        cache = _cache_fields(k_cache, v_cache, bf16)
+        slots_ptr = _plain_cuda(slots, "slots", torch.int64, (M,))
+    a = _pack_rope(qkv.data_ptr(), qkv_stride, M, q_heads, kv_heads, D, q_gamma_ptr, k_gamma_ptr, eps,
+                   rope_ptr, max_pos, rot_dim, bool(interleaved), positions_ptr, q_out.data_ptr(), q_stride,
+                   k_ptr, k_stride, *cache, slots_ptr)
     o = _opts(pdl, None)
     st = load_library().qk_norm_rope_bf16(a, None if o is None else ctypes.byref(o),
                                           _stream_handle(stream))
@@ -499,32 +499,31 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
     for one kept per stream (a call under graph capture gets its own). Returns ``out``.
     """
     import torch
-    q_stride = _rows(q, "q")
+    bf16 = torch.bfloat16
+    q_stride = _rows(q, "q", bf16)
     shape = q.shape
     if len(shape) != 3:
         raise ValueError(f"q must be [rows, q_heads, head_dim], got {tuple(shape)}")
     rows, q_heads, D = shape
-    cache = _cache_fields(k_cache, v_cache)
+    cache = _cache_fields(k_cache, v_cache, bf16)
     if cache[5] != D:
         raise ValueError(f"q has heads of {D}, the cache of {cache[5]}")
-    _bf16_cuda(out, "out", shape)
+    out_ptr = _plain_cuda(out, "out", bf16, shape)
     if block_table.dtype != torch.int32 or not block_table.is_cuda:
         raise TypeError("block_table must be a CUDA int32 tensor")
-    if block_table.dim() != 2 or block_table.shape[0] != rows or \
-            (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+    table_shape, table_stride = block_table.shape, block_table.stride()
+    if len(table_shape) != 2 or table_shape[0] != rows or (table_stride[1] != 1 and table_shape[1] > 1):
         raise ValueError(f"block_table must be [{rows}, table_width] with contiguous rows")
-    _plain_cuda(lengths, "lengths", torch.int32, (rows,))
-    if lse is not None:
-        _plain_cuda(lse, "lse", torch.float32, (rows, q_heads))
+    lengths_ptr = _plain_cuda(lengths, "lengths", torch.int32, (rows,))
+    lse_ptr = 0 if lse is None else _plain_cuda(lse, "lse", torch.float32, (rows, q_heads))
     handle = _stream_handle(stream)
     if workspace is None:
         workspace = _own_workspace(q.device.index, handle)
-    width = block_table.shape[1]
+    width = table_shape[1]
     a = _pack_attention(
         q.data_ptr(), q_stride, rows, q_heads, *cache, block_table.data_ptr(),
-        block_table.stride(0) if rows > 1 else width, width, lengths.data_ptr(), window, sinks,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-        workspace.data_ptr(), workspace.nbytes)
+        table_stride[0] if rows > 1 else width, width, lengths_ptr, window, sinks,
+        D ** -0.5 if scale is None else scale, out_ptr, lse_ptr, workspace.data_ptr(), workspace.nbytes)
     o = _opts(pdl, None)
     st = load_library().decode_attention_bf16(a, None if o is None else ctypes.byref(o), handle)
     _check(st, "decode_attention_bf16")

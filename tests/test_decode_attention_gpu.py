@@ -227,6 +227,42 @@ def test_offsets_past_32_bits(cuda_ok):
     run_and_check(q, k, v, ints([[2, 0, 1], [1, 2, 0]]), ints([150, 192]))
 
 
+def test_offsets_past_36_bits(cuda_ok):
+    """Pages 2^34 + 64 elements apart: the pool spans more than 2^32 chunks of 16 bytes, which
+    the kernel's short addresses do not reach."""
+    D, page, step = 128, 16, (1 << 34) + 64
+    free, _ = torch.cuda.mem_get_info()
+    if free < (80 << 30):
+        pytest.skip("needs 80 GB of free memory")
+    pool = torch.empty(2 * step + 4 * page * D, dtype=torch.bfloat16, device="cuda")
+    k = pool.as_strided((3, page, 1, D), (step, D, D, 1))
+    v = pool.as_strided((3, page, 1, D), (step, D, D, 1), storage_offset=2 * page * D)
+    for t in (k, v):
+        t.copy_(torch.randn(3, page, 1, D, device="cuda"))
+    for heads in (4, 12):
+        q = torch.randn(2, heads, D, device="cuda").to(torch.bfloat16)
+        run_and_check(q, k, v, ints([[2, 0, 1], [1, 2, 0]]), ints([48, 37]))
+    del pool, k, v
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(1024, 1024, 64), (1024, 8, 64), (512, 512, 128)])
+def test_most_heads(cuda_ok, Hq, Hkv, D):
+    run_and_check(*setup([33, 70], Hq, Hkv, D, 16, seed=Hq))
+
+
+def test_given_stream(cuda_ok):
+    """The stream argument, with the calling thread's current stream another one."""
+    args = setup([3000, 40], 8, 2, 128, 16)
+    want, _ = run_and_check(*args)
+    st = torch.cuda.Stream()
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    sk.decode_attention_bf16(*args, out, stream=st)
+    st.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_same_bits_every_time_and_workspace_left_zeroed(cuda_ok):
     ws = sk.attention_workspace()
     args = setup([30000, 5, 800], 16, 2, 128, 32)

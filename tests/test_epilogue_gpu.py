@@ -100,6 +100,17 @@ def test_plain_call_has_the_gemm_bits(cuda_ok, M, N, K):
     assert torch.equal(run(x, W, None, "none", None).view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("M,N,K", [(8, 65536, 64), (64, 50001, 128), (31, 40000, 200), (64, 40000, 1000)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_many_tiles_a_cta(cuda_ok, M, N, K, in_place):
+    """Several tiles a CTA: whole ones between the split ends, both accumulators in turn."""
+    x, W = gemm_inputs_device(M, N, K, workloads.seed_for("epi2", M, N, K), kind="int")
+    bias, res = extras(M, N, 8, "int")
+    got = run(x, W, bias, "relu", res, in_place)
+    want = activate(x.to(F64) @ W.to(F64).t() + bias.to(F64), "relu") + res.to(F64)
+    assert torch.equal(got, want.float().to(torch.bfloat16))
+
+
 def test_activation_tails(cuda_ok):
     """Sums from -200 to 200 through each activation: no NaN where exp or its inverse
     overflows."""

@@ -130,6 +130,31 @@ def test_bad_positions_and_slots_are_reported_and_not_written(cuda_ok):
     assert torch.equal(k, k0) and torch.equal(v, v0)
 
 
+def test_bad_rows_among_many(cuda_ok):
+    """Blocks that go through many rows leave the bad ones out and go on."""
+    M, Hq, Hkv, D, page = 5000, 7, 1, 128, 16
+    qkv, qg, kg, rope, pos = inputs(M, Hq, Hkv, D, D)
+    k, v = make_cache(M // page + 1, page, Hkv, D, "nhd", 3)
+    k0 = k.clone()
+    slots = torch.arange(M, device="cuda")
+    bad = torch.arange(3, M, 7, device="cuda")
+    pos[bad[::2]] = -5
+    slots[bad[1::2]] = 2 ** 33
+    q = torch.full((M, Hq, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    sk.qk_norm_rope_bf16(qkv, Hq, Hkv, qg, kg, rope, pos, q, k_cache=k, v_cache=v, slots=slots)
+    assert sk.device_error() == (11, 256)
+    good = torch.ones(M, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    x = qkv.view(M, -1, D)
+    want, tol = norm_rope_reference(x[:, :Hq], qg, rope, pos.clamp(0), False, 1e-6)
+    check_close(q[good], want[good], tol[good], "q")
+    assert (q[bad] == 5).all()
+    want, tol = norm_rope_reference(x[:, Hq:Hq + Hkv], kg, rope, pos.clamp(0), False, 1e-6)
+    flat, flat0 = k.view(-1, Hkv, D)[:M], k0.view(-1, Hkv, D)[:M]
+    check_close(flat[good], want[good], tol[good], "k")
+    assert torch.equal(flat[bad], flat0[bad])
+
+
 def test_slots_past_32_bits(cuda_ok):
     """The last page starts 8 GB into the pool."""
     D, page, step = 64, 16, (1 << 31) + 64
