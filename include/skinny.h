@@ -382,6 +382,7 @@ typedef struct {
  *   rows' padding included).
  *   A position outside [0, max_pos) or a slot past the last page: nothing of that row
  *   is written and skinny_device_error() reports bit 256.
+ *   No call has to be made outside stream capture first.
  *   Errors: SKINNY_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARG, _DEVICE, _LAUNCH.
  */
 typedef struct {
@@ -448,7 +449,8 @@ SKINNY_API int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *args,
  *   must not overlap anything.
  *   On the device, a length outside [0, table_width * page_size] is taken as the
  *   nearest, a token on a page outside [0, num_pages) as not seen, and
- *   skinny_device_error() reports bit 256.
+ *   skinny_device_error() reports bit 256. No call has to be made outside stream
+ *   capture first.
  *   Errors: SKINNY_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARG, _DEVICE, _LAUNCH.
  */
 typedef struct {

@@ -61,14 +61,14 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kWarps = kAttnWarps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxGroups = 32;   // groups of the second level of a join
-constexpr int kSnapChunk = 8;    // items of so many tiles are not cut by chunks,
-constexpr int kSnapShare = 2;    // and of so many by warps' shares
+constexpr int kSnapShare = 2;    // items of so many tiles are not cut by warps' shares
 __device__ int g_attn_err;  // nonzero: a length or page index was out of range
 
 template <int D, int NB>
 struct Shape {
-    // A tile is a warp's step: 16 tokens, or two such sets side by side where the
-    // registers allow (their chains of dependent instructions overlap).
+    // A tile is a warp's step: 16 tokens, or two such sets side by side, whose chains of
+    // dependent instructions overlap, where registers and rings allow (131071 tokens of
+    // 128-wide heads: 94 us with two sets and 4 warps an SM, 101 with one and 8).
     static constexpr int kSets = NB == 1 && D <= 192 ? 2 : 1;
     static constexpr int kSub = 16 * kSets;
     static constexpr int kRowBytes = D * 2;
@@ -172,7 +172,7 @@ __device__ __forceinline__ Seen seen_of(int n, int window, int sinks) {
 // less than one, which the remainder's sign shows. A third of an integer division's time.
 __device__ __forceinline__ int quotient(int x, int d) {
     const int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(d)));
-    const int r = x - q * d;
+    const int r = static_cast<int>(static_cast<unsigned>(x) - static_cast<unsigned>(q) * static_cast<unsigned>(d));
     return r < 0 ? q - 1 : r >= d ? q + 1 : q;
 }
 
@@ -265,12 +265,17 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
     const int items_per_row = a.kv_heads * a.head_blocks;
     const int total = prefix[a.rows] * items_per_row;  // below 2^31 (host check)
     if (total == 0) return;
-    // Fewer CTAs where each would have less than kMinTiles a warp: a step costs less than
-    // a join.
-    constexpr int kMinTiles = 2;
-    const int chunks = min(static_cast<int>(gridDim.x), (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles));
+    // No fewer tiles a warp than `least`: one where items are short (64 rows to 200 tokens:
+    // 8.4 us with one, 11.2 with two), two where every further piece makes a join longer
+    // (4 rows to 9000: 14.1 us with two, 15.3 with one).
+    const int least = quotient(total, a.rows * items_per_row) <= 32 ? 1 : 2;
+    const int chunks = min(static_cast<int>(gridDim.x), (total + kWarps * least - 1) / (kWarps * least));
     if (cta >= chunks) return;
     const Cut cut(total, chunks);
+    // Chunks do not cut items of up to `uncut` tiles: a few tiles more or less cost less than
+    // a join over CTAs (32 rows of 8 heads to 1000 tokens: 20.6 us with 16, 22.4 with 8; one
+    // row of 8 heads of 500 tokens, in chunks of 4 to 8 tiles: 9.3 with 8, 10.0 with 16).
+    const int uncut = cut.base >= 8 ? 16 : 8;
 
     // A place in the tile sequence: tile `tile` of item `item` (key head and head block)
     // of row `row`.
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         }
     };
     // The end of a chunk or share that would be at tile x, at place p: not within an item of
-    // at most `most` tiles (a few tiles more or less cost less than a join).
+    // at most `most` tiles.
     auto snap = [&](int x, Place &p, int most) -> int {
         const int tiles = prefix[p.row + 1] - prefix[p.row];
         if (p.tile == 0 || tiles > most) return x;
@@ -324,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         Place p[2];
         int b = cut.begin(cta), e = cut.begin(cta + 1);
         find(b, min(e, last), p);
-        b = snap(b, p[0], kSnapChunk);
-        if (e < total) e = snap(e, p[1], kSnapChunk);
+        b = snap(b, p[0], uncut);
+        if (e < total) e = snap(e, p[1], uncut);
         x = b + (e - b) * warp / kWarps;
         x_end = b + (e - b) * (warp + 1) / kWarps;
         find(min(x, last), min(x_end, last), p);
@@ -726,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         const int item_x = prefix[row] * items_per_row + item * row_tiles;
         // Chunks first .. first + pieces - 1 hold a piece of this item each (a short one is in
         // one chunk, wherever the even cut would be).
-        const bool within = row_tiles <= kSnapChunk;
+        const bool within = row_tiles <= uncut;
         const int first = within ? cta : cut.owner(item_x);
         const int pieces = within ? 1 : cut.owner(item_x + row_tiles - 1) - first + 1;
         const Heads heads = heads_of(row, item);

@@ -157,3 +157,42 @@ def test_two_layers_keep_the_plain_calls_bits(cuda_ok):
         ends.append(y)
     torch.cuda.synchronize()
     assert torch.equal(*ends)
+
+
+FIRST_CALLS_CAPTURED = """
+import torch, skinny_bf16_gemm_gb300 as sk
+D = 128
+qkv = torch.randn(3, 9 * D, device="cuda").bfloat16()
+gamma = torch.ones(D, device="cuda").bfloat16()
+rope = torch.randn(100, D, device="cuda")
+pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+q = torch.empty(3, 7, D, device="cuda", dtype=torch.bfloat16)
+k = torch.randn(10, 16, 1, D, device="cuda").bfloat16()
+v = k.clone()
+slots = torch.arange(3, device="cuda")
+table = torch.arange(9, dtype=torch.int32, device="cuda").view(3, 3)
+lengths = torch.tensor([40, 3, 20], dtype=torch.int32, device="cuda")
+out = torch.zeros_like(q)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    sk.qk_norm_rope_bf16(qkv, 7, 1, gamma, gamma, rope, pos, q, k_cache=k, v_cache=v, slots=slots)
+    sk.decode_attention_bf16(q, k, v, table, lengths, out)
+graph.replay()
+torch.cuda.synchronize()
+replayed = out.clone()
+sk.decode_attention_bf16(q, k, v, table, lengths, out)
+assert torch.equal(replayed, out) and out.any() and sk.device_error() == (0, 0)
+print("ok")
+"""
+
+
+def test_first_calls_of_a_process_captured(cuda_ok):
+    """Rotation and attention may be captured from a process's first call on."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], capture_output=True, text=True, cwd=root,
+                       timeout=300)
+    assert p.returncode == 0 and "ok" in p.stdout, p.stderr
