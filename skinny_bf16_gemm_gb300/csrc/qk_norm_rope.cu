@@ -21,7 +21,7 @@
 // U = 4 keeps the loads of four heads in flight, U = 1 spreads few rows over the most
 // threads. Measured on GB300, 8191 rows of 56 + 2 x 8 heads of 128: 57 us, 5.3 TB/s
 // (one row a block: 87 us; kinds mixed, scalar: 88 us; U = 2: 69 us; 768 threads an SM:
-// 82 us); 64 rows 3.6 us and one row of 9 heads 1.9 us in a graph.
+// 82 us); 64 rows 3.5 us and one row of 9 heads 2.2 us in a graph.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -257,9 +257,11 @@ cudaError_t launch(const RopeArgs &a, int num_sms, cudaStream_t stream, bool pdl
 
 template <int L>
 cudaError_t launch_lanes(const RopeArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
-    // Few heads in all: one per group, so that they spread over the SMs.
+    // U = 1 for few heads in all, so that they spread over the SMs: one row of 9 heads of 128
+    // 2.1 us, 2.5 with U = 4; 64 rows of 9 heads 2.7 and 3.0; 64 rows of 72, close to the
+    // limit, 3.5 both; 128 rows of 72 4.3 and 3.7.
     const long long heads = static_cast<long long>(a.rows) * (a.q_heads + 2 * a.kv_heads);
-    const bool halves = a.rot_dim > 0 && !a.interleaved, few = heads * L < num_sms * 2048ll;
+    const bool halves = a.rot_dim > 0 && !a.interleaved, few = heads * L < num_sms * 512ll;
     if (halves) {
         if (few) return launch<L, 1, true>(a, num_sms, stream, pdl);
         return launch<L, 4, true>(a, num_sms, stream, pdl);
