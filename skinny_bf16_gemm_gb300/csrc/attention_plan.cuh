@@ -16,8 +16,11 @@ namespace skinny {
 constexpr int kAttnMinTile = 16;    // tokens of the smallest tile
 constexpr int kAttnMaxRows = 1024;  // rows whose prefix sums a CTA keeps
 constexpr int kAttnWarps = 4;
-constexpr int kAttnGroup = 20;      // chunks' partials joined at a time
-constexpr int kAttnMaxSms = 256;    // SMs used: two levels of joins reach 20 * 32 CTAs
+// Partials of an item that are joined at once; more are joined in groups (16 rows to 2000,
+// 16 heads of 128: 19.0 us, 22.2 in groups from 13 on; two items of 32 parts, 256-wide:
+// 23.8 us in groups, 37.8 at once).
+constexpr int kAttnOneLevel = 20;
+constexpr int kAttnMaxSms = 256;    // SMs used: groups of up to 23 of 512 CTAs
 
 inline int attn_sms(int num_sms) { return num_sms < kAttnMaxSms ? num_sms : kAttnMaxSms; }
 
@@ -26,9 +29,10 @@ inline int attn_sms(int num_sms) { return num_sms < kAttnMaxSms ? num_sms : kAtt
 __host__ __device__ inline int attn_max_nb(int head_dim) { return head_dim <= 128 ? 4 : 2; }
 
 // Two CTAs an SM where the rings fit and a warp's step leaves gaps: small heads (64 ragged
-// rows to 16384 of 64-wide heads: 176 us, 208 with one CTA and twice the ring), and many
-// query heads to a key head (16 rows to 8192, 128-wide, 16 heads: 50 us, 53 with one; 32
-// heads: 82, 99 with one).
+// rows to 16384 of 64-wide heads, pages by head: 163 us, 194 with one CTA and more stages),
+// and many query heads to a key head (16 rows to 8192, 128-wide, 16 heads: 46 us, 50 with
+// one; 32 heads: 66, 85 with one). One for 192-wide heads, 16 to a key head: 45 us, 49 with
+// two, whose copies queue too long.
 constexpr int attn_ctas_per_sm(int head_dim, int nb) { return head_dim <= 64 || (nb > 1 && head_dim <= 128) ? 2 : 1; }
 
 // A partial: heads * head_dim sums, then the heads' maxima and sums of weights. Every

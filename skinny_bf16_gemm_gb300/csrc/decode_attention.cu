@@ -29,20 +29,22 @@
 // are joined by the CTA through shared memory, and an item whose tiles span several CTAs
 // by whichever of them is last to publish its part (a counter in the workspace): it adds
 // the parts in order, so the bits do not depend on who was last. More than 20 parts are
-// joined in two such levels, to keep the last reader's share short. No CTA waits for
-// another.
+// joined in two such levels, in about as many groups as a group has parts, to keep the last
+// reader's share short. No CTA waits for another.
 //
 // Measured on GB300 (graph of calls; bytes of keys and values over the time): 131071
-// tokens of 8 key heads of 128, 56 query heads, 95 us, 5.7 TB/s; 64 ragged rows to 16384
-// of 8 x 64 170-195 us (the two layouts), 5.4-6.2 TB/s; a window of 4096 in 32 rows 86 us,
-// 5.5 TB/s; 64 ragged rows to 4000 of one key head 20 us; one row of 129 tokens 7.2 us.
+// tokens of 8 key heads of 128, 56 query heads, 88 us, 6.1 TB/s; 64 ragged rows to 16384
+// of 8 x 64 163-187 us (the two layouts), 5.6-6.4 TB/s; a window of 4096 in 32 rows 82 us,
+// 5.8 TB/s; 64 ragged rows to 4000 of one key head 20 us; one row of 129 tokens 7.2 us.
 // What is left over the floor: about 1.5 us until the lengths' prefix sums and shares are
-// known and 1.5 us to the first tile; SMs that get up to 15 % less of the memory's
-// bandwidth than the average (their CTAs end last); the joins, 3 us for one level and
-// 3 us more for a second. Tried and not faster: keys refilled before the softmax (the
-// copies' issue waits for the memory system, and the softmax with it), 8 warps a CTA,
-// two CTAs an SM with half the ring for 128-wide heads, L2 prefetch sizes on the copies,
-// chunks dealt out as CTAs come free (each costs a join).
+// known and 1.5 us to the first tile; SMs that get less of the memory's bandwidth than the
+// average (their CTAs end last); the joins, 3 us for one level and 3 us more for a second;
+// from 16 heads to a key head on, and at 192 and 256, the chain of instructions of a step.
+// Tried and not faster: keys refilled before the softmax (the copies' issue waits for the
+// memory system, and the softmax with it), 8 warps a CTA, two CTAs an SM of 128-wide heads
+// with one set of 16 tokens a step (131071 tokens 92-96 us; 64 rows to 4000 18.3), L2
+// prefetch sizes on the copies, chunks dealt out as CTAs come free (each costs a join),
+// several items of a CTA joined by a warp or two each (3 % slower for one row of one item).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -67,17 +69,22 @@ __device__ int g_attn_err;  // nonzero: a length or page index was out of range
 template <int D, int NB>
 struct Shape {
     // A tile is a warp's step: 16 tokens, or two such sets side by side, whose chains of
-    // dependent instructions overlap, where registers and rings allow (131071 tokens of
-    // 128-wide heads: 94 us with two sets and 4 warps an SM, 101 with one and 8).
-    static constexpr int kSets = NB == 1 && D <= 192 ? 2 : 1;
+    // dependent instructions overlap, where registers and rings allow (16 rows to 8192 of
+    // 128-wide heads 39.5 us, 42.4 with one set, three stages and two CTAs an SM; of 192-wide,
+    // whose two sets' copies queue too long, 36.9 us with two and 34.6 with one).
+    static constexpr int kSets = NB == 1 && D <= 128 ? 2 : 1;
     static constexpr int kSub = 16 * kSets;
     static constexpr int kRowBytes = D * 2;
     static constexpr int kStageBytes = 2 * kSub * kRowBytes;  // keys, then values
-    static constexpr int kStages = D > 192 ? 3 : D > 128 ? 4 / kSets : D > 96 ? 3 : D > 64 ? 4 : NB > 1 ? 4 : 3;
+    // One stage is read while the other's copies are on their way: 64 KB an SM for 64-, 128-
+    // and 256-wide heads. A third is slower everywhere (131071 tokens of 128: 90 us, 95 with
+    // three; 16 heads to a key head 46 and 50; 256-wide 37 and 43): with more of every SM's
+    // copies queued the SMs that get less of the memory's bandwidth fall further behind.
+    static constexpr int kStages = 2;
     static constexpr int kSlots = kStages + 1;  // lookups on their way
     static constexpr int kHeads = 8 * NB;
-    static constexpr int kRingBytes = kStages * kStageBytes;  // per warp
     static constexpr int kSlotFloats = attn_slot_floats(D, NB);
+    static constexpr int kRingBytes = std::max(kStages * kStageBytes, kSlotFloats * 4);  // per warp
     static constexpr int kMaximaAt = kHeads * D;  // in a partial: the maxima, then the sums
     // A warp's last partial is kept in its ring, which is empty by then; one of an item
     // that ends earlier in its share here, if there is room, else in the workspace.
@@ -87,10 +94,10 @@ struct Shape {
     static constexpr int kMlOffset = kFactorOffset + kMaxGroups * kHeads * 4;  // factors [kMaxGroups][kHeads]
     static constexpr int kLookOffset = kMlOffset + 2 * kHeads * 4;             // m, l of a join
     static constexpr int kRowsOffset = kLookOffset + kWarps * kSlots * (kSub + 1) * 8;  // prefix, lengths
-    static_assert(kSlotFloats * 4 <= kRingBytes, "a partial fits the ring");
+    static_assert(kRingBytes % 16 == 0, "16-byte copies");
     static_assert(kSub >= kAttnMinTile, "the host counts tiles of kAttnMinTile");
     static_assert(kLookOffset % 8 == 0, "64-bit places");
-    static_assert(kRowsOffset + (2 * kAttnMaxRows + 1) * 4 + 1024 <= 232448, "a block's shared memory");
+    static_assert(kRowsOffset + (2 * kAttnMaxRows + 1) * 4 + 3072 <= 232448, "a block's shared memory");
     static int bytes(int rows) { return kRowsOffset + (2 * rows + 1) * 4; }
 };
 
@@ -206,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
     constexpr bool kWide = kChunks % 8 == 0;
     auto swizzle = [](int r) { return kWide ? r & 7 : (r >> 1) & 3; };
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint4 sm_q[kWarps][32];
     __shared__ uint32_t sm_valid[kWarps][S::kStages];
     __shared__ uint32_t sm_places[kWarps][kSub];
     __shared__ int sm_scan[kWarps];
@@ -445,7 +453,15 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
     cp_async_commit();
 
     // Queries as the MMA's B: head lane / 4 of each block of 8, values 2 (lane % 4) on.
+    // 16-byte loads through L1 (the warps of a CTA share them), then the fragments by way of
+    // 512 bytes of shared memory. The next item's are on their way from the last scores on
+    // where there are registers for them (one row of 7 heads to 4000: 10.6 us, 10.9 without;
+    // 16 rows to 8192, 32 heads of 128 to a key head: 97 us with them, for spills, 64 without).
+    // Loads of a fragment each, 4 bytes a lane, kept one row's CTAs waiting for the L2 slices
+    // that hold its queries (131071 tokens of one key head: 22.8 us, 19.1 this way).
+    constexpr bool kQueriesAhead = D * NB <= 256;
     uint32_t qf[kSteps][NB][2];
+    uint4 qw[NB][kChunks / 4];
     auto load_queries = [&](const Place &p) {
         const int kv_head = quotient(p.item, a.head_blocks);
         const int g0 = (p.item - kv_head * a.head_blocks) * a.block_heads;
@@ -453,16 +469,32 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int h = b * 8 + lane / 4;
-            const unsigned *q = reinterpret_cast<const unsigned *>(
-                a.q + p.row * a.q_stride + static_cast<long long>(kv_head * a.group + g0 + h) * D + (lane & 3) * 2);
+            const uint4 *q = reinterpret_cast<const uint4 *>(
+                a.q + p.row * a.q_stride + static_cast<long long>(kv_head * a.group + g0 + h) * D) + (lane & 3);
 #pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks) {
-                qf[ks][b][0] = h < n ? __ldcg(q + ks * 8) : 0u;
-                qf[ks][b][1] = h < n ? __ldcg(q + ks * 8 + 4) : 0u;
-            }
+            for (int i = 0; i < kChunks / 4; ++i) qw[b][i] = h < n ? q[i * 4] : make_uint4(0, 0, 0, 0);
         }
     };
-    if (x < x_end) load_queries(here);
+    auto place_queries = [&]() {
+        const int put = (lane & ~3) | ((lane ^ (lane >> 3)) & 3);
+        const uint32_t get = ptx::smem_addr(sm_q[warp]) +
+                             (((lane & 7) * 4 + (((lane >> 3) ^ ((lane & 7) >> 1)) & 3)) << 4);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < kChunks / 4; ++i) {
+                sm_q[warp][put] = qw[b][i];
+                __syncwarp();
+                uint32_t r[4];
+                ldmatrix4(r, get);
+                __syncwarp();
+                qf[2 * i][b][0] = r[0];
+                qf[2 * i][b][1] = r[1];
+                qf[2 * i + 1][b][0] = r[2];
+                qf[2 * i + 1][b][1] = r[3];
+            }
+    };
+    if (kQueriesAhead && x < x_end) load_queries(here);
     cp_async_wait<0>();
     __syncwarp();
 #pragma unroll 1
@@ -517,6 +549,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         const int row = here.row, item = here.item;
         const bool more = x + n_tiles < x_end;
 
+        if (!kQueriesAhead) load_queries(here);
+        place_queries();
         float o[kSteps][NB][4];
         float m[NB][2], l[NB][2];
 #pragma unroll
@@ -558,9 +592,9 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
                             mma16816(ks % kChains == 0 ? sc[t][b] : sd[t][b], kf, qf[ks][b][0], qf[ks][b][1]);
                     }
             }
-            if (more && i == n_tiles - 1) {  // the next item's queries are on their way
+            if (more && i == n_tiles - 1) {
                 next_item(here);
-                load_queries(here);
+                if (kQueriesAhead) load_queries(here);
             }
 #pragma unroll
             for (int t = 0; t < kSets; ++t)
@@ -708,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
 
     // ---- join what the warps have left, item by item ----
     // Each warp takes its share of the fragments (16 values of 8 heads).
-    constexpr int kJobs = (kSteps + kWarps - 1) / kWarps * NB;
-    auto frag_of = [&](int job) { return (warp * (kJobs / NB) + job / NB) * NB + job % NB; };
+    constexpr int kPer = (kSteps + kWarps - 1) / kWarps, kJobs = kPer * NB;
+    auto frag_of = [&](int job) { return (warp * kPer + job / NB) * NB + job % NB; };
     auto slot_of = [&](int first, int q) { return 2 * (first + q) + (q == 0 ? 1 : 0); };  // piece q of an item
     const int my_key = lane < 2 * kWarps ? sm_key[lane] : -1;
     unsigned alike = 0;  // entries of the same item
@@ -790,12 +824,15 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         if (last) *counter = 0u;
         return last;
     };
-    auto group_of = [&](int first) { return quotient(cta - first, kAttnGroup) * kAttnGroup; };
+    auto group_size = [&](int pieces) {
+        return pieces <= kAttnOneLevel ? kAttnOneLevel : static_cast<int>(ceilf(sqrtf(static_cast<float>(pieces))));
+    };
+    auto group_of = [&](int first, int size) { return quotient(cta - first, size) * size; };
     __syncthreads();  // every thread's stores are done
     if (tid % 32 == 0 && warp < crossings) {
         const Crossing &c = warp == 0 ? crossing[0] : crossing[1];
-        const int q0 = group_of(c.first);
-        sm_last[warp] = arrive(c.first, q0, 0, min(kAttnGroup, c.pieces - q0));
+        const int size = group_size(c.pieces), q0 = group_of(c.first, size);
+        sm_last[warp] = arrive(c.first, q0, 0, min(size, c.pieces - q0));
     }
     __syncthreads();
     for (int i = 0; i < crossings; ++i) {
@@ -807,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
         const Heads heads = heads_of(row, key - row * items_per_row);
         float *factor = reinterpret_cast<float *>(smem + S::kFactorOffset);
         float *sm_m = reinterpret_cast<float *>(smem + S::kMlOffset), *sm_l = sm_m + S::kHeads;
-        const int groups = (pieces + kAttnGroup - 1) / kAttnGroup;
-        int q0 = group_of(first), q_step = 1, n = min(kAttnGroup, pieces - q0);
+        const int size = group_size(pieces), groups = quotient(pieces + size - 1, size);
+        int q0 = group_of(first, size), q_step = 1, n = min(size, pieces - q0);
         for (int level = 0; level < 2; ++level) {
             if (level == 1) {
                 __syncthreads();  // every thread's stores are done
@@ -816,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
                 __syncthreads();
                 if (!sm_last[2]) break;
                 q0 = 0;
-                q_step = kAttnGroup;
+                q_step = size;
                 n = groups;
             }
             const int dst = level == 1 || groups == 1 ? -1 : slot_of(first, q0);
