@@ -453,12 +453,12 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
     cp_async_commit();
 
     // Queries as the MMA's B: head lane / 4 of each block of 8, values 2 (lane % 4) on.
-    // 16-byte loads through L1 (the warps of a CTA share them), then the fragments by way of
-    // 512 bytes of shared memory. The next item's are on their way from the last scores on
-    // where there are registers for them (one row of 7 heads to 4000: 10.6 us, 10.9 without;
-    // 16 rows to 8192, 32 heads of 128 to a key head: 97 us with them, for spills, 64 without).
-    // Loads of a fragment each, 4 bytes a lane, kept one row's CTAs waiting for the L2 slices
-    // that hold its queries (131071 tokens of one key head: 22.8 us, 19.1 this way).
+    // 16-byte loads, then the fragments by way of 512 bytes of shared memory: loads of a
+    // fragment each, 4 bytes a lane, kept one row's CTAs waiting for the L2 slices that hold
+    // its queries (131071 tokens of one key head: 22.8 us, 19.1 this way). They are on their
+    // way from the item before's last scores on where there are registers for them (one row
+    // of 7 heads to 4000: 10.6 us, 10.9 without; 16 rows to 8192, 32 heads of 128 to a key
+    // head: 97 us, for spills, 64 without).
     constexpr bool kQueriesAhead = D * NB <= 256;
     uint32_t qf[kSteps][NB][2];
     uint4 qw[NB][kChunks / 4];
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
             const uint4 *q = reinterpret_cast<const uint4 *>(
                 a.q + p.row * a.q_stride + static_cast<long long>(kv_head * a.group + g0 + h) * D) + (lane & 3);
 #pragma unroll
-            for (int i = 0; i < kChunks / 4; ++i) qw[b][i] = h < n ? q[i * 4] : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kChunks / 4; ++i) qw[b][i] = h < n ? __ldcg(q + i * 4) : make_uint4(0, 0, 0, 0);
         }
     };
     auto place_queries = [&]() {

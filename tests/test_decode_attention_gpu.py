@@ -73,6 +73,14 @@ def test_long_rows_are_split_and_joined(cuda_ok, R, n, Hq, Hkv, D):
     run_and_check(*setup([n] * R, Hq, Hkv, D, 64, seed=n))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 128), (14, 2, 128), (16, 1, 256), (32, 1, 128), (8, 1, 192), (4, 1, 64)])
+@pytest.mark.parametrize("parts", [19, 20, 21, 26, 37])
+def test_joins_around_the_second_level(cuda_ok, parts, Hq, Hkv, D):
+    """A row of about so many chunks a key head, 8 tiles each; two key heads meet in a chunk."""
+    tile = 32 if Hq // Hkv <= 8 and D <= 128 else 16
+    run_and_check(*setup([parts * 8 * tile - 3], Hq, Hkv, D, 64, seed=parts))
+
+
 def test_many_rows(cuda_ok):
     """1024 rows, from empty to a few tiles; the fused table is wider than any row."""
     g = torch.Generator()
