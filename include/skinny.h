@@ -362,9 +362,10 @@ typedef struct {
  *              Values from rot_dim on are not rotated.
  *   positions  [M] int32.
  *   q_out      rows of q_heads * head_dim, q_stride elements apart. May be qkv itself
- *              with q_stride == qkv_stride (in place).
+ *              with q_stride == qkv_stride (in place; any stride for one row).
  *   k_out      rows of kv_heads * head_dim, k_stride apart, or NULL. May be the key
- *              heads of qkv in place (qkv + q_heads * head_dim, k_stride == qkv_stride).
+ *              heads of qkv in place (qkv + q_heads * head_dim, k_stride == qkv_stride or
+ *              one row).
  *   cache      cache.k and cache.v NULL: nothing is appended. kv_heads and head_dim as
  *              in the call; along an axis longer than one, its elements must not
  *              overlap (stride >= head_dim).

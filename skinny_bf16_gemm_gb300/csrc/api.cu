@@ -737,7 +737,8 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
         if (cache->k == cache->v) return SKINNY_ERR_ALIAS;
     }
     // Every output against every input and the other outputs; q_out and k_out may be
-    // their own heads of qkv in place.
+    // their own heads of qkv in place. One row has no distance to a next one: its strides
+    // need not agree (a view of a single row has its own width there).
     const struct { const void *p; size_t n; } in[] = {
         {p->qkv, row_span(p->M, p->qkv_stride, width)},
         {p->q_gamma, static_cast<size_t>(D) * 2},
@@ -745,9 +746,9 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
         {p->rot_dim ? p->rope : nullptr, static_cast<size_t>(p->max_pos) * p->rot_dim * 4},
         {p->rot_dim ? p->positions : nullptr, static_cast<size_t>(p->M) * 4},
         {has_cache ? p->slots : nullptr, static_cast<size_t>(p->M) * 8}};
-    const bool q_in_place = p->q_out == p->qkv && p->q_stride == p->qkv_stride;
+    const bool q_in_place = p->q_out == p->qkv && (p->M == 1 || p->q_stride == p->qkv_stride);
     const bool k_in_place = p->k_out == static_cast<const uint16_t *>(p->qkv) + q_width &&
-                            p->k_stride == p->qkv_stride;
+                            (p->M == 1 || p->k_stride == p->qkv_stride);
     const struct { const void *p; size_t n; bool in_place; } outs[] = {
         {p->q_out, row_span(p->M, p->q_stride, q_width), q_in_place},
         {p->k_out, p->k_out ? row_span(p->M, p->k_stride, kv_width) : 0, k_in_place},
