@@ -458,8 +458,9 @@ ATTENTION_COUNTER_BYTES = 8192
 
 
 def attention_workspace(device=None):
-    """A workspace for decode_attention_bf16 on a device; every call leaves it ready for the
-    next. Calls that may run at the same time need one each."""
+    """A workspace for decode_attention_bf16 on a device, made ready on the current stream;
+    every call leaves it ready for the next. Calls that may run at the same time need one
+    each."""
     import torch
     dev = torch.cuda.current_device() if device is None else device
     sms = torch.cuda.get_device_properties(dev).multi_processor_count
@@ -473,17 +474,27 @@ _workspaces = {}  # (device, stream) -> the workspace of calls that bring none
 
 
 def _own_workspace(device, stream):
-    """The workspace of a call that brings none: calls on one stream run one after
-    another and share one; a call being captured gets its own, zeroed in the graph, so
-    that graphs replayed side by side do not meet."""
+    """The workspace of a call on ``stream`` (a handle) that brings none. Calls on one
+    stream run one after another and share one; a call being captured gets its own,
+    zeroed in the graph, so that graphs replayed side by side do not meet. Both are made
+    with the launch stream current, whatever the caller's is: the zeroing comes before
+    the kernel, and the memory goes to no other stream's call while the kernel runs."""
+    import torch
+    handle = stream.value or 0
+    if handle != torch._C._cuda_getCurrentRawStream(device):
+        on = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+        with torch.cuda.stream(on):
+            return _current_workspace(device, handle)
+    return _current_workspace(device, handle)
+
+
+def _current_workspace(device, handle):
     import torch
     if torch._C._cuda_isCurrentStreamCapturing():
         return attention_workspace(device)
-    key = (device, stream.value)
-    ws = _workspaces.get(key)
+    ws = _workspaces.get((device, handle))
     if ws is None:
-        ws = _workspaces[key] = attention_workspace(device)
-        torch.cuda.current_stream(device).synchronize()  # zeroed before another stream's first use
+        ws = _workspaces.setdefault((device, handle), attention_workspace(device))
     return ws
 
 
@@ -496,7 +507,9 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
     table_width] int32; lengths [rows] int32; out like q, contiguous; lse [rows, q_heads]
     FP32 or None. scale: 1 / sqrt(head_dim) if None. window > 0: a row sees its last
     ``window`` tokens and its first ``sinks``. workspace: attention_workspace(), or None
-    for one kept per stream (a call under graph capture gets its own). Returns ``out``.
+    for one kept per stream; a call whose stream is captured by torch.cuda.graph gets its
+    own (a capture begun by other means needs a workspace that lives as long as its graph).
+    Returns ``out``.
     """
     import torch
     bf16 = torch.bfloat16
@@ -518,7 +531,10 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
     lse_ptr = 0 if lse is None else _plain_cuda(lse, "lse", torch.float32, (rows, q_heads))
     handle = _stream_handle(stream)
     if workspace is None:
-        workspace = _own_workspace(q.device.index, handle)
+        device = torch._C._cuda_getDevice()
+        if q.device.index != device:
+            _check(4, "decode_attention_bf16")  # as the call itself would say
+        workspace = _own_workspace(device, handle)
     width = table_shape[1]
     a = _pack_attention(
         q.data_ptr(), q_stride, rows, q_heads, *cache, block_table.data_ptr(),

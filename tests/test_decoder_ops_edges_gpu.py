@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import skinny_bf16_gemm_gb300 as sk
+from test_decode_attention_gpu import setup
 from test_decoder_layer_gpu import H, build, check_stages, place
 from test_qk_norm_rope_gpu import inputs
 
@@ -47,3 +48,92 @@ def test_layer_of_one_token(cuda_ok, pdl):
     layer.replay()
     torch.cuda.synchronize()
     check_stages(layer, y_in)
+
+
+def attention_calls(n, longest=12000):
+    """(arguments, expected output) of n calls whose items span many CTAs."""
+    calls = []
+    for s in range(n):
+        args = setup([longest + 7 * s, 300], 14, 2, 128, 16, seed=40 + s)
+        out = torch.empty_like(args[0])
+        sk.decode_attention_bf16(*args, out, workspace=sk.attention_workspace())
+        calls.append((args, out))
+    torch.cuda.synchronize()
+    return calls
+
+
+def test_captured_on_streams_forked_from_the_current_one(cuda_ok):
+    """Calls without a workspace on two branches of a capture, while the branch that is the
+    current stream takes memory of the workspaces' size and writes over it."""
+    calls = attention_calls(3)
+    outs = [torch.zeros_like(w) for _, w in calls]
+    size = sk.attention_workspace().nbytes
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for _ in range(3):
+            for side in sides:
+                side.wait_stream(main)
+            for side, (args, _), out in zip(sides, calls, outs):
+                sk.decode_attention_bf16(*args, out, stream=side)
+                torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+            sk.decode_attention_bf16(*calls[2][0], outs[2])
+            torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+            for side in sides:
+                main.wait_stream(side)
+    for _ in range(20):
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for out, (_, want) in zip(outs, calls):
+            assert torch.equal(out, want)
+
+
+def test_captured_stream_that_is_not_the_current_one(cuda_ok):
+    """A graph of calls on its own stream, replayed beside eager calls on that stream and
+    beside a second such graph."""
+    calls = attention_calls(3)
+    outs = [torch.zeros_like(w) for _, w in calls]
+    st, other = torch.cuda.Stream(), torch.cuda.Stream()
+    sk.decode_attention_bf16(*calls[2][0], outs[2], stream=st)  # the stream's own workspace is there already
+    graphs = []
+    torch.cuda.synchronize()
+    for (args, _), out in zip(calls[:2], outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            with torch.cuda.stream(other):
+                sk.decode_attention_bf16(*args, out, stream=st)
+        graphs.append(graph)
+    lanes = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for lane, graph in zip(lanes, graphs):
+            with torch.cuda.stream(lane):
+                graph.replay()
+        sk.decode_attention_bf16(*calls[2][0], outs[2], stream=st)
+        torch.cuda.synchronize()
+        for out, (_, want) in zip(outs, calls):
+            assert torch.equal(out, want)
+
+
+def test_given_streams_take_turns_with_the_current_one(cuda_ok):
+    """Eager calls on streams given by object and by handle, their workspaces made on the way."""
+    calls = attention_calls(3)
+    outs = [torch.zeros_like(w) for _, w in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream().cuda_stream, None]
+    for _ in range(20):
+        for st, (args, _), out in zip(streams, calls, outs):
+            sk.decode_attention_bf16(*args, out, stream=st)
+    torch.cuda.synchronize()
+    for out, (_, want) in zip(outs, calls):
+        assert torch.equal(out, want)
+    default = torch.zeros_like(outs[0])
+    with torch.cuda.stream(streams[0]):
+        sk.decode_attention_bf16(*calls[0][0], default, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(default, calls[0][1])

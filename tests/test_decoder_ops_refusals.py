@@ -33,3 +33,64 @@ def test_one_row_in_place_whatever_the_strides(lib, mem, q_stride, qkv_stride):
     assert call(q_out=p + 128, q_stride=q_stride) == ALIAS
     assert call(q_out=k_heads, q_stride=q_stride) == ALIAS
     assert call(q_out=p, q_stride=q_stride, k_out=p, k_stride=2 * 64) == ALIAS
+
+
+class FakeStreams:
+    """The streams of a process without a GPU: a current one, and those being captured."""
+
+    def __init__(self, monkeypatch, current, capturing):
+        import contextlib
+
+        import torch
+        self.current, self.made = current, []
+
+        @contextlib.contextmanager
+        def on(stream):
+            before, self.current = self.current, stream
+            yield
+            self.current = before
+
+        def make(device=None):
+            self.made.append(self.current)
+            return object()
+        for name, f in (("_cuda_getDevice", lambda: 0), ("_cuda_getCurrentRawStream", lambda d: self.current),
+                        ("_cuda_isCurrentStreamCapturing", lambda: self.current in capturing)):
+            monkeypatch.setattr(torch._C, name, f)
+        for name, f in (("stream", on), ("ExternalStream", lambda s, device=None: s),
+                        ("default_stream", lambda device=None: 0),
+                        ("current_stream", lambda d=None: type("S", (), {"synchronize": lambda s: None})())):
+            monkeypatch.setattr(torch.cuda, name, f)
+        monkeypatch.setattr(sk, "attention_workspace", make)
+        monkeypatch.setattr(sk, "_workspaces", {})
+
+    def workspace(self, stream):
+        return sk._own_workspace(0, ctypes.c_void_p(stream))
+
+
+@pytest.mark.parametrize("capturing", [{11}, {11, 22}, {22}, set()])
+def test_a_call_without_workspace_gets_it_on_the_stream_it_runs_on(monkeypatch, capturing):
+    """Made and zeroed on the launch stream, so that both come before the kernel and the memory
+    is not given to others while it runs; under a capture of that stream, and only then, one
+    for the call alone."""
+    f = FakeStreams(monkeypatch, 11, capturing)
+    a, b = f.workspace(22), f.workspace(22)
+    assert f.made == ([22, 22] if 22 in capturing else [22])
+    assert (a is b) == (22 not in capturing)
+    assert f.current == 11
+    f.made.clear()
+    a, b = f.workspace(11), f.workspace(11)
+    assert f.made == ([11, 11] if 11 in capturing else [11])
+    assert (a is b) == (11 not in capturing)
+    f.made.clear()
+    f.workspace(0)  # the default stream, from another one
+    assert f.made == [0]
+
+
+def test_an_eager_call_after_a_capture_does_not_share_its_workspace(monkeypatch):
+    """The graph's workspace is not kept for the stream."""
+    capturing = {22}
+    f = FakeStreams(monkeypatch, 11, capturing)
+    a = f.workspace(22)
+    capturing.clear()
+    b = f.workspace(22)
+    assert a is not b and f.workspace(22) is b
