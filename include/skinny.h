@@ -188,7 +188,8 @@ typedef enum {
  *   opts      host pointer, or NULL for the process-wide settings (see
  *             decode_gemm_bf16_ex).
  *   out[m][n] = BF16(act(s + bias[n]) + residual[m][n]), s the FP32 sum over k of
- *   x[m,k] W[n,k]: every step in FP32, one rounding. With neither bias nor residual
+ *   x[m,k] W[n,k]: every step in FP32, one rounding; the activations keep their relative
+ *   precision down to values of about 1e-36, below which they may be -0. With neither bias nor residual
  *   and SKINNY_ACT_NONE the bits are decode_gemm_bf16's. With programmatic dependent
  *   launch bias and residual are read after the wait for the previous kernel.
  *   Other rules (sizes, the device's scratch) and errors as decode_gemm_bf16_ex;

@@ -19,7 +19,11 @@ struct Epilogue {
 
 __device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
 
-// The activation of n values; one branch, not one a value.
+// The activation of n values; one branch, not one a value. The GELUs by the complement,
+// v erfc(-v / sqrt 2) / 2, and by v / (1 + exp(-2u)) = v (1 + tanh u) / 2: 1 + erf and 1 + tanh
+// cancel for negative v (30 % off at -5, 0 from -5.5 on). Where the exponential overflows the
+// value is under 1e-36 and comes out as -0. The approximate quotient is 2 ulp off (64 x 18432
+// x 7168: 47.6 us, 50.3 with the IEEE one); erfcf costs 1 us more there than erff did.
 template <int n>
 __device__ __forceinline__ void activate(float (&v)[n], int activation) {
     switch (activation) {
@@ -33,12 +37,12 @@ __device__ __forceinline__ void activate(float (&v)[n], int activation) {
             break;
         case kActGelu:
 #pragma unroll
-            for (int i = 0; i < n; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
+            for (int i = 0; i < n; ++i) v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678118654752f);
             break;
         case kActGeluTanh:
 #pragma unroll
             for (int i = 0; i < n; ++i)
-                v[i] = 0.5f * v[i] * (1.0f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+                v[i] = __fdividef(v[i], 1.0f + expf(-1.59576912160573071f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
             break;
         default: break;
     }

@@ -1,9 +1,12 @@
 """The decoder-layer operators on the GPU at the edges of what they accept: a single token,
 the far ends of the activations, weights that underflow, captures on a given stream."""
+import math
+
 import pytest
 import torch
 
 import skinny_bf16_gemm_gb300 as sk
+from attention_helpers import F64, HALF_BF16, check_close
 from test_decode_attention_gpu import setup
 from test_decoder_layer_gpu import H, build, check_stages, place
 from test_qk_norm_rope_gpu import inputs
@@ -137,3 +140,43 @@ def test_given_streams_take_turns_with_the_current_one(cuda_ok):
         sk.decode_attention_bf16(*calls[0][0], default, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(default, calls[0][1])
+
+
+@pytest.mark.parametrize("M,K", [(1, 8), (16, 7168), (40, 64), (64, 7168)])
+@pytest.mark.parametrize("act,lowest", [("silu", -80.0), ("gelu", -12.5), ("gelu_tanh", -10.0)])
+def test_activation_tails_keep_their_relative_precision(cuda_ok, M, K, act, lowest):
+    """Sums that are the bias exactly (all else is zero), from where a value is about 1e-36 to
+    10, every BF16 value on the way: relative to the value, half a BF16 step and what FP32
+    leaves of the definition v Phi(v) or v sigmoid(s):
+      erf form: v / sqrt 2 is off by 2 U32 at most, by which erfc moves (2 x^2 + 1) times as
+      much, x = 12.5 / sqrt 2: 158 * 2 U32; erfc itself 8 steps (16 U32), two products 2 U32:
+      below 336 U32 = 2^-15;
+      sigmoid forms: s = -2 u to 88, its roundings and its constants' 10 U32 in all, which
+      exp multiplies by 88; exp 2 steps, the sum and the quotient 9 U32: below 2^-14."""
+    v = torch.arange(0, 2 ** 16, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    v = v[torch.isfinite(v) & (v >= lowest) & (v <= 10) & (v.abs() > 1e-30)].contiguous()
+    N = v.numel()
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    sk.decode_gemm_bf16_epilogue(x, W, out, v, act)
+    d = v.to(F64)
+    if act == "gelu":
+        want = 0.5 * d * torch.special.erfc(-d / math.sqrt(2))
+    else:
+        s = d if act == "silu" else 2 * math.sqrt(2 / math.pi) * (d + 0.044715 * d ** 3)
+        want = d * torch.sigmoid(s)
+    tol = want.abs() * (HALF_BF16 * (1 + 2.0 ** -14) + 2.0 ** -14)
+    check_close(out, want.expand(M, N), tol.expand(M, N), act)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_past_their_tails(cuda_ok, act):
+    """To the largest finite sums: the sum itself, or next to nothing, never NaN."""
+    v = torch.tensor([-3e38, -1e20, -1e13, -500, -120, 0.0, -0.0, 120, 500, 1e13, 1e20, 3e38],
+                     device="cuda").to(torch.bfloat16)
+    x = torch.zeros(1, 8, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(v.numel(), 8, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(1, v.numel(), dtype=torch.bfloat16, device="cuda")
+    sk.decode_gemm_bf16_epilogue(x, W, out, v, act)
+    assert torch.equal(out[0], v.clamp(min=0))
