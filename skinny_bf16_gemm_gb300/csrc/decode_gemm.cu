@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kRows / 2; ++i) res[i] = ahead[i];
                 if (m0 + kRows < g.M) load_residual(n, m0 + kRows);
                 if (from_tmem) {
+                    __syncwarp();  // lanes past the right edge went another way; the load is the whole warp's
                     ptx::tmem_ld_now(taddr + m0, w);
                 } else {
 #pragma unroll
@@ -447,15 +448,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (args.epi.bias != nullptr) v[i] = __fadd_rn(v[i], bias);
                 }
                 activate(v, args.epi.activation);
-                if (n >= g.N) continue;
-                uint16_t *dst = args.out + static_cast<size_t>(m0) * g.N + n;
+                if (n < g.N) {
+                    uint16_t *dst = args.out + static_cast<size_t>(m0) * g.N + n;
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    if (args.epi.residual != nullptr)
-                        v[i] = __fadd_rn(v[i], bf16_value((i & 1) ? res[i / 2] >> 16 : res[i / 2] & 0xFFFFu));
-                    if (m0 + i < g.M) dst[static_cast<size_t>(i) * g.N] = to_bf16_bits(v[i]);
+                    for (int i = 0; i < kRows; ++i) {
+                        if (args.epi.residual != nullptr)
+                            v[i] = __fadd_rn(v[i], bf16_value((i & 1) ? res[i / 2] >> 16 : res[i / 2] & 0xFFFFu));
+                        if (m0 + i < g.M) dst[static_cast<size_t>(i) * g.N] = to_bf16_bits(v[i]);
+                    }
                 }
             }
+            __syncwarp();
         };
 
         // Finish split tile t. This CTA holds the tile's first K blocks, so the

@@ -6,9 +6,12 @@ import pytest
 import torch
 
 import skinny_bf16_gemm_gb300 as sk
+import workloads
 from attention_helpers import F64, HALF_BF16, check_close
+from gpu_helpers import Guarded, gemm_inputs_device
 from test_decode_attention_gpu import setup
 from test_decoder_layer_gpu import H, build, check_stages, place
+from test_epilogue_gpu import extras
 from test_qk_norm_rope_gpu import inputs
 
 pytestmark = pytest.mark.gpu
@@ -180,3 +183,20 @@ def test_activations_past_their_tails(cuda_ok, act):
     out = torch.empty(1, v.numel(), dtype=torch.bfloat16, device="cuda")
     sk.decode_gemm_bf16_epilogue(x, W, out, v, act)
     assert torch.equal(out[0], v.clamp(min=0))
+
+
+@pytest.mark.parametrize("M", [5, 16, 33, 64])
+@pytest.mark.parametrize("ragged", [1, 8, 31, 33, 100])
+def test_whole_tiles_with_lanes_past_the_right_edge(cuda_ok, M, ragged):
+    """The last tile ends inside a warp's 32 columns and takes several rounds of rows: integers,
+    bit for bit."""
+    N, K = 160 * 128 + ragged, 64
+    x, W = gemm_inputs_device(M, N, K, workloads.seed_for("edge", M, N, K), kind="int")
+    bias, res = extras(M, N, 9, "int")
+    out = Guarded((M, N))
+    sk.decode_gemm_bf16_epilogue(x, W, out.tensor, bias, "relu", res)
+    torch.cuda.synchronize()
+    out.check()
+    assert sk.device_error() == (0, 0)
+    want = (x.to(F64) @ W.to(F64).t() + bias.to(F64)).clamp(min=0) + res.to(F64)
+    assert torch.equal(out.tensor, want.float().to(torch.bfloat16))
