@@ -445,10 +445,11 @@ SKINNY_API int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *args,
  *   output is zero.
  *   1 <= rows <= 1024; q_heads a multiple of kv_heads, kv_heads >= 1, q_heads <= 1024;
  *   head_dim 64, 96, 128, 192 or 256; page_size, num_pages, table_width >= 1;
- *   table_width * page_size < 2^30; rows * key heads * head blocks * tiles of 64 tokens
- *   < 2^31; window, sinks >= 0; q_stride a multiple of 8, at least the row; q, k, v, out
- *   and workspace 16-byte aligned, tables, lengths and lse 4. out, lse and the workspace
- *   must not overlap anything.
+ *   table_width * page_size < 2^30; rows * kv_heads * head blocks * tiles < 2^31, a tile 16
+ *   tokens of table_width * page_size, a head block up to 32 (head_dim 192, 256: 16) of the
+ *   query heads of a key head; table_stride >= table_width; window, sinks >= 0; q_stride a
+ *   multiple of 8, at least the row; q, k, v, out and workspace 16-byte aligned, tables,
+ *   lengths and lse 4. out, lse and the workspace must not overlap anything.
  *   On the device, a length outside [0, table_width * page_size] is taken as the
  *   nearest, a token on a page outside [0, num_pages) as not seen, and
  *   skinny_device_error() reports bit 256. No call has to be made outside stream

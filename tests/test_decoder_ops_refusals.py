@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import skinny_bf16_gemm_gb300 as sk
-from test_attention_abi import ALIAS, DEVICE, MB, cache_at, lib, mem, rope_args  # noqa: F401
+from test_attention_abi import ALIAS, DEVICE, MB, SHAPE, cache_at, lib, mem, rope_args  # noqa: F401
 
 
 def accepted(status):
@@ -94,3 +94,24 @@ def test_an_eager_call_after_a_capture_does_not_share_its_workspace(monkeypatch)
     capturing.clear()
     b = f.workspace(22)
     assert a is not b and f.workspace(22) is b
+
+
+@pytest.mark.parametrize("rows,kv_heads,group,page,tiles16", [
+    (1024, 8, 7, 16, (1 << 31) // (1024 * 8)), (64, 1, 1, 1, (1 << 31) // 64), (1024, 2, 100, 32, (1 << 31) // (1024 * 2 * 4))])
+def test_most_tokens_of_the_tables(lib, mem, rows, kv_heads, group, page, tiles16):
+    """rows * key heads * head blocks * tiles of 16 tokens below 2^31, and a table below 2^30
+    tokens: the last width that is accepted, and the first that is not."""
+    _, p = mem
+    far = 1 << 44  # addresses that are only compared: nothing is read before the device check
+
+    def call(width):
+        a = sk.DecodeAttentionArgs(
+            q=p, q_stride=kv_heads * group * 64, rows=rows, q_heads=kv_heads * group, block_table=far,
+            table_stride=width, table_width=width, lengths=p, scale=1.0, out=far << 1,
+            workspace=far << 2, workspace_bytes=1 << 30)
+        a.cache = cache_at(p, v=p + MB, page_size=page, kv_heads=kv_heads, num_pages=1, page_stride=0,
+                           token_stride=64, head_stride=64)
+        return lib.decode_attention_bf16(ctypes.byref(a), None, None)
+    tokens = min((tiles16 - 1) * 16, (1 << 30) - 1)
+    assert accepted(call(tokens // page))
+    assert call(tokens // page + 1) == SHAPE
