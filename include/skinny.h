@@ -443,6 +443,9 @@ SKINNY_API int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *args,
  *   rounded once. Deterministic: the same inputs on the same device give the same bits.
  *   A score of NaN or +inf makes the head's output NaN; if every score is -inf the
  *   output is zero.
+ *   A weight below about exp(-80) of the head's largest may underflow and then adds nothing
+ *   of a finite value, NaN of an infinite one; a larger one shows an infinite value. The
+ *   weighted sum is FP32 before its division: values from 2^120 / length on may overflow.
  *   1 <= rows <= 1024; q_heads a multiple of kv_heads, kv_heads >= 1, q_heads <= 1024;
  *   head_dim 64, 96, 128, 192 or 256; page_size, num_pages, table_width >= 1;
  *   table_width * page_size < 2^30; rows * kv_heads * head blocks * tiles < 2^31, a tile 16

@@ -152,11 +152,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
            (static_cast<uint32_t>(__bfloat16_as_ushort(b.y)) << 16);
 }
 
-// What truncating a weight p >= 0 to BF16 leaves. Never zero: both terms of a weight
-// stay positive, so that an infinite value comes out infinite and not 0 * inf or
-// inf - inf. 2^-126 is below half a step of any p above 2^-118.
+// What truncating a weight p >= 0 to BF16 leaves, of a weight above 0 at least BF16's
+// smallest value: both its terms are then positive, so that an infinite value comes out
+// infinite and not 0 * inf or inf - inf. That is under 2^-15 of any weight from 2^-118 on. A
+// weight that underflowed, to 0 below 2^-126, adds nothing of a finite value. (One more
+// minimum a weight: 32 heads of 128 to a key head 67.4 us, 66.9 without; else no difference.)
 __device__ __forceinline__ float rest_of(float p) {
-    return fmaxf(p - __uint_as_float(__float_as_uint(p) & 0xFFFF0000u), 1.17549435e-38f);
+    return fmaxf(p - __uint_as_float(__float_as_uint(p) & 0xFFFF0000u), fminf(p, 9.18354962e-41f));
 }
 
 // Tokens a row of length n sees, and what lies between its sinks and its window.

@@ -200,3 +200,50 @@ def test_whole_tiles_with_lanes_past_the_right_edge(cuda_ok, M, ragged):
     assert sk.device_error() == (0, 0)
     want = (x.to(F64) @ W.to(F64).t() + bias.to(F64)).clamp(min=0) + res.to(F64)
     assert torch.equal(out.tensor, want.float().to(torch.bfloat16))
+
+
+def one_token_apart(G, D, n, j, score, value):
+    """One row of n tokens of score 0 and small values, token j's score and value given: the
+    output of G heads on one key head."""
+    page = 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(G + D)
+    pages = -(-n // page)
+    k = torch.zeros(pages, page, 1, D, dtype=torch.bfloat16, device="cuda")
+    v = (torch.randn(pages, page, 1, D, generator=g, device="cuda") * 1e-3).to(torch.bfloat16)
+    k[j // page, j % page, 0, 0] = score
+    v[j // page, j % page] = value
+    q = torch.zeros(1, G, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    out = torch.empty(1, G, D, dtype=torch.bfloat16, device="cuda")
+    sk.decode_attention_bf16(q, k, v, table, torch.tensor([n], dtype=torch.int32, device="cuda"), out, scale=1.0)
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("G", [1, 16, 32])
+def test_weights_that_underflow_add_nothing(cuda_ok, D, G):
+    """exp(-300) is 0 in FP32: whatever finite value the token has, the bits are those of a
+    value of 0."""
+    for n, j in ((40, 7), (700, 650)):
+        want = one_token_apart(G, D, n, j, -300.0, 0.0)
+        for value in (1.0, 1e30, 3e38, -3e38):
+            assert torch.equal(one_token_apart(G, D, n, j, -300.0, value), want)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("G", [1, 16, 32])
+def test_small_weights_count(cuda_ok, D, G):
+    """A weight of exp(-60) with a value of 2^100 is all of the output but 2^-60 of it; the
+    exponent, 87 binary places, is off by 4 roundings of it, 87 * 4 * 2^-24 = 2^-15.6, the
+    weight's two terms by 2^-15, the sums by less than 2^-16. A weight above 2^-126 shows an
+    infinite value, a weight of exactly 1 too."""
+    n, j = 40, 7
+    got = one_token_apart(G, D, n, j, -60.0, 2.0 ** 100).to(F64)
+    want = torch.full_like(got, math.exp(-60) * 2.0 ** 100 / (n - 1))
+    check_close(got, want, want * (HALF_BF16 * 1.01 + 2.0 ** -13), "out")
+    for score in (0.0, -60.0, -85.0):
+        assert torch.equal(one_token_apart(G, D, n, j, score, math.inf), torch.full_like(want, math.inf).to(torch.bfloat16))
+        assert torch.equal(one_token_apart(G, D, n, j, score, -math.inf), torch.full_like(want, -math.inf).to(torch.bfloat16))
