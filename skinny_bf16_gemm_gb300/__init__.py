@@ -354,16 +354,25 @@ def gather_shards_bf16(shards, out, stream=None):
     return out
 
 
+def _type_error(t, name, dtype):
+    """The exception for a t that is no CUDA tensor of a dtype."""
+    if not (hasattr(t, "dtype") and hasattr(t, "device")):
+        return TypeError(f"{name} must be a torch.Tensor")
+    return TypeError(f"{name} must be a CUDA {dtype} tensor (got {t.dtype} on {t.device})")
+
+
 def _rows(t, name, bf16, width=None, rows=None):
     """A CUDA bfloat16 tensor whose rows (all but its first axis) are contiguous: the
     stride between rows, in elements (the row's width for a single row)."""
     try:
         good = t.dtype == bf16 and t.is_cuda
     except AttributeError:
-        raise TypeError(f"{name} must be a torch.Tensor") from None
+        good = False
     if not good:
-        raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
+        raise _type_error(t, name, bf16)
     shape = t.shape
+    if not shape:
+        raise ValueError(f"{name} must have rows")
     if rows is not None and shape[0] != rows:
         raise ValueError(f"{name} has {shape[0]} rows, expected {rows}")
     stride = t.stride()
@@ -379,8 +388,12 @@ def _rows(t, name, bf16, width=None, rows=None):
 
 def _plain_cuda(t, name, dtype, shape):
     """The address of a contiguous CUDA tensor of a dtype and shape."""
-    if t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA {dtype} tensor (got {t.dtype} on {t.device})")
+    try:
+        good = t.dtype == dtype and t.is_cuda
+    except AttributeError:
+        good = False
+    if not good:
+        raise _type_error(t, name, dtype)
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
@@ -388,8 +401,13 @@ def _plain_cuda(t, name, dtype, shape):
 
 def _cache_fields(k_cache, v_cache, bf16):
     """The fields of skinny_kv_cache for two [pages, page_size, kv_heads, head_dim] views."""
-    if k_cache.dtype != bf16 or v_cache.dtype != bf16 or not (k_cache.is_cuda and v_cache.is_cuda):
-        raise TypeError("k_cache and v_cache must be CUDA bfloat16 tensors")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        try:
+            good = t.dtype == bf16 and t.is_cuda
+        except AttributeError:
+            good = False
+        if not good:
+            raise _type_error(t, name, bf16)
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must be "
@@ -430,23 +448,29 @@ def qk_norm_rope_bf16(qkv, q_heads, kv_heads, q_gamma, k_gamma, rope, positions,
     max_pos = rot_dim = 0
     cache = _NO_CACHE
     if k_out is not None:
-        k_ptr, k_stride = k_out.data_ptr(), _rows(k_out, "k_out", bf16, kv_heads * D, M)
+        k_stride, k_ptr = _rows(k_out, "k_out", bf16, kv_heads * D, M), k_out.data_ptr()
     if q_gamma is not None:
         q_gamma_ptr = _plain_cuda(q_gamma, "q_gamma", bf16, (D,))
     if k_gamma is not None:
         k_gamma_ptr = _plain_cuda(k_gamma, "k_gamma", bf16, (D,))
     if rope is not None:
-        max_pos, rot_dim = rope.shape if rope.dim() == 2 else (0, 0)
-        rope_ptr = _plain_cuda(rope, "rope", torch.float32, (max_pos, rot_dim))
+        shape = getattr(rope, "shape", None)
+        rope_ptr = _plain_cuda(rope, "rope", torch.float32, shape)
+        if len(shape) != 2:
+            raise ValueError(f"rope must be [max_pos, rot_dim], got {tuple(shape)}")
+        max_pos, rot_dim = shape
         positions_ptr = _plain_cuda(positions, "positions", torch.int32, (M,))
     if k_cache is not None or v_cache is not None:
         if k_cache is None or v_cache is None or slots is None:
             raise ValueError("k_cache, v_cache and slots go together")
         cache = _cache_fields(k_cache, v_cache, bf16)
         slots_ptr = _plain_cuda(slots, "slots", torch.int64, (M,))
-    a = _pack_rope(qkv.data_ptr(), qkv_stride, M, q_heads, kv_heads, D, q_gamma_ptr, k_gamma_ptr, eps,
-                   rope_ptr, max_pos, rot_dim, bool(interleaved), positions_ptr, q_out.data_ptr(), q_stride,
-                   k_ptr, k_stride, *cache, slots_ptr)
+    try:
+        a = _pack_rope(qkv.data_ptr(), qkv_stride, M, q_heads, kv_heads, D, q_gamma_ptr, k_gamma_ptr, eps,
+                       rope_ptr, max_pos, rot_dim, bool(interleaved), positions_ptr, q_out.data_ptr(), q_stride,
+                       k_ptr, k_stride, *cache, slots_ptr)
+    except struct.error as e:  # a number of the wrong kind, or past the field's range
+        raise ValueError(f"qk_norm_rope_bf16: {e}") from None
     o = _opts(pdl, None)
     st = load_library().qk_norm_rope_bf16(a, None if o is None else ctypes.byref(o),
                                           _stream_handle(stream))
@@ -522,8 +546,12 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
     if cache[5] != D:
         raise ValueError(f"q has heads of {D}, the cache of {cache[5]}")
     out_ptr = _plain_cuda(out, "out", bf16, shape)
-    if block_table.dtype != torch.int32 or not block_table.is_cuda:
-        raise TypeError("block_table must be a CUDA int32 tensor")
+    try:
+        good = block_table.dtype == torch.int32 and block_table.is_cuda
+    except AttributeError:
+        good = False
+    if not good:
+        raise _type_error(block_table, "block_table", torch.int32)
     table_shape, table_stride = block_table.shape, block_table.stride()
     if len(table_shape) != 2 or table_shape[0] != rows or (table_stride[1] != 1 and table_shape[1] > 1):
         raise ValueError(f"block_table must be [{rows}, table_width] with contiguous rows")
@@ -535,11 +563,16 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
         if q.device.index != device:
             _check(4, "decode_attention_bf16")  # as the call itself would say
         workspace = _own_workspace(device, handle)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     width = table_shape[1]
-    a = _pack_attention(
-        q.data_ptr(), q_stride, rows, q_heads, *cache, block_table.data_ptr(),
-        table_stride[0] if rows > 1 else width, width, lengths_ptr, window, sinks,
-        D ** -0.5 if scale is None else scale, out_ptr, lse_ptr, workspace.data_ptr(), workspace.nbytes)
+    try:
+        a = _pack_attention(
+            q.data_ptr(), q_stride, rows, q_heads, *cache, block_table.data_ptr(),
+            table_stride[0] if rows > 1 else width, width, lengths_ptr, window, sinks,
+            D ** -0.5 if scale is None else scale, out_ptr, lse_ptr, workspace.data_ptr(), workspace.nbytes)
+    except struct.error as e:  # a number of the wrong kind, or past the field's range
+        raise ValueError(f"decode_attention_bf16: {e}") from None
     o = _opts(pdl, None)
     st = load_library().decode_attention_bf16(a, None if o is None else ctypes.byref(o), handle)
     _check(st, "decode_attention_bf16")

@@ -115,3 +115,77 @@ def test_most_tokens_of_the_tables(lib, mem, rows, kv_heads, group, page, tiles1
     tokens = min((tiles16 - 1) * 16, (1 << 30) - 1)
     assert accepted(call(tokens // page))
     assert call(tokens // page + 1) == SHAPE
+
+
+def fake_cuda(*shape, dtype=None):
+    """A host tensor that says it is on a GPU: good for the wrappers' checks only."""
+    import torch
+
+    class Fake(torch.Tensor):
+        is_cuda = True
+    return torch.zeros(shape, dtype=dtype or torch.bfloat16).as_subclass(Fake)
+
+
+def rope_call(**kw):
+    import torch
+    a = dict(qkv=fake_cuda(3, 8 * 64), q_heads=4, kv_heads=2, q_gamma=fake_cuda(64), k_gamma=fake_cuda(64),
+             rope=fake_cuda(32, 64, dtype=torch.float32), positions=fake_cuda(3, dtype=torch.int32),
+             q_out=fake_cuda(3, 4, 64), k_out=fake_cuda(3, 2, 64), k_cache=fake_cuda(4, 16, 2, 64),
+             v_cache=fake_cuda(4, 16, 2, 64), slots=fake_cuda(3, dtype=torch.int64), stream=0)
+    a.update(kw)
+    return sk.qk_norm_rope_bf16(**a)
+
+
+def attention_call(**kw):
+    import torch
+    a = dict(q=fake_cuda(3, 4, 64), k_cache=fake_cuda(4, 16, 2, 64), v_cache=fake_cuda(4, 16, 2, 64),
+             block_table=fake_cuda(3, 4, dtype=torch.int32), lengths=fake_cuda(3, dtype=torch.int32),
+             out=fake_cuda(3, 4, 64), lse=fake_cuda(3, 4, dtype=torch.float32),
+             workspace=fake_cuda(64 << 20, dtype=torch.uint8), stream=0)
+    a.update(kw)
+    return sk.decode_attention_bf16(**a)
+
+
+@pytest.mark.parametrize("call,names", [
+    (rope_call, ["qkv", "q_gamma", "k_gamma", "rope", "positions", "q_out", "k_out", "k_cache", "v_cache", "slots"]),
+    (attention_call, ["q", "k_cache", "v_cache", "block_table", "lengths", "out", "lse", "workspace"])])
+def test_what_is_no_tensor_is_named(lib, call, names):
+    for name in names:
+        for bad in (3, "x", [1.0]):
+            with pytest.raises(TypeError, match=name):
+                call(**{name: bad})
+
+
+def test_missing_tensors_are_named(lib):
+    for name in ("qkv", "positions", "q_out"):
+        with pytest.raises(TypeError, match=name):
+            rope_call(**{name: None})
+    for name in ("q", "k_cache", "v_cache", "block_table", "lengths", "out"):
+        with pytest.raises(TypeError, match=name):
+            attention_call(**{name: None})
+    for name in ("k_cache", "v_cache", "slots"):
+        with pytest.raises(ValueError, match="go together"):
+            rope_call(**{name: None})
+
+
+def test_tensors_without_axes_and_numbers_out_of_range(lib):
+    import torch
+    for name in ("qkv", "q_out", "k_out", "rope", "positions", "slots", "k_cache"):
+        with pytest.raises(ValueError, match=name):
+            rope_call(**{name: fake_cuda(dtype={"rope": torch.float32, "positions": torch.int32,
+                                                "slots": torch.int64}.get(name))})
+    for name in ("q", "out", "block_table", "lengths", "k_cache"):
+        with pytest.raises(ValueError, match=name):
+            attention_call(**{name: fake_cuda(dtype={"block_table": torch.int32, "lengths": torch.int32}.get(name))})
+    for kw in (dict(window=1 << 31), dict(sinks=1 << 40), dict(window=1.5), dict(scale="1")):
+        with pytest.raises(ValueError, match="decode_attention_bf16"):
+            attention_call(**kw)
+    with pytest.raises(ValueError, match="qk_norm_rope_bf16"):
+        rope_call(eps="1")
+
+
+def test_calls_with_every_tensor_in_order_reach_the_library(lib):
+    for call in (rope_call, attention_call):
+        with pytest.raises(sk.SkinnyError) as e:
+            call()
+        assert accepted(e.value.status)
