@@ -368,8 +368,9 @@ typedef struct {
  *              heads of qkv in place (qkv + q_heads * head_dim, k_stride == qkv_stride or
  *              one row).
  *   cache      cache.k and cache.v NULL: nothing is appended. kv_heads and head_dim as
- *              in the call; along an axis longer than one, its elements must not
- *              overlap (stride >= head_dim).
+ *              in the call. No two of its elements may share a place: of the axes longer
+ *              than one, each stride clears all that the smaller ones reach, and the
+ *              values lie clear of the keys (between them, if the strides leave room).
  *   slots      [M] int64, with a cache: row m's key and value heads go to token
  *              slots[m] % page_size of page slots[m] / page_size. A negative slot is
  *              not stored (padding rows). Two rows with the same slot leave either

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -463,6 +464,41 @@ size_t row_span(int rows, long long stride, long long width) {
     return (static_cast<size_t>(rows - 1) * stride + width) * 2;
 }
 
+// Whether a pool that is written has two elements in one place. Its axes must lie within each
+// other: each stride clears all that the smaller ones reach. The values then meet the keys
+// where their distance is a sum of steps along the axes, give or take a head: at each axis,
+// the largest first, only the two numbers of steps around the distance can come near enough.
+struct PoolAxis {
+    long long stride;
+    int size;
+};
+bool steps_meet(long long distance, const PoolAxis *axes, int n, int head_dim) {
+    if (n == 0) return distance > -head_dim && distance < head_dim;
+    const long long s = axes[n - 1].stride;
+    const long long below = distance >= 0 ? distance / s : -((-distance + s - 1) / s);
+    for (long long t = below; t <= below + 1; ++t)
+        if (t > -axes[n - 1].size && t < axes[n - 1].size && steps_meet(distance - t * s, axes, n - 1, head_dim))
+            return true;
+    return false;
+}
+bool pool_meets_itself(const skinny_kv_cache *c) {
+    PoolAxis axes[3];
+    int n = 0;
+    for (const PoolAxis &a : {PoolAxis{c->page_stride, c->num_pages}, PoolAxis{c->token_stride, c->page_size},
+                              PoolAxis{c->head_stride, c->kv_heads}})
+        if (a.size > 1) axes[n++] = a;
+    std::sort(axes, axes + n, [](const PoolAxis &a, const PoolAxis &b) { return a.stride < b.stride; });
+    long long extent = c->head_dim;
+    for (int i = 0; i < n; ++i) {
+        if (axes[i].stride < extent) return true;
+        extent += axes[i].stride * (axes[i].size - 1);
+    }
+    const uintptr_t k = reinterpret_cast<uintptr_t>(c->k), v = reinterpret_cast<uintptr_t>(c->v);
+    const unsigned long long apart = (k < v ? v - k : k - v) / 2;
+    return apart < static_cast<unsigned long long>(extent) &&
+           steps_meet(static_cast<long long>(apart), axes, n, c->head_dim);
+}
+
 // A cache's own rules, and the bytes its keys (or values) span.
 int check_cache(const skinny_kv_cache *c, bool write, size_t *span) {
     if (!c->k || !c->v) return SKINNY_ERR_NULL;
@@ -475,13 +511,13 @@ int check_cache(const skinny_kv_cache *c, bool write, size_t *span) {
     for (int i = 0; i < 3; ++i) {
         if (strides[i] < 0 || strides[i] > (1ll << 40)) return SKINNY_ERR_SHAPE;
         if (strides[i] % 8 != 0) return SKINNY_ERR_ALIGN;
-        if (write && sizes[i] > 1 && strides[i] < c->head_dim) return SKINNY_ERR_ALIAS;
         // At most 3 * 2^31 * 2^40: no overflow of the unsigned 128-bit sum.
         const unsigned __int128 more = static_cast<unsigned __int128>(sizes[i] - 1) * strides[i];
         if (more > (1ull << 44)) return SKINNY_ERR_SHAPE;
         last += static_cast<unsigned long long>(more);
     }
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return SKINNY_ERR_ALIGN;
+    if (write && pool_meets_itself(c)) return SKINNY_ERR_ALIAS;
     *span = static_cast<size_t>(last + c->head_dim) * 2;
     return SKINNY_OK;
 }
@@ -734,7 +770,6 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
     if (has_cache) {
         if (cache->kv_heads != p->kv_heads || cache->head_dim != D) return SKINNY_ERR_SHAPE;
         if ((st = check_cache(cache, true, &pool))) return st;
-        if (cache->k == cache->v) return SKINNY_ERR_ALIAS;
     }
     // Every output against every input and the other outputs; q_out and k_out may be
     // their own heads of qkv in place. One row has no distance to a next one: its strides

@@ -189,3 +189,61 @@ def test_calls_with_every_tensor_in_order_reach_the_library(lib):
         with pytest.raises(sk.SkinnyError) as e:
             call()
         assert accepted(e.value.status)
+
+
+def elements(page, token, head, sizes, D, base=0):
+    """Every element that a pool's keys (or values) touch, in 8-element chunks."""
+    return [base + i * page + j * token + h * head + c
+            for i in range(sizes[0]) for j in range(sizes[1]) for h in range(sizes[2]) for c in range(0, D, 8)]
+
+
+def test_pools_whose_elements_meet_are_refused_for_writing(lib, mem):
+    """Seeded small layouts, by enumeration: a pool that would store two elements in one place
+    is refused; one whose axes lie within each other is accepted."""
+    import random
+    _, p = mem
+    r = random.Random(4)
+    seen = {True: 0, False: 0}
+    for _ in range(4000):
+        D = 8 * r.choice([1, 2, 3])
+        sizes = [r.choice([1, 2, 3, 4]) for _ in range(3)]
+        order = r.sample(range(3), 3)
+        strides, extent = [0, 0, 0], D
+        for axis in order:  # innermost first, padded now and then, sometimes too near
+            strides[axis] = extent + 8 * r.choice([0, 0, 0, 1, 5]) - 8 * r.choice([0, 0, 0, 0, 0, 1, 2])
+            extent += strides[axis] * (sizes[axis] - 1) + r.choice([0, 0, D])
+        if any(n > 1 and s < D for n, s in zip(sizes, strides)):
+            continue
+        gap = 8 * r.choice([1, D // 8, strides[order[0]] // 8, extent // 8, extent // 8 + 3, r.randint(1, extent // 4)])
+        gap *= r.choice([1, -1])
+        base = p + 8 * MB
+        cache = cache_at(base, v=base + 2 * gap, num_pages=sizes[0], page_size=sizes[1], kv_heads=sizes[2],
+                         head_dim=D, page_stride=strides[0], token_stride=strides[1], head_stride=strides[2])
+        a = rope_args(p, cache, kv_heads=sizes[2], head_dim=D, rot_dim=0, k_out=None)
+        got = lib.qk_norm_rope_bf16(ctypes.byref(a), None, None)
+        if min(strides) < 0:
+            assert got == SHAPE
+            continue
+        k = elements(*strides, sizes, D)
+        kv = k + [e + gap for e in k]
+        meets = len(set(kv)) < len(kv)
+        nested, end = True, D
+        for s, n in sorted((s, n) for s, n in zip(strides, sizes) if n > 1):
+            nested, end = nested and s >= end, end + s * (n - 1)
+        if meets:
+            assert got == ALIAS, (sizes, strides, D, gap)
+        elif nested:
+            assert accepted(got), (sizes, strides, D, gap)
+        seen[meets] += 1
+    assert min(seen.values()) > 500
+
+
+def test_pools_only_read_may_repeat(lib, mem):
+    """Keys and values that are only read may lie anywhere: one head's for all, a page's for all."""
+    _, p = mem
+    for kw in (dict(head_stride=0), dict(page_stride=0), dict(token_stride=0), dict(v=p + 6 * MB)):
+        a = sk.DecodeAttentionArgs(q=p, q_stride=256, rows=3, q_heads=4, block_table=p + 2 * MB, table_stride=4,
+                                   table_width=4, lengths=p + 3 * MB, scale=0.125, out=p + 4 * MB,
+                                   workspace=p + 8 * MB, workspace_bytes=64 << 20)
+        a.cache = cache_at(p + 6 * MB, **dict(dict(v=p + 7 * MB), **kw))
+        assert accepted(lib.decode_attention_bf16(ctypes.byref(a), None, None))
