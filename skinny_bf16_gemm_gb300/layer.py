@@ -12,8 +12,10 @@ stream after the layer:
     h      = act(x Wup^T + bup)                  decode_gemm_bf16_epilogue
     y      = h Wdown^T + res                     decode_gemm_bf16_epilogue
 
-Slots 1.. of ``partials`` hold the other tensor-parallel ranks' rows of the output
-linear, as in LayerChain. The class owns the device buffers and orders the calls on one
+The attention may be split by heads over tensor-parallel ranks: slots 1.. of ``partials``
+then hold the other ranks' rows of the output linear, as in LayerChain. The feed-forward
+pair is whole on every rank (W_up, W_down [HIDDEN, F] with all of F): y is the stream
+itself, with nothing left to add. The class owns the device buffers and orders the calls on one
 stream, optionally as one CUDA graph; the caches, tables, lengths, positions and slots
 are the caller's tensors, updated in place between steps.
 """
