@@ -64,8 +64,8 @@ def parse():
                     help="per-config GB/s of every GEMM and reduce config instead of the chain")
     ap.add_argument("--sweep-calls", type=int, default=200)
     ap.add_argument("--configs", type=int, default=1,
-                    help="add the per-config block (every GEMM / reduce / gather config of "
-                         "the workloads, with the oracle per config kind) to the line")
+                    help="print the per-config block (every GEMM / reduce / gather config of "
+                         "the workloads, with the oracle per config kind) on stderr")
     ap.add_argument("--profile", action="store_true",
                     help="a few launches of each chain kernel, for ncu captures")
     ap.add_argument("--profile-configs", action="store_true",
@@ -677,6 +677,20 @@ def run_profile(args):
 
 # ---- our arm ------------------------------------------------------------------------
 
+def print_result(line):
+    """The result as one JSON line on stdout, and the long reports (parity, every config,
+    the oracle on one core) as one on stderr: with them the line was 23 KB, of which a log
+    that keeps the end of the output had the middle of a list."""
+    line = dict(line)
+    report = {k: line.pop(k) for k in ("parity", "configs") if k in line}
+    if "one_thread" in line.get("cpu_baseline", {}):
+        line["cpu_baseline"] = dict(line["cpu_baseline"])
+        report["cpu_baseline_one_thread"] = line["cpu_baseline"].pop("one_thread")
+    if report:
+        print(json.dumps(report), file=sys.stderr, flush=True)
+    print(json.dumps(line), flush=True)
+
+
 def main():
     args = parse()
     rank, world, local = dist_info()
@@ -948,7 +962,7 @@ def main():
                                          pdl=bool(args.pdl),
                                          with_oracle=world == 1 and not args.no_cpu_baseline)
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        print_result(line)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
