@@ -401,13 +401,16 @@ def _plain_cuda(t, name, dtype, shape):
 
 def _cache_fields(k_cache, v_cache, bf16):
     """The fields of skinny_kv_cache for two [pages, page_size, kv_heads, head_dim] views."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        try:
-            good = t.dtype == bf16 and t.is_cuda
-        except AttributeError:
-            good = False
-        if not good:
-            raise _type_error(t, name, bf16)
+    bad = (k_cache, "k_cache")
+    try:
+        good = k_cache.dtype == bf16 and k_cache.is_cuda
+        if good:
+            bad = (v_cache, "v_cache")
+            good = v_cache.dtype == bf16 and v_cache.is_cuda
+    except AttributeError:
+        good = False
+    if not good:
+        raise _type_error(*bad, bf16)
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must be "
@@ -559,10 +562,13 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
     lse_ptr = 0 if lse is None else _plain_cuda(lse, "lse", torch.float32, (rows, q_heads))
     handle = _stream_handle(stream)
     if workspace is None:
-        device = torch._C._cuda_getDevice()
-        if q.device.index != device:
+        device = q.device.index
+        if stream is None:
+            workspace = _current_workspace(device, handle.value or 0)
+        elif device != torch._C._cuda_getDevice():
             _check(4, "decode_attention_bf16")  # as the call itself would say
-        workspace = _own_workspace(device, handle)
+        else:
+            workspace = _own_workspace(device, handle)
     elif not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
     width = table_shape[1]
