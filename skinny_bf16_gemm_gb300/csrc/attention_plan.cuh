@@ -30,8 +30,8 @@ __host__ __device__ inline int attn_max_nb(int head_dim) { return head_dim <= 12
 
 // Two CTAs an SM where the rings fit and a warp's step leaves gaps: small heads (64 ragged
 // rows to 16384 of 64-wide heads, pages by head: 163 us, 194 with one CTA and more stages),
-// and many query heads to a key head (16 rows to 8192, 128-wide, 16 heads: 46 us, 50 with
-// one; 32 heads: 66, 85 with one). One for 192-wide heads, 16 to a key head: 45 us, 49 with
+// and many query heads to a key head (16 rows to 8192, 128-wide, 16 heads: 43 us, 50 with
+// one; 32 heads: 67, 83 with one). One for 192-wide heads, 16 to a key head: 45 us, 49 with
 // two, whose copies queue too long.
 constexpr int attn_ctas_per_sm(int head_dim, int nb) { return head_dim <= 64 || (nb > 1 && head_dim <= 128) ? 2 : 1; }
 

@@ -458,9 +458,9 @@ __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_atte
     // 16-byte loads, then the fragments by way of 512 bytes of shared memory: loads of a
     // fragment each, 4 bytes a lane, kept one row's CTAs waiting for the L2 slices that hold
     // its queries (131071 tokens of one key head: 22.8 us, 19.1 this way). They are on their
-    // way from the item before's last scores on where there are registers for them (one row
-    // of 7 heads to 4000: 10.6 us, 10.9 without; 16 rows to 8192, 32 heads of 128 to a key
-    // head: 97 us, for spills, 64 without).
+    // way from the item before's last scores on where there are registers for them (16 rows to
+    // 8192, 16 heads of 128 to a key head: 43.4 us, 45.1 without; 32 heads: 67 us without, which
+    // spills 180 bytes, and 98 with them).
     constexpr bool kQueriesAhead = D * NB <= 256;
     uint32_t qf[kSteps][NB][2];
     uint4 qw[NB][kChunks / 4];
