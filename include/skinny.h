@@ -378,7 +378,7 @@ typedef struct {
  *   Per head, FP32: y = x * rsqrt(sum(x^2) / head_dim + eps) * gamma; the pairs (a, b)
  *   of the first rot_dim values become (a cos - b sin, b cos + a sin); one rounding.
  *   Value heads are copied. k_out and the cache get the same bits.
- *   1 <= M; 1 <= q_heads, kv_heads <= 1024; head_dim a multiple of 8 in [8, 256];
+ *   1 <= M <= 2^30; 1 <= q_heads, kv_heads <= 1024; head_dim a multiple of 8 in [8, 256];
  *   rot_dim a multiple of 16 in [0, head_dim]; strides multiples of 8 and at least the
  *   row; data pointers 16-byte aligned, positions 4, slots 8; eps > 0, finite.
  *   Outputs must not overlap inputs or each other but as said (address ranges count,

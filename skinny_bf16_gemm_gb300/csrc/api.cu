@@ -747,7 +747,8 @@ int qk_norm_rope_bf16(const skinny_qk_norm_rope_args *p, const skinny_launch_opt
         (has_cache && !p->slots))
         return SKINNY_ERR_NULL;
     const int D = p->head_dim;
-    if (p->M < 1 || p->q_heads < 1 || p->q_heads > kMaxHeads || p->kv_heads < 1 ||
+    constexpr int kMaxRows = 1 << 30;  // the kernel looks two of its rounds ahead in 32 bits
+    if (p->M < 1 || p->M > kMaxRows || p->q_heads < 1 || p->q_heads > kMaxHeads || p->kv_heads < 1 ||
         p->kv_heads > kMaxHeads || D < 8 || D > kMaxHeadDim || D % 8 != 0 || p->rot_dim < 0 ||
         p->rot_dim > D || p->rot_dim % 16 != 0 || (p->rot_dim > 0 && p->max_pos < 1))
         return SKINNY_ERR_SHAPE;

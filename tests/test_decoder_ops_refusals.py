@@ -247,3 +247,15 @@ def test_pools_only_read_may_repeat(lib, mem):
                                    workspace=p + 8 * MB, workspace_bytes=64 << 20)
         a.cache = cache_at(p + 6 * MB, **dict(dict(v=p + 7 * MB), **kw))
         assert accepted(lib.decode_attention_bf16(ctypes.byref(a), None, None))
+
+
+def test_most_rows_of_the_rotation(lib, mem):
+    """Rows are numbered in 32 bits, and the rows after the next one with them."""
+    far = 1 << 40  # addresses that are only compared
+
+    def call(M):
+        a = sk.QkNormRopeArgs(qkv=far, qkv_stride=24, M=M, q_heads=1, kv_heads=1, head_dim=8, eps=1e-6,
+                              q_out=far << 1, q_stride=8)
+        return lib.qk_norm_rope_bf16(ctypes.byref(a), None, None)
+    assert accepted(call(1 << 30))
+    assert call((1 << 30) + 1) == SHAPE and call((1 << 31) - 1) == SHAPE
