@@ -97,7 +97,7 @@ struct Shape {
     static_assert(kRingBytes % 16 == 0, "16-byte copies");
     static_assert(kSub >= kAttnMinTile, "the host counts tiles of kAttnMinTile");
     static_assert(kLookOffset % 8 == 0, "64-bit places");
-    static_assert(kRowsOffset + (2 * kAttnMaxRows + 1) * 4 + 3072 <= 232448, "a block's shared memory");
+    static_assert(kRowsOffset + (2 * kAttnMaxRows + 1) * 4 + 3 * 1024 <= 232448, "with the static arrays");
     static int bytes(int rows) { return kRowsOffset + (2 * rows + 1) * 4; }
 };
 
