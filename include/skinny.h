@@ -189,9 +189,9 @@ typedef enum {
  *             decode_gemm_bf16_ex).
  *   out[m][n] = BF16(act(s + bias[n]) + residual[m][n]), s the FP32 sum over k of
  *   x[m,k] W[n,k]: every step in FP32, one rounding; the activations keep their relative
- *   precision down to values of about 1e-36, below which they may be -0. With neither bias nor residual
- *   and SKINNY_ACT_NONE the bits are decode_gemm_bf16's. With programmatic dependent
- *   launch bias and residual are read after the wait for the previous kernel.
+ *   precision down to values of about 1e-36, below which they may be -0. With neither bias
+ *   nor residual and SKINNY_ACT_NONE the bits are decode_gemm_bf16's. With programmatic
+ *   dependent launch bias and residual are read after the wait for the previous kernel.
  *   Other rules (sizes, the device's scratch) and errors as decode_gemm_bf16_ex;
  *   SKINNY_ERR_ARG for an unknown activation.
  */

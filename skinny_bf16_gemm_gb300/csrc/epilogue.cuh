@@ -41,8 +41,10 @@ __device__ __forceinline__ void activate(float (&v)[n], int activation) {
             break;
         case kActGeluTanh:
 #pragma unroll
-            for (int i = 0; i < n; ++i)
-                v[i] = __fdividef(v[i], 1.0f + expf(-1.59576912160573071f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+            for (int i = 0; i < n; ++i) {
+                const float u2 = 1.59576912160573071f * (v[i] + 0.044715f * v[i] * v[i] * v[i]);  // 2u
+                v[i] = __fdividef(v[i], 1.0f + expf(-u2));
+            }
             break;
         default: break;
     }
