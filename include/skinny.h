@@ -482,6 +482,54 @@ SKINNY_API int decode_attention_bf16(const skinny_decode_attention_args *args,
 /* Bytes of the workspace on a device with num_sms SMs (0 for num_sms < 1). */
 SKINNY_API size_t skinny_attention_workspace_bytes(int num_sms);
 
+/* Largest number of alternatives, and of rows, of token_logprobs_bf16. */
+#define SKINNY_LOGPROBS_MAX_TOP 32
+#define SKINNY_LOGPROBS_MAX_ROWS (1 << 24)
+
+/*
+ * token_logprobs_bf16 -- log probabilities of given tokens, the entropy and the most
+ *   likely tokens of every row of logits, in one pass over them. The drafter pages have no
+ *   counterpart; their draft_logits (decode_gemm_bf16_logits) makes the logits.
+ *
+ *   logits        rows of V BF16, logits_stride elements apart (any stride from V on, any
+ *                 2-byte alignment; 16-byte aligned rows read no single values).
+ *   tokens        [M, given] int64: the tokens whose log probabilities are wanted. A
+ *                 negative one is not asked for (padding): its log probability comes out
+ *                 as 0. given = 0: none (tokens and logprobs unused, may be NULL).
+ *   logprobs      [M, given] FP32: x_t - lse.
+ *   entropy       [M] FP32 or NULL: -sum p log p, in nats. Tokens of p = 0 add nothing.
+ *   lse           [M] FP32 or NULL: log sum exp(x).
+ *   top           number of most likely tokens wanted, in [0, min(V, 32)].
+ *   top_logprobs, top_tokens  [M, top] FP32 and int64 (either may be NULL): in falling order
+ *                 of the logits, of equal ones (+0 and -0 among them) the lower index
+ *                 first. NaN counts as -inf in that order.
+ *   Maxima, sums and results are FP32: exp is within 2 ulp, the sums run over a thread's
+ *   values, then joins in a fixed order. Deterministic: the same inputs give the same bits.
+ *   A row with a NaN or +inf gives NaN for everything but top_tokens; a row of -inf alone
+ *   an lse of -inf, and NaN for the rest.
+ *   1 <= M <= 2^24; 1 <= V <= 2^30; 0 <= given <= 2^20; V <= logits_stride <= 2^32; logits
+ *   2-byte aligned, tokens and top_tokens 8, the others 4. At least one result. Results
+ *   must not overlap the inputs or each other.
+ *   A token of V or more: its log probability is NaN and skinny_device_error() reports
+ *   bit 256. No call has to be made outside stream capture first; no workspace.
+ *   Errors: SKINNY_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARG, _DEVICE, _LAUNCH.
+ */
+typedef struct {
+    const void *logits;
+    long long logits_stride;
+    int M, V;
+    const void *tokens;
+    int given;
+    void *logprobs;
+    void *entropy;
+    void *lse;
+    int top;
+    void *top_logprobs;
+    void *top_tokens;
+} skinny_token_logprobs_args;
+SKINNY_API int token_logprobs_bf16(const skinny_token_logprobs_args *args,
+                                   const skinny_launch_opts *opts, void *stream);
+
 /* Human-readable text of a skinny_status code (static storage). */
 SKINNY_API const char *skinny_status_string(int status);
 
@@ -491,8 +539,9 @@ SKINNY_API const char *skinny_status_string(int status);
  *   recorded a problem since the last read, else SKINNY_ERR_TIMEOUT, and writes
  *   the raw word (a bit set per waiting role that gave up; 64 if only the
  *   host-mapped word was set; 128 if a reduce_residual_rmsnorm cluster's
- *   exchange of its sums of squares ran out; 256 if qk_norm_rope_bf16 or
- *   decode_attention_bf16 met an index out of range, and if that is the only bit the
+ *   exchange of its sums of squares ran out; 256 if a kernel that reads
+ *   indices from device memory (qk_norm_rope_bf16, decode_attention_bf16,
+ *   token_logprobs_bf16) met one out of range, and if that is the only bit the
  *   status is SKINNY_ERR_INDEX) to *word if word is not NULL. Clearing also
  *   re-arms the decode GEMM's scratch flags, so the next call starts clean and
  *   calls stop returning SKINNY_ERR_TIMEOUT. Host pointer: word.

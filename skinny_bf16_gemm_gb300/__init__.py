@@ -13,6 +13,8 @@ operations raises.
                                                      out = act(x @ W^T + bias) + residual
     qk_norm_rope_bf16(qkv, ...)                      per-head norm, rotation, cache append
     decode_attention_bf16(q, k_cache, v_cache, ...)  one token per row over a paged cache
+    token_logprobs_bf16(logits, tokens, logprobs, ...)
+                                                     log probabilities, entropy, top tokens
 """
 import ctypes
 import os
@@ -84,6 +86,15 @@ class QkNormRopeArgs(ctypes.Structure):
                 ("slots", ctypes.c_void_p)]
 
 
+class TokenLogprobsArgs(ctypes.Structure):
+    """skinny_token_logprobs_args."""
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_longlong),
+                ("M", ctypes.c_int), ("V", ctypes.c_int), ("tokens", ctypes.c_void_p),
+                ("given", ctypes.c_int), ("logprobs", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("top", ctypes.c_int),
+                ("top_logprobs", ctypes.c_void_p), ("top_tokens", ctypes.c_void_p)]
+
+
 class DecodeAttentionArgs(ctypes.Structure):
     """skinny_decode_attention_args."""
     _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("rows", ctypes.c_int),
@@ -95,11 +106,12 @@ class DecodeAttentionArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
-# The same two structures as one packed string each: a third of the host time of
+# The same structures as one packed string each: a third of the host time of
 # filling a ctypes.Structure field by field.
 _CACHE = "PPiiiiqqq"
 _pack_rope = struct.Struct("@PqiiiiPPfPiiiPPqPq" + _CACHE + "P").pack
 _pack_attention = struct.Struct("@Pqii" + _CACHE + "PqiPiifPPPN").pack
+_pack_logprobs = struct.Struct("@PqiiPiPPPiPP").pack
 _NO_CACHE = (0,) * 9
 
 
@@ -139,6 +151,8 @@ def load_library(path: str = LIBRARY):
     lib.qk_norm_rope_bf16.restype = i32
     lib.decode_attention_bf16.argtypes = [vp, op, vp]
     lib.decode_attention_bf16.restype = i32
+    lib.token_logprobs_bf16.argtypes = [vp, op, vp]
+    lib.token_logprobs_bf16.restype = i32
     lib.skinny_attention_workspace_bytes.argtypes = [i32]
     lib.skinny_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.gather_shards_bf16.argtypes = [vp, i32, i32, i32, vp, vp]
@@ -583,6 +597,57 @@ def decode_attention_bf16(q, k_cache, v_cache, block_table, lengths, out, scale=
     st = load_library().decode_attention_bf16(a, None if o is None else ctypes.byref(o), handle)
     _check(st, "decode_attention_bf16")
     return out
+
+
+def token_logprobs_bf16(logits, tokens, logprobs, entropy=None, lse=None, top_logprobs=None,
+                        top_tokens=None, stream=None, pdl=None):
+    """Log probabilities of given tokens, the entropy and the most likely tokens of rows of logits.
+
+    logits [M, V] bfloat16, rows contiguous, any row stride; tokens [M] or [M, given] int64
+    (negative: not asked for, 0 comes out) or None; logprobs FP32 of tokens' shape (None if
+    tokens is); entropy, lse [M] FP32 or None; top_logprobs [M, top] FP32 and top_tokens
+    [M, top] int64, either or both None; top <= min(V, 32), of equal logits the lower index
+    first. Returns ``logprobs``.
+    """
+    import torch
+    stride = _rows(logits, "logits", torch.bfloat16)
+    shape = logits.shape
+    if len(shape) != 2:
+        raise ValueError(f"logits must be [M, V], got {tuple(shape)}")
+    M, V = shape
+    f32, i64 = torch.float32, torch.int64
+    given = top = tokens_ptr = logprobs_ptr = entropy_ptr = lse_ptr = top_lp_ptr = top_tok_ptr = 0
+    if tokens is not None or logprobs is not None:
+        if tokens is None or logprobs is None:
+            raise ValueError("tokens and logprobs go together")
+        shape = getattr(tokens, "shape", ())
+        tokens_ptr = _plain_cuda(tokens, "tokens", i64, shape)
+        if len(shape) not in (1, 2) or shape[0] != M:
+            raise ValueError(f"tokens must be [{M}] or [{M}, given], got {tuple(shape)}")
+        given = shape[1] if len(shape) == 2 else 1
+        logprobs_ptr = _plain_cuda(logprobs, "logprobs", f32, shape)
+    if entropy is not None:
+        entropy_ptr = _plain_cuda(entropy, "entropy", f32, (M,))
+    if lse is not None:
+        lse_ptr = _plain_cuda(lse, "lse", f32, (M,))
+    if top_logprobs is not None or top_tokens is not None:
+        shape = getattr(top_tokens if top_logprobs is None else top_logprobs, "shape", ())
+        if len(shape) != 2 or shape[0] != M:
+            raise ValueError(f"top_logprobs and top_tokens must be [{M}, top]")
+        top = shape[1]
+        if top_logprobs is not None:
+            top_lp_ptr = _plain_cuda(top_logprobs, "top_logprobs", f32, shape)
+        if top_tokens is not None:
+            top_tok_ptr = _plain_cuda(top_tokens, "top_tokens", i64, shape)
+    try:
+        a = _pack_logprobs(logits.data_ptr(), stride, M, V, tokens_ptr, given, logprobs_ptr, entropy_ptr, lse_ptr,
+                           top, top_lp_ptr, top_tok_ptr)
+    except struct.error as e:  # a size past the field's range
+        raise ValueError(f"token_logprobs_bf16: {e}") from None
+    o = _opts(pdl, None)
+    st = load_library().token_logprobs_bf16(a, None if o is None else ctypes.byref(o), _stream_handle(stream))
+    _check(st, "token_logprobs_bf16")
+    return logprobs
 
 
 def device_error(device=None):

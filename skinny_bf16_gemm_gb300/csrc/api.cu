@@ -10,6 +10,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_internal.h"
 #include "attention_plan.cuh"
 #include "kernels.h"
 #include "plan.cuh"
@@ -18,31 +19,8 @@
 namespace skinny {
 namespace {
 
-constexpr int kMaxDevices = 64;
-constexpr int kMaxHeads = 1024;
 constexpr int kMaxHeadDim = 256;
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // 1 s per internal wait
-
-struct DeviceState {
-    bool ready = false;
-    int sms = 0;
-    int major = 0, minor = 0;
-    // Split-K scratch of the decode GEMM, sized for one CTA per SM.
-    void *scratch = nullptr;
-    float *partials = nullptr;
-    unsigned *flags = nullptr;
-    int *err = nullptr;
-    size_t flag_bytes = 0;
-    // decode_gemm_bf16_reduce_rmsnorm's "its GEMM is complete" word (in the
-    // scratch's last 256 bytes, after the error word).
-    unsigned *gemm_done = nullptr;
-    // A host-mapped word the decode GEMM sets when one of its waits runs out:
-    // the host reads it without synchronising, so the next call can refuse to
-    // run on scratch a kernel left half used (host_err) -- and the kernel's
-    // address of it (host_err_dev).
-    int *host_err = nullptr;
-    int *host_err_dev = nullptr;
-};
 
 std::mutex g_mutex;
 DeviceState g_devices[kMaxDevices];
@@ -55,6 +33,8 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
+}  // namespace
+
 int current_device(int *dev) {
     if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) {
         cudaGetLastError();
@@ -62,6 +42,8 @@ int current_device(int *dev) {
     }
     return SKINNY_OK;
 }
+
+namespace {
 
 // Device properties (once per device). Caller holds g_mutex.
 int device_state_locked(int dev, DeviceState **out) {
@@ -81,10 +63,14 @@ int device_state_locked(int dev, DeviceState **out) {
     return SKINNY_OK;
 }
 
+}  // namespace
+
 int device_state(int dev, DeviceState **out) {
     std::lock_guard<std::mutex> lock(g_mutex);
     return device_state_locked(dev, out);
 }
+
+namespace {
 
 // The decode GEMM's scratch: allocated and zeroed once per device.
 int ensure_scratch(int dev, cudaStream_t stream, DeviceState **out) {
@@ -155,6 +141,8 @@ int encoder(EncodeTiledFn *fn) {
     return SKINNY_OK;
 }
 
+}  // namespace
+
 // The pointer must be device (or managed) memory of device `dev`.
 int check_device_pointer(const void *p, int dev) {
     cudaPointerAttributes a;
@@ -167,12 +155,7 @@ int check_device_pointer(const void *p, int dev) {
     return SKINNY_OK;
 }
 
-bool overlaps(const void *a, size_t an, const void *b, size_t bn) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + bn && b0 < a0 + an;
-}
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+namespace {
 
 // 2-D BF16 tensor map over a row-major [rows, cols] array, box [box_rows, 64].
 int encode_2d(EncodeTiledFn enc, CUtensorMap *map, const void *base, uint64_t rows,
@@ -209,13 +192,7 @@ int pending_timeout(const DeviceState *d) {
     return SKINNY_OK;
 }
 
-// The launch settings of one call: the caller's options where given, else the
-// process-wide settings (skinny_set_pdl, skinny_set_l2_prefetch).
-struct LaunchSettings {
-    bool pdl;
-    int l2_lead;
-    int l2_after_reduce;
-};
+}  // namespace
 
 int resolve_settings(const skinny_launch_opts *opts, LaunchSettings *out) {
     if (opts != nullptr) {
@@ -236,6 +213,8 @@ int resolve_settings(const skinny_launch_opts *opts, LaunchSettings *out) {
     }
     return SKINNY_OK;
 }
+
+namespace {
 
 int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, void *stream,
                 const skinny_launch_opts *opts, int selftest, unsigned long long limit_ns,
@@ -457,13 +436,6 @@ int reduce_device_checks(const void *partials, const void *residual, const void 
     return SKINNY_OK;
 }
 
-int log2_or_minus_one(int n) { return (n & (n - 1)) == 0 ? __builtin_ctz(n) : -1; }
-
-// Bytes from a row's first element to past the last row's last.
-size_t row_span(int rows, long long stride, long long width) {
-    return (static_cast<size_t>(rows - 1) * stride + width) * 2;
-}
-
 // Whether a pool that is written has two elements in one place. Its axes must lie within each
 // other: each stride clears all that the smaller ones reach. The values then meet the keys
 // where their distance is a sum of steps along the axes, give or take a head: at each axis,
@@ -499,6 +471,8 @@ bool pool_meets_itself(const skinny_kv_cache *c) {
            steps_meet(static_cast<long long>(apart), axes, n, c->head_dim);
 }
 
+}  // namespace
+
 // A cache's own rules, and the bytes its keys (or values) span.
 int check_cache(const skinny_kv_cache *c, bool write, size_t *span) {
     if (!c->k || !c->v) return SKINNY_ERR_NULL;
@@ -522,7 +496,6 @@ int check_cache(const skinny_kv_cache *c, bool write, size_t *span) {
     return SKINNY_OK;
 }
 
-}  // namespace
 }  // namespace skinny
 
 using namespace skinny;
@@ -1005,13 +978,14 @@ int skinny_device_error(int device, int *word) {
     }
     if (reduce_word) value |= kErrReduceExchange;
     // The words of the kernels that read indices from device memory.
-    int rope_word = 0, attention_word = 0;
+    int rope_word = 0, attention_word = 0, logprob_word = 0;
     if (st == SKINNY_OK && (rope_error_word(&rope_word, true) != cudaSuccess ||
-                            attention_error_word(&attention_word, true) != cudaSuccess)) {
+                            attention_error_word(&attention_word, true) != cudaSuccess ||
+                            logprob_error_word(&logprob_word, true) != cudaSuccess)) {
         cudaGetLastError();
         st = SKINNY_ERR_DEVICE;
     }
-    if (rope_word || attention_word) value |= kErrIndex;
+    if (rope_word || attention_word || logprob_word) value |= kErrIndex;
     cudaSetDevice(prev);
     if (word) *word = value;
     if (st != SKINNY_OK) return st;

@@ -184,4 +184,21 @@ cudaError_t launch_decode_attention(const AttentionArgs &a, int head_dim, int nu
                                     cudaStream_t stream, bool pdl);
 cudaError_t attention_error_word(int *value, bool clear);
 
+// Log probabilities, entropy and top alternatives of rows of logits (token_logprobs_bf16).
+constexpr int kLogprobMaxTop = 32;
+struct LogprobArgs {
+    const uint16_t *logits;
+    long long stride;
+    int M, V;
+    const long long *tokens;  // [M][given]
+    int given;
+    float *logprobs;
+    float *entropy, *lse;  // [M] or nullptr
+    int top;
+    float *top_logprobs;    // [M][top] or nullptr
+    long long *top_tokens;  // [M][top] or nullptr
+};
+cudaError_t launch_token_logprobs(const LogprobArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t logprob_error_word(int *value, bool clear);
+
 }  // namespace skinny
