@@ -201,6 +201,41 @@ SKINNY_API int decode_gemm_bf16_epilogue(const void *x, const void *W, const voi
                                          void *stream);
 
 /*
+ * decode_gemm_bf16_lora -- out = act(x @ W^T + c_a (x @ A_a^T) @ B_a^T + bias) + residual
+ *   A linear of a batch whose rows (requests) each have a low-rank adapter a of their own,
+ *   or none, beside the weight that all share: decode_gemm_bf16_epilogue with the adapters'
+ *   product added to the FP32 sum. The drafter pages have no counterpart.
+ *
+ *   lora->A         [num_adapters, rank, K] BF16, contiguous, 16-byte aligned.
+ *   lora->B         [num_adapters, N, rank] BF16, contiguous, 16-byte aligned.
+ *   lora->adapters  [M] int32: row m's adapter; negative: none. Rows may share one. One of
+ *                   num_adapters or more counts as none and skinny_device_error() reports
+ *                   bit 256.
+ *   lora->scales    [num_adapters] FP32 (c), or NULL: 1.
+ *   rank a multiple of 8 in [8, 128] (smaller adapters of a pool are padded with zero rows
+ *   of A and columns of B); 1 <= num_adapters <= 2^20.
+ *   A x is an FP32 sum, scaled and multiplied by B in FP32: no rounding before the one to
+ *   BF16. Only adapters in use are read. A row without one gets decode_gemm_bf16_epilogue's
+ *   bits. Deterministic. Two kernels; the GEMM streams its weights while the first runs.
+ *   Uses the decode GEMM's per-device scratch (same rules on streams and on the first call).
+ *   With programmatic dependent launch A, B, scales, adapters, bias and residual are read
+ *   after the wait for the previous kernel.
+ *   Other arguments, rules and errors as decode_gemm_bf16_epilogue.
+ */
+typedef struct {
+    const void *A;
+    const void *B;
+    const void *adapters;
+    const void *scales;
+    int num_adapters;
+    int rank;
+} skinny_lora;
+SKINNY_API int decode_gemm_bf16_lora(const void *x, const void *W, const skinny_lora *lora,
+                                     const void *bias, const void *residual, void *out, int M,
+                                     int N, int K, int activation,
+                                     const skinny_launch_opts *opts, void *stream);
+
+/*
  * decode_gemm_bf16_noalloc -- decode_gemm_bf16 that allocates no device memory
  *   The drafter pages have no counterpart to this entry point. It is for callers
  *   that cannot let a library call cudaMalloc: serving engines that hand all
@@ -540,8 +575,8 @@ SKINNY_API const char *skinny_status_string(int status);
  *   the raw word (a bit set per waiting role that gave up; 64 if only the
  *   host-mapped word was set; 128 if a reduce_residual_rmsnorm cluster's
  *   exchange of its sums of squares ran out; 256 if a kernel that reads
- *   indices from device memory (qk_norm_rope_bf16, decode_attention_bf16,
- *   token_logprobs_bf16) met one out of range, and if that is the only bit the
+ *   indices from device memory (decode_gemm_bf16_lora, qk_norm_rope_bf16,
+ *   decode_attention_bf16, token_logprobs_bf16) met one out of range, and if that is the only bit the
  *   status is SKINNY_ERR_INDEX) to *word if word is not NULL. Clearing also
  *   re-arms the decode GEMM's scratch flags, so the next call starts clean and
  *   calls stop returning SKINNY_ERR_TIMEOUT. Host pointer: word.

@@ -11,6 +11,8 @@ operations raises.
     gather_shards_bf16(shards, out)                  TP shards side by side
     decode_gemm_bf16_epilogue(x, W, out, bias, activation, residual)
                                                      out = act(x @ W^T + bias) + residual
+    decode_gemm_bf16_lora(x, W, out, A, B, adapters, ...)
+                                                     the same with an adapter for each row
     qk_norm_rope_bf16(qkv, ...)                      per-head norm, rotation, cache append
     decode_attention_bf16(q, k_cache, v_cache, ...)  one token per row over a paged cache
     token_logprobs_bf16(logits, tokens, logprobs, ...)
@@ -86,6 +88,12 @@ class QkNormRopeArgs(ctypes.Structure):
                 ("slots", ctypes.c_void_p)]
 
 
+class LoraArgs(ctypes.Structure):
+    """skinny_lora."""
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("adapters", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("num_adapters", ctypes.c_int), ("rank", ctypes.c_int)]
+
+
 class TokenLogprobsArgs(ctypes.Structure):
     """skinny_token_logprobs_args."""
     _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_longlong),
@@ -112,6 +120,7 @@ _CACHE = "PPiiiiqqq"
 _pack_rope = struct.Struct("@PqiiiiPPfPiiiPPqPq" + _CACHE + "P").pack
 _pack_attention = struct.Struct("@Pqii" + _CACHE + "PqiPiifPPPN").pack
 _pack_logprobs = struct.Struct("@PqiiPiPPPiPP").pack
+_pack_lora = struct.Struct("@PPPPii").pack
 _NO_CACHE = (0,) * 9
 
 
@@ -141,6 +150,8 @@ def load_library(path: str = LIBRARY):
     lib.decode_gemm_bf16_logits.restype = i32
     lib.decode_gemm_bf16_epilogue.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, op, vp]
     lib.decode_gemm_bf16_epilogue.restype = i32
+    lib.decode_gemm_bf16_lora.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, op, vp]
+    lib.decode_gemm_bf16_lora.restype = i32
     lib.decode_gemm_bf16_reduce_rmsnorm.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32,
                                                     f32, vp]
     lib.decode_gemm_bf16_reduce_rmsnorm.restype = i32
@@ -283,6 +294,45 @@ def decode_gemm_bf16_epilogue(x, W, out, bias=None, activation="none", residual=
         None if residual is None else residual.data_ptr(), out.data_ptr(), M, N, K, act,
         None if o is None else ctypes.byref(o), _stream_handle(stream))
     _check(st, "decode_gemm_bf16_epilogue")
+    return out
+
+
+def decode_gemm_bf16_lora(x, W, out, A, B, adapters, scales=None, bias=None, activation="none",
+                          residual=None, stream=None, pdl=None, l2_prefetch=None):
+    """out[M, N] = act(x @ W^T + c_a (x @ A_a^T) @ B_a^T + bias) + residual, a = adapters[m].
+
+    A [num_adapters, rank, K] and B [num_adapters, N, rank], contiguous CUDA bfloat16;
+    adapters [M] int32 (negative: the row has none); scales [num_adapters] FP32 or None (1).
+    rank: a multiple of 8 up to 128. The rest as for decode_gemm_bf16_epilogue. Returns ``out``.
+    """
+    import torch
+    _bf16_cuda(x, "x")
+    _bf16_cuda(W, "W")
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} and W {tuple(W.shape)} must be [M,K] and [N,K]")
+    M, K = x.shape
+    N = W.shape[0]
+    _bf16_cuda(out, "out", (M, N))
+    _bf16_cuda(A, "A")
+    if A.dim() != 3 or A.shape[2] != K:
+        raise ValueError(f"A must be [num_adapters, rank, {K}], got {tuple(A.shape)}")
+    count, rank = A.shape[:2]
+    _bf16_cuda(B, "B", (count, N, rank))
+    adapters_ptr = _plain_cuda(adapters, "adapters", torch.int32, (M,))
+    scales_ptr = 0 if scales is None else _plain_cuda(scales, "scales", torch.float32, (count,))
+    if bias is not None:
+        _bf16_cuda(bias, "bias", (N,))
+    if residual is not None:
+        _bf16_cuda(residual, "residual", (M, N))
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    o = _opts(pdl, l2_prefetch)
+    st = load_library().decode_gemm_bf16_lora(
+        x.data_ptr(), W.data_ptr(), _pack_lora(A.data_ptr(), B.data_ptr(), adapters_ptr, scales_ptr, count, rank),
+        None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
+        out.data_ptr(), M, N, K, act, None if o is None else ctypes.byref(o), _stream_handle(stream))
+    _check(st, "decode_gemm_bf16_lora")
     return out
 
 

@@ -87,7 +87,8 @@ int ensure_scratch(int dev, cudaStream_t stream, DeviceState **out) {
         if (cap != cudaStreamCaptureStatusNone) return SKINNY_ERR_CAPTURE;
         const size_t partial_bytes = static_cast<size_t>(2) * d->sms * kSlotFloats * sizeof(float);
         const size_t flag_bytes = (static_cast<size_t>(2) * d->sms * sizeof(unsigned) + 255) / 256 * 256;
-        const size_t bytes = partial_bytes + flag_bytes + 256;
+        const size_t lora_at = partial_bytes + flag_bytes + 256;
+        const size_t bytes = lora_at + kLoraScratchFloats * sizeof(float);
         void *p = nullptr;
         if (cudaMalloc(&p, bytes) != cudaSuccess) {
             cudaGetLastError();
@@ -119,6 +120,7 @@ int ensure_scratch(int dev, cudaStream_t stream, DeviceState **out) {
         d->err = reinterpret_cast<int *>(static_cast<char *>(p) + partial_bytes + flag_bytes);
         d->flag_bytes = flag_bytes;
         d->gemm_done = reinterpret_cast<unsigned *>(d->err) + 32;
+        d->lora_sums = reinterpret_cast<float *>(static_cast<char *>(p) + lora_at);
     }
     *out = d;
     return SKINNY_OK;
@@ -219,16 +221,28 @@ namespace {
 int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, void *stream,
                 const skinny_launch_opts *opts, int selftest, unsigned long long limit_ns,
                 int logits = 0, float soft_cap = 0.0f, float scale = 1.0f,
-                const Epilogue *epi = nullptr) {
-    if (!x || !W || !out) return SKINNY_ERR_NULL;
+                const Epilogue *epi = nullptr, const skinny_lora *lora = nullptr) {
+    if (!x || !W || !out || (lora && (!lora->A || !lora->B || !lora->adapters))) return SKINNY_ERR_NULL;
     int st = gemm_shape_ok(M, N, K);
     if (st) return st;
+    if (lora && (lora->rank < 8 || lora->rank > kLoraMaxRank || lora->rank % 8 != 0 ||
+                 lora->num_adapters < 1 || lora->num_adapters > (1 << 20)))
+        return SKINNY_ERR_SHAPE;
     const void *bias = epi ? epi->bias : nullptr, *residual = epi ? epi->residual : nullptr;
     if (!aligned(x, 16) || !aligned(W, 16) || !aligned(out, 2) || !aligned(bias, 2) ||
-        !aligned(residual, 2))
+        !aligned(residual, 2) ||
+        (lora && (!aligned(lora->A, 16) || !aligned(lora->B, 16) || !aligned(lora->adapters, 4) ||
+                  !aligned(lora->scales, 4))))
         return SKINNY_ERR_ALIGN;
     const size_t xb = static_cast<size_t>(M) * K * 2, wb = static_cast<size_t>(N) * K * 2,
                  ob = static_cast<size_t>(M) * N * 2;
+    const size_t pool = lora ? static_cast<size_t>(lora->num_adapters) * lora->rank * 2 : 0;
+    const struct { const void *p; size_t n; } lora_in[] = {
+        {lora ? lora->A : nullptr, pool * K}, {lora ? lora->B : nullptr, pool * N},
+        {lora ? lora->adapters : nullptr, static_cast<size_t>(M) * 4},
+        {lora ? lora->scales : nullptr, lora ? static_cast<size_t>(lora->num_adapters) * 4 : 0}};
+    for (const auto &b : lora_in)
+        if (b.p && overlaps(out, ob, b.p, b.n)) return SKINNY_ERR_ALIAS;
     // out may be the residual itself (element-wise in place), nothing else.
     if (overlaps(out, ob, x, xb) || overlaps(out, ob, W, wb) ||
         (bias && overlaps(out, ob, bias, static_cast<size_t>(N) * 2)) ||
@@ -243,6 +257,8 @@ int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, vo
         (bias && (st = check_device_pointer(bias, dev))) ||
         (residual && residual != out && (st = check_device_pointer(residual, dev))))
         return st;
+    for (const auto &b : lora_in)
+        if (b.p && (st = check_device_pointer(b.p, dev))) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DeviceState *d = nullptr;
     if ((st = ensure_scratch(dev, s, &d))) return st;
@@ -277,6 +293,20 @@ int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, vo
     a.l2_lead = ls.l2_lead;
     a.gemm_done = d->gemm_done;
     a.l2_after_reduce = ls.l2_after_reduce;
+    if (lora) {
+        a.lora.A = static_cast<const uint16_t *>(lora->A);
+        a.lora.B = static_cast<const uint16_t *>(lora->B);
+        a.lora.adapters = static_cast<const int *>(lora->adapters);
+        a.lora.scales = static_cast<const float *>(lora->scales);
+        a.lora.count = lora->num_adapters;
+        a.lora.rank = lora->rank;
+        a.lora.splits = lora_splits(M, K, lora->rank, d->sms);
+        a.lora.sums = d->lora_sums;
+        if (launch_lora_shrink(x, a.lora, M, K, s, pdl) != cudaSuccess) {
+            cudaGetLastError();
+            return SKINNY_ERR_LAUNCH;
+        }
+    }
     // Split tiles of 64-row accumulators, every CTA within at most two tiles (two
     // scratch slots), plain output: the GEMM only publishes its partials and a
     // small kernel finishes them (same order, same bits). A finisher CTA would
@@ -634,6 +664,18 @@ int decode_gemm_bf16_epilogue(const void *x, const void *W, const void *bias,
     return gemm_launch(x, W, out, M, N, K, stream, opts, 0, kWaitLimitNs, 0, 0.0f, 1.0f, &epi);
 }
 
+int decode_gemm_bf16_lora(const void *x, const void *W, const skinny_lora *lora, const void *bias,
+                          const void *residual, void *out, int M, int N, int K, int activation,
+                          const skinny_launch_opts *opts, void *stream) {
+    if (!lora) return SKINNY_ERR_NULL;
+    if (activation < SKINNY_ACT_NONE || activation > SKINNY_ACT_GELU_TANH) return SKINNY_ERR_ARG;
+    Epilogue epi = {};
+    epi.bias = static_cast<const uint16_t *>(bias);
+    epi.residual = static_cast<const uint16_t *>(residual);
+    epi.activation = activation;
+    return gemm_launch(x, W, out, M, N, K, stream, opts, 0, kWaitLimitNs, 0, 0.0f, 1.0f, &epi, lora);
+}
+
 int skinny_watchdog_selftest(const void *x, const void *W, void *out, int M, int N, int K,
                              long long timeout_ns, void *stream) {
     if (timeout_ns < 1000 || timeout_ns > 2000000000LL) return SKINNY_ERR_ARG;
@@ -978,14 +1020,15 @@ int skinny_device_error(int device, int *word) {
     }
     if (reduce_word) value |= kErrReduceExchange;
     // The words of the kernels that read indices from device memory.
-    int rope_word = 0, attention_word = 0, logprob_word = 0;
+    int rope_word = 0, attention_word = 0, logprob_word = 0, lora_word = 0;
     if (st == SKINNY_OK && (rope_error_word(&rope_word, true) != cudaSuccess ||
                             attention_error_word(&attention_word, true) != cudaSuccess ||
-                            logprob_error_word(&logprob_word, true) != cudaSuccess)) {
+                            logprob_error_word(&logprob_word, true) != cudaSuccess ||
+                            lora_error_word(&lora_word, true) != cudaSuccess)) {
         cudaGetLastError();
         st = SKINNY_ERR_DEVICE;
     }
-    if (rope_word || attention_word || logprob_word) value |= kErrIndex;
+    if (rope_word || attention_word || logprob_word || lora_word) value |= kErrIndex;
     cudaSetDevice(prev);
     if (word) *word = value;
     if (st != SKINNY_OK) return st;

@@ -27,6 +27,7 @@ struct DeviceState {
     // decode_gemm_bf16_reduce_rmsnorm's "its GEMM is complete" word (in the
     // scratch's last 256 bytes, after the error word).
     unsigned *gemm_done = nullptr;
+    float *lora_sums = nullptr;  // decode_gemm_bf16_lora's A x, kLoraScratchFloats
     // A host-mapped word the decode GEMM sets when one of its waits runs out:
     // the host reads it without synchronising, so the next call can refuse to
     // run on scratch a kernel left half used (host_err) -- and the kernel's

@@ -67,19 +67,25 @@ constexpr int kMaxShallowStages = 6;  // shallow rings have 5..6 stages, deep on
 // the next kernel's CTAs be resident on the same SM while this one finishes, so
 // with programmatic dependent launch they stream weights across the boundary
 // (plan.cuh use_shallow_ring picks one by the weight bytes per CTA).
-template <int MP, int STAGES>
+template <int MP, int STAGES, bool LORA = false>
 struct Layout {
     static constexpr int kStages = STAGES;
     static constexpr int kAccCols = MP == 64 ? 64 : 32;  // TMEM columns per accumulator
-    static constexpr int kTmemCols = 2 * kAccCols;       // two accumulator buffers
+    // Two accumulator buffers; LORA: the adapters' part of a tile, in the columns after them
+    // (a power of two of columns in all).
+    static constexpr int kTmemCols = (LORA ? 4 : 2) * kAccCols;
+    static constexpr int kLoraCol = 2 * kAccCols;
     static constexpr int kXBytes = MP * kBlockK * 2;
     static constexpr int kStageBytes = kWBytes + kXBytes;
     static constexpr int kBarOffset = kStages * kStageBytes;
     static constexpr int kNumBars = 2 * kStages + 7;
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;
-    static constexpr int kBytes = kMiscOffset + 16;
+    // LORA: the rows' adapters, then scale A x [M][rank] (as many bytes as the call needs).
+    static constexpr int kLoraOffset = kMiscOffset + 24;
+    static constexpr int kBytes = LORA ? kLoraOffset + kMaxM * 4 : kMiscOffset + 16;
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
+    static_assert(!LORA || kLoraOffset % 16 == 0, "16-byte loads of A x");
     static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment");
 };
 
@@ -175,13 +181,21 @@ __device__ __forceinline__ void store_tile_staged(const float (&v)[MP], uint16_t
     }
 }
 
-// EPI: the epilogue of epilogue.cuh. A template so that the plain kernel keeps its
+// EPI: the epilogue of epilogue.cuh. LORA (with EPI): the adapters' second half,
+// scale B_a (A_a x), a the row's adapter. Templates so that the plain kernel keeps its
 // registers.
-template <int MP, int STAGES, bool EPI>
+//
+// LORA: the kernel is launched behind lora_shrink_kernel, which lets it start once x is
+// there, so nothing but the epilogue waits for that kernel. While a tile's weights stream the
+// epilogue's threads, idle otherwise, work its part out: thread = output column n, which reads
+// row n of every B in use (each once, but for rows that share an adapter: those find it in
+// L2) and A x from shared memory, in FP32; the result waits in tensor memory. A
+// tile's contributors (split K) share the rows out. Measured in the file's end.
+template <int MP, int STAGES, bool EPI, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_gemm_kernel(const __grid_constant__ CUtensorMap w_map,
                        const __grid_constant__ CUtensorMap x_map, const GemmArgs args) {
-    using L = Layout<MP, STAGES>;
+    using L = Layout<MP, STAGES, LORA>;
     constexpr int S = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -304,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            ptx::pdl_wait();  // x may be the predecessor's output
+            if (!LORA) ptx::pdl_wait();  // x may be the predecessor's output
             BlockCursor xc = start;
             for (int j = 0; j < npre; ++j) {
                 const uint32_t st = sbase + j * L::kStageBytes;
@@ -337,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             // ---------------- MMA issuer ----------------
             constexpr uint32_t idesc = ptx::idesc_bf16_f32(kBlockN, MP);
-            ptx::pdl_wait();  // start the bounded waits' clocks after the predecessor
+            if (!LORA) ptx::pdl_wait();  // start the bounded waits' clocks after the predecessor
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -426,6 +440,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ahead[i] = lo | (hi << 16);
             }
         };
+        // LORA: the rows' adapters and scale A x, the K slices' sums added in order; and the rows
+        // of this piece whose part is in tensor memory.
+        [[maybe_unused]] int *sm_adapter = reinterpret_cast<int *>(smem + L::kLoraOffset);
+        [[maybe_unused]] float *sm_ax = reinterpret_cast<float *>(smem + L::kLoraOffset + kMaxM * 4);
+        [[maybe_unused]] uint64_t lora_rows = 0;
+        [[maybe_unused]] const uint32_t lora_taddr =
+            tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + L::kLoraCol;
+        if constexpr (LORA) {
+            const LoraArgs &l = args.lora;
+            if (etid < kMaxM) {
+                const int id = etid < g.M ? __ldcg(l.adapters + etid) : -1;
+                sm_adapter[etid] = id < l.count ? id : -1;
+            }
+            ptx::named_barrier_sync(1, kEpilogueThreads);
+            const int values = g.M * l.rank;
+            for (int i = etid; i < values; i += kEpilogueThreads) {
+                const int id = sm_adapter[i / l.rank];
+                if (id < 0) continue;
+                const float *from = l.sums + i;
+                float sum = 0.0f;
+                for (int s0 = 0; s0 < l.splits; s0 += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        v[u] = s0 + u < l.splits ? __ldcg(from + static_cast<size_t>(s0 + u) * values) : 0.0f;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) sum = __fadd_rn(sum, v[u]);
+                }
+                sm_ax[i] = l.scales != nullptr ? __fmul_rn(sum, __ldcg(l.scales + id)) : sum;
+            }
+            ptx::named_barrier_sync(1, kEpilogueThreads);
+        }
+        // The adapters' part of column n for the rows m = share (mod shares) of a piece.
+        [[maybe_unused]] auto lora_part = [&](int n, int share, int shares) {
+            const LoraArgs &l = args.lora;
+            auto wanted = [&](int m) { return m < g.M && sm_adapter[m] >= 0 && m % shares == share; };
+            lora_rows = __ballot_sync(0xFFFFFFFFu, wanted(lane)) |
+                        static_cast<uint64_t>(MP > 32 ? __ballot_sync(0xFFFFFFFFu, wanted(lane + 32)) : 0u) << 32;
+            constexpr int kAtOnce = MP == 16 ? 4 : 8;  // rows whose loads are on their way together
+            const uint16_t *column = l.B + static_cast<size_t>(n < g.N ? n : 0) * l.rank;
+            for (uint64_t rest = lora_rows; rest != 0;) {
+                int m[kAtOnce];
+                const uint4 *b[kAtOnce];
+                float v[kAtOnce];
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    m[u] = rest != 0 ? __ffsll(static_cast<long long>(rest)) - 1 : -1;
+                    rest &= rest - 1;
+                    const size_t id = m[u] < 0 ? 0 : sm_adapter[m[u]];
+                    b[u] = reinterpret_cast<const uint4 *>(column + id * g.N * l.rank);
+                    v[u] = 0.0f;
+                }
+                for (int j = 0; j < l.rank; j += 16) {
+                    uint4 w[kAtOnce][2];
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            w[u][h] = m[u] >= 0 && j + 8 * h < l.rank ? __ldg(b[u] + j / 8 + h) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        if (m[u] < 0) break;
+                        const float4 *ax = reinterpret_cast<const float4 *>(sm_ax + m[u] * l.rank + j);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (j + 8 * h >= l.rank) break;
+                            const float4 t0 = ax[2 * h], t1 = ax[2 * h + 1];
+                            v[u] = fmaf(t0.x, __uint_as_float(w[u][h].x << 16), v[u]);
+                            v[u] = fmaf(t0.y, __uint_as_float(w[u][h].x & 0xFFFF0000u), v[u]);
+                            v[u] = fmaf(t0.z, __uint_as_float(w[u][h].y << 16), v[u]);
+                            v[u] = fmaf(t0.w, __uint_as_float(w[u][h].y & 0xFFFF0000u), v[u]);
+                            v[u] = fmaf(t1.x, __uint_as_float(w[u][h].z << 16), v[u]);
+                            v[u] = fmaf(t1.y, __uint_as_float(w[u][h].z & 0xFFFF0000u), v[u]);
+                            v[u] = fmaf(t1.z, __uint_as_float(w[u][h].w << 16), v[u]);
+                            v[u] = fmaf(t1.w, __uint_as_float(w[u][h].w & 0xFFFF0000u), v[u]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u)
+                    if (m[u] >= 0) ptx::tmem_st1(lora_taddr + m[u], __float_as_uint(v[u]));
+            }
+            ptx::tmem_st_wait();
+            __syncwarp();
+        };
         auto emit = [&](int n, bool from_tmem, uint32_t taddr) {
 #pragma unroll 1
             for (int m0 = 0; m0 < g.M; m0 += kRows) {
@@ -436,6 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (from_tmem) {
                     __syncwarp();  // lanes past the right edge went another way; the load is the whole warp's
                     ptx::tmem_ld_now(taddr + m0, w);
+                    if constexpr (LORA) {
+                        uint32_t part[kRows];
+                        ptx::tmem_ld_now(lora_taddr + m0, part);
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i)
+                            if (lora_rows >> (m0 + i) & 1)
+                                w[i] = __float_as_uint(__fadd_rn(__uint_as_float(w[i]), __uint_as_float(part[i])));
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < kRows; ++i)
@@ -553,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (args.epi.bias != nullptr && n < g.N) bias = bf16_value(args.epi.bias[n]);
                 load_residual(n, 0);
             }
+            if constexpr (LORA) lora_part(p.tile * kBlockN + row, cta - first, last - first + 1);
             const int b = q & 1;
             const uint32_t aph = (q >> 1) & 1;
             const int r = bounded_wait(bar_acc_full + 8 * b, aph, abort_flag, limit);
@@ -579,6 +687,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_ld_wait(v);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) acc[c + i] = __uint_as_float(v[i]);
+                    if constexpr (LORA) {
+                        ptx::tmem_ld_now(lora_taddr + c, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (lora_rows >> (c + i) & 1) acc[c + i] = __fadd_rn(acc[c + i], __uint_as_float(v[i]));
+                    }
                 }
             }
             ptx::tc_fence_before_sync();
@@ -669,40 +783,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int MP, int STAGES, bool EPI>
+template <int MP, int STAGES, bool EPI, bool LORA>
 cudaError_t launch_kernel(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            const GemmArgs &args, int ctas, cudaStream_t stream, bool pdl,
                            int device) {
-    using L = Layout<MP, STAGES>;
+    using L = Layout<MP, STAGES, LORA>;
+    constexpr int kMostBytes = L::kDynamicBytes + (LORA ? MP * kLoraMaxRank * 4 : 0);
+    static_assert(kMostBytes <= 232448, "shared memory of a CTA");
     static bool configured[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (!configured[device]) {
-        cudaError_t e = cudaFuncSetAttribute(decode_gemm_kernel<MP, STAGES, EPI>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             L::kDynamicBytes);
+        cudaError_t e = cudaFuncSetAttribute(decode_gemm_kernel<MP, STAGES, EPI, LORA>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
         if (e != cudaSuccess) return e;
         configured[device] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = L::kDynamicBytes;
+    cfg.dynamicSmemBytes = L::kDynamicBytes + (LORA ? args.M * args.lora.rank * 4 : 0);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_gemm_kernel<MP, STAGES, EPI>, w_map, x_map, args);
+    // LORA: always, behind the library's own first half (whatever comes before that is
+    // waited for there).
+    cfg.numAttrs = pdl || LORA ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, decode_gemm_kernel<MP, STAGES, EPI, LORA>, w_map, x_map, args);
 }
 
 template <int MP, int STAGES>
 cudaError_t launch_variant(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            const GemmArgs &args, int ctas, cudaStream_t stream, bool pdl,
                            int device) {
+    if (args.lora.rank > 0) {
+        // A x takes one stage of the rings that fill the shared memory (up to 32 KB).
+        constexpr int kLoraStages = STAGES - (MP >= 32 && STAGES > kMaxShallowStages ? 1 : 0);
+        return launch_kernel<MP, kLoraStages, true, true>(w_map, x_map, args, ctas, stream, pdl, device);
+    }
     if (args.epilogue)
-        return launch_kernel<MP, STAGES, true>(w_map, x_map, args, ctas, stream, pdl, device);
-    return launch_kernel<MP, STAGES, false>(w_map, x_map, args, ctas, stream, pdl, device);
+        return launch_kernel<MP, STAGES, true, false>(w_map, x_map, args, ctas, stream, pdl, device);
+    return launch_kernel<MP, STAGES, false, false>(w_map, x_map, args, ctas, stream, pdl, device);
 }
 
 // Deep rings: about 185 KB for 16 rows, near the 227 KB a CTA may use for 32 and

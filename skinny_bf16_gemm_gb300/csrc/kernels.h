@@ -22,6 +22,20 @@ enum ErrorBits : int {
     kErrIndex = 256,  // a position, slot, length or page index on the device was out of range
 };
 
+// Low-rank adapters beside a decode GEMM (decode_gemm_bf16_lora): row m's adapter is
+// adapters[m], none if it is negative.
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraScratchFloats = 1 << 16;
+struct LoraArgs {
+    const uint16_t *A;    // [count][rank][K]
+    const uint16_t *B;    // [count][N][rank]
+    const int *adapters;  // [M]
+    const float *scales;  // [count] or nullptr: 1
+    int count, rank;
+    int splits;   // K slices of A x
+    float *sums;  // [splits][M][rank] FP32, rows without an adapter unwritten
+};
+
 struct GemmArgs {
     int M, N, K;
     uint16_t *out;          // [M, N] BF16 patterns
@@ -53,6 +67,8 @@ struct GemmArgs {
     // epilogue = 1: bias, activation and residual (epilogue.cuh) on the FP32 sum.
     int epilogue;
     Epilogue epi;
+    // lora.rank > 0: the adapters' second half, added to the FP32 sum before the epilogue.
+    LoraArgs lora;
 };
 
 // Default and largest l2_lead. Measured on GB300: 6 suits back-to-back GEMMs
@@ -81,6 +97,11 @@ int gemm_smem_bytes(int mma_n, bool shallow);
 cudaError_t launch_decode_gemm(const CUtensorMap &w_map, const CUtensorMap &x_map,
                                const GemmArgs &args, int mma_n, int ctas, cudaStream_t stream,
                                bool pdl, bool shallow, int device);
+
+// The adapters' first half (lora_shrink.cu): K slices for a call, and l.sums from x.
+int lora_splits(int M, int K, int rank, int num_sms);
+cudaError_t launch_lora_shrink(const void *x, const LoraArgs &l, int M, int K, cudaStream_t stream, bool pdl);
+cudaError_t lora_error_word(int *value, bool clear);
 
 // Split-K scratch held in a static device array (decode_gemm_bf16_noalloc).
 constexpr int kStaticScratchCtas = 160;   // CTAs the array holds partial tiles for

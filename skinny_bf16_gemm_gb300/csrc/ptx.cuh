@@ -211,6 +211,12 @@ __device__ __forceinline__ void tmem_ld_now(uint32_t taddr, uint32_t (&r)[16]) {
     tmem_ld_wait(r);
 }
 
+// One column of the warp's 32 TMEM lanes; complete for this warp's loads after tmem_st_wait.
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ---- global memory ---------------------------------------------------------------
 
 __device__ __forceinline__ unsigned ld_acquire_gpu(const unsigned *p) {
