@@ -517,6 +517,64 @@ SKINNY_API int decode_attention_bf16(const skinny_decode_attention_args *args,
 /* Bytes of the workspace on a device with num_sms SMs (0 for num_sms < 1). */
 SKINNY_API size_t skinny_attention_workspace_bytes(int num_sms);
 
+/*
+ * decode_attention_shared_prefix_bf16 -- attention of one new token per row over a prefix
+ *   that all rows share and the row's own tokens after it. The drafter pages have no
+ *   counterpart. For a batch behind one long prompt, and for the drafted tokens of one
+ *   sequence: decode_attention_bf16 reads shared pages once a row, this reads the prefix
+ *   once for up to 256 of a key head's query rows (rows * q_heads / kv_heads), on the tensor
+ *   cores.
+ *
+ *   prefix_table   [prefix_width] int32: token j of the prefix is token j % page_size of page
+ *                  prefix_table[j / page_size] of the cache.
+ *   prefix_length  one int32 on the device: the prefix's tokens. Every row sees them all.
+ *   block_table, lengths  as in decode_attention_bf16, of the row's own tokens: those after
+ *                  the prefix (the new token's among them). A row of length 0 sees the prefix
+ *                  alone; with a prefix of length 0 too it gets zeros and a log-sum of -inf.
+ *   workspace      device memory of skinny_shared_prefix_workspace_bytes(...) bytes, 16-byte
+ *                  aligned, its first SKINNY_ATTENTION_COUNTER_BYTES zero before its first
+ *                  use; every call leaves it ready for the next, of any sizes that it is large
+ *                  enough for. Calls that may run at the same time need one each.
+ *   Three kernels: the prefix, the rows' own tokens while it runs out, and the join. Scores,
+ *   maxima, sums and partial outputs are FP32; the prefix's weights are rounded to BF16 (to
+ *   nearest) for the product with the values, the own tokens' as in decode_attention_bf16;
+ *   the output is rounded once. Deterministic.
+ *   prefix_width >= 1; prefix_width * page_size < 2^30; key heads * blocks of query rows (of
+ *   256; of 128 for head_dim 192 and 256) * tiles of the table (of 128 tokens; 64) < 2^31;
+ *   tables and lengths 4-byte aligned. Every other argument, rule and limit is
+ *   decode_attention_bf16's, without a window.
+ *   On the device a length out of range is taken as the nearest, a token on a page out of
+ *   range as not seen, and skinny_device_error() reports bit 256. Every wait is bounded (1 s);
+ *   one that runs out leaves the call's output unspecified and is reported as bit 512
+ *   (SKINNY_ERR_TIMEOUT); nothing outlives the call.
+ *   Errors: SKINNY_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARG, _DEVICE, _LAUNCH.
+ */
+typedef struct {
+    const void *q;
+    long long q_stride;
+    int rows, q_heads;
+    skinny_kv_cache cache;
+    const void *prefix_table;
+    int prefix_width;
+    const void *prefix_length;
+    const void *block_table;
+    long long table_stride;
+    int table_width;
+    const void *lengths;
+    float scale;
+    void *out;
+    void *lse;
+    void *workspace;
+    size_t workspace_bytes;
+} skinny_shared_prefix_attention_args;
+SKINNY_API int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_args *args,
+                                                   const skinny_launch_opts *opts, void *stream);
+
+/* Bytes of the workspace for these sizes on a device with num_sms SMs (0 for sizes that the
+ * call refuses); no less for more rows or more query heads. */
+SKINNY_API size_t skinny_shared_prefix_workspace_bytes(int rows, int q_heads, int kv_heads,
+                                                       int head_dim, int num_sms);
+
 /* Largest number of alternatives, and of rows, of token_logprobs_bf16. */
 #define SKINNY_LOGPROBS_MAX_TOP 32
 #define SKINNY_LOGPROBS_MAX_ROWS (1 << 24)
@@ -576,7 +634,8 @@ SKINNY_API const char *skinny_status_string(int status);
  *   host-mapped word was set; 128 if a reduce_residual_rmsnorm cluster's
  *   exchange of its sums of squares ran out; 256 if a kernel that reads
  *   indices from device memory (decode_gemm_bf16_lora, qk_norm_rope_bf16,
- *   decode_attention_bf16, token_logprobs_bf16) met one out of range, and if that is the only bit the
+ *   decode_attention_bf16, decode_attention_shared_prefix_bf16, token_logprobs_bf16) met
+ *   one out of range, and if that is the only bit the
  *   status is SKINNY_ERR_INDEX) to *word if word is not NULL. Clearing also
  *   re-arms the decode GEMM's scratch flags, so the next call starts clean and
  *   calls stop returning SKINNY_ERR_TIMEOUT. Host pointer: word.

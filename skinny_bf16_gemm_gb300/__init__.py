@@ -15,6 +15,8 @@ operations raises.
                                                      the same with an adapter for each row
     qk_norm_rope_bf16(qkv, ...)                      per-head norm, rotation, cache append
     decode_attention_bf16(q, k_cache, v_cache, ...)  one token per row over a paged cache
+    decode_attention_shared_prefix_bf16(q, k_cache, v_cache, ...)
+                                                     the same behind a prefix all rows share
     token_logprobs_bf16(logits, tokens, logprobs, ...)
                                                      log probabilities, entropy, top tokens
 """
@@ -88,6 +90,18 @@ class QkNormRopeArgs(ctypes.Structure):
                 ("slots", ctypes.c_void_p)]
 
 
+class SharedPrefixAttentionArgs(ctypes.Structure):
+    """skinny_shared_prefix_attention_args."""
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("rows", ctypes.c_int),
+                ("q_heads", ctypes.c_int), ("cache", KVCacheArgs),
+                ("prefix_table", ctypes.c_void_p), ("prefix_width", ctypes.c_int),
+                ("prefix_length", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_longlong), ("table_width", ctypes.c_int),
+                ("lengths", ctypes.c_void_p), ("scale", ctypes.c_float), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 class LoraArgs(ctypes.Structure):
     """skinny_lora."""
     _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("adapters", ctypes.c_void_p),
@@ -119,6 +133,7 @@ class DecodeAttentionArgs(ctypes.Structure):
 _CACHE = "PPiiiiqqq"
 _pack_rope = struct.Struct("@PqiiiiPPfPiiiPPqPq" + _CACHE + "P").pack
 _pack_attention = struct.Struct("@Pqii" + _CACHE + "PqiPiifPPPN").pack
+_pack_prefix = struct.Struct("@Pqii" + _CACHE + "PiPPqiPfPPPN").pack
 _pack_logprobs = struct.Struct("@PqiiPiPPPiPP").pack
 _pack_lora = struct.Struct("@PPPPii").pack
 _NO_CACHE = (0,) * 9
@@ -164,6 +179,10 @@ def load_library(path: str = LIBRARY):
     lib.decode_attention_bf16.restype = i32
     lib.token_logprobs_bf16.argtypes = [vp, op, vp]
     lib.token_logprobs_bf16.restype = i32
+    lib.decode_attention_shared_prefix_bf16.argtypes = [vp, op, vp]
+    lib.decode_attention_shared_prefix_bf16.restype = i32
+    lib.skinny_shared_prefix_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.skinny_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
     lib.skinny_attention_workspace_bytes.argtypes = [i32]
     lib.skinny_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.gather_shards_bf16.argtypes = [vp, i32, i32, i32, vp, vp]
@@ -564,19 +583,20 @@ def attention_workspace(device=None):
 _workspaces = {}  # (device, stream) -> the workspace of calls that bring none
 
 
-def _own_workspace(device, stream):
+def _own_workspace(device, stream, find=None, *args):
     """The workspace of a call on ``stream`` (a handle) that brings none. Calls on one
     stream run one after another and share one; a call being captured gets its own,
     zeroed in the graph, so that graphs replayed side by side do not meet. Both are made
     with the launch stream current, whatever the caller's is: the zeroing comes before
     the kernel, and the memory goes to no other stream's call while the kernel runs."""
     import torch
+    find = find or _current_workspace
     handle = stream.value or 0
     if handle != torch._C._cuda_getCurrentRawStream(device):
         on = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
         with torch.cuda.stream(on):
-            return _current_workspace(device, handle)
-    return _current_workspace(device, handle)
+            return find(device, handle, *args)
+    return find(device, handle, *args)
 
 
 def _current_workspace(device, handle):
@@ -698,6 +718,115 @@ def token_logprobs_bf16(logits, tokens, logprobs, entropy=None, lse=None, top_lo
     st = load_library().token_logprobs_bf16(a, None if o is None else ctypes.byref(o), _stream_handle(stream))
     _check(st, "token_logprobs_bf16")
     return logprobs
+
+
+def shared_prefix_workspace(rows, q_heads, kv_heads, head_dim, device=None):
+    """A workspace for decode_attention_shared_prefix_bf16 of up to these rows and query heads
+    on a device, made ready on the current stream; every call leaves it ready for the next.
+    Calls that may run at the same time need one each."""
+    import torch
+    dev = torch.cuda.current_device() if device is None else device
+    n = _prefix_bytes(rows, q_heads, kv_heads, head_dim, dev)
+    if not n:
+        raise ValueError(f"no shared-prefix attention of {rows} rows, {q_heads} heads on {kv_heads}, {head_dim} wide")
+    return _zeroed(n, dev)
+
+
+_sms = {}  # device -> its SMs
+
+
+def _prefix_bytes(rows, q_heads, kv_heads, head_dim, dev):
+    import torch
+    sms = _sms.get(dev)
+    if sms is None:
+        sms = _sms[dev] = torch.cuda.get_device_properties(dev).multi_processor_count
+    return load_library().skinny_shared_prefix_workspace_bytes(rows, q_heads, kv_heads, head_dim, sms)
+
+
+def _zeroed(n, dev):
+    """n bytes on a device, the counters at their start zero."""
+    import torch
+    ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev) if isinstance(dev, int) else dev)
+    ws[:ATTENTION_COUNTER_BYTES].zero_()
+    return ws
+
+
+_prefix_workspaces = {}  # (device, stream) -> the workspace of calls that bring none
+
+
+def _current_prefix_workspace(device, handle, n):
+    """As _current_workspace, of n bytes or more: a larger one takes a smaller one's place,
+    whose memory the stream's next allocations get behind the calls that use it."""
+    import torch
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return _zeroed(n, device)
+    ws = _prefix_workspaces.get((device, handle))
+    if ws is None or ws.nbytes < n:
+        ws = _prefix_workspaces[(device, handle)] = _zeroed(n, device)
+    return ws
+
+
+def decode_attention_shared_prefix_bf16(q, k_cache, v_cache, prefix_table, prefix_length, block_table, lengths,
+                                        out, scale=None, lse=None, workspace=None, stream=None, pdl=None):
+    """Attention of one new token per row over a prefix that all rows share and the row's own
+    tokens after it, both in a paged key-value cache; the prefix is read once for all rows.
+
+    prefix_table [prefix_width] int32: the prefix's pages; prefix_length [1] int32 on the
+    device. block_table [rows, table_width] and lengths [rows] int32 are of the rows' own
+    tokens (a row of length 0 sees the prefix alone). workspace: shared_prefix_workspace(), or
+    None for one kept per stream, as in decode_attention_bf16, which the other arguments
+    follow too. Returns ``out``.
+    """
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    q_stride = _rows(q, "q", bf16)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must be [rows, q_heads, head_dim], got {tuple(shape)}")
+    rows, q_heads, D = shape
+    cache = _cache_fields(k_cache, v_cache, bf16)
+    if cache[5] != D:
+        raise ValueError(f"q has heads of {D}, the cache of {cache[5]}")
+    out_ptr = _plain_cuda(out, "out", bf16, shape)
+    prefix_shape = getattr(prefix_table, "shape", ())
+    prefix_ptr = _plain_cuda(prefix_table, "prefix_table", i32, prefix_shape)
+    if len(prefix_shape) != 1:
+        raise ValueError(f"prefix_table must be [prefix_width], got {tuple(prefix_shape)}")
+    length_ptr = _plain_cuda(prefix_length, "prefix_length", i32, (1,))
+    try:
+        good = block_table.dtype == i32 and block_table.is_cuda
+    except AttributeError:
+        good = False
+    if not good:
+        raise _type_error(block_table, "block_table", i32)
+    table_shape, table_stride = block_table.shape, block_table.stride()
+    if len(table_shape) != 2 or table_shape[0] != rows or (table_stride[1] != 1 and table_shape[1] > 1):
+        raise ValueError(f"block_table must be [{rows}, table_width] with contiguous rows")
+    lengths_ptr = _plain_cuda(lengths, "lengths", i32, (rows,))
+    lse_ptr = 0 if lse is None else _plain_cuda(lse, "lse", torch.float32, (rows, q_heads))
+    handle = _stream_handle(stream)
+    if workspace is None:
+        device = q.device.index
+        if device != torch._C._cuda_getDevice():
+            _check(4, "decode_attention_shared_prefix_bf16")  # as the call itself would say
+        n = _prefix_bytes(rows, q_heads, cache[4], D, device)
+        if not n:
+            _check(2, "decode_attention_shared_prefix_bf16")
+        workspace = _own_workspace(device, handle, _current_prefix_workspace, n)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    width = table_shape[1]
+    try:
+        a = _pack_prefix(
+            q.data_ptr(), q_stride, rows, q_heads, *cache, prefix_ptr, prefix_shape[0], length_ptr,
+            block_table.data_ptr(), table_stride[0] if rows > 1 else width, width, lengths_ptr,
+            D ** -0.5 if scale is None else scale, out_ptr, lse_ptr, workspace.data_ptr(), workspace.nbytes)
+    except struct.error as e:  # a number of the wrong kind, or past the field's range
+        raise ValueError(f"decode_attention_shared_prefix_bf16: {e}") from None
+    o = _opts(pdl, None)
+    st = load_library().decode_attention_shared_prefix_bf16(a, None if o is None else ctypes.byref(o), handle)
+    _check(st, "decode_attention_shared_prefix_bf16")
+    return out
 
 
 def device_error(device=None):

@@ -867,13 +867,13 @@ size_t skinny_attention_workspace_bytes(int num_sms) {
     return num_sms < 1 ? 0 : attn_workspace_bytes(attn_sms(num_sms));
 }
 
-int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_launch_opts *opts,
-                          void *stream) {
+}  // extern "C"
+
+int skinny::check_attention(const skinny_decode_attention_args *p, size_t *pool) {
     if (!p || !p->q || !p->block_table || !p->lengths || !p->out || !p->workspace)
         return SKINNY_ERR_NULL;
     const skinny_kv_cache *c = &p->cache;
-    size_t pool = 0;
-    int st = check_cache(c, false, &pool);
+    int st = check_cache(c, false, pool);
     if (st) return st;
     const int D = c->head_dim;
     if (D != 64 && D != 96 && D != 128 && D != 192 && D != 256) return SKINNY_ERR_SHAPE;
@@ -894,6 +894,56 @@ int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_la
         !aligned(p->block_table, 4) || !aligned(p->lengths, 4) || !aligned(p->lse, 4) ||
         p->q_stride % 8 != 0)
         return SKINNY_ERR_ALIGN;
+    return SKINNY_OK;
+}
+
+void skinny::attention_args(const skinny_decode_attention_args *p, size_t pool, AttentionArgs *out) {
+    const skinny_kv_cache *c = &p->cache;
+    const int group = p->q_heads / c->kv_heads, most = 8 * attn_max_nb(c->head_dim);
+    const int head_blocks = (group + most - 1) / most;
+    AttentionArgs &a = *out;
+    a = {};
+    a.q = static_cast<const uint16_t *>(p->q);
+    a.q_stride = p->q_stride;
+    a.k = static_cast<const uint16_t *>(c->k);
+    a.v = static_cast<const uint16_t *>(c->v);
+    a.num_pages = c->num_pages;
+    a.page_size = c->page_size;
+    a.page_shift = log2_or_minus_one(c->page_size);
+    a.page_stride = c->page_stride;
+    a.token_stride = c->token_stride;
+    a.head_stride = c->head_stride;
+    a.block_table = static_cast<const int *>(p->block_table);
+    a.table_stride = p->table_stride;
+    a.lengths = static_cast<const int *>(p->lengths);
+    a.rows = p->rows;
+    a.q_heads = p->q_heads;
+    a.kv_heads = c->kv_heads;
+    a.group = group;
+    a.head_blocks = head_blocks;
+    a.block_heads = (group + head_blocks - 1) / head_blocks;
+    a.capacity = p->table_width * c->page_size;
+    a.wide = pool > (1ull << 36);
+    a.window = p->window;
+    a.sinks = p->sinks;
+    a.scale_log2 = p->scale * 1.44269504088896341f;
+    a.out = static_cast<uint16_t *>(p->out);
+    a.lse = static_cast<float *>(p->lse);
+    a.counters = static_cast<unsigned *>(p->workspace);
+    static_assert(kAttnCounterBytes == SKINNY_ATTENTION_COUNTER_BYTES, "the header's number");
+    a.partials = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + kAttnCounterBytes);
+}
+
+extern "C" {
+
+int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_launch_opts *opts,
+                          void *stream) {
+    size_t pool = 0;
+    int st = check_attention(p, &pool);
+    if (st) return st;
+    const skinny_kv_cache *c = &p->cache;
+    const int D = c->head_dim;
+    const long long q_width = static_cast<long long>(p->q_heads) * D;
     const size_t heads = static_cast<size_t>(p->rows) * p->q_heads;
     const struct { const void *p; size_t n; } in[] = {
         {p->q, row_span(p->rows, p->q_stride, q_width)}, {c->k, pool}, {c->v, pool},
@@ -920,36 +970,8 @@ int decode_attention_bf16(const skinny_decode_attention_args *p, const skinny_la
         if ((st = check_device_pointer(b.p, dev))) return st;
     for (const auto &b : outs)
         if (b.p && (st = check_device_pointer(b.p, dev))) return st;
-    AttentionArgs a = {};
-    a.q = static_cast<const uint16_t *>(p->q);
-    a.q_stride = p->q_stride;
-    a.k = static_cast<const uint16_t *>(c->k);
-    a.v = static_cast<const uint16_t *>(c->v);
-    a.num_pages = c->num_pages;
-    a.page_size = c->page_size;
-    a.page_shift = log2_or_minus_one(c->page_size);
-    a.page_stride = c->page_stride;
-    a.token_stride = c->token_stride;
-    a.head_stride = c->head_stride;
-    a.block_table = static_cast<const int *>(p->block_table);
-    a.table_stride = p->table_stride;
-    a.lengths = static_cast<const int *>(p->lengths);
-    a.rows = p->rows;
-    a.q_heads = p->q_heads;
-    a.kv_heads = c->kv_heads;
-    a.group = group;
-    a.head_blocks = head_blocks;
-    a.block_heads = (group + head_blocks - 1) / head_blocks;
-    a.capacity = static_cast<int>(capacity);
-    a.wide = pool > (1ull << 36);
-    a.window = p->window;
-    a.sinks = p->sinks;
-    a.scale_log2 = p->scale * 1.44269504088896341f;
-    a.out = static_cast<uint16_t *>(p->out);
-    a.lse = static_cast<float *>(p->lse);
-    a.counters = static_cast<unsigned *>(p->workspace);
-    static_assert(kAttnCounterBytes == SKINNY_ATTENTION_COUNTER_BYTES, "the header's number");
-    a.partials = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + kAttnCounterBytes);
+    AttentionArgs a;
+    attention_args(p, pool, &a);
     if (launch_decode_attention(a, D, sms, dev, static_cast<cudaStream_t>(stream), ls.pdl) !=
         cudaSuccess) {
         cudaGetLastError();
@@ -1020,15 +1042,19 @@ int skinny_device_error(int device, int *word) {
     }
     if (reduce_word) value |= kErrReduceExchange;
     // The words of the kernels that read indices from device memory.
-    int rope_word = 0, attention_word = 0, logprob_word = 0, lora_word = 0;
+    int rope_word = 0, attention_word = 0, logprob_word = 0, lora_word = 0,
+        part_word = 0, prefix_word = 0;
     if (st == SKINNY_OK && (rope_error_word(&rope_word, true) != cudaSuccess ||
                             attention_error_word(&attention_word, true) != cudaSuccess ||
                             logprob_error_word(&logprob_word, true) != cudaSuccess ||
-                            lora_error_word(&lora_word, true) != cudaSuccess)) {
+                            lora_error_word(&lora_word, true) != cudaSuccess ||
+                            attention_part_error_word(&part_word, true) != cudaSuccess ||
+                            prefix_error_word(&prefix_word, true) != cudaSuccess)) {
         cudaGetLastError();
         st = SKINNY_ERR_DEVICE;
     }
-    if (rope_word || attention_word || logprob_word || lora_word) value |= kErrIndex;
+    if (rope_word || attention_word || logprob_word || lora_word || part_word || (prefix_word & 2)) value |= kErrIndex;
+    if (prefix_word & 1) value |= kErrPrefixWait;
     cudaSetDevice(prev);
     if (word) *word = value;
     if (st != SKINNY_OK) return st;

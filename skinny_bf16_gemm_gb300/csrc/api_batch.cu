@@ -6,6 +6,7 @@
 
 #include "api_internal.h"
 #include "kernels.h"
+#include "prefix_plan.cuh"
 #include "skinny.h"
 
 using namespace skinny;
@@ -80,6 +81,103 @@ int token_logprobs_bf16(const skinny_token_logprobs_args *p, const skinny_launch
     a.top_logprobs = static_cast<float *>(p->top_logprobs);
     a.top_tokens = static_cast<long long *>(p->top_tokens);
     if (launch_token_logprobs(a, d->sms, static_cast<cudaStream_t>(stream), ls.pdl) != cudaSuccess) {
+        cudaGetLastError();
+        return SKINNY_ERR_LAUNCH;
+    }
+    return SKINNY_OK;
+}
+
+size_t skinny_shared_prefix_workspace_bytes(int rows, int q_heads, int kv_heads, int head_dim, int num_sms) {
+    if (rows < 1 || rows > SKINNY_ATTENTION_MAX_ROWS || kv_heads < 1 || q_heads < 1 || q_heads > kMaxHeads ||
+        q_heads % kv_heads != 0 || num_sms < 1 ||
+        (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 192 && head_dim != 256))
+        return 0;
+    return prefix_workspace(rows, q_heads, kv_heads, head_dim, attn_sms(num_sms)).bytes;
+}
+
+int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_args *p,
+                                        const skinny_launch_opts *opts, void *stream) {
+    if (!p || !p->prefix_table || !p->prefix_length) return SKINNY_ERR_NULL;
+    // The rows' own tokens follow the rules of decode_attention_bf16.
+    skinny_decode_attention_args own = {};
+    own.q = p->q;
+    own.q_stride = p->q_stride;
+    own.rows = p->rows;
+    own.q_heads = p->q_heads;
+    own.cache = p->cache;
+    own.block_table = p->block_table;
+    own.table_stride = p->table_stride;
+    own.table_width = p->table_width;
+    own.lengths = p->lengths;
+    own.scale = p->scale;
+    own.out = p->out;
+    own.lse = p->lse;
+    own.workspace = p->workspace;
+    own.workspace_bytes = p->workspace_bytes;
+    size_t pool = 0;
+    int st = check_attention(&own, &pool);
+    if (st) return st;
+    const skinny_kv_cache *c = &p->cache;
+    const int D = c->head_dim, group = p->q_heads / c->kv_heads;
+    const PrefixPlan plan = prefix_plan(p->rows, group, c->kv_heads, D);
+    const long long capacity = static_cast<long long>(p->prefix_width) * c->page_size;
+    if (p->prefix_width < 1 || capacity >= (1ll << 30) ||
+        (capacity + prefix_tokens(D) - 1) / prefix_tokens(D) * plan.units >= (1ll << 31))
+        return SKINNY_ERR_SHAPE;
+    if (!aligned(p->prefix_table, 4) || !aligned(p->prefix_length, 4)) return SKINNY_ERR_ALIGN;
+    const size_t heads = static_cast<size_t>(p->rows) * p->q_heads;
+    const Range in[] = {{p->q, row_span(p->rows, p->q_stride, static_cast<long long>(p->q_heads) * D)},
+                        {c->k, pool}, {c->v, pool},
+                        {p->prefix_table, static_cast<size_t>(p->prefix_width) * 4}, {p->prefix_length, 4},
+                        {p->block_table, (static_cast<size_t>(p->rows - 1) * p->table_stride + p->table_width) * 4},
+                        {p->lengths, static_cast<size_t>(p->rows) * 4}};
+    const Range outs[] = {{p->out, heads * D * 2}, {p->lse, heads * 4}, {p->workspace, p->workspace_bytes}};
+    if (!outputs_clear(in, outs)) return SKINNY_ERR_ALIAS;
+    LaunchSettings ls;
+    int dev;
+    DeviceState *d = nullptr;
+    if ((st = resolve_settings(opts, &ls)) || (st = current_device(&dev)) || (st = device_state(dev, &d))) return st;
+    const int sms = attn_sms(d->sms);
+    const PrefixWorkspace ws = prefix_workspace(p->rows, p->q_heads, c->kv_heads, D, sms);
+    if (p->workspace_bytes < ws.bytes) return SKINNY_ERR_SHAPE;
+    if ((st = check_on_device(in, dev)) || (st = check_on_device(outs, dev))) return st;
+    char *base = static_cast<char *>(p->workspace);
+    AttentionArgs o;
+    attention_args(&own, pool, &o);
+    o.out = nullptr;
+    o.part = reinterpret_cast<float *>(base + ws.own_out);
+    o.lse = reinterpret_cast<float *>(base + ws.own_lse);
+    PrefixArgs a = {};
+    a.q = o.q;
+    a.q_stride = o.q_stride;
+    a.k = o.k;
+    a.v = o.v;
+    a.num_pages = o.num_pages;
+    a.page_size = o.page_size;
+    a.page_shift = o.page_shift;
+    a.page_stride = o.page_stride;
+    a.token_stride = o.token_stride;
+    a.head_stride = o.head_stride;
+    a.table = static_cast<const int *>(p->prefix_table);
+    a.length = static_cast<const int *>(p->prefix_length);
+    a.capacity = static_cast<int>(capacity);
+    a.rows = p->rows;
+    a.q_heads = p->q_heads;
+    a.kv_heads = c->kv_heads;
+    a.group = group;
+    a.blocks = plan.blocks;
+    a.units = plan.units;
+    a.scale_log2 = o.scale_log2;
+    a.slots = reinterpret_cast<float *>(base + ws.slots);
+    a.slot_floats = static_cast<int>(prefix_slot_floats(D, static_cast<long long>(p->rows) * group));
+    a.own_out = o.part;
+    a.own_lse = o.lse;
+    a.out = static_cast<uint16_t *>(p->out);
+    a.lse = static_cast<float *>(p->lse);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_prefix_attention(a, D, sms, dev, s, ls.pdl) != cudaSuccess ||
+        launch_decode_attention_part(o, D, sms, dev, s) != cudaSuccess ||
+        launch_prefix_join(a, D, sms, s) != cudaSuccess) {
         cudaGetLastError();
         return SKINNY_ERR_LAUNCH;
     }

@@ -7,6 +7,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "kernels.h"
 #include "skinny.h"
 
 namespace skinny {
@@ -53,6 +54,10 @@ int resolve_settings(const skinny_launch_opts *opts, LaunchSettings *out);
 
 // A cache's own rules, and the bytes its keys (or values) span.
 int check_cache(const skinny_kv_cache *c, bool write, size_t *span);
+
+// decode_attention_bf16's rules that need no device, and its kernel's arguments.
+int check_attention(const skinny_decode_attention_args *p, size_t *pool);
+void attention_args(const skinny_decode_attention_args *p, size_t pool, AttentionArgs *out);
 
 inline bool overlaps(const void *a, size_t an, const void *b, size_t bn) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);

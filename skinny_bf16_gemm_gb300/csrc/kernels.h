@@ -20,6 +20,7 @@ enum ErrorBits : int {
     kErrUnknown = 64,       // the host-mapped word was set but the device word was not
     kErrReduceExchange = 128,  // reduce: a cluster exchange wait ran out
     kErrIndex = 256,  // a position, slot, length or page index on the device was out of range
+    kErrPrefixWait = 512,  // attention over a shared prefix: a wait ran out
 };
 
 // Low-rank adapters beside a decode GEMM (decode_gemm_bf16_lora): row m's adapter is
@@ -197,6 +198,7 @@ struct AttentionArgs {
     int window, sinks;
     float scale_log2;  // scale * log2(e)
     uint16_t *out;     // [rows][q_heads][head_dim]
+    float *part;       // the FP32 form: [rows][q_heads][head_dim] in place of out
     float *lse;        // [rows][q_heads] or nullptr
     unsigned *counters;  // workspace (attention_plan.cuh): zero between calls
     float *partials;     // workspace: the slots
@@ -204,6 +206,37 @@ struct AttentionArgs {
 cudaError_t launch_decode_attention(const AttentionArgs &a, int head_dim, int num_sms, int device,
                                     cudaStream_t stream, bool pdl);
 cudaError_t attention_error_word(int *value, bool clear);
+
+// Attention over a prefix that all rows share (decode_attention_shared_prefix_bf16): the
+// prefix's partials, the rows' own tokens in FP32, and the join (three launches, in this
+// order; prefix_plan.cuh). Strides in elements.
+struct PrefixArgs {
+    const uint16_t *q;  // rows of q_heads * head_dim
+    long long q_stride;
+    const uint16_t *k, *v;
+    int num_pages, page_size;
+    int page_shift;  // log2(page_size), or -1
+    long long page_stride, token_stride, head_stride;
+    const int *table;   // [capacity / page_size]
+    const int *length;  // one
+    int capacity;       // tokens the table holds
+    int rows, q_heads, kv_heads;
+    int group;          // query heads per key head
+    int blocks, units;  // PrefixPlan
+    float scale_log2;
+    float *slots;       // workspace
+    int slot_floats;
+    const float *own_out, *own_lse;  // workspace: [rows][q_heads][head_dim] and [rows][q_heads]
+    uint16_t *out;
+    float *lse;  // or nullptr
+};
+cudaError_t launch_prefix_attention(const PrefixArgs &a, int head_dim, int num_sms, int device,
+                                    cudaStream_t stream, bool pdl);
+cudaError_t launch_decode_attention_part(const AttentionArgs &a, int head_dim, int num_sms, int device,
+                                         cudaStream_t stream);
+cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t prefix_error_word(int *value, bool clear);
+cudaError_t attention_part_error_word(int *value, bool clear);
 
 // Log probabilities, entropy and top alternatives of rows of logits (token_logprobs_bf16).
 constexpr int kLogprobMaxTop = 32;

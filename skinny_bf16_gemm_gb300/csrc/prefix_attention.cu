@@ -1,0 +1,640 @@
+// Attention of all rows of a decode batch over a prefix that they share, on GB300 (sm_103a):
+// the part of decode_attention_shared_prefix_bf16 that is computed once for all, and the
+// join with the rows' own tokens.
+//
+//   s_ij = scale q_i.k_j,  m_i = max_j s_ij,  l_i = sum_j exp(s_ij - m_i),
+//   o_i = sum_j exp(s_ij - m_i) v_j      over the prefix's tokens j
+// for the query rows i of a key head: every row's heads that share it (prefix_plan.cuh). The
+// prefix is read once for up to 256 of them, so from some 300 on the tensor cores are the
+// bound, below it HBM.
+//
+// A CTA has one or two tiles of 128 query rows in shared memory and a ring of tiles of the
+// prefix's keys and values, in turn. Roles:
+//   warps 0-3 (4-7)   softmax of the first (second) tile: thread = query row = TMEM lane;
+//   4 loader warps    the ring, by 16-byte cp.async with each token's address from the page
+//                     table, so pages of any size and any strides are the same to them, laid
+//                     down in the 128-byte swizzle that the MMA's descriptors name;
+//   1 MMA warp        S = Q K^T from shared memory (both K-major) into tensor memory, and
+//                     O += P V with P in tensor memory (it takes the place of S there) and V
+//                     as it lies, MN-major.
+// The two tiles take turns: while one's softmax runs, the other's products do. With one tile
+// S has two places instead, so that the next S is computed while the softmax runs.
+// The maximum is kept until a score is 2^8 past it; only then O is rescaled, by the softmax
+// threads, in tensor memory. P is rounded to BF16 (to nearest: within 2^-8 of each weight):
+// the roundings of different tokens are independent, so they average out in o as the weights
+// do, and add at most as much as the output's own rounding. A second BF16 term, as
+// decode_attention_bf16 has where the products are free, would cost half the tensor time
+// again. Maxima, sums and o are FP32.
+//
+// Every wait is bounded; one that runs out is recorded, the CTA waits for its own copies and
+// MMAs, frees its tensor memory and ends.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "prefix_plan.cuh"
+#include "ptx.cuh"
+
+namespace skinny {
+namespace {
+
+constexpr float kNoMaximum = -3.402823466e+38f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s
+constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s for work already issued
+constexpr int kErrWait = 1, kErrRange = 2;
+__device__ int g_prefix_err;  // kErrWait: a wait ran out; kErrRange: a length or page out of range
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void cp_async16_or_zeros(uint32_t dst, const void *src, bool full) {
+    const int bytes = full ? 16 : 0;  // 0: the 16 bytes are zero-filled, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Barrier-wide OR of a predicate over the loader's 128 threads (named barrier 3).
+__device__ __forceinline__ bool loader_any(bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\t"
+        "setp.ne.u32 a, %1, 0;\n\t"
+        "bar.red.or.pred b, 3, 128, a;\n\t"
+        "selp.u32 %0, 1, 0, b;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(p))
+        : "memory");
+    return r != 0;
+}
+
+template <int D, int NT>
+struct Shape {
+    static constexpr int kTokens = prefix_tokens(D);
+    static constexpr int kChunks = (D + 63) / 64;               // 128-byte chunks of a row
+    static constexpr int kUnitBytes = kChunks * kTokens * 128;  // a tile's keys, or values
+    static constexpr int kQChunkBytes = kPrefixRows * 128;
+    static constexpr int kQBytes = kChunks * kQChunkBytes;      // one tile of queries
+    static constexpr int kMiscBytes = 2048;
+    static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes);
+    static constexpr int kLag = kStages - 2;  // units whose copies are on their way
+    static_assert(kStages >= 4, "a key and a value tile in use while others are on their way");
+    static constexpr int kRingOffset = NT * kQBytes;
+    static constexpr int kOffsetsOffset = kRingOffset + kStages * kUnitBytes;  // [kTokens] places of a tile
+    static constexpr int kBarOffset = kOffsetsOffset + kTokens * 8;
+    static constexpr int kBars = 2 * kStages + 2 * 4 + 1;
+    static constexpr int kTailOffset = kBarOffset + kBars * 8;  // tensor memory base, abort flag
+    static constexpr int kBytes = kTailOffset + 16;
+    static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
+    static_assert(kDynamicBytes <= 232448, "shared memory of a CTA");
+    static constexpr int kSoftmaxThreads = NT * 128;
+    static constexpr int kLoaderWarp = NT * 4, kMmaWarp = NT * 4 + 4;
+    static constexpr int kThreads = (NT * 4 + 5) * 32;
+    // Tensor memory: S (and P) twice, then O of each tile.
+    static constexpr int kOCol = 2 * kTokens;
+    static constexpr int kTmemCols = kOCol + NT * D <= 256 ? 256 : 512;
+    static_assert(kOCol + NT * D <= 512, "tensor memory");
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_kernel(const PrefixArgs a) {
+    using S = Shape<D, NT>;
+    constexpr int kTokens = S::kTokens, kStages = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = ptx::smem_addr(smem);
+    const uint32_t bar_full = sbase + S::kBarOffset;     // + 8 stage
+    const uint32_t bar_empty = bar_full + 8 * kStages;   // + 8 stage
+    const uint32_t bar_q = bar_empty + 8 * kStages;      // + 8 tile: the queries are there
+    const uint32_t bar_s = bar_q + 16;                   // + 8 place: S is there
+    const uint32_t bar_p = bar_s + 16;                   // + 8 place: P is there
+    const uint32_t bar_pv = bar_p + 16;                  // + 8 tile: O has a step's product
+    const uint32_t bar_drain = bar_pv + 16;
+    volatile uint32_t *tail = reinterpret_cast<volatile uint32_t *>(smem + S::kTailOffset);
+    volatile uint32_t *abort_flag = tail + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 128);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar_q + 8 * i, 128);
+            ptx::mbar_init(bar_s + 8 * i, 1);
+            ptx::mbar_init(bar_p + 8 * i, 128);
+            ptx::mbar_init(bar_pv + 8 * i, 1);
+        }
+        ptx::mbar_init(bar_drain, 1);
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+    }
+    if (warp == S::kMmaWarp) {
+        ptx::tmem_alloc(sbase + S::kTailOffset, S::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = tail[0];
+
+    // The kernels behind this one may start once what is before it is complete: the rows' own
+    // tokens do not wait for the prefix.
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+
+    int length = __ldcg(a.length);
+    if (length < 0 || length > a.capacity) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_prefix_err, kErrRange);
+        length = length < 0 ? 0 : a.capacity;
+    }
+    const int steps = (length + kTokens - 1) / kTokens;  // of a unit
+    const int total = steps * a.units;                   // below 2^31 (host check)
+    const int ctas = prefix_ctas(gridDim.x, total), cta = blockIdx.x;
+    const int x_begin = cta < ctas ? prefix_begin(total, ctas, cta) : 0;
+    const int x_end = cta < ctas ? prefix_begin(total, ctas, cta + 1) : 0;
+    const int query_rows = a.rows * a.group;
+
+    // Wait for the phase of a barrier with this parity; false: aborted.
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = ptx::global_timer_ns();
+        for (uint32_t spin = 1;; ++spin) {
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+            if ((spin & 15u) == 0) {
+                if (*abort_flag) return false;
+                if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
+                    atomicOr(&g_prefix_err, kErrWait);
+                    *abort_flag = 1u;
+                    return false;
+                }
+            }
+        }
+    };
+    auto warp_wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+    // The token of a tile and its page: its element offset within the keys, or -1.
+    auto place = [&](int head, int token) -> long long {
+        if (token >= length) return -1;
+        const int e = a.page_shift >= 0 ? token >> a.page_shift : token / a.page_size;
+        const int page = __ldcg(a.table + e);
+        if (page < 0 || page >= a.num_pages) return -1;
+        return page * a.page_stride + (token - e * a.page_size) * a.token_stride + head * a.head_stride;
+    };
+    // A unit's segment of this CTA's range.
+    struct Segment {
+        int unit, head, q0, tiles, t, n;  // first query row, tiles of query rows, first step, steps
+    };
+    auto segment = [&](int x) {
+        Segment s;
+        s.unit = x / steps;
+        s.head = s.unit / a.blocks;
+        s.q0 = (s.unit - s.head * a.blocks) * NT * kPrefixRows;
+        s.tiles = NT == 2 && query_rows - s.q0 > kPrefixRows ? 2 : 1;
+        s.t = x - s.unit * steps;
+        s.n = min(steps - s.t, x_end - x);
+        return s;
+    };
+
+    if (warp < S::kLoaderWarp) {
+        // ---------------- softmax: thread = query row ----------------
+        const int tile = warp / 4, row = threadIdx.x % 128;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+        const uint32_t o_addr = lanes + S::kOCol + tile * D;
+        const float c = fabsf(a.scale_log2);
+        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // of the queries' signs
+        uint32_t count = 0, segments = 0;  // steps and segments of this tile so far
+        bool ok = true;
+        for (int x = x_begin; ok && x < x_end;) {
+            const Segment seg = segment(x);
+            x += seg.n;
+            if (tile >= seg.tiles) continue;
+            // The queries: 16 bytes at a time, consecutive lanes along a row.
+            constexpr int kRowChunks = D / 8;
+            for (int i = row; i < kPrefixRows * kRowChunks; i += 128) {
+                const int r = i / kRowChunks, ch = i % kRowChunks, at = seg.q0 + tile * kPrefixRows + r;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (at < query_rows) {
+                    const int q_row = at / a.group, g = at - q_row * a.group;
+                    v = __ldcg(reinterpret_cast<const uint4 *>(
+                        a.q + q_row * a.q_stride + static_cast<long long>(seg.head * a.group + g) * D + ch * 8));
+                    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+                }
+                *reinterpret_cast<uint4 *>(smem + tile * S::kQBytes + ch / 8 * S::kQChunkBytes + r * 128 +
+                                           ((ch ^ r) & 7) * 16) = v;
+            }
+            ptx::fence_proxy_async_shared();
+            ptx::mbar_arrive(bar_q + 8 * tile);
+            ++segments;
+
+            float m = kNoMaximum, l = 0.0f;  // in units of log2
+            for (int j = 0; j < seg.n; ++j, ++count) {
+                const int buffer = NT == 2 ? tile : count & 1;
+                const uint32_t parity = NT == 2 ? count & 1 : (count >> 1) & 1;
+                // Which tokens are there, lane by lane.
+                uint32_t there[kTokens / 32];
+                bool all = true;
+#pragma unroll
+                for (int i = 0; i < kTokens / 32; ++i) {
+                    there[i] = __ballot_sync(0xFFFFFFFFu, place(0, (seg.t + j) * kTokens + i * 32 + lane) >= 0);
+                    all &= there[i] == 0xFFFFFFFFu;
+                }
+                if (!(ok = warp_wait(bar_s + 8 * buffer, parity))) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t s_addr = lanes + buffer * kTokens;
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kTokens / 32; ++i) {
+                    uint32_t w[32];
+                    ptx::tmem_ld32(s_addr + i * 32, w);
+                    ptx::tmem_wait32(w);
+                    if (all) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(w[e]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (there[i] >> e & 1) top = fmaxf(top, __uint_as_float(w[e]));
+                    }
+                }
+                // -inf (no score, or only such) times 0 would be NaN.
+                top = top == -INFINITY ? -INFINITY : top * c;
+                if (__any_sync(0xFFFFFFFFu, top > m + 8.0f)) {
+                    const float next = fmaxf(m, top), f = exp2_approx(m - next);
+                    m = next;
+                    l *= f;
+                    if (j > 0) {
+                        if (!(ok = warp_wait(bar_pv + 8 * tile, (count - 1) & 1))) break;
+                        ptx::tc_fence_after_sync();
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 32) {
+                            uint32_t w[32];
+                            ptx::tmem_ld32(o_addr + i, w);
+                            ptx::tmem_wait32(w);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                            ptx::tmem_st32(o_addr + i, w);
+                        }
+                    }
+                }
+                float sum[4] = {};
+#pragma unroll
+                for (int i = 0; i < kTokens / 32; ++i) {
+                    uint32_t w[32], p[16];
+                    ptx::tmem_ld32(s_addr + i * 32, w);
+                    ptx::tmem_wait32(w);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float v = exp2_approx(fmaf(__uint_as_float(w[e]), c, -m));
+                        if (!all && !(there[i] >> e & 1)) v = 0.0f;
+                        sum[e & 3] += v;
+                        w[e] = __float_as_uint(v);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        p[e] = pack_bf16(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+                    ptx::tmem_st16(s_addr + i * 16, p);  // over scores that are read already
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(bar_p + 8 * buffer);
+            }
+            if (!ok) break;
+            if (!(ok = warp_wait(bar_pv + 8 * tile, (count - 1) & 1))) break;
+            ptx::tc_fence_after_sync();
+            // This segment's partial.
+            const int at = tile * kPrefixRows + row;
+            float *slot = a.slots + static_cast<size_t>(cta + seg.unit) * a.slot_floats;
+            float *to = slot + static_cast<size_t>(at) * D;
+            const bool real = seg.q0 + at < query_rows;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+                uint32_t w[32];
+                ptx::tmem_ld32(o_addr + i, w);
+                ptx::tmem_wait32(w);
+                if (real)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        __stcg(reinterpret_cast<uint4 *>(to + i) + e, make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
+            }
+            if (real) {
+                __stcg(slot + NT * kPrefixRows * D + at, m);
+                __stcg(slot + NT * kPrefixRows * (D + 1) + at, l);
+            }
+            ptx::tc_fence_before_sync();  // O is read: before the next segment's arrival
+        }
+    } else if (warp < S::kMmaWarp) {
+        // ---------------- loader ----------------
+        const int tid = threadIdx.x - S::kSoftmaxThreads;
+        long long *places = reinterpret_cast<long long *>(smem + S::kOffsetsOffset);
+        constexpr int kRowChunks = D / 8, kCopies = kTokens * kRowChunks / 128;
+        static_assert(kTokens * kRowChunks % 128 == 0, "whole rounds of copies");
+        int unit = 0;  // of the ring, so far
+        bool ok = true;
+        auto publish = [&](int u) {  // a unit whose copies are complete
+            ptx::fence_proxy_async_shared();
+            ptx::mbar_arrive(bar_full + 8 * (u % kStages));
+        };
+        int head = 0, t = 0;
+        if (x_begin < x_end) {
+            const Segment seg = segment(x_begin);
+            head = seg.head;
+            t = seg.t;
+        }
+        long long next = tid < kTokens && x_begin < x_end ? place(head, t * kTokens + tid) : -1;
+        int segment_unit = x_begin < x_end ? x_begin / steps : 0;
+        for (int x = x_begin; ok && x < x_end; ++x) {
+            ptx::named_barrier_sync(2, 128);  // the places of the tile before are read
+            if (tid < kTokens) {
+                if (next < 0 && t * kTokens + tid < length) atomicOr(&g_prefix_err, kErrRange);
+                places[tid] = next;  // read behind the barrier of the unit's wait
+            }
+            if (++t == steps) {
+                t = 0;
+                head = ++segment_unit / a.blocks;
+            }
+            if (tid < kTokens && x + 1 < x_end) next = place(head, t * kTokens + tid);
+            for (int kv = 0; kv < 2; ++kv, ++unit) {
+                const int s = unit % kStages;
+                // The first round finds the stages free.
+                if (!(ok = !loader_any(!wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1)))) break;
+                const uint16_t *from = kv == 0 ? a.k : a.v;
+                const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const int id = i * 128 + tid, r = id / kRowChunks, ch = id % kRowChunks;
+                    const long long at = places[r];
+                    cp_async16_or_zeros(to + ch / 8 * (kTokens * 128) + r * 128 + ((ch ^ r) & 7) * 16,
+                                        from + (at < 0 ? 0 : at) + ch * 8, at >= 0);
+                }
+                cp_async_commit();
+                if (unit >= S::kLag) {
+                    cp_async_wait<S::kLag>();
+                    publish(unit - S::kLag);
+                }
+            }
+        }
+        cp_async_wait<0>();
+        if (ok)
+            for (int u = max(0, unit - S::kLag); u < unit; ++u) publish(u);
+    } else if (lane == 0) {
+        // ---------------- MMA issuer ----------------
+        constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kPrefixRows, kTokens);
+        constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(kPrefixRows, D) | ptx::kIdescBMnMajor;
+        int unit = 0;
+        uint32_t count[2] = {}, segments[2] = {};  // steps whose S was issued, and segments, by tile
+        bool ok = true;
+        auto full = [&](int u) {
+            if (!wait(bar_full + 8 * (u % kStages), (u / kStages) & 1)) return false;
+            ptx::tc_fence_after_sync();
+            return true;
+        };
+        auto scores = [&](int i, int buffer, int u) {  // S of tile i with the keys of unit u
+            const uint32_t q = sbase + i * S::kQBytes, k = sbase + S::kRingOffset + u % kStages * S::kUnitBytes;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+                ptx::mma_bf16(tmem + buffer * kTokens,
+                              ptx::smem_desc_sw128_kmajor(q + s / 4 * S::kQChunkBytes + s % 4 * 32),
+                              ptx::smem_desc_sw128_kmajor(k + s / 4 * (kTokens * 128) + s % 4 * 32), idesc_s, s > 0);
+            ptx::mma_commit(bar_s + 8 * buffer);
+        };
+        auto values = [&](int i, int buffer, int u, bool first) {  // O of tile i += P V of unit u
+            const uint32_t v = sbase + S::kRingOffset + u % kStages * S::kUnitBytes;
+#pragma unroll
+            for (int s = 0; s < kTokens / 16; ++s)
+                ptx::mma_bf16_tmem_a(tmem + S::kOCol + i * D, tmem + buffer * kTokens + s * 8,
+                                     ptx::smem_desc_sw128_mnmajor(v + s * 2048, kTokens * 128), idesc_o,
+                                     s > 0 || !first);
+            ptx::mma_commit(bar_pv + 8 * i);
+        };
+        for (int x = x_begin; ok && x < x_end;) {
+            const Segment seg = segment(x);
+            x += seg.n;
+            for (int i = 0; ok && i < seg.tiles; ++i) ok = wait(bar_q + 8 * i, segments[i]++ & 1);
+            if (!ok || !(ok = full(unit))) break;
+            if constexpr (NT == 2) {
+                for (int i = 0; i < seg.tiles; ++i) scores(i, i, unit);
+                ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+                ++unit;
+                for (int j = 0; ok && j < seg.n; ++j) {
+                    const bool more = j + 1 < seg.n;
+                    if (!(ok = full(unit))) break;
+                    for (int i = 0; i < seg.tiles; ++i) {
+                        const uint32_t parity = count[i]++ & 1;
+                        if (!(ok = wait(bar_p + 8 * i, parity))) break;
+                        ptx::tc_fence_after_sync();
+                        values(i, i, unit, j == 0);
+                        if (i == seg.tiles - 1) ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+                        if (!more) continue;
+                        // The next S goes where P is: its product must be complete.
+                        if (!(ok = full(unit + 1)) || !(ok = wait(bar_pv + 8 * i, parity))) break;
+                        scores(i, i, unit + 1);
+                        if (i == seg.tiles - 1) ptx::mma_commit(bar_empty + 8 * ((unit + 1) % kStages));
+                    }
+                    unit += more ? 2 : 1;
+                }
+            } else {
+                scores(0, count[0] & 1, unit);
+                ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+                ++unit;
+                for (int j = 0; ok && j < seg.n; ++j, ++count[0]) {
+                    const bool more = j + 1 < seg.n;
+                    const uint32_t n = count[0];
+                    if (more) {
+                        // The next S goes where the last step's P was.
+                        if (!(ok = full(unit + 1)) || (j > 0 && !(ok = wait(bar_pv, (n - 1) & 1)))) break;
+                        scores(0, (n + 1) & 1, unit + 1);
+                        ptx::mma_commit(bar_empty + 8 * ((unit + 1) % kStages));
+                    }
+                    if (!(ok = full(unit)) || !(ok = wait(bar_p + 8 * (n & 1), (n >> 1) & 1))) break;
+                    ptx::tc_fence_after_sync();
+                    values(0, n & 1, unit, j == 0);
+                    ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+                    unit += more ? 2 : 1;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (*abort_flag) {
+        // Nothing may still read this CTA's shared or tensor memory when it ends.
+        if (warp == S::kMmaWarp && lane == 0) {
+            ptx::mma_commit(bar_drain);
+            const uint64_t t0 = ptx::global_timer_ns();
+            while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::global_timer_ns() - t0 < kDrainLimitNs) {
+            }
+        }
+        __syncthreads();
+    }
+    if (warp == S::kMmaWarp) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+// ---- the join ----
+// One warp for one head of one row: the prefix's partials of its query row, in order, and the
+// row's own tokens' result. Read once each, all in L2.
+constexpr int kJoinWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const PrefixArgs a, int grid) {
+    constexpr int kValues = D / 32, kAhead = D <= 128 ? 8 : 4;
+    const int lane = threadIdx.x % 32;
+    const int job = blockIdx.x * kJoinWarps + threadIdx.x / 32;
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    if (job >= a.rows * a.q_heads) return;
+    const int row = job / a.q_heads, h = job - row * a.q_heads;
+    const int head = h / a.group, at = row * a.group + h - head * a.group;  // query row of the key head
+    const int length = min(max(__ldcg(a.length), 0), a.capacity);
+    const int tokens = prefix_tokens(D), per = kPrefixRows * prefix_tiles(D, static_cast<long long>(a.rows) * a.group);
+    const int steps = (length + tokens - 1) / tokens, total = steps * a.units;
+    const int ctas = prefix_ctas(grid, total);
+    const int unit = head * a.blocks + at / per, in_unit = at % per;
+    const int first = total > 0 ? prefix_owner(total, ctas, unit * steps) : 0;
+    const int parts = total > 0 ? prefix_owner(total, ctas, unit * steps + steps - 1) - first + 1 : 0;
+    const float *slots = a.slots + static_cast<size_t>(first + unit) * a.slot_floats;
+    const float *maxima = slots + static_cast<size_t>(per) * D + in_unit, *sums = maxima + per;
+    const float *values = slots + static_cast<size_t>(in_unit) * D + lane;
+
+    const float own = __ldcg(a.own_lse + job) * kLog2e;  // its sum of weights is 2^own
+    float o[kValues], top = fmaxf(own, kNoMaximum);
+    for (int s = lane; s < parts; s += 32) top = fmaxf(top, __ldcg(maxima + s * a.slot_floats));
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+    float total_weight = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kValues; ++e) o[e] = 0.0f;
+    if (own != -INFINITY) {
+        const float w = exp2_approx(own - top);
+        total_weight = w;
+#pragma unroll
+        for (int e = 0; e < kValues; ++e) o[e] = w * __ldcg(a.own_out + static_cast<size_t>(job) * D + lane + e * 32);
+    }
+    for (int s0 = 0; s0 < parts; s0 += kAhead) {
+        float m[kAhead], l[kAhead], v[kAhead][kValues];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (s0 + u >= parts) break;
+            m[u] = __ldcg(maxima + (s0 + u) * a.slot_floats);
+            l[u] = __ldcg(sums + (s0 + u) * a.slot_floats);
+#pragma unroll
+            for (int e = 0; e < kValues; ++e) v[u][e] = __ldcg(values + (s0 + u) * a.slot_floats + e * 32);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (s0 + u >= parts) break;
+            const float w = exp2_approx(m[u] - top);
+            total_weight += w * l[u];
+#pragma unroll
+            for (int e = 0; e < kValues; ++e) o[e] += w * v[u][e];
+        }
+    }
+    const float inv = total_weight == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_weight);
+#pragma unroll
+    for (int e = 0; e < kValues; ++e)
+        a.out[static_cast<size_t>(job) * D + lane + e * 32] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * inv));
+    if (a.lse != nullptr && lane == 0)
+        a.lse[job] = total_weight > 0.0f || total_weight != total_weight ? (top + log2f(total_weight)) * kLn2 : -INFINITY;
+}
+
+template <int D, int NT>
+cudaError_t launch_prefix(const PrefixArgs &a, int grid, int device, cudaStream_t stream, bool pdl) {
+    using S = Shape<D, NT>;
+    static bool configured[64] = {};
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    if (!configured[device]) {
+        cudaError_t e = cudaFuncSetAttribute(prefix_attention_kernel<D, NT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, S::kDynamicBytes);
+        if (e != cudaSuccess) return e;
+        configured[device] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(S::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = S::kDynamicBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<D, NT>, a);
+}
+
+template <int D>
+cudaError_t launch_join(const PrefixArgs &a, int grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    const int jobs = a.rows * a.q_heads;
+    cfg.gridDim = dim3((jobs + kJoinWarps - 1) / kJoinWarps, 1, 1);
+    cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;  // behind the library's own kernels
+    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<D>, a, grid);
+}
+
+// CTAs of the prefix's kernel: no more than the table could ever hold steps.
+int grid_of(const PrefixArgs &a, int head_dim, int num_sms) {
+    const long long tokens = prefix_tokens(head_dim);
+    return static_cast<int>(std::min<long long>(num_sms, (a.capacity + tokens - 1) / tokens * a.units));
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_attention(const PrefixArgs &a, int head_dim, int num_sms, int device,
+                                    cudaStream_t stream, bool pdl) {
+    const int grid = grid_of(a, head_dim, num_sms);
+    const bool two = prefix_tiles(head_dim, static_cast<long long>(a.rows) * a.group) == 2;
+    switch (head_dim) {
+        case 64: return two ? launch_prefix<64, 2>(a, grid, device, stream, pdl) : launch_prefix<64, 1>(a, grid, device, stream, pdl);
+        case 96: return two ? launch_prefix<96, 2>(a, grid, device, stream, pdl) : launch_prefix<96, 1>(a, grid, device, stream, pdl);
+        case 128: return two ? launch_prefix<128, 2>(a, grid, device, stream, pdl) : launch_prefix<128, 1>(a, grid, device, stream, pdl);
+        case 192: return launch_prefix<192, 1>(a, grid, device, stream, pdl);
+        case 256: return launch_prefix<256, 1>(a, grid, device, stream, pdl);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream) {
+    const int grid = grid_of(a, head_dim, num_sms);
+    switch (head_dim) {
+        case 64: return launch_join<64>(a, grid, stream);
+        case 96: return launch_join<96>(a, grid, stream);
+        case 128: return launch_join<128>(a, grid, stream);
+        case 192: return launch_join<192>(a, grid, stream);
+        case 256: return launch_join<256>(a, grid, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t prefix_error_word(int *value, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_prefix_err, sizeof(int));
+    if (e != cudaSuccess || !clear || *value == 0) return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_prefix_err, &zero, sizeof(int));
+}
+
+}  // namespace skinny
