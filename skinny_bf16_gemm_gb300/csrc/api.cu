@@ -173,6 +173,29 @@ int encode_2d(EncodeTiledFn enc, CUtensorMap *map, const void *base, uint64_t ro
     return r == CUDA_SUCCESS ? SKINNY_OK : SKINNY_ERR_LAUNCH;
 }
 
+}  // namespace
+
+bool encode_cache_map(CUtensorMap *map, const void *base, const skinny_kv_cache *c, int box_rows) {
+    EncodeTiledFn enc;
+    if (encoder(&enc) != SKINNY_OK) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
+                                static_cast<cuuint64_t>(c->kv_heads), static_cast<cuuint64_t>(c->num_pages)};
+    // The stride of an axis of one element says nothing, and may be 0; one of 0 elsewhere has
+    // no map.
+    const long long given[3] = {c->token_stride, c->head_stride, c->page_stride};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(given[i]) * 2;
+    for (cuuint64_t st : strides)
+        if (st == 0 || st >= (1ull << 40)) return false;
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estride,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
 int gemm_shape_ok(int M, int N, int K) {
     if (M < 1 || M > kMaxM || N < 1 || K < 8 || (K % 8) != 0) return SKINNY_ERR_SHAPE;
     // The kernel counts 128 x 64 weight blocks in 32-bit integers (a weight of

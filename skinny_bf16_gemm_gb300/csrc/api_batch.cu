@@ -175,7 +175,11 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     a.out = static_cast<uint16_t *>(p->out);
     a.lse = static_cast<float *>(p->lse);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_prefix_attention(a, D, sms, dev, s, ls.pdl) != cudaSuccess ||
+    alignas(64) CUtensorMap k_map = {}, v_map = {};
+    a.box_rows = prefix_box_rows(c->page_size, D);
+    if (a.box_rows > 0 && !(encode_cache_map(&k_map, c->k, c, a.box_rows) && encode_cache_map(&v_map, c->v, c, a.box_rows)))
+        a.box_rows = 0;
+    if (launch_prefix_attention(k_map, v_map, a, D, sms, dev, s, ls.pdl) != cudaSuccess ||
         launch_decode_attention_part(o, D, sms, dev, s) != cudaSuccess ||
         launch_prefix_join(a, D, sms, s) != cudaSuccess) {
         cudaGetLastError();

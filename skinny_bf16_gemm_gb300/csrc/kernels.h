@@ -224,14 +224,18 @@ struct PrefixArgs {
     int group;          // query heads per key head
     int blocks, units;  // PrefixPlan
     float scale_log2;
+    int box_rows;       // tokens of a tensor map's box, or 0: no maps
     float *slots;       // workspace
     int slot_floats;
     const float *own_out, *own_lse;  // workspace: [rows][q_heads][head_dim] and [rows][q_heads]
     uint16_t *out;
     float *lse;  // or nullptr
 };
-cudaError_t launch_prefix_attention(const PrefixArgs &a, int head_dim, int num_sms, int device,
-                                    cudaStream_t stream, bool pdl);
+// Tokens of a TMA box of the keys and values: 64 of head_dim by so many tokens of one page, or
+// 0 if boxes will not do (tiles must be whole boxes, and a box whole swizzle atoms).
+int prefix_box_rows(int page_size, int head_dim);
+cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
+                                    int head_dim, int num_sms, int device, cudaStream_t stream, bool pdl);
 cudaError_t launch_decode_attention_part(const AttentionArgs &a, int head_dim, int num_sms, int device,
                                          cudaStream_t stream);
 cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream);

@@ -11,9 +11,11 @@
 // A CTA has one or two tiles of 128 query rows in shared memory and a ring of tiles of the
 // prefix's keys and values, in turn. Roles:
 //   warps 0-3 (4-7)   softmax of the first (second) tile: thread = query row = TMEM lane;
-//   4 loader warps    the ring, by 16-byte cp.async with each token's address from the page
-//                     table, so pages of any size and any strides are the same to them, laid
-//                     down in the 128-byte swizzle that the MMA's descriptors name;
+//   2 loader warps    the ring, in the 128-byte swizzle that the MMA's descriptors name: by TMA
+//                     boxes of as many tokens as pages and tiles both are multiples of, one
+//                     lane a box, or, for pages of no multiple of 8 and for a tile that the
+//                     prefix ends in (what is behind its end must come out as zeros), by
+//                     16-byte cp.async with each token's address;
 //   1 MMA warp        S = Q K^T from shared memory (both K-major) into tensor memory, and
 //                     O += P V with P in tensor memory (it takes the place of S there) and V
 //                     as it lies, MN-major.
@@ -69,13 +71,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-// Barrier-wide OR of a predicate over the loader's 128 threads (named barrier 3).
+constexpr int kLoaders = 64;    // threads
+constexpr int kMaskRing = 16;   // tiles whose masks are kept: more than the loader is ahead
+
+// Barrier-wide OR of a predicate over the loader's threads (named barrier 3).
 __device__ __forceinline__ bool loader_any(bool p) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred a, b;\n\t"
         "setp.ne.u32 a, %1, 0;\n\t"
-        "bar.red.or.pred b, 3, 128, a;\n\t"
+        "bar.red.or.pred b, 3, 64, a;\n\t"
         "selp.u32 %0, 1, 0, b;\n\t}"
         : "=r"(r)
         : "r"(static_cast<uint32_t>(p))
@@ -92,19 +97,25 @@ struct Shape {
     static constexpr int kQBytes = kChunks * kQChunkBytes;      // one tile of queries
     static constexpr int kMiscBytes = 2048;
     static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes);
-    static constexpr int kLag = kStages - 2;  // units whose copies are on their way
+    // cp.async: units whose copies are on their way, while as many are there for the MMAs.
+    static constexpr int kLag = kStages / 2;
     static_assert(kStages >= 4, "a key and a value tile in use while others are on their way");
     static constexpr int kRingOffset = NT * kQBytes;
-    static constexpr int kOffsetsOffset = kRingOffset + kStages * kUnitBytes;  // [kTokens] places of a tile
-    static constexpr int kBarOffset = kOffsetsOffset + kTokens * 8;
+    static constexpr int kPlacesOffset = kRingOffset + kStages * kUnitBytes;  // [kTokens] of a tile
+    static constexpr int kMaskWords = kTokens / 32;
+    static constexpr int kMaskOffset = kPlacesOffset + kTokens * 8;  // [kMaskRing][kMaskWords]
+    static constexpr int kBarOffset = kMaskOffset + kMaskRing * kMaskWords * 4;
     static constexpr int kBars = 2 * kStages + 2 * 4 + 1;
     static constexpr int kTailOffset = kBarOffset + kBars * 8;  // tensor memory base, abort flag
     static constexpr int kBytes = kTailOffset + 16;
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
     static_assert(kDynamicBytes <= 232448, "shared memory of a CTA");
-    static constexpr int kSoftmaxThreads = NT * 128;
-    static constexpr int kLoaderWarp = NT * 4, kMmaWarp = NT * 4 + 4;
-    static constexpr int kThreads = (NT * 4 + 5) * 32;
+    static constexpr int kLoaderWarp = NT * 4, kMmaWarp = NT * 4 + 2;
+    static constexpr int kThreads = (NT * 4 + 4) * 32;  // one warp of the last four is idle
+    // Registers a thread: a row of scores is kept in them. Three groups of four warps get
+    // 168 each at the launch; the softmax takes what the others give.
+    static constexpr int kSoftmaxRegisters = 200, kOtherRegisters = 104;
+    static_assert(2 * kSoftmaxRegisters + kOtherRegisters <= 3 * 168, "registers of the block");
     // Tensor memory: S (and P) twice, then O of each tile.
     static constexpr int kOCol = 2 * kTokens;
     static constexpr int kTmemCols = kOCol + NT * D <= 256 ? 256 : 512;
@@ -112,7 +123,9 @@ struct Shape {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_kernel(const PrefixArgs a) {
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
+    prefix_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                            const PrefixArgs a) {
     using S = Shape<D, NT>;
     constexpr int kTokens = S::kTokens, kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -132,12 +145,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_ke
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 128);
+            ptx::mbar_init(bar_full + 8 * s, kLoaders);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar_q + 8 * i, 128);
-            ptx::mbar_init(bar_s + 8 * i, 1);
+            ptx::mbar_init(bar_s + 8 * i, 2);  // the products, and the issuer (the mask is there)
             ptx::mbar_init(bar_p + 8 * i, 128);
             ptx::mbar_init(bar_pv + 8 * i, 1);
         }
@@ -211,18 +224,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_ke
         return s;
     };
 
+    int issued = 0;  // units that the loader has begun
     if (warp < S::kLoaderWarp) {
         // ---------------- softmax: thread = query row ----------------
+        if constexpr (NT == 2) ptx::take_registers<S::kSoftmaxRegisters>();
         const int tile = warp / 4, row = threadIdx.x % 128;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
         const uint32_t o_addr = lanes + S::kOCol + tile * D;
         const float c = fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // of the queries' signs
-        uint32_t count = 0, segments = 0;  // steps and segments of this tile so far
+        const uint32_t *masks = reinterpret_cast<const uint32_t *>(smem + S::kMaskOffset);
+        uint32_t count = 0;       // steps of this tile of query rows so far
+        uint32_t tile_count = 0;  // the CTA's steps before this segment
         bool ok = true;
         for (int x = x_begin; ok && x < x_end;) {
             const Segment seg = segment(x);
             x += seg.n;
+            tile_count = x - seg.n - x_begin;
             if (tile >= seg.tiles) continue;
             // The queries: 16 bytes at a time, consecutive lanes along a row.
             constexpr int kRowChunks = D / 8;
@@ -240,38 +258,31 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_ke
             }
             ptx::fence_proxy_async_shared();
             ptx::mbar_arrive(bar_q + 8 * tile);
-            ++segments;
 
             float m = kNoMaximum, l = 0.0f;  // in units of log2
             for (int j = 0; j < seg.n; ++j, ++count) {
                 const int buffer = NT == 2 ? tile : count & 1;
                 const uint32_t parity = NT == 2 ? count & 1 : (count >> 1) & 1;
-                // Which tokens are there, lane by lane.
-                uint32_t there[kTokens / 32];
-                bool all = true;
-#pragma unroll
-                for (int i = 0; i < kTokens / 32; ++i) {
-                    there[i] = __ballot_sync(0xFFFFFFFFu, place(0, (seg.t + j) * kTokens + i * 32 + lane) >= 0);
-                    all &= there[i] == 0xFFFFFFFFu;
-                }
                 if (!(ok = warp_wait(bar_s + 8 * buffer, parity))) break;
                 ptx::tc_fence_after_sync();
                 const uint32_t s_addr = lanes + buffer * kTokens;
-                float top = -INFINITY;
+                uint32_t w[kTokens];
+                ptx::tmem_ld_now(s_addr, w);
+                const uint32_t *mask = masks + (tile_count + j) % kMaskRing * S::kMaskWords;
+                bool all = true;
 #pragma unroll
-                for (int i = 0; i < kTokens / 32; ++i) {
-                    uint32_t w[32];
-                    ptx::tmem_ld32(s_addr + i * 32, w);
-                    ptx::tmem_wait32(w);
-                    if (all) {
+                for (int i = 0; i < kTokens / 32; ++i) all &= mask[i] == 0xFFFFFFFFu;
+                if (!all) {  // a NaN stays out of the maximum, and its weight is made 0 below
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(w[e]));
-                    } else {
+                    for (int i = 0; i < kTokens / 32; ++i)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (there[i] >> e & 1) top = fmaxf(top, __uint_as_float(w[e]));
-                    }
+                            if (!(mask[i] >> e & 1)) w[i * 32 + e] = 0x7FC00000u;
                 }
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < kTokens; ++e) tops[e & 3] = fmaxf(tops[e & 3], __uint_as_float(w[e]));
+                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 // -inf (no score, or only such) times 0 would be NaN.
                 top = top == -INFINITY ? -INFINITY : top * c;
                 if (__any_sync(0xFFFFFFFFu, top > m + 8.0f)) {
@@ -283,34 +294,36 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_ke
                         ptx::tc_fence_after_sync();
 #pragma unroll 1
                         for (int i = 0; i < D; i += 32) {
-                            uint32_t w[32];
-                            ptx::tmem_ld32(o_addr + i, w);
-                            ptx::tmem_wait32(w);
+                            uint32_t o[32];
+                            ptx::tmem_ld_now(o_addr + i, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-                            ptx::tmem_st32(o_addr + i, w);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            ptx::tmem_st32(o_addr + i, o);
                         }
                     }
                 }
                 float sum[4] = {};
 #pragma unroll
                 for (int i = 0; i < kTokens / 32; ++i) {
-                    uint32_t w[32], p[16];
-                    ptx::tmem_ld32(s_addr + i * 32, w);
-                    ptx::tmem_wait32(w);
+                    float v[32];
+                    uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float v = exp2_approx(fmaf(__uint_as_float(w[e]), c, -m));
-                        if (!all && !(there[i] >> e & 1)) v = 0.0f;
-                        sum[e & 3] += v;
-                        w[e] = __float_as_uint(v);
+                    for (int e = 0; e < 32; ++e) v[e] = exp2_approx(fmaf(__uint_as_float(w[i * 32 + e]), c, -m));
+                    if (!all) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(mask[i] >> e & 1)) v[e] = 0.0f;
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        p[e] = pack_bf16(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
-                    ptx::tmem_st16(s_addr + i * 16, p);  // over scores that are read already
+                    for (int e = 0; e < 32; ++e) sum[e & 3] += v[e];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                    ptx::tmem_st16(s_addr + i * 16, p);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                // Every phase of bar_pv is waited for in its turn, or a later wait could take the one
+                // before for its own. With two tiles S(j) came after the product of step j - 1.
+                if (NT == 1 && j > 0 && !(ok = warp_wait(bar_pv, (count - 1) & 1))) break;
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(bar_p + 8 * buffer);
@@ -326,8 +339,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_ke
 #pragma unroll 1
             for (int i = 0; i < D; i += 32) {
                 uint32_t w[32];
-                ptx::tmem_ld32(o_addr + i, w);
-                ptx::tmem_wait32(w);
+                ptx::tmem_ld_now(o_addr + i, w);
                 if (real)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -341,59 +353,125 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_ke
         }
     } else if (warp < S::kMmaWarp) {
         // ---------------- loader ----------------
-        const int tid = threadIdx.x - S::kSoftmaxThreads;
-        long long *places = reinterpret_cast<long long *>(smem + S::kOffsetsOffset);
-        constexpr int kRowChunks = D / 8, kCopies = kTokens * kRowChunks / 128;
-        static_assert(kTokens * kRowChunks % 128 == 0, "whole rounds of copies");
+        if constexpr (NT == 2) ptx::give_registers<S::kOtherRegisters>();
+        const int tid = threadIdx.x - S::kLoaderWarp * 32;
+        long long *places = reinterpret_cast<long long *>(smem + S::kPlacesOffset);
+        uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::kMaskOffset);
+        constexpr int kRowChunks = D / 8, kCopies = kTokens * kRowChunks / kLoaders;
+        constexpr int kMine = kTokens / kLoaders;  // tokens whose places a thread looks up
+        static_assert(kTokens * kRowChunks % kLoaders == 0 && kTokens % kLoaders == 0, "whole rounds");
         int unit = 0;  // of the ring, so far
         bool ok = true;
         auto publish = [&](int u) {  // a unit whose copies are complete
             ptx::fence_proxy_async_shared();
             ptx::mbar_arrive(bar_full + 8 * (u % kStages));
         };
-        int head = 0, t = 0;
+        int segment_unit = 0, head = 0, t = 0;
+        // A tile's boxes: lane = (box, chunk). No more than a warp has lanes.
+        static_assert(kTokens / 8 * S::kChunks <= 32, "a lane a box");
+        const int boxes = a.box_rows > 0 ? kTokens / a.box_rows : 0;
+        const int box = lane / S::kChunks, chunk = lane - box * S::kChunks;
+        auto boxed = [&](int tile) { return boxes > 0 && (tile + 1) * kTokens <= length; };
+        // The next tile's places: of a box (page and token within it) or of tokens.
+        long long next[kMine];
+        int next_page = 0, next_token = 0;
+        auto look_up = [&]() {
+            if (boxed(t)) {
+                if (box >= boxes) return;
+                const int token = t * kTokens + box * a.box_rows;
+                const int e = a.page_shift >= 0 ? token >> a.page_shift : token / a.page_size;
+                next_page = __ldcg(a.table + e);
+                next_token = token - e * a.page_size;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) next[i] = place(head, t * kTokens + i * kLoaders + tid);
+            }
+        };
         if (x_begin < x_end) {
-            const Segment seg = segment(x_begin);
-            head = seg.head;
-            t = seg.t;
+            segment_unit = x_begin / steps;
+            head = segment_unit / a.blocks;
+            t = x_begin - segment_unit * steps;
+            look_up();
         }
-        long long next = tid < kTokens && x_begin < x_end ? place(head, t * kTokens + tid) : -1;
-        int segment_unit = x_begin < x_end ? x_begin / steps : 0;
         for (int x = x_begin; ok && x < x_end; ++x) {
-            ptx::named_barrier_sync(2, 128);  // the places of the tile before are read
-            if (tid < kTokens) {
-                if (next < 0 && t * kTokens + tid < length) atomicOr(&g_prefix_err, kErrRange);
-                places[tid] = next;  // read behind the barrier of the unit's wait
+            uint32_t *mask = masks + (x - x_begin) % kMaskRing * S::kMaskWords;
+            const bool by_box = boxed(t);
+            const int this_head = head;
+            int page = next_page;
+            const int token = next_token;
+            if (by_box) {
+                const bool there = box >= boxes || (page >= 0 && page < a.num_pages);
+                const uint32_t good = __ballot_sync(0xFFFFFFFFu, there);
+                if (!there) {
+                    atomicOr(&g_prefix_err, kErrRange);
+                    page = a.num_pages;  // past the end: zeros
+                }
+                if (tid < S::kMaskWords) {
+                    uint32_t bits = 0xFFFFFFFFu;
+                    if (good != 0xFFFFFFFFu) {
+                        bits = 0;
+                        for (int e = 0; e < 32; ++e)
+                            bits |= (good >> ((tid * 32 + e) / a.box_rows * S::kChunks) & 1u) << e;
+                    }
+                    mask[tid] = bits;
+                }
+            } else {
+                ptx::named_barrier_sync(2, kLoaders);  // the places of the tile before are read
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    if (next[i] < 0 && t * kTokens + i * kLoaders + tid < length) atomicOr(&g_prefix_err, kErrRange);
+                    places[i * kLoaders + tid] = next[i];  // read behind the barrier of the unit's wait
+                    const uint32_t there = __ballot_sync(0xFFFFFFFFu, next[i] >= 0);
+                    if (lane == 0) mask[i * (kLoaders / 32) + tid / 32] = there;
+                }
             }
             if (++t == steps) {
                 t = 0;
                 head = ++segment_unit / a.blocks;
             }
-            if (tid < kTokens && x + 1 < x_end) next = place(head, t * kTokens + tid);
+            if (x + 1 < x_end) look_up();
             for (int kv = 0; kv < 2; ++kv, ++unit) {
                 const int s = unit % kStages;
                 // The first round finds the stages free.
                 if (!(ok = !loader_any(!wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1)))) break;
-                const uint16_t *from = kv == 0 ? a.k : a.v;
                 const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
-#pragma unroll
+                if (by_box) {
+                    if (tid == 0)
+                        ptx::mbar_arrive_expect_tx(bar_full + 8 * s, S::kUnitBytes);
+                    else
+                        ptx::mbar_arrive(bar_full + 8 * s);
+                    __syncwarp();
+                    if (tid < 32 && box < boxes)
+                        ptx::tma_load_4d(to + chunk * (kTokens * 128) + box * a.box_rows * 128, kv == 0 ? &k_map : &v_map,
+                                         bar_full + 8 * s, chunk * 64, token, this_head, page);
+                    continue;
+                }
+                const uint16_t *from = kv == 0 ? a.k : a.v;
+#pragma unroll 8
                 for (int i = 0; i < kCopies; ++i) {
-                    const int id = i * 128 + tid, r = id / kRowChunks, ch = id % kRowChunks;
+                    const int id = i * kLoaders + tid, r = id / kRowChunks, ch = id % kRowChunks;
                     const long long at = places[r];
                     cp_async16_or_zeros(to + ch / 8 * (kTokens * 128) + r * 128 + ((ch ^ r) & 7) * 16,
                                         from + (at < 0 ? 0 : at) + ch * 8, at >= 0);
                 }
                 cp_async_commit();
-                if (unit >= S::kLag) {
+                if (boxes > 0) {  // the tile that a unit ends with
+                    cp_async_wait<0>();
+                    publish(unit);
+                } else if (unit >= S::kLag) {
                     cp_async_wait<S::kLag>();
                     publish(unit - S::kLag);
                 }
             }
         }
+        issued = boxes > 0 ? unit : 0;
         cp_async_wait<0>();
-        if (ok)
+        if (ok && boxes == 0)
             for (int u = max(0, unit - S::kLag); u < unit; ++u) publish(u);
-    } else if (lane == 0) {
+    } else {
+        if constexpr (NT == 2) ptx::give_registers<S::kOtherRegisters>();
+    }
+    if (warp == S::kMmaWarp && lane == 0) {
         // ---------------- MMA issuer ----------------
         constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kPrefixRows, kTokens);
         constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(kPrefixRows, D) | ptx::kIdescBMnMajor;
@@ -413,6 +491,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_ke
                               ptx::smem_desc_sw128_kmajor(q + s / 4 * S::kQChunkBytes + s % 4 * 32),
                               ptx::smem_desc_sw128_kmajor(k + s / 4 * (kTokens * 128) + s % 4 * 32), idesc_s, s > 0);
             ptx::mma_commit(bar_s + 8 * buffer);
+            ptx::mbar_arrive(bar_s + 8 * buffer);  // what the loader wrote before the keys, too
         };
         auto values = [&](int i, int buffer, int u, bool first) {  // O of tile i += P V of unit u
             const uint32_t v = sbase + S::kRingOffset + u % kStages * S::kUnitBytes;
@@ -481,6 +560,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) prefix_attention_ke
             const uint64_t t0 = ptx::global_timer_ns();
             while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::global_timer_ns() - t0 < kDrainLimitNs) {
             }
+        }
+        if (warp == S::kLoaderWarp && lane == 0) {
+            const uint64_t t0 = ptx::global_timer_ns();
+            for (int u = max(0, issued - kStages); u < issued; ++u)
+                while (!ptx::mbar_try_wait(bar_full + 8 * (u % kStages), (u / kStages) & 1) &&
+                       ptx::global_timer_ns() - t0 < kDrainLimitNs) {
+                }
         }
         __syncthreads();
     }
@@ -558,7 +644,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const Pref
 }
 
 template <int D, int NT>
-cudaError_t launch_prefix(const PrefixArgs &a, int grid, int device, cudaStream_t stream, bool pdl) {
+cudaError_t launch_prefix(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a, int grid,
+                          int device, cudaStream_t stream, bool pdl) {
     using S = Shape<D, NT>;
     static bool configured[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
@@ -578,7 +665,7 @@ cudaError_t launch_prefix(const PrefixArgs &a, int grid, int device, cudaStream_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<D, NT>, a);
+    return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<D, NT>, k_map, v_map, a);
 }
 
 template <int D>
@@ -604,16 +691,28 @@ int grid_of(const PrefixArgs &a, int head_dim, int num_sms) {
 
 }  // namespace
 
-cudaError_t launch_prefix_attention(const PrefixArgs &a, int head_dim, int num_sms, int device,
-                                    cudaStream_t stream, bool pdl) {
+int prefix_box_rows(int page_size, int head_dim) {
+    const int tokens = prefix_tokens(head_dim);
+    int rows = page_size & -page_size;  // the largest power of two that pages are multiples of
+    return rows >= 8 ? std::min(rows, tokens) : 0;
+}
+
+cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
+                                    int head_dim, int num_sms, int device, cudaStream_t stream, bool pdl) {
     const int grid = grid_of(a, head_dim, num_sms);
     const bool two = prefix_tiles(head_dim, static_cast<long long>(a.rows) * a.group) == 2;
     switch (head_dim) {
-        case 64: return two ? launch_prefix<64, 2>(a, grid, device, stream, pdl) : launch_prefix<64, 1>(a, grid, device, stream, pdl);
-        case 96: return two ? launch_prefix<96, 2>(a, grid, device, stream, pdl) : launch_prefix<96, 1>(a, grid, device, stream, pdl);
-        case 128: return two ? launch_prefix<128, 2>(a, grid, device, stream, pdl) : launch_prefix<128, 1>(a, grid, device, stream, pdl);
-        case 192: return launch_prefix<192, 1>(a, grid, device, stream, pdl);
-        case 256: return launch_prefix<256, 1>(a, grid, device, stream, pdl);
+        case 64:
+            if (two) return launch_prefix<64, 2>(k_map, v_map, a, grid, device, stream, pdl);
+            return launch_prefix<64, 1>(k_map, v_map, a, grid, device, stream, pdl);
+        case 96:
+            if (two) return launch_prefix<96, 2>(k_map, v_map, a, grid, device, stream, pdl);
+            return launch_prefix<96, 1>(k_map, v_map, a, grid, device, stream, pdl);
+        case 128:
+            if (two) return launch_prefix<128, 2>(k_map, v_map, a, grid, device, stream, pdl);
+            return launch_prefix<128, 1>(k_map, v_map, a, grid, device, stream, pdl);
+        case 192: return launch_prefix<192, 1>(k_map, v_map, a, grid, device, stream, pdl);
+        case 256: return launch_prefix<256, 1>(k_map, v_map, a, grid, device, stream, pdl);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -638,3 +737,4 @@ cudaError_t prefix_error_word(int *value, bool clear) {
 }
 
 }  // namespace skinny
+
