@@ -122,7 +122,7 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     const PrefixPlan plan = prefix_plan(p->rows, group, c->kv_heads, D);
     const long long capacity = static_cast<long long>(p->prefix_width) * c->page_size;
     if (p->prefix_width < 1 || capacity >= (1ll << 30) ||
-        (capacity + prefix_tokens(D) - 1) / prefix_tokens(D) * plan.units >= (1ll << 31))
+        (capacity + plan.tokens - 1) / plan.tokens * plan.units >= (1ll << 31))
         return SKINNY_ERR_SHAPE;
     if (!aligned(p->prefix_table, 4) || !aligned(p->prefix_length, 4)) return SKINNY_ERR_ALIGN;
     const size_t heads = static_cast<size_t>(p->rows) * p->q_heads;
@@ -165,6 +165,7 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     a.q_heads = p->q_heads;
     a.kv_heads = c->kv_heads;
     a.group = group;
+    a.tokens = plan.tokens;
     a.blocks = plan.blocks;
     a.units = plan.units;
     a.scale_log2 = o.scale_log2;
@@ -176,7 +177,7 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     a.lse = static_cast<float *>(p->lse);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     alignas(64) CUtensorMap k_map = {}, v_map = {};
-    a.box_rows = prefix_box_rows(c->page_size, D);
+    a.box_rows = prefix_box_rows(c->page_size, plan.tokens);
     if (a.box_rows > 0 && !(encode_cache_map(&k_map, c->k, c, a.box_rows) && encode_cache_map(&v_map, c->v, c, a.box_rows)))
         a.box_rows = 0;
     if (launch_prefix_attention(k_map, v_map, a, D, sms, dev, s, ls.pdl) != cudaSuccess ||

@@ -222,7 +222,7 @@ struct PrefixArgs {
     int capacity;       // tokens the table holds
     int rows, q_heads, kv_heads;
     int group;          // query heads per key head
-    int blocks, units;  // PrefixPlan
+    int tokens, blocks, units;  // PrefixPlan
     float scale_log2;
     int box_rows;       // tokens of a tensor map's box, or 0: no maps
     float *slots;       // workspace
@@ -233,7 +233,7 @@ struct PrefixArgs {
 };
 // Tokens of a TMA box of the keys and values: 64 of head_dim by so many tokens of one page, or
 // 0 if boxes will not do (tiles must be whole boxes, and a box whole swizzle atoms).
-int prefix_box_rows(int page_size, int head_dim);
+int prefix_box_rows(int page_size, int tokens);
 cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
                                     int head_dim, int num_sms, int device, cudaStream_t stream, bool pdl);
 cudaError_t launch_decode_attention_part(const AttentionArgs &a, int head_dim, int num_sms, int device,

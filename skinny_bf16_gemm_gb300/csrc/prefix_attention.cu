@@ -19,8 +19,9 @@
 //   1 MMA warp        S = Q K^T from shared memory (both K-major) into tensor memory, and
 //                     O += P V with P in tensor memory (it takes the place of S there) and V
 //                     as it lies, MN-major.
-// The two tiles take turns: while one's softmax runs, the other's products do. With one tile
-// S has two places instead, so that the next S is computed while the softmax runs.
+// Scores, weights and output have places of their own in tensor memory: a softmax thread takes
+// its row of scores into registers and sets their place free, so that the next step's are
+// computed while it works, and the two tiles' softmaxes and products fill each other's gaps.
 // The maximum is kept until a score is 2^8 past it; only then O is rescaled, by the softmax
 // threads, in tensor memory. P is rounded to BF16 (to nearest: within 2^-8 of each weight):
 // the roundings of different tokens are independent, so they average out in o as the weights
@@ -34,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "prefix_plan.cuh"
@@ -65,6 +67,22 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+// Two FP32 operations an instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float c, float d) {
+    asm("{\n\t.reg .b64 a, b, e;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 e, {%3, %3};\n\t"
+        "fma.rn.f32x2 a, a, b, e;\n\tmov.b64 {%0, %1}, a;\n\t}" : "+f"(x), "+f"(y) : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float c, float d) {
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}" : "+f"(x), "+f"(y) : "f"(c), "f"(d));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -90,7 +108,7 @@ __device__ __forceinline__ bool loader_any(bool p) {
 
 template <int D, int NT>
 struct Shape {
-    static constexpr int kTokens = prefix_tokens(D);
+    static constexpr int kTokens = prefix_tokens(D, NT);
     static constexpr int kChunks = (D + 63) / 64;               // 128-byte chunks of a row
     static constexpr int kUnitBytes = kChunks * kTokens * 128;  // a tile's keys, or values
     static constexpr int kQChunkBytes = kPrefixRows * 128;
@@ -102,10 +120,10 @@ struct Shape {
     static_assert(kStages >= 4, "a key and a value tile in use while others are on their way");
     static constexpr int kRingOffset = NT * kQBytes;
     static constexpr int kPlacesOffset = kRingOffset + kStages * kUnitBytes;  // [kTokens] of a tile
-    static constexpr int kMaskWords = kTokens / 32;
+    static constexpr int kMaskWords = (kTokens + 31) / 32;
     static constexpr int kMaskOffset = kPlacesOffset + kTokens * 8;  // [kMaskRing][kMaskWords]
     static constexpr int kBarOffset = kMaskOffset + kMaskRing * kMaskWords * 4;
-    static constexpr int kBars = 2 * kStages + 2 * 4 + 1;
+    static constexpr int kBars = 2 * kStages + 2 * 5 + 1;
     static constexpr int kTailOffset = kBarOffset + kBars * 8;  // tensor memory base, abort flag
     static constexpr int kBytes = kTailOffset + 16;
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
@@ -116,8 +134,8 @@ struct Shape {
     // 168 each at the launch; the softmax takes what the others give.
     static constexpr int kSoftmaxRegisters = 200, kOtherRegisters = 104;
     static_assert(2 * kSoftmaxRegisters + kOtherRegisters <= 3 * 168, "registers of the block");
-    // Tensor memory: S (and P) twice, then O of each tile.
-    static constexpr int kOCol = 2 * kTokens;
+    // Tensor memory: scores, weights and output of each tile.
+    static constexpr int kPCol = NT * kTokens, kOCol = kPCol + NT * (kTokens / 2);
     static constexpr int kTmemCols = kOCol + NT * D <= 256 ? 256 : 512;
     static_assert(kOCol + NT * D <= 512, "tensor memory");
 };
@@ -135,9 +153,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     const uint32_t bar_full = sbase + S::kBarOffset;     // + 8 stage
     const uint32_t bar_empty = bar_full + 8 * kStages;   // + 8 stage
     const uint32_t bar_q = bar_empty + 8 * kStages;      // + 8 tile: the queries are there
-    const uint32_t bar_s = bar_q + 16;                   // + 8 place: S is there
-    const uint32_t bar_p = bar_s + 16;                   // + 8 place: P is there
-    const uint32_t bar_pv = bar_p + 16;                  // + 8 tile: O has a step's product
+    const uint32_t bar_s = bar_q + 16;                   // + 8 tile: a step's scores are there
+    const uint32_t bar_free = bar_s + 16;                // + 8 tile: they are read
+    const uint32_t bar_p = bar_free + 16;                // + 8 tile: its weights are there
+    const uint32_t bar_pv = bar_p + 16;                  // + 8 tile: O has its product
     const uint32_t bar_drain = bar_pv + 16;
     volatile uint32_t *tail = reinterpret_cast<volatile uint32_t *>(smem + S::kTailOffset);
     volatile uint32_t *abort_flag = tail + 1;
@@ -151,6 +170,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar_q + 8 * i, 128);
             ptx::mbar_init(bar_s + 8 * i, 2);  // the products, and the issuer (the mask is there)
+            ptx::mbar_init(bar_free + 8 * i, 128);
             ptx::mbar_init(bar_p + 8 * i, 128);
             ptx::mbar_init(bar_pv + 8 * i, 1);
         }
@@ -209,6 +229,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         if (page < 0 || page >= a.num_pages) return -1;
         return page * a.page_stride + (token - e * a.page_size) * a.token_stride + head * a.head_stride;
     };
+    // The mask words of a tile whose tokens are all there.
+    auto whole_mask = [](int i) { return kTokens - i * 32 >= 32 ? 0xFFFFFFFFu : (1u << (kTokens - i * 32) % 32) - 1u; };
     // A unit's segment of this CTA's range.
     struct Segment {
         int unit, head, q0, tiles, t, n;  // first query row, tiles of query rows, first step, steps
@@ -230,6 +252,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         if constexpr (NT == 2) ptx::take_registers<S::kSoftmaxRegisters>();
         const int tile = warp / 4, row = threadIdx.x % 128;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+        const uint32_t s_addr = lanes + tile * kTokens, p_addr = lanes + S::kPCol + tile * (kTokens / 2);
         const uint32_t o_addr = lanes + S::kOCol + tile * D;
         const float c = fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // of the queries' signs
@@ -261,36 +284,39 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 
             float m = kNoMaximum, l = 0.0f;  // in units of log2
             for (int j = 0; j < seg.n; ++j, ++count) {
-                const int buffer = NT == 2 ? tile : count & 1;
-                const uint32_t parity = NT == 2 ? count & 1 : (count >> 1) & 1;
-                if (!(ok = warp_wait(bar_s + 8 * buffer, parity))) break;
+                if (!(ok = warp_wait(bar_s + 8 * tile, count & 1))) break;
                 ptx::tc_fence_after_sync();
-                const uint32_t s_addr = lanes + buffer * kTokens;
                 uint32_t w[kTokens];
                 ptx::tmem_ld_now(s_addr, w);
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(bar_free + 8 * tile);
                 const uint32_t *mask = masks + (tile_count + j) % kMaskRing * S::kMaskWords;
                 bool all = true;
 #pragma unroll
-                for (int i = 0; i < kTokens / 32; ++i) all &= mask[i] == 0xFFFFFFFFu;
+                for (int i = 0; i < S::kMaskWords; ++i) all &= mask[i] == whole_mask(i);
                 if (!all) {  // a NaN stays out of the maximum, and its weight is made 0 below
 #pragma unroll
-                    for (int i = 0; i < kTokens / 32; ++i)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(mask[i] >> e & 1)) w[i * 32 + e] = 0x7FC00000u;
+                    for (int e = 0; e < kTokens; ++e)
+                        if (!(mask[e / 32] >> (e % 32) & 1)) w[e] = 0x7FC00000u;
                 }
-                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float tops[4];
 #pragma unroll
-                for (int e = 0; e < kTokens; ++e) tops[e & 3] = fmaxf(tops[e & 3], __uint_as_float(w[e]));
-                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                for (int e = 0; e < 4; ++e) tops[e] = __uint_as_float(w[e]);
+#pragma unroll
+                for (int e = 4; e + 1 < kTokens; e += 2)
+                    tops[e / 2 & 3] = max3(tops[e / 2 & 3], __uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+                float top = fmaxf(max3(tops[0], tops[1], tops[2]), fmaxf(tops[3], -INFINITY));
                 // -inf (no score, or only such) times 0 would be NaN.
                 top = top == -INFINITY ? -INFINITY : top * c;
+                // Every phase of bar_pv is waited for, in its turn.
+                bool added = j == 0;
                 if (__any_sync(0xFFFFFFFFu, top > m + 8.0f)) {
                     const float next = fmaxf(m, top), f = exp2_approx(m - next);
                     m = next;
                     l *= f;
                     if (j > 0) {
                         if (!(ok = warp_wait(bar_pv + 8 * tile, (count - 1) & 1))) break;
+                        added = true;
                         ptx::tc_fence_after_sync();
 #pragma unroll 1
                         for (int i = 0; i < D; i += 32) {
@@ -303,30 +329,40 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                     }
                 }
                 float sum[4] = {};
+                auto weights = [&](auto masked) {
 #pragma unroll
-                for (int i = 0; i < kTokens / 32; ++i) {
-                    float v[32];
-                    uint32_t p[16];
+                    for (int i = 0; i < kTokens; i += 16) {
+                        float v[16];
+                        uint32_t p[8];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = exp2_approx(fmaf(__uint_as_float(w[i * 32 + e]), c, -m));
-                    if (!all) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(mask[i] >> e & 1)) v[e] = 0.0f;
+                        for (int e = 0; e < 16; e += 2) {
+                            v[e] = __uint_as_float(w[i + e]), v[e + 1] = __uint_as_float(w[i + e + 1]);
+                            fma2(v[e], v[e + 1], c, -m);
+                            v[e] = exp2_approx(v[e]);
+                            v[e + 1] = exp2_approx(v[e + 1]);
+                            if (masked) {
+                                if (!(mask[(i + e) / 32] >> ((i + e) % 32) & 1)) v[e] = 0.0f;
+                                if (!(mask[(i + e) / 32] >> ((i + e) % 32) & 2)) v[e + 1] = 0.0f;
+                            }
+                            add2(sum[e & 2], sum[(e & 2) + 1], v[e], v[e + 1]);
+                            p[e / 2] = pack_bf16(v[e], v[e + 1]);
+                        }
+                        if (i == 0 && !added) {  // the weights before are multiplied
+                            ok = warp_wait(bar_pv + 8 * tile, (count - 1) & 1);
+                            ptx::tc_fence_after_sync();
+                        }
+                        ptx::tmem_st8(p_addr + i / 2, p);
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) sum[e & 3] += v[e];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) p[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-                    ptx::tmem_st16(s_addr + i * 16, p);
-                }
+                };
+                if (all)
+                    weights(std::false_type{});
+                else
+                    weights(std::true_type{});
+                if (!ok) break;
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                // Every phase of bar_pv is waited for in its turn, or a later wait could take the one
-                // before for its own. With two tiles S(j) came after the product of step j - 1.
-                if (NT == 1 && j > 0 && !(ok = warp_wait(bar_pv, (count - 1) & 1))) break;
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bar_p + 8 * buffer);
+                ptx::mbar_arrive(bar_p + 8 * tile);
             }
             if (!ok) break;
             if (!(ok = warp_wait(bar_pv + 8 * tile, (count - 1) & 1))) break;
@@ -358,8 +394,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         long long *places = reinterpret_cast<long long *>(smem + S::kPlacesOffset);
         uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::kMaskOffset);
         constexpr int kRowChunks = D / 8, kCopies = kTokens * kRowChunks / kLoaders;
-        constexpr int kMine = kTokens / kLoaders;  // tokens whose places a thread looks up
-        static_assert(kTokens * kRowChunks % kLoaders == 0 && kTokens % kLoaders == 0, "whole rounds");
+        constexpr int kMine = (kTokens + kLoaders - 1) / kLoaders;  // tokens whose places a thread looks up
+        static_assert(kTokens * kRowChunks % kLoaders == 0 && kTokens % 16 == 0, "whole rounds");
         int unit = 0;  // of the ring, so far
         bool ok = true;
         auto publish = [&](int u) {  // a unit whose copies are complete
@@ -384,7 +420,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 next_token = token - e * a.page_size;
             } else {
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) next[i] = place(head, t * kTokens + i * kLoaders + tid);
+                for (int i = 0; i < kMine; ++i)
+                    next[i] = i * kLoaders + tid < kTokens ? place(head, t * kTokens + i * kLoaders + tid) : -1;
             }
         };
         if (x_begin < x_end) {
@@ -407,10 +444,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                     page = a.num_pages;  // past the end: zeros
                 }
                 if (tid < S::kMaskWords) {
-                    uint32_t bits = 0xFFFFFFFFu;
+                    uint32_t bits = whole_mask(tid);
                     if (good != 0xFFFFFFFFu) {
                         bits = 0;
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 32 && tid * 32 + e < kTokens; ++e)
                             bits |= (good >> ((tid * 32 + e) / a.box_rows * S::kChunks) & 1u) << e;
                     }
                     mask[tid] = bits;
@@ -419,10 +456,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 ptx::named_barrier_sync(2, kLoaders);  // the places of the tile before are read
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
-                    if (next[i] < 0 && t * kTokens + i * kLoaders + tid < length) atomicOr(&g_prefix_err, kErrRange);
-                    places[i * kLoaders + tid] = next[i];  // read behind the barrier of the unit's wait
+                    const int at = i * kLoaders + tid;
                     const uint32_t there = __ballot_sync(0xFFFFFFFFu, next[i] >= 0);
-                    if (lane == 0) mask[i * (kLoaders / 32) + tid / 32] = there;
+                    if (at >= kTokens) continue;
+                    if (next[i] < 0 && t * kTokens + at < length) atomicOr(&g_prefix_err, kErrRange);
+                    places[at] = next[i];  // read behind the barrier of the unit's wait
+                    if (lane == 0) mask[at / 32] = there;
                 }
             }
             if (++t == steps) {
@@ -476,77 +515,60 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kPrefixRows, kTokens);
         constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(kPrefixRows, D) | ptx::kIdescBMnMajor;
         int unit = 0;
-        uint32_t count[2] = {}, segments[2] = {};  // steps whose S was issued, and segments, by tile
+        uint32_t scored[2] = {}, added[2] = {}, segments[2] = {};  // steps and segments, by tile
         bool ok = true;
         auto full = [&](int u) {
             if (!wait(bar_full + 8 * (u % kStages), (u / kStages) & 1)) return false;
             ptx::tc_fence_after_sync();
             return true;
         };
-        auto scores = [&](int i, int buffer, int u) {  // S of tile i with the keys of unit u
-            const uint32_t q = sbase + i * S::kQBytes, k = sbase + S::kRingOffset + u % kStages * S::kUnitBytes;
+        // The scores of tile i's next step, with the keys of unit u; the step's before are read.
+        auto scores = [&](int i, int u) {
+            if (scored[i] > 0 && !wait(bar_free + 8 * i, (scored[i] - 1) & 1)) return false;
+            if (!full(u)) return false;
+            const uint64_t q = ptx::smem_desc_sw128_kmajor(sbase + i * S::kQBytes);
+            const uint64_t k = ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + u % kStages * S::kUnitBytes);
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-                ptx::mma_bf16(tmem + buffer * kTokens,
-                              ptx::smem_desc_sw128_kmajor(q + s / 4 * S::kQChunkBytes + s % 4 * 32),
-                              ptx::smem_desc_sw128_kmajor(k + s / 4 * (kTokens * 128) + s % 4 * 32), idesc_s, s > 0);
-            ptx::mma_commit(bar_s + 8 * buffer);
-            ptx::mbar_arrive(bar_s + 8 * buffer);  // what the loader wrote before the keys, too
+            for (int s = 0; s < D / 16; ++s)  // addresses in the descriptors are in units of 16 bytes
+                ptx::mma_bf16(tmem + i * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
+                              k + s / 4 * (kTokens * 8) + s % 4 * 2, idesc_s, s > 0);
+            ptx::mma_commit(bar_s + 8 * i);
+            ptx::mbar_arrive(bar_s + 8 * i);  // what the loader wrote before the keys, too
+            ++scored[i];
+            return true;
         };
-        auto values = [&](int i, int buffer, int u, bool first) {  // O of tile i += P V of unit u
-            const uint32_t v = sbase + S::kRingOffset + u % kStages * S::kUnitBytes;
+        // O of tile i += its step's weights by the values of unit u.
+        auto values = [&](int i, int u, bool first) {
+            if (!full(u) || !wait(bar_p + 8 * i, added[i]++ & 1)) return false;
+            ptx::tc_fence_after_sync();
+            const uint64_t v =
+                ptx::smem_desc_sw128_mnmajor(sbase + S::kRingOffset + u % kStages * S::kUnitBytes, kTokens * 128);
 #pragma unroll
             for (int s = 0; s < kTokens / 16; ++s)
-                ptx::mma_bf16_tmem_a(tmem + S::kOCol + i * D, tmem + buffer * kTokens + s * 8,
-                                     ptx::smem_desc_sw128_mnmajor(v + s * 2048, kTokens * 128), idesc_o,
-                                     s > 0 || !first);
+                ptx::mma_bf16_tmem_a(tmem + S::kOCol + i * D, tmem + S::kPCol + i * (kTokens / 2) + s * 8, v + s * 128,
+                                     idesc_o, s > 0 || !first);
             ptx::mma_commit(bar_pv + 8 * i);
+            return true;
         };
         for (int x = x_begin; ok && x < x_end;) {
             const Segment seg = segment(x);
             x += seg.n;
-            for (int i = 0; ok && i < seg.tiles; ++i) ok = wait(bar_q + 8 * i, segments[i]++ & 1);
-            if (!ok || !(ok = full(unit))) break;
-            if constexpr (NT == 2) {
-                for (int i = 0; i < seg.tiles; ++i) scores(i, i, unit);
-                ptx::mma_commit(bar_empty + 8 * (unit % kStages));
-                ++unit;
-                for (int j = 0; ok && j < seg.n; ++j) {
-                    const bool more = j + 1 < seg.n;
-                    if (!(ok = full(unit))) break;
-                    for (int i = 0; i < seg.tiles; ++i) {
-                        const uint32_t parity = count[i]++ & 1;
-                        if (!(ok = wait(bar_p + 8 * i, parity))) break;
-                        ptx::tc_fence_after_sync();
-                        values(i, i, unit, j == 0);
-                        if (i == seg.tiles - 1) ptx::mma_commit(bar_empty + 8 * (unit % kStages));
-                        if (!more) continue;
-                        // The next S goes where P is: its product must be complete.
-                        if (!(ok = full(unit + 1)) || !(ok = wait(bar_pv + 8 * i, parity))) break;
-                        scores(i, i, unit + 1);
-                        if (i == seg.tiles - 1) ptx::mma_commit(bar_empty + 8 * ((unit + 1) % kStages));
-                    }
-                    unit += more ? 2 : 1;
-                }
-            } else {
-                scores(0, count[0] & 1, unit);
-                ptx::mma_commit(bar_empty + 8 * (unit % kStages));
-                ++unit;
-                for (int j = 0; ok && j < seg.n; ++j, ++count[0]) {
-                    const bool more = j + 1 < seg.n;
-                    const uint32_t n = count[0];
+            const int last = seg.tiles - 1;
+            for (int i = 0; ok && i <= last; ++i) ok = wait(bar_q + 8 * i, segments[i]++ & 1) && scores(i, unit);
+            if (!ok) break;
+            ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+            ++unit;
+            for (int j = 0; ok && j < seg.n; ++j) {
+                const bool more = j + 1 < seg.n;
+                for (int i = 0; i <= last; ++i) {
                     if (more) {
-                        // The next S goes where the last step's P was.
-                        if (!(ok = full(unit + 1)) || (j > 0 && !(ok = wait(bar_pv, (n - 1) & 1)))) break;
-                        scores(0, (n + 1) & 1, unit + 1);
-                        ptx::mma_commit(bar_empty + 8 * ((unit + 1) % kStages));
+                        if (!(ok = scores(i, unit + 1))) break;
+                        if (i == last) ptx::mma_commit(bar_empty + 8 * ((unit + 1) % kStages));
                     }
-                    if (!(ok = full(unit)) || !(ok = wait(bar_p + 8 * (n & 1), (n >> 1) & 1))) break;
-                    ptx::tc_fence_after_sync();
-                    values(0, n & 1, unit, j == 0);
-                    ptx::mma_commit(bar_empty + 8 * (unit % kStages));
-                    unit += more ? 2 : 1;
+                    if (!(ok = values(i, unit, j == 0))) break;
+                    if (i == last) ptx::mma_commit(bar_empty + 8 * (unit % kStages));
                 }
+                unit += more ? 2 : 1;
             }
         }
     }
@@ -592,7 +614,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const Pref
     const int row = job / a.q_heads, h = job - row * a.q_heads;
     const int head = h / a.group, at = row * a.group + h - head * a.group;  // query row of the key head
     const int length = min(max(__ldcg(a.length), 0), a.capacity);
-    const int tokens = prefix_tokens(D), per = kPrefixRows * prefix_tiles(D, static_cast<long long>(a.rows) * a.group);
+    const int tokens = a.tokens, per = kPrefixRows * prefix_tiles(D, static_cast<long long>(a.rows) * a.group);
     const int steps = (length + tokens - 1) / tokens, total = steps * a.units;
     const int ctas = prefix_ctas(grid, total);
     const int unit = head * a.blocks + at / per, in_unit = at % per;
@@ -684,22 +706,20 @@ cudaError_t launch_join(const PrefixArgs &a, int grid, cudaStream_t stream) {
 }
 
 // CTAs of the prefix's kernel: no more than the table could ever hold steps.
-int grid_of(const PrefixArgs &a, int head_dim, int num_sms) {
-    const long long tokens = prefix_tokens(head_dim);
-    return static_cast<int>(std::min<long long>(num_sms, (a.capacity + tokens - 1) / tokens * a.units));
+int grid_of(const PrefixArgs &a, int num_sms) {
+    return static_cast<int>(std::min<long long>(num_sms, (a.capacity + a.tokens - 1ll) / a.tokens * a.units));
 }
 
 }  // namespace
 
-int prefix_box_rows(int page_size, int head_dim) {
-    const int tokens = prefix_tokens(head_dim);
-    int rows = page_size & -page_size;  // the largest power of two that pages are multiples of
-    return rows >= 8 ? std::min(rows, tokens) : 0;
+int prefix_box_rows(int page_size, int tokens) {
+    const int both = page_size | tokens, rows = both & -both;  // the largest power of two that divides both
+    return rows >= 8 ? rows : 0;
 }
 
 cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
                                     int head_dim, int num_sms, int device, cudaStream_t stream, bool pdl) {
-    const int grid = grid_of(a, head_dim, num_sms);
+    const int grid = grid_of(a, num_sms);
     const bool two = prefix_tiles(head_dim, static_cast<long long>(a.rows) * a.group) == 2;
     switch (head_dim) {
         case 64:
@@ -718,7 +738,7 @@ cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap 
 }
 
 cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream) {
-    const int grid = grid_of(a, head_dim, num_sms);
+    const int grid = grid_of(a, num_sms);
     switch (head_dim) {
         case 64: return launch_join<64>(a, grid, stream);
         case 96: return launch_join<96>(a, grid, stream);

@@ -19,23 +19,32 @@ namespace skinny {
 
 constexpr int kPrefixRows = 128;  // query rows of a tile: the MMA's M
 
-// Tokens of a step: 64 for wide heads, whose keys and values fill the ring otherwise.
-__host__ __device__ constexpr int prefix_tokens(int head_dim) { return head_dim <= 128 ? 128 : 64; }
-
 // Tiles of 128 query rows a CTA has at once: two, whose softmaxes and products take turns,
 // where there are that many rows and the tensor memory holds both.
 __host__ __device__ constexpr int prefix_tiles(int head_dim, long long query_rows) {
     return head_dim <= 128 && query_rows > kPrefixRows ? 2 : 1;
 }
 
+
+// Tokens of a step. In tensor memory (512 columns) every tile has a place for its scores (one
+// column a token), one for its weights (half a column) and one for its output (head_dim
+// columns), all apart, so that the next scores are computed while the softmax runs: 80 or 96
+// tokens for two tiles of wide heads. 64 from 192 on, whose keys and values fill the ring
+// otherwise.
+__host__ __device__ constexpr int prefix_tokens(int head_dim, int tiles) {
+    return head_dim > 128 ? 64 : tiles == 1 || head_dim <= 64 ? 128 : head_dim <= 96 ? 96 : 80;
+}
+
 struct PrefixPlan {
+    int tokens;  // of a step
     int blocks;  // blocks of query rows of a key head
     int units;   // key heads * blocks
 };
 __host__ __device__ inline PrefixPlan prefix_plan(int rows, int group, int kv_heads, int head_dim) {
     const long long q = static_cast<long long>(rows) * group;
-    const int per = kPrefixRows * prefix_tiles(head_dim, q);
+    const int tiles = prefix_tiles(head_dim, q), per = kPrefixRows * tiles;
     PrefixPlan p;
+    p.tokens = prefix_tokens(head_dim, tiles);
     p.blocks = static_cast<int>((q + per - 1) / per);
     p.units = p.blocks * kv_heads;
     return p;
