@@ -16,7 +16,7 @@
 //                     lane a box, or, for pages of no multiple of 8 and for a tile that the
 //                     prefix ends in (what is behind its end must come out as zeros), by
 //                     16-byte cp.async with each token's address;
-//   1 MMA warp        S = Q K^T from shared memory (both K-major) into tensor memory, and
+//   1 MMA warp a tile S = Q K^T from shared memory (both K-major) into tensor memory, and
 //                     O += P V with P in tensor memory (it takes the place of S there) and V
 //                     as it lies, MN-major.
 // Scores, weights and output have places of their own in tensor memory: a softmax thread takes
@@ -129,7 +129,7 @@ struct Shape {
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
     static_assert(kDynamicBytes <= 232448, "shared memory of a CTA");
     static constexpr int kLoaderWarp = NT * 4, kMmaWarp = NT * 4 + 2;
-    static constexpr int kThreads = (NT * 4 + 4) * 32;  // one warp of the last four is idle
+    static constexpr int kThreads = (NT * 4 + 4) * 32;  // NT = 1: one warp of the last four is idle
     // Registers a thread: a row of scores is kept in them. Three groups of four warps get
     // 168 each at the launch; the softmax takes what the others give.
     static constexpr int kSoftmaxRegisters = 200, kOtherRegisters = 104;
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(bar_full + 8 * s, kLoaders);
-            ptx::mbar_init(bar_empty + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, NT);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar_q + 8 * i, 128);
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             ptx::mbar_init(bar_p + 8 * i, 128);
             ptx::mbar_init(bar_pv + 8 * i, 1);
         }
-        ptx::mbar_init(bar_drain, 1);
+        ptx::mbar_init(bar_drain, NT);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
     }
@@ -510,64 +510,74 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     } else {
         if constexpr (NT == 2) ptx::give_registers<S::kOtherRegisters>();
     }
-    if (warp == S::kMmaWarp && lane == 0) {
-        // ---------------- MMA issuer ----------------
+    if (warp >= S::kMmaWarp && warp < S::kMmaWarp + NT && lane == 0) {
+        // ---------------- MMA issuer of one tile ----------------
+        // One for each: the waits and commits of one (about half of a step's time for a single
+        // issuer: 155 us for 65521 tokens of 8 key heads and 448 query rows) pass while the
+        // other's products run.
+        const int tile = warp - S::kMmaWarp;
         constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kPrefixRows, kTokens);
         constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(kPrefixRows, D) | ptx::kIdescBMnMajor;
         int unit = 0;
-        uint32_t scored[2] = {}, added[2] = {}, segments[2] = {};  // steps and segments, by tile
+        uint32_t scored = 0, added = 0, segments = 0;  // steps and segments of this tile
         bool ok = true;
         auto full = [&](int u) {
             if (!wait(bar_full + 8 * (u % kStages), (u / kStages) & 1)) return false;
             ptx::tc_fence_after_sync();
             return true;
         };
-        // The scores of tile i's next step, with the keys of unit u; the step's before are read.
-        auto scores = [&](int i, int u) {
-            if (scored[i] > 0 && !wait(bar_free + 8 * i, (scored[i] - 1) & 1)) return false;
+        // A unit is free when every tile's products with it are complete; a segment's only tile
+        // speaks for both.
+        auto release = [&](int u, bool alone) {
+            ptx::mma_commit(bar_empty + 8 * (u % kStages));
+            if (NT == 2 && alone) ptx::mma_commit(bar_empty + 8 * (u % kStages));
+        };
+        // The scores of the next step, with the keys of unit u; the step's before are read.
+        auto scores = [&](int u) {
+            if (scored > 0 && !wait(bar_free + 8 * tile, (scored - 1) & 1)) return false;
             if (!full(u)) return false;
-            const uint64_t q = ptx::smem_desc_sw128_kmajor(sbase + i * S::kQBytes);
+            const uint64_t q = ptx::smem_desc_sw128_kmajor(sbase + tile * S::kQBytes);
             const uint64_t k = ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + u % kStages * S::kUnitBytes);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s)  // addresses in the descriptors are in units of 16 bytes
-                ptx::mma_bf16(tmem + i * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
+                ptx::mma_bf16(tmem + tile * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
                               k + s / 4 * (kTokens * 8) + s % 4 * 2, idesc_s, s > 0);
-            ptx::mma_commit(bar_s + 8 * i);
-            ptx::mbar_arrive(bar_s + 8 * i);  // what the loader wrote before the keys, too
-            ++scored[i];
+            ptx::mma_commit(bar_s + 8 * tile);
+            ptx::mbar_arrive(bar_s + 8 * tile);  // what the loader wrote before the keys, too
+            ++scored;
             return true;
         };
-        // O of tile i += its step's weights by the values of unit u.
-        auto values = [&](int i, int u, bool first) {
-            if (!full(u) || !wait(bar_p + 8 * i, added[i]++ & 1)) return false;
+        // O += the step's weights by the values of unit u.
+        auto values = [&](int u, bool first) {
+            if (!full(u) || !wait(bar_p + 8 * tile, added++ & 1)) return false;
             ptx::tc_fence_after_sync();
             const uint64_t v =
                 ptx::smem_desc_sw128_mnmajor(sbase + S::kRingOffset + u % kStages * S::kUnitBytes, kTokens * 128);
 #pragma unroll
             for (int s = 0; s < kTokens / 16; ++s)
-                ptx::mma_bf16_tmem_a(tmem + S::kOCol + i * D, tmem + S::kPCol + i * (kTokens / 2) + s * 8, v + s * 128,
-                                     idesc_o, s > 0 || !first);
-            ptx::mma_commit(bar_pv + 8 * i);
+                ptx::mma_bf16_tmem_a(tmem + S::kOCol + tile * D, tmem + S::kPCol + tile * (kTokens / 2) + s * 8,
+                                     v + s * 128, idesc_o, s > 0 || !first);
+            ptx::mma_commit(bar_pv + 8 * tile);
             return true;
         };
         for (int x = x_begin; ok && x < x_end;) {
             const Segment seg = segment(x);
             x += seg.n;
-            const int last = seg.tiles - 1;
-            for (int i = 0; ok && i <= last; ++i) ok = wait(bar_q + 8 * i, segments[i]++ & 1) && scores(i, unit);
-            if (!ok) break;
-            ptx::mma_commit(bar_empty + 8 * (unit % kStages));
-            ++unit;
-            for (int j = 0; ok && j < seg.n; ++j) {
+            if (tile >= seg.tiles) {
+                unit += 2 * seg.n;
+                continue;
+            }
+            const bool alone = seg.tiles == 1;
+            if (!(ok = wait(bar_q + 8 * tile, segments++ & 1) && scores(unit))) break;
+            release(unit++, alone);
+            for (int j = 0; j < seg.n; ++j) {
                 const bool more = j + 1 < seg.n;
-                for (int i = 0; i <= last; ++i) {
-                    if (more) {
-                        if (!(ok = scores(i, unit + 1))) break;
-                        if (i == last) ptx::mma_commit(bar_empty + 8 * ((unit + 1) % kStages));
-                    }
-                    if (!(ok = values(i, unit, j == 0))) break;
-                    if (i == last) ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+                if (more) {
+                    if (!(ok = scores(unit + 1))) break;
+                    release(unit + 1, alone);
                 }
+                if (!(ok = values(unit, j == 0))) break;
+                release(unit, alone);
                 unit += more ? 2 : 1;
             }
         }
@@ -577,7 +587,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     __syncthreads();
     if (*abort_flag) {
         // Nothing may still read this CTA's shared or tensor memory when it ends.
-        if (warp == S::kMmaWarp && lane == 0) {
+        if (warp >= S::kMmaWarp && warp < S::kMmaWarp + NT && lane == 0) {
             ptx::mma_commit(bar_drain);
             const uint64_t t0 = ptx::global_timer_ns();
             while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::global_timer_ns() - t0 < kDrainLimitNs) {
