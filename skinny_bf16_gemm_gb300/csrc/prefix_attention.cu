@@ -11,11 +11,11 @@
 // A CTA has one or two tiles of 128 query rows in shared memory and a ring of tiles of the
 // prefix's keys and values, in turn. Roles:
 //   warps 0-3 (4-7)   softmax of the first (second) tile: thread = query row = TMEM lane;
-//   2 loader warps    the ring, in the 128-byte swizzle that the MMA's descriptors name: by TMA
-//                     boxes of as many tokens as pages and tiles both are multiples of, one
-//                     lane a box, or, for pages of no multiple of 8 and for a tile that the
-//                     prefix ends in (what is behind its end must come out as zeros), by
-//                     16-byte cp.async with each token's address;
+//   2 loader warps    the ring, one the keys and one the values, in the 128-byte swizzle that
+//                     the MMA's descriptors name: by TMA boxes of as many tokens as pages
+//                     and tiles both are multiples of, or, for pages of no multiple of 8 and
+//                     for a tile that the prefix ends in (what is behind its end must come
+//                     out as zeros), by 16-byte cp.async with each token's address;
 //   1 MMA warp a tile S = Q K^T from shared memory (both K-major) into tensor memory, and
 //                     O += P V with P in tensor memory (it takes the place of S there) and V
 //                     as it lies, MN-major.
@@ -89,22 +89,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-constexpr int kLoaders = 64;    // threads
-constexpr int kMaskRing = 16;   // tiles whose masks are kept: more than the loader is ahead
-
-// Barrier-wide OR of a predicate over the loader's threads (named barrier 3).
-__device__ __forceinline__ bool loader_any(bool p) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred a, b;\n\t"
-        "setp.ne.u32 a, %1, 0;\n\t"
-        "bar.red.or.pred b, 3, 64, a;\n\t"
-        "selp.u32 %0, 1, 0, b;\n\t}"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(p))
-        : "memory");
-    return r != 0;
-}
+constexpr int kMaskRing = 16;  // tiles whose masks are kept: more than the loader is ahead
 
 template <int D, int NT>
 struct Shape {
@@ -113,15 +98,16 @@ struct Shape {
     static constexpr int kUnitBytes = kChunks * kTokens * 128;  // a tile's keys, or values
     static constexpr int kQChunkBytes = kPrefixRows * 128;
     static constexpr int kQBytes = kChunks * kQChunkBytes;      // one tile of queries
-    static constexpr int kMiscBytes = 2048;
+    static constexpr int kMiscBytes = 2 * kTokens * 8 + 768;
     static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes);
-    // cp.async: units whose copies are on their way, while as many are there for the MMAs.
-    static constexpr int kLag = kStages / 2;
+    // cp.async: units of a loader warp (every other one of the ring) whose copies are on their
+    // way. At most so many that the next keys come without the last values' place.
+    static constexpr int kLag = (kStages - 2) / 2;
     static_assert(kStages >= 4, "a key and a value tile in use while others are on their way");
     static constexpr int kRingOffset = NT * kQBytes;
-    static constexpr int kPlacesOffset = kRingOffset + kStages * kUnitBytes;  // [kTokens] of a tile
+    static constexpr int kPlacesOffset = kRingOffset + kStages * kUnitBytes;  // [2][kTokens] of a tile
     static constexpr int kMaskWords = (kTokens + 31) / 32;
-    static constexpr int kMaskOffset = kPlacesOffset + kTokens * 8;  // [kMaskRing][kMaskWords]
+    static constexpr int kMaskOffset = kPlacesOffset + 2 * kTokens * 8;  // [kMaskRing][kMaskWords]
     static constexpr int kBarOffset = kMaskOffset + kMaskRing * kMaskWords * 4;
     static constexpr int kBars = 2 * kStages + 2 * 5 + 1;
     static constexpr int kTailOffset = kBarOffset + kBars * 8;  // tensor memory base, abort flag
@@ -164,7 +150,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, kLoaders);
+            ptx::mbar_init(bar_full + 8 * s, 32);
             ptx::mbar_init(bar_empty + 8 * s, NT);
         }
         for (int i = 0; i < 2; ++i) {
@@ -390,38 +376,39 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     } else if (warp < S::kMmaWarp) {
         // ---------------- loader ----------------
         if constexpr (NT == 2) ptx::give_registers<S::kOtherRegisters>();
-        const int tid = threadIdx.x - S::kLoaderWarp * 32;
-        long long *places = reinterpret_cast<long long *>(smem + S::kPlacesOffset);
+        const int kv = warp - S::kLoaderWarp;  // 0: keys, 1: values
+        const uint16_t *from = kv == 0 ? a.k : a.v;
+        const CUtensorMap *map = kv == 0 ? &k_map : &v_map;
+        // Element offsets of a tile's tokens, -1: none.
+        long long *places = reinterpret_cast<long long *>(smem + S::kPlacesOffset) + kv * kTokens;
         uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::kMaskOffset);
-        constexpr int kRowChunks = D / 8, kCopies = kTokens * kRowChunks / kLoaders;
-        constexpr int kMine = (kTokens + kLoaders - 1) / kLoaders;  // tokens whose places a thread looks up
-        static_assert(kTokens * kRowChunks % kLoaders == 0 && kTokens % 16 == 0, "whole rounds");
-        int unit = 0;  // of the ring, so far
+        constexpr int kRowChunks = D / 8, kCopies = kTokens * kRowChunks / 32;
+        constexpr int kMine = (kTokens + 31) / 32;  // tokens whose places a lane looks up
+        static_assert(kTokens * kRowChunks % 32 == 0 && kTokens % 16 == 0, "whole rounds");
+        int unit = kv;  // of the ring, so far
         bool ok = true;
         auto publish = [&](int u) {  // a unit whose copies are complete
             ptx::fence_proxy_async_shared();
             ptx::mbar_arrive(bar_full + 8 * (u % kStages));
         };
-        int segment_unit = 0, head = 0, t = 0;
-        // A tile's boxes: lane = (box, chunk). No more than a warp has lanes.
-        static_assert(kTokens / 8 * S::kChunks <= 32, "a lane a box");
+        static_assert(kTokens / 8 <= 32, "a lane a box");
         const int boxes = a.box_rows > 0 ? kTokens / a.box_rows : 0;
-        const int box = lane / S::kChunks, chunk = lane - box * S::kChunks;
         auto boxed = [&](int tile) { return boxes > 0 && (tile + 1) * kTokens <= length; };
+        int segment_unit = 0, head = 0, t = 0;
         // The next tile's places: of a box (page and token within it) or of tokens.
         long long next[kMine];
         int next_page = 0, next_token = 0;
         auto look_up = [&]() {
             if (boxed(t)) {
-                if (box >= boxes) return;
-                const int token = t * kTokens + box * a.box_rows;
+                if (lane >= boxes) return;
+                const int token = t * kTokens + lane * a.box_rows;
                 const int e = a.page_shift >= 0 ? token >> a.page_shift : token / a.page_size;
                 next_page = __ldcg(a.table + e);
                 next_token = token - e * a.page_size;
             } else {
 #pragma unroll
                 for (int i = 0; i < kMine; ++i)
-                    next[i] = i * kLoaders + tid < kTokens ? place(head, t * kTokens + i * kLoaders + tid) : -1;
+                    next[i] = i * 32 + lane < kTokens ? place(head, t * kTokens + i * 32 + lane) : -1;
             }
         };
         if (x_begin < x_end) {
@@ -430,83 +417,85 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             t = x_begin - segment_unit * steps;
             look_up();
         }
-        for (int x = x_begin; ok && x < x_end; ++x) {
+        for (int x = x_begin; x < x_end; ++x, unit += 2) {
             uint32_t *mask = masks + (x - x_begin) % kMaskRing * S::kMaskWords;
             const bool by_box = boxed(t);
-            const int this_head = head;
+            const int this_head = head, s = unit % kStages, token = next_token;
+            const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
             int page = next_page;
-            const int token = next_token;
             if (by_box) {
-                const bool there = box >= boxes || (page >= 0 && page < a.num_pages);
+                const bool there = lane >= boxes || (page >= 0 && page < a.num_pages);
                 const uint32_t good = __ballot_sync(0xFFFFFFFFu, there);
                 if (!there) {
                     atomicOr(&g_prefix_err, kErrRange);
                     page = a.num_pages;  // past the end: zeros
                 }
-                if (tid < S::kMaskWords) {
-                    uint32_t bits = whole_mask(tid);
+                if (kv == 0 && lane < S::kMaskWords) {
+                    uint32_t bits = whole_mask(lane);
                     if (good != 0xFFFFFFFFu) {
                         bits = 0;
-                        for (int e = 0; e < 32 && tid * 32 + e < kTokens; ++e)
-                            bits |= (good >> ((tid * 32 + e) / a.box_rows * S::kChunks) & 1u) << e;
+                        for (int e = 0; e < 32 && lane * 32 + e < kTokens; ++e)
+                            bits |= (good >> ((lane * 32 + e) / a.box_rows) & 1u) << e;
                     }
-                    mask[tid] = bits;
+                    mask[lane] = bits;
                 }
             } else {
-                ptx::named_barrier_sync(2, kLoaders);  // the places of the tile before are read
+                __syncwarp();  // the places of the tile before are read
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
-                    const int at = i * kLoaders + tid;
+                    const int at = i * 32 + lane;
                     const uint32_t there = __ballot_sync(0xFFFFFFFFu, next[i] >= 0);
                     if (at >= kTokens) continue;
                     if (next[i] < 0 && t * kTokens + at < length) atomicOr(&g_prefix_err, kErrRange);
-                    places[at] = next[i];  // read behind the barrier of the unit's wait
-                    if (lane == 0) mask[at / 32] = there;
+                    places[at] = next[i];
+                    if (kv == 0 && lane == 0) mask[i] = there;
                 }
+                __syncwarp();
             }
             if (++t == steps) {
                 t = 0;
                 head = ++segment_unit / a.blocks;
             }
             if (x + 1 < x_end) look_up();
-            for (int kv = 0; kv < 2; ++kv, ++unit) {
-                const int s = unit % kStages;
-                // The first round finds the stages free.
-                if (!(ok = !loader_any(!wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1)))) break;
-                const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
-                if (by_box) {
-                    if (tid == 0)
-                        ptx::mbar_arrive_expect_tx(bar_full + 8 * s, S::kUnitBytes);
-                    else
-                        ptx::mbar_arrive(bar_full + 8 * s);
-                    __syncwarp();
-                    if (tid < 32 && box < boxes)
-                        ptx::tma_load_4d(to + chunk * (kTokens * 128) + box * a.box_rows * 128, kv == 0 ? &k_map : &v_map,
-                                         bar_full + 8 * s, chunk * 64, token, this_head, page);
-                    continue;
+            // The first round finds the stages free.
+            if (!(ok = warp_wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1))) break;
+            if (by_box) {
+                if (lane == 0)
+                    ptx::mbar_arrive_expect_tx(bar_full + 8 * s, S::kUnitBytes);
+                else
+                    ptx::mbar_arrive(bar_full + 8 * s);
+                // One lane issues: with a lane a box the boxes come one after another too, and the
+                // loop that makes them is longer.
+                for (int b = 0; b < boxes; ++b) {
+                    const int box_page = __shfl_sync(0xFFFFFFFFu, page, b), box_token = __shfl_sync(0xFFFFFFFFu, token, b);
+                    if (lane == 0)
+#pragma unroll
+                        for (int ch = 0; ch < S::kChunks; ++ch)
+                            ptx::tma_load_4d(to + ch * (kTokens * 128) + b * a.box_rows * 128, map, bar_full + 8 * s,
+                                             ch * 64, box_token, this_head, box_page);
                 }
-                const uint16_t *from = kv == 0 ? a.k : a.v;
+                continue;
+            }
 #pragma unroll 8
-                for (int i = 0; i < kCopies; ++i) {
-                    const int id = i * kLoaders + tid, r = id / kRowChunks, ch = id % kRowChunks;
-                    const long long at = places[r];
-                    cp_async16_or_zeros(to + ch / 8 * (kTokens * 128) + r * 128 + ((ch ^ r) & 7) * 16,
-                                        from + (at < 0 ? 0 : at) + ch * 8, at >= 0);
-                }
-                cp_async_commit();
-                if (boxes > 0) {  // the tile that a unit ends with
-                    cp_async_wait<0>();
-                    publish(unit);
-                } else if (unit >= S::kLag) {
-                    cp_async_wait<S::kLag>();
-                    publish(unit - S::kLag);
-                }
+            for (int i = 0; i < kCopies; ++i) {
+                const int id = i * 32 + lane, r = id / kRowChunks, ch = id % kRowChunks;
+                const long long at = places[r];
+                cp_async16_or_zeros(to + ch / 8 * (kTokens * 128) + r * 128 + ((ch ^ r) & 7) * 16,
+                                    from + (at < 0 ? 0 : at) + ch * 8, at >= 0);
+            }
+            cp_async_commit();
+            if (boxes > 0) {  // the tile that the prefix ends in
+                cp_async_wait<0>();
+                publish(unit);
+            } else if (unit >= 2 * S::kLag) {
+                cp_async_wait<S::kLag>();
+                publish(unit - 2 * S::kLag);
             }
         }
         issued = boxes > 0 ? unit : 0;
         cp_async_wait<0>();
         if (ok && boxes == 0)
-            for (int u = max(0, unit - S::kLag); u < unit; ++u) publish(u);
+            for (int u = max(kv, unit - 2 * S::kLag); u < unit; u += 2) publish(u);
     } else {
         if constexpr (NT == 2) ptx::give_registers<S::kOtherRegisters>();
     }
@@ -593,9 +582,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::global_timer_ns() - t0 < kDrainLimitNs) {
             }
         }
-        if (warp == S::kLoaderWarp && lane == 0) {
+        if (warp >= S::kLoaderWarp && warp < S::kMmaWarp && lane == 0) {
             const uint64_t t0 = ptx::global_timer_ns();
-            for (int u = max(0, issued - kStages); u < issued; ++u)
+            for (int u = max(warp - S::kLoaderWarp, issued - kStages / 2 * 2); u < issued; u += 2)
                 while (!ptx::mbar_try_wait(bar_full + 8 * (u % kStages), (u / kStages) & 1) &&
                        ptx::global_timer_ns() - t0 < kDrainLimitNs) {
                 }
