@@ -539,9 +539,8 @@ SKINNY_API size_t skinny_attention_workspace_bytes(int num_sms);
  *   maxima, sums and partial outputs are FP32; the prefix's weights are rounded to BF16 (to
  *   nearest) for the product with the values, the own tokens' as in decode_attention_bf16;
  *   the output is rounded once. Deterministic.
- *   prefix_width >= 1; prefix_width * page_size < 2^30; key heads * blocks of query rows (of
- *   256; of 128 for head_dim 192 and 256) * tiles of the table (of 128 tokens; 64) < 2^31;
- *   tables and lengths 4-byte aligned. Every other argument, rule and limit is
+ *   prefix_width >= 1; prefix_width * page_size < 2^30; key heads * tiles of the table (of 64
+ *   tokens) < 2^31; tables and lengths 4-byte aligned. Every other argument, rule and limit is
  *   decode_attention_bf16's, without a window.
  *   On the device a length out of range is taken as the nearest, a token on a page out of
  *   range as not seen, and skinny_device_error() reports bit 256. Every wait is bounded (1 s);

@@ -2,6 +2,7 @@
 // argument checks and launches. Every check runs before any launch.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "api_internal.h"
@@ -119,10 +120,10 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     if (st) return st;
     const skinny_kv_cache *c = &p->cache;
     const int D = c->head_dim, group = p->q_heads / c->kv_heads;
-    const PrefixPlan plan = prefix_plan(p->rows, group, c->kv_heads, D);
+    const PrefixPlan plan = prefix_plan(p->rows, group, D);
     const long long capacity = static_cast<long long>(p->prefix_width) * c->page_size;
     if (p->prefix_width < 1 || capacity >= (1ll << 30) ||
-        (capacity + plan.tokens - 1) / plan.tokens * plan.units >= (1ll << 31))
+        (capacity + 63) / 64 * c->kv_heads >= (1ll << 31))
         return SKINNY_ERR_SHAPE;
     if (!aligned(p->prefix_table, 4) || !aligned(p->prefix_length, 4)) return SKINNY_ERR_ALIGN;
     const size_t heads = static_cast<size_t>(p->rows) * p->q_heads;
@@ -167,7 +168,10 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     a.group = group;
     a.tokens = plan.tokens;
     a.blocks = plan.blocks;
-    a.units = plan.units;
+    a.lanes = prefix_lanes(plan.blocks, sms);
+    // No more ranges than the table could ever hold tiles.
+    a.ranges = static_cast<int>(std::min<long long>(prefix_ranges(plan.blocks, sms),
+                                                    (capacity + plan.tokens - 1) / plan.tokens * c->kv_heads));
     a.scale_log2 = o.scale_log2;
     a.slots = reinterpret_cast<float *>(base + ws.slots);
     a.slot_floats = static_cast<int>(prefix_slot_floats(D, static_cast<long long>(p->rows) * group));
@@ -180,9 +184,9 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     a.box_rows = prefix_box_rows(c->page_size, plan.tokens);
     if (a.box_rows > 0 && !(encode_cache_map(&k_map, c->k, c, a.box_rows) && encode_cache_map(&v_map, c->v, c, a.box_rows)))
         a.box_rows = 0;
-    if (launch_prefix_attention(k_map, v_map, a, D, sms, dev, s, ls.pdl) != cudaSuccess ||
+    if (launch_prefix_attention(k_map, v_map, a, D, dev, s, ls.pdl) != cudaSuccess ||
         launch_decode_attention_part(o, D, sms, dev, s) != cudaSuccess ||
-        launch_prefix_join(a, D, sms, s) != cudaSuccess) {
+        launch_prefix_join(a, D, s) != cudaSuccess) {
         cudaGetLastError();
         return SKINNY_ERR_LAUNCH;
     }

@@ -222,7 +222,8 @@ struct PrefixArgs {
     int capacity;       // tokens the table holds
     int rows, q_heads, kv_heads;
     int group;          // query heads per key head
-    int tokens, blocks, units;  // PrefixPlan
+    int tokens, blocks;  // PrefixPlan
+    int lanes, ranges;   // blocks side by side, and the most ranges
     float scale_log2;
     int box_rows;       // tokens of a tensor map's box, or 0: no maps
     float *slots;       // workspace
@@ -235,10 +236,10 @@ struct PrefixArgs {
 // 0 if boxes will not do (tiles must be whole boxes, and a box whole swizzle atoms).
 int prefix_box_rows(int page_size, int tokens);
 cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
-                                    int head_dim, int num_sms, int device, cudaStream_t stream, bool pdl);
+                                    int head_dim, int device, cudaStream_t stream, bool pdl);
 cudaError_t launch_decode_attention_part(const AttentionArgs &a, int head_dim, int num_sms, int device,
                                          cudaStream_t stream);
-cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, cudaStream_t stream);
 cudaError_t prefix_error_word(int *value, bool clear);
 cudaError_t attention_part_error_word(int *value, bool clear);
 

@@ -4,21 +4,22 @@
 //
 //   s_ij = scale q_i.k_j,  m_i = max_j s_ij,  l_i = sum_j exp(s_ij - m_i),
 //   o_i = sum_j exp(s_ij - m_i) v_j      over the prefix's tokens j
-// for the query rows i of a key head: every row's heads that share it (prefix_plan.cuh). The
-// prefix is read once for up to 256 of them, so from some 300 on the tensor cores are the
-// bound, below it HBM.
+// for the query rows i of a key head: every row's heads that share it (prefix_plan.cuh). All of
+// them go through the prefix at the same time, so that it is read once; from some 300 query
+// rows on the tensor cores are the bound, below it HBM.
 //
 // A CTA has one or two tiles of 128 query rows in shared memory and a ring of tiles of the
 // prefix's keys and values, in turn. Roles:
 //   warps 0-3 (4-7)   softmax of the first (second) tile: thread = query row = TMEM lane;
-//   2 loader warps    the ring, one the keys and one the values, in the 128-byte swizzle that
-//                     the MMA's descriptors name: by TMA boxes of as many tokens as pages
-//                     and tiles both are multiples of, or, for pages of no multiple of 8 and
-//                     for a tile that the prefix ends in (what is behind its end must come
-//                     out as zeros), by 16-byte cp.async with each token's address;
-//   1 MMA warp a tile S = Q K^T from shared memory (both K-major) into tensor memory, and
-//                     O += P V with P in tensor memory (it takes the place of S there) and V
-//                     as it lies, MN-major.
+//   4 loader warps    the ring, in the 128-byte swizzle that the MMA's descriptors name: by TMA
+//                     boxes of as many tokens as pages and tiles both are multiples of, or,
+//                     for pages of no multiple of 8 and for a tile that the prefix ends in
+//                     (what is behind its end must come out as zeros), by 16-byte cp.async
+//                     with each token's address. Four, because a thread takes some 200 clocks
+//                     to issue a box, of whatever size, and the threads of a warp take turns;
+//   1 MMA warp        the scores of both tiles, S = Q K^T, from shared memory (both K-major)
+//                     into tensor memory;
+//   1 MMA warp a tile O += P V, P in tensor memory and V as it lies, MN-major.
 // Scores, weights and output have places of their own in tensor memory: a softmax thread takes
 // its row of scores into registers and sets their place free, so that the next step's are
 // computed while it works, and the two tiles' softmaxes and products fill each other's gaps.
@@ -98,28 +99,29 @@ struct Shape {
     static constexpr int kUnitBytes = kChunks * kTokens * 128;  // a tile's keys, or values
     static constexpr int kQChunkBytes = kPrefixRows * 128;
     static constexpr int kQBytes = kChunks * kQChunkBytes;      // one tile of queries
-    static constexpr int kMiscBytes = 2 * kTokens * 8 + 768;
-    static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes);
-    // cp.async: units of a loader warp (every other one of the ring) whose copies are on their
-    // way. At most so many that the next keys come without the last values' place.
-    static constexpr int kLag = (kStages - 2) / 2;
+    static constexpr int kMiscBytes = 768;
+    // Keys in the even stages, values in the odd ones.
+    static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes / 2 * 2);
+    // cp.async: units whose copies are on their way. At most so many that the next keys come
+    // without the last values' place.
+    static constexpr int kLag = kStages / 2;
     static_assert(kStages >= 4, "a key and a value tile in use while others are on their way");
     static constexpr int kRingOffset = NT * kQBytes;
-    static constexpr int kPlacesOffset = kRingOffset + kStages * kUnitBytes;  // [2][kTokens] of a tile
     static constexpr int kMaskWords = (kTokens + 31) / 32;
-    static constexpr int kMaskOffset = kPlacesOffset + 2 * kTokens * 8;  // [kMaskRing][kMaskWords]
+    static constexpr int kMaskOffset = kRingOffset + kStages * kUnitBytes;  // [kMaskRing][kMaskWords]
     static constexpr int kBarOffset = kMaskOffset + kMaskRing * kMaskWords * 4;
     static constexpr int kBars = 2 * kStages + 2 * 5 + 1;
     static constexpr int kTailOffset = kBarOffset + kBars * 8;  // tensor memory base, abort flag
     static constexpr int kBytes = kTailOffset + 16;
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
     static_assert(kDynamicBytes <= 232448, "shared memory of a CTA");
-    static constexpr int kLoaderWarp = NT * 4, kMmaWarp = NT * 4 + 2;
-    static constexpr int kThreads = (NT * 4 + 4) * 32;  // NT = 1: one warp of the last four is idle
-    // Registers a thread: a row of scores is kept in them. Three groups of four warps get
-    // 168 each at the launch; the softmax takes what the others give.
-    static constexpr int kSoftmaxRegisters = 200, kOtherRegisters = 104;
-    static_assert(2 * kSoftmaxRegisters + kOtherRegisters <= 3 * 168, "registers of the block");
+    static constexpr int kLoaders = 4;  // warps
+    static constexpr int kLoaderWarp = NT * 4, kScoresWarp = kLoaderWarp + kLoaders, kValuesWarp = kScoresWarp + 1;
+    static constexpr int kThreads = (NT * 4 + 8) * 32;  // groups of four warps, the last not full
+    // Registers a thread: a row of scores is kept in them. The groups get 128 each (one tile:
+    // 168) at the launch; the softmax takes what the others give.
+    static constexpr int kSoftmaxRegisters = NT == 2 ? 168 : 216, kOtherRegisters = NT == 2 ? 88 : 144;
+    static_assert(NT * kSoftmaxRegisters + 2 * kOtherRegisters <= (NT == 2 ? 4 * 128 : 3 * 168), "registers of the block");
     // Tensor memory: scores, weights and output of each tile.
     static constexpr int kPCol = NT * kTokens, kOCol = kPCol + NT * (kTokens / 2);
     static constexpr int kTmemCols = kOCol + NT * D <= 256 ? 256 : 512;
@@ -150,8 +152,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 32);
-            ptx::mbar_init(bar_empty + 8 * s, NT);
+            ptx::mbar_init(bar_full + 8 * s, S::kLoaders);
+            ptx::mbar_init(bar_empty + 8 * s, s % 2 == 0 ? 1 : NT);  // what reads keys, values
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar_q + 8 * i, 128);
@@ -160,11 +162,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             ptx::mbar_init(bar_p + 8 * i, 128);
             ptx::mbar_init(bar_pv + 8 * i, 1);
         }
-        ptx::mbar_init(bar_drain, NT);
+        ptx::mbar_init(bar_drain, 1 + NT);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
     }
-    if (warp == S::kMmaWarp) {
+    if (warp == S::kScoresWarp) {
         ptx::tmem_alloc(sbase + S::kTailOffset, S::kTmemCols);
         ptx::tmem_relinquish();
     }
@@ -183,11 +185,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_prefix_err, kErrRange);
         length = length < 0 ? 0 : a.capacity;
     }
-    const int steps = (length + kTokens - 1) / kTokens;  // of a unit
-    const int total = steps * a.units;                   // below 2^31 (host check)
-    const int ctas = prefix_ctas(gridDim.x, total), cta = blockIdx.x;
-    const int x_begin = cta < ctas ? prefix_begin(total, ctas, cta) : 0;
-    const int x_end = cta < ctas ? prefix_begin(total, ctas, cta + 1) : 0;
+    const int steps = (length + kTokens - 1) / kTokens;  // of a key head
+    const int total = steps * a.kv_heads;                // below 2^31 (host check)
+    const int ranges = prefix_cut(a.ranges, total);
+    // This CTA's range of tiles, and the blocks that it goes through it for: lane, lane + lanes, ..
+    const int range = blockIdx.x / a.lanes, lane_block = blockIdx.x - range * a.lanes;
+    const int x_begin = range < ranges ? prefix_begin(total, ranges, range) : 0;
+    const int x_end = range < ranges ? prefix_begin(total, ranges, range + 1) : 0;
     const int query_rows = a.rows * a.group;
 
     // Wait for the phase of a barrier with this parity; false: aborted.
@@ -217,25 +221,34 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     };
     // The mask words of a tile whose tokens are all there.
     auto whole_mask = [](int i) { return kTokens - i * 32 >= 32 ? 0xFFFFFFFFu : (1u << (kTokens - i * 32) % 32) - 1u; };
-    // A unit's segment of this CTA's range.
+    // The part of this CTA's range in one key head, for one block; in the order of blocks, then
+    // key heads.
     struct Segment {
-        int unit, head, q0, tiles, t, n;  // first query row, tiles of query rows, first step, steps
+        int block, head, q0, tiles, t, n;  // first query row, tiles of query rows, first tile, steps
     };
-    auto segment = [&](int x) {
+    auto segment = [&](int block, int x) {
         Segment s;
-        s.unit = x / steps;
-        s.head = s.unit / a.blocks;
-        s.q0 = (s.unit - s.head * a.blocks) * NT * kPrefixRows;
+        s.block = block;
+        s.head = x / steps;
+        s.q0 = block * NT * kPrefixRows;
         s.tiles = NT == 2 && query_rows - s.q0 > kPrefixRows ? 2 : 1;
-        s.t = x - s.unit * steps;
+        s.t = x - s.head * steps;
         s.n = min(steps - s.t, x_end - x);
         return s;
     };
-
+    // All segments in turn: f(segment) until it is false.
+    auto segments = [&](auto &&f) {
+        for (int block = lane_block; block < a.blocks; block += a.lanes)
+            for (int x = x_begin; x < x_end;) {
+                const Segment s = segment(block, x);
+                if (!f(s)) return;
+                x += s.n;
+            }
+    };
     int issued = 0;  // units that the loader has begun
     if (warp < S::kLoaderWarp) {
         // ---------------- softmax: thread = query row ----------------
-        if constexpr (NT == 2) ptx::take_registers<S::kSoftmaxRegisters>();
+        ptx::take_registers<S::kSoftmaxRegisters>();
         const int tile = warp / 4, row = threadIdx.x % 128;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
         const uint32_t s_addr = lanes + tile * kTokens, p_addr = lanes + S::kPCol + tile * (kTokens / 2);
@@ -245,25 +258,34 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         const uint32_t *masks = reinterpret_cast<const uint32_t *>(smem + S::kMaskOffset);
         uint32_t count = 0;       // steps of this tile of query rows so far
         uint32_t tile_count = 0;  // the CTA's steps before this segment
-        bool ok = true;
-        for (int x = x_begin; ok && x < x_end;) {
-            const Segment seg = segment(x);
-            x += seg.n;
-            tile_count = x - seg.n - x_begin;
-            if (tile >= seg.tiles) continue;
+        segments([&](const Segment &seg) -> bool {
+            const uint32_t first = tile_count;
+            tile_count += seg.n;
+            if (tile >= seg.tiles) return true;
+            bool ok = true;
             // The queries: 16 bytes at a time, consecutive lanes along a row.
             constexpr int kRowChunks = D / 8;
-            for (int i = row; i < kPrefixRows * kRowChunks; i += 128) {
-                const int r = i / kRowChunks, ch = i % kRowChunks, at = seg.q0 + tile * kPrefixRows + r;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (at < query_rows) {
-                    const int q_row = at / a.group, g = at - q_row * a.group;
-                    v = __ldcg(reinterpret_cast<const uint4 *>(
-                        a.q + q_row * a.q_stride + static_cast<long long>(seg.head * a.group + g) * D + ch * 8));
-                    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+            static_assert(kRowChunks % 4 == 0, "whole rounds of loads");
+#pragma unroll 1
+            for (int i0 = row; i0 < kPrefixRows * kRowChunks; i0 += 4 * 128) {
+                uint4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + u * 128, at = seg.q0 + tile * kPrefixRows + i / kRowChunks;
+                    v[u] = make_uint4(0, 0, 0, 0);
+                    if (at < query_rows) {
+                        const int q_row = at / a.group, g = at - q_row * a.group;
+                        v[u] = __ldcg(reinterpret_cast<const uint4 *>(
+                            a.q + q_row * a.q_stride + static_cast<long long>(seg.head * a.group + g) * D + i % kRowChunks * 8));
+                    }
                 }
-                *reinterpret_cast<uint4 *>(smem + tile * S::kQBytes + ch / 8 * S::kQChunkBytes + r * 128 +
-                                           ((ch ^ r) & 7) * 16) = v;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + u * 128, r = i / kRowChunks, ch = i % kRowChunks;
+                    v[u].x ^= flip, v[u].y ^= flip, v[u].z ^= flip, v[u].w ^= flip;
+                    *reinterpret_cast<uint4 *>(smem + tile * S::kQBytes + ch / 8 * S::kQChunkBytes + r * 128 +
+                                               ((ch ^ r) & 7) * 16) = v[u];
+                }
             }
             ptx::fence_proxy_async_shared();
             ptx::mbar_arrive(bar_q + 8 * tile);
@@ -276,7 +298,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 ptx::tmem_ld_now(s_addr, w);
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(bar_free + 8 * tile);
-                const uint32_t *mask = masks + (tile_count + j) % kMaskRing * S::kMaskWords;
+                const uint32_t *mask = masks + (first + j) % kMaskRing * S::kMaskWords;
                 bool all = true;
 #pragma unroll
                 for (int i = 0; i < S::kMaskWords; ++i) all &= mask[i] == whole_mask(i);
@@ -350,12 +372,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(bar_p + 8 * tile);
             }
-            if (!ok) break;
-            if (!(ok = warp_wait(bar_pv + 8 * tile, (count - 1) & 1))) break;
+            if (!ok || !warp_wait(bar_pv + 8 * tile, (count - 1) & 1)) return false;
             ptx::tc_fence_after_sync();
             // This segment's partial.
             const int at = tile * kPrefixRows + row;
-            float *slot = a.slots + static_cast<size_t>(cta + seg.unit) * a.slot_floats;
+            float *slot = a.slots + (static_cast<size_t>(range + seg.head) * a.blocks + seg.block) * a.slot_floats;
             float *to = slot + static_cast<size_t>(at) * D;
             const bool real = seg.q0 + at < query_rows;
 #pragma unroll 1
@@ -372,31 +393,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 __stcg(slot + NT * kPrefixRows * (D + 1) + at, l);
             }
             ptx::tc_fence_before_sync();  // O is read: before the next segment's arrival
-        }
-    } else if (warp < S::kMmaWarp) {
-        // ---------------- loader ----------------
-        if constexpr (NT == 2) ptx::give_registers<S::kOtherRegisters>();
-        const int kv = warp - S::kLoaderWarp;  // 0: keys, 1: values
-        const uint16_t *from = kv == 0 ? a.k : a.v;
-        const CUtensorMap *map = kv == 0 ? &k_map : &v_map;
-        // Element offsets of a tile's tokens, -1: none.
-        long long *places = reinterpret_cast<long long *>(smem + S::kPlacesOffset) + kv * kTokens;
+            return true;
+        });
+    } else if (warp < S::kScoresWarp) {
+        // ---------------- loaders ----------------
+        ptx::give_registers<S::kOtherRegisters>();
+        const int loader = warp - S::kLoaderWarp;
         uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::kMaskOffset);
-        constexpr int kRowChunks = D / 8, kCopies = kTokens * kRowChunks / 32;
-        constexpr int kMine = (kTokens + 31) / 32;  // tokens whose places a lane looks up
-        static_assert(kTokens * kRowChunks % 32 == 0 && kTokens % 16 == 0, "whole rounds");
-        int unit = kv;  // of the ring, so far
+        constexpr int kRowChunks = D / 8, kRows = kTokens / S::kLoaders;  // cp.async: a warp's rows of a tile
+        static_assert(kTokens / 8 <= 32 && kRows <= 32 && kRows * kRowChunks % 32 == 0, "a lane a box, or a row");
+        int unit = 0;  // of the ring, so far
+        uint32_t tile_count = 0;
         bool ok = true;
-        auto publish = [&](int u) {  // a unit whose copies are complete
+        auto publish = [&](int u) {  // this warp's part of a unit whose copies are complete
             ptx::fence_proxy_async_shared();
-            ptx::mbar_arrive(bar_full + 8 * (u % kStages));
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_full + 8 * (u % kStages));
         };
-        static_assert(kTokens / 8 <= 32, "a lane a box");
-        const int boxes = a.box_rows > 0 ? kTokens / a.box_rows : 0;
+        const int boxes = a.box_rows > 0 ? kTokens / a.box_rows : 0, items = boxes * S::kChunks;
+        // This warp's bytes of a unit that comes by boxes.
+        const int box_bytes = (items - loader + S::kLoaders - 1) / S::kLoaders * a.box_rows * 128;
         auto boxed = [&](int tile) { return boxes > 0 && (tile + 1) * kTokens <= length; };
-        int segment_unit = 0, head = 0, t = 0;
-        // The next tile's places: of a box (page and token within it) or of tokens.
-        long long next[kMine];
+        int head = 0, t = 0;  // of the tile that is looked up
+        // Its places: lane's box (page and token within it), or the lane's row of this warp's.
+        long long next = -1;
         int next_page = 0, next_token = 0;
         auto look_up = [&]() {
             if (boxed(t)) {
@@ -405,267 +425,277 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 const int e = a.page_shift >= 0 ? token >> a.page_shift : token / a.page_size;
                 next_page = __ldcg(a.table + e);
                 next_token = token - e * a.page_size;
-            } else {
-#pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    next[i] = i * 32 + lane < kTokens ? place(head, t * kTokens + i * 32 + lane) : -1;
+            } else if (lane < kRows) {
+                next = place(head, t * kTokens + loader * kRows + lane);
             }
         };
         if (x_begin < x_end) {
-            segment_unit = x_begin / steps;
-            head = segment_unit / a.blocks;
-            t = x_begin - segment_unit * steps;
+            head = x_begin / steps;
+            t = x_begin - head * steps;
             look_up();
         }
-        for (int x = x_begin; x < x_end; ++x, unit += 2) {
-            uint32_t *mask = masks + (x - x_begin) % kMaskRing * S::kMaskWords;
-            const bool by_box = boxed(t);
-            const int this_head = head, s = unit % kStages, token = next_token;
-            const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
-            int page = next_page;
-            if (by_box) {
-                const bool there = lane >= boxes || (page >= 0 && page < a.num_pages);
-                const uint32_t good = __ballot_sync(0xFFFFFFFFu, there);
-                if (!there) {
-                    atomicOr(&g_prefix_err, kErrRange);
-                    page = a.num_pages;  // past the end: zeros
-                }
-                if (kv == 0 && lane < S::kMaskWords) {
-                    uint32_t bits = whole_mask(lane);
-                    if (good != 0xFFFFFFFFu) {
-                        bits = 0;
-                        for (int e = 0; e < 32 && lane * 32 + e < kTokens; ++e)
-                            bits |= (good >> ((lane * 32 + e) / a.box_rows) & 1u) << e;
+        const int first_head = head, first_t = t;
+        for (int block = lane_block; ok && block < a.blocks; block += a.lanes) {
+            for (int x = x_begin; ok && x < x_end; ++x, ++tile_count) {
+                uint32_t *mask = masks + tile_count % kMaskRing * S::kMaskWords;
+                const bool by_box = boxed(t);
+                const int this_head = head, token = next_token;
+                const long long row_at = next;
+                int page = next_page;
+                if (by_box) {
+                    const bool there = lane >= boxes || (page >= 0 && page < a.num_pages);
+                    const uint32_t good = __ballot_sync(0xFFFFFFFFu, there);
+                    if (!there) {
+                        atomicOr(&g_prefix_err, kErrRange);
+                        page = a.num_pages;  // past the end: zeros
                     }
-                    mask[lane] = bits;
+                    if (loader == 0 && lane < S::kMaskWords) {
+                        uint32_t bits = whole_mask(lane);
+                        if (good != 0xFFFFFFFFu) {
+                            bits = 0;
+                            for (int e = 0; e < 32 && lane * 32 + e < kTokens; ++e)
+                                bits |= (good >> ((lane * 32 + e) / a.box_rows) & 1u) << e;
+                        }
+                        mask[lane] = bits;
+                    }
+                } else {
+                    if (lane < kRows && row_at < 0 && t * kTokens + loader * kRows + lane < length)
+                        atomicOr(&g_prefix_err, kErrRange);
+                    if (loader == 0) {
+                        for (int i = 0; i < S::kMaskWords; ++i) {
+                            const int at = i * 32 + lane;
+                            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, at < kTokens && place(head, t * kTokens + at) >= 0);
+                            if (lane == 0) mask[i] = bits;
+                        }
+                    }
                 }
-            } else {
-                __syncwarp();  // the places of the tile before are read
-#pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    const int at = i * 32 + lane;
-                    const uint32_t there = __ballot_sync(0xFFFFFFFFu, next[i] >= 0);
-                    if (at >= kTokens) continue;
-                    if (next[i] < 0 && t * kTokens + at < length) atomicOr(&g_prefix_err, kErrRange);
-                    places[at] = next[i];
-                    if (kv == 0 && lane == 0) mask[i] = there;
+                if (x + 1 == x_end) {  // the next block's first
+                    head = first_head;
+                    t = first_t;
+                } else if (++t == steps) {
+                    t = 0;
+                    ++head;
                 }
-                __syncwarp();
-            }
-            if (++t == steps) {
-                t = 0;
-                head = ++segment_unit / a.blocks;
-            }
-            if (x + 1 < x_end) look_up();
-            // The first round finds the stages free.
-            if (!(ok = warp_wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1))) break;
-            if (by_box) {
-                if (lane == 0)
-                    ptx::mbar_arrive_expect_tx(bar_full + 8 * s, S::kUnitBytes);
-                else
-                    ptx::mbar_arrive(bar_full + 8 * s);
-                // One lane issues: with a lane a box the boxes come one after another too, and the
-                // loop that makes them is longer.
-                for (int b = 0; b < boxes; ++b) {
-                    const int box_page = __shfl_sync(0xFFFFFFFFu, page, b), box_token = __shfl_sync(0xFFFFFFFFu, token, b);
-                    if (lane == 0)
-#pragma unroll
-                        for (int ch = 0; ch < S::kChunks; ++ch)
-                            ptx::tma_load_4d(to + ch * (kTokens * 128) + b * a.box_rows * 128, map, bar_full + 8 * s,
-                                             ch * 64, box_token, this_head, box_page);
+                if (x + 1 < x_end || block + a.lanes < a.blocks) look_up();
+                for (int kv = 0; kv < 2; ++kv, ++unit) {
+                    const int s = unit % kStages;
+                    const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
+                    // The first round finds the stages free.
+                    if (!(ok = warp_wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1))) break;
+                    if (by_box) {
+                        __syncwarp();  // loader 0: the mask is written
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full + 8 * s, box_bytes);
+                        __syncwarp();
+                        // The lanes' boxes come one after another.
+                        const int item = loader + lane * S::kLoaders, box = item / S::kChunks, ch = item - box * S::kChunks;
+                        const int box_page = __shfl_sync(0xFFFFFFFFu, page, box & 31);
+                        const int box_token = __shfl_sync(0xFFFFFFFFu, token, box & 31);
+                        if (item < items)
+                            ptx::tma_load_4d(to + ch * (kTokens * 128) + box * a.box_rows * 128, kv == 0 ? &k_map : &v_map,
+                                             bar_full + 8 * s, ch * 64, box_token, this_head, box_page);
+                        continue;
+                    }
+                    const uint16_t *from = kv == 0 ? a.k : a.v;
+#pragma unroll 4
+                    for (int i = 0; i < kRows * kRowChunks / 32; ++i) {
+                        const int id = i * 32 + lane, own = id / kRowChunks, r = loader * kRows + own, ch = id % kRowChunks;
+                        const long long at = __shfl_sync(0xFFFFFFFFu, row_at, own);
+                        cp_async16_or_zeros(to + ch / 8 * (kTokens * 128) + r * 128 + ((ch ^ r) & 7) * 16,
+                                            from + (at < 0 ? 0 : at) + ch * 8, at >= 0);
+                    }
+                    cp_async_commit();
+                    if (boxes > 0) {  // the tile that the prefix ends in
+                        cp_async_wait<0>();
+                        publish(unit);
+                    } else if (unit >= S::kLag) {
+                        cp_async_wait<S::kLag>();
+                        publish(unit - S::kLag);
+                    }
                 }
-                continue;
-            }
-#pragma unroll 8
-            for (int i = 0; i < kCopies; ++i) {
-                const int id = i * 32 + lane, r = id / kRowChunks, ch = id % kRowChunks;
-                const long long at = places[r];
-                cp_async16_or_zeros(to + ch / 8 * (kTokens * 128) + r * 128 + ((ch ^ r) & 7) * 16,
-                                    from + (at < 0 ? 0 : at) + ch * 8, at >= 0);
-            }
-            cp_async_commit();
-            if (boxes > 0) {  // the tile that the prefix ends in
-                cp_async_wait<0>();
-                publish(unit);
-            } else if (unit >= 2 * S::kLag) {
-                cp_async_wait<S::kLag>();
-                publish(unit - 2 * S::kLag);
             }
         }
         issued = boxes > 0 ? unit : 0;
         cp_async_wait<0>();
         if (ok && boxes == 0)
-            for (int u = max(kv, unit - 2 * S::kLag); u < unit; u += 2) publish(u);
+            for (int u = max(0, unit - S::kLag); u < unit; ++u) publish(u);
     } else {
-        if constexpr (NT == 2) ptx::give_registers<S::kOtherRegisters>();
+        ptx::give_registers<S::kOtherRegisters>();
     }
-    if (warp >= S::kMmaWarp && warp < S::kMmaWarp + NT && lane == 0) {
-        // ---------------- MMA issuer of one tile ----------------
-        // One for each: the waits and commits of one (about half of a step's time for a single
-        // issuer: 155 us for 65521 tokens of 8 key heads and 448 query rows) pass while the
-        // other's products run.
-        const int tile = warp - S::kMmaWarp;
-        constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kPrefixRows, kTokens);
-        constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(kPrefixRows, D) | ptx::kIdescBMnMajor;
+    auto full = [&](int u) {
+        if (!wait(bar_full + 8 * (u % kStages), (u / kStages) & 1)) return false;
+        ptx::tc_fence_after_sync();
+        return true;
+    };
+    // The issuers are one thread each: the waits and commits of one (half of a step's time for a
+    // single issuer) pass while another's products run.
+    if (warp == S::kScoresWarp && lane == 0) {
+        // ---------------- MMA issuer: scores ----------------
+        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kPrefixRows, kTokens);
         int unit = 0;
-        uint32_t scored = 0, added = 0, segments = 0;  // steps and segments of this tile
-        bool ok = true;
-        auto full = [&](int u) {
-            if (!wait(bar_full + 8 * (u % kStages), (u / kStages) & 1)) return false;
-            ptx::tc_fence_after_sync();
-            return true;
-        };
-        // A unit is free when every tile's products with it are complete; a segment's only tile
-        // speaks for both.
-        auto release = [&](int u, bool alone) {
-            ptx::mma_commit(bar_empty + 8 * (u % kStages));
-            if (NT == 2 && alone) ptx::mma_commit(bar_empty + 8 * (u % kStages));
-        };
-        // The scores of the next step, with the keys of unit u; the step's before are read.
-        auto scores = [&](int u) {
-            if (scored > 0 && !wait(bar_free + 8 * tile, (scored - 1) & 1)) return false;
-            if (!full(u)) return false;
-            const uint64_t q = ptx::smem_desc_sw128_kmajor(sbase + tile * S::kQBytes);
-            const uint64_t k = ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + u % kStages * S::kUnitBytes);
+        uint32_t scored[2] = {}, loaded[2] = {};  // steps and segments, by tile
+        segments([&](const Segment &seg) -> bool {
+            for (int j = 0; j < seg.n; ++j, unit += 2) {
+                const uint64_t k = ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes);
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)  // addresses in the descriptors are in units of 16 bytes
-                ptx::mma_bf16(tmem + tile * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
-                              k + s / 4 * (kTokens * 8) + s % 4 * 2, idesc_s, s > 0);
-            ptx::mma_commit(bar_s + 8 * tile);
-            ptx::mbar_arrive(bar_s + 8 * tile);  // what the loader wrote before the keys, too
-            ++scored;
-            return true;
-        };
-        // O += the step's weights by the values of unit u.
-        auto values = [&](int u, bool first) {
-            if (!full(u) || !wait(bar_p + 8 * tile, added++ & 1)) return false;
-            ptx::tc_fence_after_sync();
-            const uint64_t v =
-                ptx::smem_desc_sw128_mnmajor(sbase + S::kRingOffset + u % kStages * S::kUnitBytes, kTokens * 128);
+                for (int i = 0; i < NT; ++i) {
+                    if (i >= seg.tiles) break;
+                    if (j == 0 && !wait(bar_q + 8 * i, loaded[i]++ & 1)) return false;
+                    if (i == 0 && !full(unit)) return false;
+                    // The step's before are read.
+                    if (scored[i] > 0 && !wait(bar_free + 8 * i, (scored[i] - 1) & 1)) return false;
+                    ptx::tc_fence_after_sync();
+                    const uint64_t q = ptx::smem_desc_sw128_kmajor(sbase + i * S::kQBytes);
 #pragma unroll
-            for (int s = 0; s < kTokens / 16; ++s)
-                ptx::mma_bf16_tmem_a(tmem + S::kOCol + tile * D, tmem + S::kPCol + tile * (kTokens / 2) + s * 8,
-                                     v + s * 128, idesc_o, s > 0 || !first);
-            ptx::mma_commit(bar_pv + 8 * tile);
+                    for (int s = 0; s < D / 16; ++s)  // addresses in the descriptors are in units of 16 bytes
+                        ptx::mma_bf16(tmem + i * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
+                                      k + s / 4 * (kTokens * 8) + s % 4 * 2, idesc, s > 0);
+                    ptx::mma_commit(bar_s + 8 * i);
+                    ptx::mbar_arrive(bar_s + 8 * i);  // what the loader wrote before the keys, too
+                    ++scored[i];
+                }
+                ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+            }
             return true;
-        };
-        for (int x = x_begin; ok && x < x_end;) {
-            const Segment seg = segment(x);
-            x += seg.n;
+        });
+    } else if (warp >= S::kValuesWarp && warp < S::kValuesWarp + NT && lane == 0) {
+        // ---------------- MMA issuer: one tile's output ----------------
+        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kPrefixRows, D) | ptx::kIdescBMnMajor;
+        const int tile = warp - S::kValuesWarp;
+        int unit = 1;
+        uint32_t added = 0;
+        segments([&](const Segment &seg) -> bool {
             if (tile >= seg.tiles) {
                 unit += 2 * seg.n;
-                continue;
+                return true;
             }
-            const bool alone = seg.tiles == 1;
-            if (!(ok = wait(bar_q + 8 * tile, segments++ & 1) && scores(unit))) break;
-            release(unit++, alone);
-            for (int j = 0; j < seg.n; ++j) {
-                const bool more = j + 1 < seg.n;
-                if (more) {
-                    if (!(ok = scores(unit + 1))) break;
-                    release(unit + 1, alone);
-                }
-                if (!(ok = values(unit, j == 0))) break;
-                release(unit, alone);
-                unit += more ? 2 : 1;
+            for (int j = 0; j < seg.n; ++j, unit += 2) {
+                if (!full(unit) || !wait(bar_p + 8 * tile, added++ & 1)) return false;
+                ptx::tc_fence_after_sync();
+                const uint64_t v =
+                    ptx::smem_desc_sw128_mnmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes, kTokens * 128);
+#pragma unroll
+                for (int s = 0; s < kTokens / 16; ++s)
+                    ptx::mma_bf16_tmem_a(tmem + S::kOCol + tile * D, tmem + S::kPCol + tile * (kTokens / 2) + s * 8,
+                                         v + s * 128, idesc, s > 0 || j > 0);
+                ptx::mma_commit(bar_pv + 8 * tile);
+                ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+                // A segment's only tile speaks for both.
+                if (NT == 2 && seg.tiles == 1) ptx::mma_commit(bar_empty + 8 * (unit % kStages));
             }
-        }
+            return true;
+        });
     }
     __syncwarp();
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (*abort_flag) {
         // Nothing may still read this CTA's shared or tensor memory when it ends.
-        if (warp >= S::kMmaWarp && warp < S::kMmaWarp + NT && lane == 0) {
+        if (warp >= S::kScoresWarp && warp < S::kValuesWarp + NT && lane == 0) {
             ptx::mma_commit(bar_drain);
             const uint64_t t0 = ptx::global_timer_ns();
             while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::global_timer_ns() - t0 < kDrainLimitNs) {
             }
         }
-        if (warp >= S::kLoaderWarp && warp < S::kMmaWarp && lane == 0) {
+        if (warp >= S::kLoaderWarp && warp < S::kScoresWarp && lane == 0) {
             const uint64_t t0 = ptx::global_timer_ns();
-            for (int u = max(warp - S::kLoaderWarp, issued - kStages / 2 * 2); u < issued; u += 2)
+            for (int u = max(0, issued - kStages); u < issued; ++u)
                 while (!ptx::mbar_try_wait(bar_full + 8 * (u % kStages), (u / kStages) & 1) &&
                        ptx::global_timer_ns() - t0 < kDrainLimitNs) {
                 }
         }
         __syncthreads();
     }
-    if (warp == S::kMmaWarp) {
+    if (warp == S::kScoresWarp) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, S::kTmemCols);
     }
 }
 
 // ---- the join ----
-// One warp for one head of one row: the prefix's partials of its query row, in order, and the
-// row's own tokens' result. Read once each, all in L2.
+// One CTA for one head of one row: the prefix's partials of its query row, dealt to the warps,
+// and the row's own tokens' result; then the warps' sums in order. All in L2, read once.
 constexpr int kJoinWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const PrefixArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const PrefixArgs a) {
     constexpr int kValues = D / 32, kAhead = D <= 128 ? 8 : 4;
-    const int lane = threadIdx.x % 32;
-    const int job = blockIdx.x * kJoinWarps + threadIdx.x / 32;
+    __shared__ float sm_top[kJoinWarps], sm_weight[kJoinWarps], sm_o[kJoinWarps][D];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int job = blockIdx.x;
     ptx::pdl_launch_dependents();
-    ptx::pdl_wait();
-    if (job >= a.rows * a.q_heads) return;
     const int row = job / a.q_heads, h = job - row * a.q_heads;
     const int head = h / a.group, at = row * a.group + h - head * a.group;  // query row of the key head
+    const int per = kPrefixRows * prefix_tiles(D, static_cast<long long>(a.rows) * a.group);
+    const int block = at / per, in_block = at - block * per;
+    ptx::pdl_wait();
     const int length = min(max(__ldcg(a.length), 0), a.capacity);
-    const int tokens = a.tokens, per = kPrefixRows * prefix_tiles(D, static_cast<long long>(a.rows) * a.group);
-    const int steps = (length + tokens - 1) / tokens, total = steps * a.units;
-    const int ctas = prefix_ctas(grid, total);
-    const int unit = head * a.blocks + at / per, in_unit = at % per;
-    const int first = total > 0 ? prefix_owner(total, ctas, unit * steps) : 0;
-    const int parts = total > 0 ? prefix_owner(total, ctas, unit * steps + steps - 1) - first + 1 : 0;
-    const float *slots = a.slots + static_cast<size_t>(first + unit) * a.slot_floats;
-    const float *maxima = slots + static_cast<size_t>(per) * D + in_unit, *sums = maxima + per;
-    const float *values = slots + static_cast<size_t>(in_unit) * D + lane;
+    const int steps = (length + a.tokens - 1) / a.tokens, total = steps * a.kv_heads;
+    const int ranges = prefix_cut(a.ranges, total);
+    const int first = total > 0 ? prefix_owner(total, ranges, head * steps) : 0;
+    const int parts = total > 0 ? prefix_owner(total, ranges, head * steps + steps - 1) - first + 1 : 0;
+    const float *slots = a.slots + (static_cast<size_t>(first + head) * a.blocks + block) * a.slot_floats;
+    const size_t stride = static_cast<size_t>(a.blocks) * a.slot_floats;  // from part to part
+    const float *maxima = slots + static_cast<size_t>(per) * D + in_block, *sums = maxima + per;
+    const float *values = slots + static_cast<size_t>(in_block) * D + lane;
 
-    const float own = __ldcg(a.own_lse + job) * kLog2e;  // its sum of weights is 2^own
-    float o[kValues], top = fmaxf(own, kNoMaximum);
-    for (int s = lane; s < parts; s += 32) top = fmaxf(top, __ldcg(maxima + s * a.slot_floats));
+    // This warp's parts, and the first warp's share in the row's own tokens (sum of weights 2^own).
+    const float own = warp == 0 ? __ldcg(a.own_lse + job) * kLog2e : -INFINITY;
+    float o[kValues], top = fmaxf(own, kNoMaximum), weight = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kValues; ++e) o[e] = own != -INFINITY ? __ldcg(a.own_out + static_cast<size_t>(job) * D + lane + e * 32) : 0.0f;
+    for (int s = warp + lane * kJoinWarps; s < parts; s += 32 * kJoinWarps) top = fmaxf(top, __ldcg(maxima + s * stride));
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-    float total_weight = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kValues; ++e) o[e] = 0.0f;
     if (own != -INFINITY) {
-        const float w = exp2_approx(own - top);
-        total_weight = w;
+        weight = exp2_approx(own - top);
 #pragma unroll
-        for (int e = 0; e < kValues; ++e) o[e] = w * __ldcg(a.own_out + static_cast<size_t>(job) * D + lane + e * 32);
+        for (int e = 0; e < kValues; ++e) o[e] *= weight;
     }
-    for (int s0 = 0; s0 < parts; s0 += kAhead) {
+    for (int s0 = warp; s0 < parts; s0 += kAhead * kJoinWarps) {
         float m[kAhead], l[kAhead], v[kAhead][kValues];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (s0 + u >= parts) break;
-            m[u] = __ldcg(maxima + (s0 + u) * a.slot_floats);
-            l[u] = __ldcg(sums + (s0 + u) * a.slot_floats);
+            const size_t s = s0 + u * kJoinWarps;
+            if (s >= static_cast<size_t>(parts)) break;
+            m[u] = __ldcg(maxima + s * stride);
+            l[u] = __ldcg(sums + s * stride);
 #pragma unroll
-            for (int e = 0; e < kValues; ++e) v[u][e] = __ldcg(values + (s0 + u) * a.slot_floats + e * 32);
+            for (int e = 0; e < kValues; ++e) v[u][e] = __ldcg(values + s * stride + e * 32);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (s0 + u >= parts) break;
+            if (s0 + u * kJoinWarps >= parts) break;
             const float w = exp2_approx(m[u] - top);
-            total_weight += w * l[u];
+            weight += w * l[u];
 #pragma unroll
             for (int e = 0; e < kValues; ++e) o[e] += w * v[u][e];
         }
     }
-    const float inv = total_weight == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_weight);
+    if (lane == 0) sm_top[warp] = top, sm_weight[warp] = weight;
 #pragma unroll
-    for (int e = 0; e < kValues; ++e)
-        a.out[static_cast<size_t>(job) * D + lane + e * 32] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * inv));
-    if (a.lse != nullptr && lane == 0)
-        a.lse[job] = total_weight > 0.0f || total_weight != total_weight ? (top + log2f(total_weight)) * kLn2 : -INFINITY;
+    for (int e = 0; e < kValues; ++e) sm_o[warp][lane + e * 32] = o[e];
+    __syncthreads();
+    float all = sm_top[0], sum = 0.0f, f[kJoinWarps];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) all = fmaxf(all, sm_top[w]);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        f[w] = exp2_approx(sm_top[w] - all);
+        sum += f[w] * sm_weight[w];
+    }
+    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+    for (int i = threadIdx.x; i < D; i += kJoinWarps * 32) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) v += f[w] * sm_o[w][i];
+        a.out[static_cast<size_t>(job) * D + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v * inv));
+    }
+    if (a.lse != nullptr && threadIdx.x == 0)
+        a.lse[job] = sum > 0.0f || sum != sum ? (all + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <int D, int NT>
-cudaError_t launch_prefix(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a, int grid,
+cudaError_t launch_prefix(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
                           int device, cudaStream_t stream, bool pdl) {
     using S = Shape<D, NT>;
     static bool configured[64] = {};
@@ -677,7 +707,7 @@ cudaError_t launch_prefix(const CUtensorMap &k_map, const CUtensorMap &v_map, co
         configured[device] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.gridDim = dim3(a.ranges * a.lanes, 1, 1);
     cfg.blockDim = dim3(S::kThreads, 1, 1);
     cfg.dynamicSmemBytes = S::kDynamicBytes;
     cfg.stream = stream;
@@ -690,10 +720,9 @@ cudaError_t launch_prefix(const CUtensorMap &k_map, const CUtensorMap &v_map, co
 }
 
 template <int D>
-cudaError_t launch_join(const PrefixArgs &a, int grid, cudaStream_t stream) {
+cudaError_t launch_join(const PrefixArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    const int jobs = a.rows * a.q_heads;
-    cfg.gridDim = dim3((jobs + kJoinWarps - 1) / kJoinWarps, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.q_heads, 1, 1);
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -701,12 +730,7 @@ cudaError_t launch_join(const PrefixArgs &a, int grid, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;  // behind the library's own kernels
-    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<D>, a, grid);
-}
-
-// CTAs of the prefix's kernel: no more than the table could ever hold steps.
-int grid_of(const PrefixArgs &a, int num_sms) {
-    return static_cast<int>(std::min<long long>(num_sms, (a.capacity + a.tokens - 1ll) / a.tokens * a.units));
+    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<D>, a);
 }
 
 }  // namespace
@@ -717,33 +741,31 @@ int prefix_box_rows(int page_size, int tokens) {
 }
 
 cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
-                                    int head_dim, int num_sms, int device, cudaStream_t stream, bool pdl) {
-    const int grid = grid_of(a, num_sms);
+                                    int head_dim, int device, cudaStream_t stream, bool pdl) {
     const bool two = prefix_tiles(head_dim, static_cast<long long>(a.rows) * a.group) == 2;
     switch (head_dim) {
         case 64:
-            if (two) return launch_prefix<64, 2>(k_map, v_map, a, grid, device, stream, pdl);
-            return launch_prefix<64, 1>(k_map, v_map, a, grid, device, stream, pdl);
+            if (two) return launch_prefix<64, 2>(k_map, v_map, a, device, stream, pdl);
+            return launch_prefix<64, 1>(k_map, v_map, a, device, stream, pdl);
         case 96:
-            if (two) return launch_prefix<96, 2>(k_map, v_map, a, grid, device, stream, pdl);
-            return launch_prefix<96, 1>(k_map, v_map, a, grid, device, stream, pdl);
+            if (two) return launch_prefix<96, 2>(k_map, v_map, a, device, stream, pdl);
+            return launch_prefix<96, 1>(k_map, v_map, a, device, stream, pdl);
         case 128:
-            if (two) return launch_prefix<128, 2>(k_map, v_map, a, grid, device, stream, pdl);
-            return launch_prefix<128, 1>(k_map, v_map, a, grid, device, stream, pdl);
-        case 192: return launch_prefix<192, 1>(k_map, v_map, a, grid, device, stream, pdl);
-        case 256: return launch_prefix<256, 1>(k_map, v_map, a, grid, device, stream, pdl);
+            if (two) return launch_prefix<128, 2>(k_map, v_map, a, device, stream, pdl);
+            return launch_prefix<128, 1>(k_map, v_map, a, device, stream, pdl);
+        case 192: return launch_prefix<192, 1>(k_map, v_map, a, device, stream, pdl);
+        case 256: return launch_prefix<256, 1>(k_map, v_map, a, device, stream, pdl);
         default: return cudaErrorInvalidValue;
     }
 }
 
-cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream) {
-    const int grid = grid_of(a, num_sms);
+cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, cudaStream_t stream) {
     switch (head_dim) {
-        case 64: return launch_join<64>(a, grid, stream);
-        case 96: return launch_join<96>(a, grid, stream);
-        case 128: return launch_join<128>(a, grid, stream);
-        case 192: return launch_join<192>(a, grid, stream);
-        case 256: return launch_join<256>(a, grid, stream);
+        case 64: return launch_join<64>(a, stream);
+        case 96: return launch_join<96>(a, stream);
+        case 128: return launch_join<128>(a, stream);
+        case 192: return launch_join<192>(a, stream);
+        case 256: return launch_join<256>(a, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -1,13 +1,15 @@
 // Work split of the attention over a shared prefix (shared by the host and the kernels).
 //
 // The query rows of a key head are all rows' heads that share it, row-major: query row
-// i = row * group + head. A unit is one key head with up to 128 (or 2 x 128) of its query
-// rows; a step is one tile of the prefix's tokens for one unit. The steps of all units in
-// (key head, block of query rows, tile) order are one sequence, cut evenly into one range per
-// CTA. A CTA leaves a partial result for every unit that its range touches: the c-th CTA's
-// part of unit u goes to slot c + u, which no other pair has (from one pair to the next in
-// order, either c or u grows by one). The prefix's length lives on the device, so
-// the kernels work the split out for themselves.
+// i = row * group + head; 128 or 2 x 128 of them are a block. A step is one tile of the
+// prefix's tokens for one block. The tiles of all key heads, in (key head, tile) order, are
+// one sequence, cut evenly into ranges; a range is gone through by one CTA for each block (or
+// for each of `lanes` blocks at a time, if there are more blocks than CTAs), all at the same
+// time, so that the keys and values that they share come from HBM once. A CTA leaves a partial
+// result for every key head that its range touches: range r's part of key head h goes to slot
+// (r + h) * blocks + block, and no two pairs have the same r + h (from one pair to the next in
+// order, either r or h grows by one). The prefix's length lives on the device, so the
+// kernels work the cut out for themselves.
 #pragma once
 
 #include <cstddef>
@@ -29,35 +31,40 @@ __host__ __device__ constexpr int prefix_tiles(int head_dim, long long query_row
 // Tokens of a step. In tensor memory (512 columns) every tile has a place for its scores (one
 // column a token), one for its weights (half a column) and one for its output (head_dim
 // columns), all apart, so that the next scores are computed while the softmax runs: 80 or 96
-// tokens for two tiles of wide heads. 64 from 192 on, whose keys and values fill the ring
-// otherwise.
+// tokens for two tiles (96 are as many as a softmax thread has registers for). 64 from 192 on,
+// whose keys and values fill the ring otherwise.
 __host__ __device__ constexpr int prefix_tokens(int head_dim, int tiles) {
-    return head_dim > 128 ? 64 : tiles == 1 || head_dim <= 64 ? 128 : head_dim <= 96 ? 96 : 80;
+    return head_dim > 128 ? 64 : tiles == 1 ? 128 : head_dim <= 96 ? 96 : 80;
 }
 
 struct PrefixPlan {
     int tokens;  // of a step
     int blocks;  // blocks of query rows of a key head
-    int units;   // key heads * blocks
 };
-__host__ __device__ inline PrefixPlan prefix_plan(int rows, int group, int kv_heads, int head_dim) {
+__host__ __device__ inline PrefixPlan prefix_plan(int rows, int group, int head_dim) {
     const long long q = static_cast<long long>(rows) * group;
     const int tiles = prefix_tiles(head_dim, q), per = kPrefixRows * tiles;
     PrefixPlan p;
     p.tokens = prefix_tokens(head_dim, tiles);
     p.blocks = static_cast<int>((q + per - 1) / per);
-    p.units = p.blocks * kv_heads;
     return p;
 }
 
-// CTAs that take part, of `grid`, for `total` steps.
-__host__ __device__ inline int prefix_ctas(int grid, int total) { return total < grid ? total : grid; }
-// First step of CTA c's range, and the CTA that a step is in.
-__host__ __device__ inline int prefix_begin(int total, int ctas, int c) {
-    return static_cast<int>(static_cast<long long>(total) * c / ctas);
+// Blocks that are gone through side by side with `ctas` CTAs, and the most ranges.
+__host__ __device__ inline int prefix_lanes(int blocks, int ctas) {
+    const int passes = (blocks + ctas - 1) / ctas;
+    return (blocks + passes - 1) / passes;
 }
-__host__ __device__ inline int prefix_owner(int total, int ctas, int x) {
-    return static_cast<int>(((static_cast<long long>(x) + 1) * ctas - 1) / total);
+__host__ __device__ inline int prefix_ranges(int blocks, int ctas) { return ctas / prefix_lanes(blocks, ctas); }
+
+// Ranges of `total` tiles, of `most`.
+__host__ __device__ inline int prefix_cut(int most, int total) { return total < most ? total : most; }
+// First tile of range r, and the range that a tile is in.
+__host__ __device__ inline int prefix_begin(int total, int ranges, int r) {
+    return static_cast<int>(static_cast<long long>(total) * r / ranges);
+}
+__host__ __device__ inline int prefix_owner(int total, int ranges, int x) {
+    return static_cast<int>(((static_cast<long long>(x) + 1) * ranges - 1) / total);
 }
 
 // A partial: for each query row of the unit head_dim sums, then all maxima, then all sums of
@@ -73,14 +80,17 @@ struct PrefixWorkspace {
 };
 inline PrefixWorkspace prefix_workspace(int rows, int q_heads, int kv_heads, int head_dim, int sms) {
     const long long q = static_cast<long long>(rows) * (q_heads / kv_heads);
-    const PrefixPlan p = prefix_plan(rows, q_heads / kv_heads, kv_heads, head_dim);
+    const PrefixPlan p = prefix_plan(rows, q_heads / kv_heads, head_dim);
+    // The slots grow with the blocks, so that a workspace does for fewer rows too: at most
+    // sms + key heads * blocks.
+    const size_t slots = static_cast<size_t>(sms) + static_cast<size_t>(kv_heads) * p.blocks;
     const size_t heads = static_cast<size_t>(rows) * q_heads;
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     PrefixWorkspace w;
     w.own_out = up(attn_workspace_bytes(sms));
     w.own_lse = w.own_out + up(heads * head_dim * sizeof(float));
     w.slots = w.own_lse + up(heads * sizeof(float));
-    w.bytes = w.slots + (static_cast<size_t>(sms) + p.units) * prefix_slot_floats(head_dim, q) * sizeof(float);
+    w.bytes = w.slots + slots * prefix_slot_floats(head_dim, q) * sizeof(float);
     return w;
 }
 
