@@ -17,9 +17,8 @@
 //                     (what is behind its end must come out as zeros), by 16-byte cp.async
 //                     with each token's address. Four, because a thread takes some 200 clocks
 //                     to issue a box, of whatever size, and the threads of a warp take turns;
-//   1 MMA warp        the scores of both tiles, S = Q K^T, from shared memory (both K-major)
-//                     into tensor memory;
-//   1 MMA warp a tile O += P V, P in tensor memory and V as it lies, MN-major.
+//   2 MMA warps a tile  the scores, S = Q K^T, from shared memory (both K-major) into tensor
+//                     memory; and O += P V, P in tensor memory and V as it lies, MN-major.
 // Scores, weights and output have places of their own in tensor memory: a softmax thread takes
 // its row of scores into registers and sets their place free, so that the next step's are
 // computed while it works, and the two tiles' softmaxes and products fill each other's gaps.
@@ -100,8 +99,7 @@ struct Shape {
     static constexpr int kQChunkBytes = kPrefixRows * 128;
     static constexpr int kQBytes = kChunks * kQChunkBytes;      // one tile of queries
     static constexpr int kMiscBytes = 768;
-    // Keys in the even stages, values in the odd ones.
-    static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes / 2 * 2);
+    static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes);
     // cp.async: units whose copies are on their way. At most so many that the next keys come
     // without the last values' place.
     static constexpr int kLag = kStages / 2;
@@ -116,7 +114,7 @@ struct Shape {
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
     static_assert(kDynamicBytes <= 232448, "shared memory of a CTA");
     static constexpr int kLoaders = 4;  // warps
-    static constexpr int kLoaderWarp = NT * 4, kScoresWarp = kLoaderWarp + kLoaders, kValuesWarp = kScoresWarp + 1;
+    static constexpr int kLoaderWarp = NT * 4, kScoresWarp = kLoaderWarp + kLoaders, kValuesWarp = kScoresWarp + NT;
     static constexpr int kThreads = (NT * 4 + 8) * 32;  // groups of four warps, the last not full
     // Registers a thread: a row of scores is kept in them. The groups get 128 each (one tile:
     // 168) at the launch; the softmax takes what the others give.
@@ -153,7 +151,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(bar_full + 8 * s, S::kLoaders);
-            ptx::mbar_init(bar_empty + 8 * s, s % 2 == 0 ? 1 : NT);  // what reads keys, values
+            ptx::mbar_init(bar_empty + 8 * s, NT);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar_q + 8 * i, 128);
@@ -162,7 +160,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             ptx::mbar_init(bar_p + 8 * i, 128);
             ptx::mbar_init(bar_pv + 8 * i, 1);
         }
-        ptx::mbar_init(bar_drain, 1 + NT);
+        ptx::mbar_init(bar_drain, 2 * NT);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
     }
@@ -526,39 +524,44 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         ptx::tc_fence_after_sync();
         return true;
     };
-    // The issuers are one thread each: the waits and commits of one (half of a step's time for a
-    // single issuer) pass while another's products run.
-    if (warp == S::kScoresWarp && lane == 0) {
-        // ---------------- MMA issuer: scores ----------------
+    // When every tile's products with a unit are complete it is free; a block's only tile speaks
+    // for both.
+    auto release = [&](int u, bool alone) {
+        ptx::mma_commit(bar_empty + 8 * (u % kStages));
+        if (NT == 2 && alone) ptx::mma_commit(bar_empty + 8 * (u % kStages));
+    };
+    // The issuers are one thread each: the waits and commits of one pass while another's products
+    // run (a single issuer for all four took twice the time).
+    if (warp >= S::kScoresWarp && warp < S::kValuesWarp && lane == 0) {
+        // ---------------- MMA issuer: a tile's scores ----------------
         constexpr uint32_t idesc = ptx::idesc_bf16_f32(kPrefixRows, kTokens);
+        const int tile = warp - S::kScoresWarp;
+        const uint64_t q = ptx::smem_desc_sw128_kmajor(sbase + tile * S::kQBytes);
         int unit = 0;
-        uint32_t scored[2] = {}, loaded[2] = {};  // steps and segments, by tile
+        uint32_t scored = 0, loaded = 0;  // steps and segments
         segments([&](const Segment &seg) -> bool {
-            for (int j = 0; j < seg.n; ++j, unit += 2) {
+            if (tile >= seg.tiles) {
+                unit += 2 * seg.n;
+                return true;
+            }
+            if (!wait(bar_q + 8 * tile, loaded++ & 1)) return false;
+            for (int j = 0; j < seg.n; ++j, ++scored, unit += 2) {
+                // The step's before are read, and the keys are there.
+                if (scored > 0 && !wait(bar_free + 8 * tile, (scored - 1) & 1)) return false;
+                if (!full(unit)) return false;
                 const uint64_t k = ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i >= seg.tiles) break;
-                    if (j == 0 && !wait(bar_q + 8 * i, loaded[i]++ & 1)) return false;
-                    if (i == 0 && !full(unit)) return false;
-                    // The step's before are read.
-                    if (scored[i] > 0 && !wait(bar_free + 8 * i, (scored[i] - 1) & 1)) return false;
-                    ptx::tc_fence_after_sync();
-                    const uint64_t q = ptx::smem_desc_sw128_kmajor(sbase + i * S::kQBytes);
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)  // addresses in the descriptors are in units of 16 bytes
-                        ptx::mma_bf16(tmem + i * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
-                                      k + s / 4 * (kTokens * 8) + s % 4 * 2, idesc, s > 0);
-                    ptx::mma_commit(bar_s + 8 * i);
-                    ptx::mbar_arrive(bar_s + 8 * i);  // what the loader wrote before the keys, too
-                    ++scored[i];
-                }
-                ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+                for (int s = 0; s < D / 16; ++s)  // addresses in the descriptors are in units of 16 bytes
+                    ptx::mma_bf16(tmem + tile * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
+                                  k + s / 4 * (kTokens * 8) + s % 4 * 2, idesc, s > 0);
+                ptx::mma_commit(bar_s + 8 * tile);
+                ptx::mbar_arrive(bar_s + 8 * tile);  // what the loader wrote before the keys, too
+                release(unit, seg.tiles == 1);
             }
             return true;
         });
     } else if (warp >= S::kValuesWarp && warp < S::kValuesWarp + NT && lane == 0) {
-        // ---------------- MMA issuer: one tile's output ----------------
+        // ---------------- MMA issuer: a tile's output ----------------
         constexpr uint32_t idesc = ptx::idesc_bf16_f32(kPrefixRows, D) | ptx::kIdescBMnMajor;
         const int tile = warp - S::kValuesWarp;
         int unit = 1;
@@ -578,9 +581,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                     ptx::mma_bf16_tmem_a(tmem + S::kOCol + tile * D, tmem + S::kPCol + tile * (kTokens / 2) + s * 8,
                                          v + s * 128, idesc, s > 0 || j > 0);
                 ptx::mma_commit(bar_pv + 8 * tile);
-                ptx::mma_commit(bar_empty + 8 * (unit % kStages));
-                // A segment's only tile speaks for both.
-                if (NT == 2 && seg.tiles == 1) ptx::mma_commit(bar_empty + 8 * (unit % kStages));
+                release(unit, seg.tiles == 1);
             }
             return true;
         });
