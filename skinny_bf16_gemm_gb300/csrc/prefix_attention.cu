@@ -118,7 +118,7 @@ struct Shape {
     static constexpr int kThreads = (NT * 4 + 8) * 32;  // groups of four warps, the last not full
     // Registers a thread: a row of scores is kept in them. The groups get 128 each (one tile:
     // 168) at the launch; the softmax takes what the others give.
-    static constexpr int kSoftmaxRegisters = NT == 2 ? 168 : 216, kOtherRegisters = NT == 2 ? 88 : 144;
+    static constexpr int kSoftmaxRegisters = NT == 2 ? 176 : 216, kOtherRegisters = NT == 2 ? 80 : 144;
     static_assert(NT * kSoftmaxRegisters + 2 * kOtherRegisters <= (NT == 2 ? 4 * 128 : 3 * 168), "registers of the block");
     // Tensor memory: scores, weights and output of each tile.
     static constexpr int kPCol = NT * kTokens, kOCol = kPCol + NT * (kTokens / 2);
@@ -164,6 +164,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         *abort_flag = 0u;
         ptx::fence_barrier_init();
     }
+    if (warp == S::kLoaderWarp && lane == 0 && a.box_rows > 0) {
+        ptx::prefetch_tensormap(&k_map);
+        ptx::prefetch_tensormap(&v_map);
+    }
     if (warp == S::kScoresWarp) {
         ptx::tmem_alloc(sbase + S::kTailOffset, S::kTmemCols);
         ptx::tmem_relinquish();
@@ -185,11 +189,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     }
     const int steps = (length + kTokens - 1) / kTokens;  // of a key head
     const int total = steps * a.kv_heads;                // below 2^31 (host check)
-    const int ranges = prefix_cut(a.ranges, total);
+    const PrefixCut cut(total, a.ranges);
     // This CTA's range of tiles, and the blocks that it goes through it for: lane, lane + lanes, ..
     const int range = blockIdx.x / a.lanes, lane_block = blockIdx.x - range * a.lanes;
-    const int x_begin = range < ranges ? prefix_begin(total, ranges, range) : 0;
-    const int x_end = range < ranges ? prefix_begin(total, ranges, range + 1) : 0;
+    const int x_begin = range < cut.ranges ? cut.begin(range) : 0;
+    const int x_end = range < cut.ranges ? cut.begin(range + 1) : 0;
     const int query_rows = a.rows * a.group;
 
     // Wait for the phase of a barrier with this parity; false: aborted.
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (warp < S::kLoaderWarp) {
         // ---------------- softmax: thread = query row ----------------
         ptx::take_registers<S::kSoftmaxRegisters>();
-        const int tile = warp / 4, row = threadIdx.x % 128;
+        const int tile = warp / 4;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
         const uint32_t s_addr = lanes + tile * kTokens, p_addr = lanes + S::kPCol + tile * (kTokens / 2);
         const uint32_t o_addr = lanes + S::kOCol + tile * D;
@@ -261,28 +265,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             tile_count += seg.n;
             if (tile >= seg.tiles) return true;
             bool ok = true;
-            // The queries: 16 bytes at a time, consecutive lanes along a row.
+            // The queries: a warp copies its own 32 rows, consecutive lanes along a row.
             constexpr int kRowChunks = D / 8;
-            static_assert(kRowChunks % 4 == 0, "whole rounds of loads");
-#pragma unroll 1
-            for (int i0 = row; i0 < kPrefixRows * kRowChunks; i0 += 4 * 128) {
-                uint4 v[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = i0 + u * 128, at = seg.q0 + tile * kPrefixRows + i / kRowChunks;
-                    v[u] = make_uint4(0, 0, 0, 0);
-                    if (at < query_rows) {
-                        const int q_row = at / a.group, g = at - q_row * a.group;
-                        v[u] = __ldcg(reinterpret_cast<const uint4 *>(
-                            a.q + q_row * a.q_stride + static_cast<long long>(seg.head * a.group + g) * D + i % kRowChunks * 8));
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = i0 + u * 128, r = i / kRowChunks, ch = i % kRowChunks;
-                    v[u].x ^= flip, v[u].y ^= flip, v[u].z ^= flip, v[u].w ^= flip;
-                    *reinterpret_cast<uint4 *>(smem + tile * S::kQBytes + ch / 8 * S::kQChunkBytes + r * 128 +
-                                               ((ch ^ r) & 7) * 16) = v[u];
+            const uint32_t q_to = sbase + tile * S::kQBytes;
+            long long q_at = -1;  // of this lane's row
+            {
+                const int at = seg.q0 + tile * kPrefixRows + warp % 4 * 32 + lane, q_row = at / a.group;
+                if (at < query_rows)
+                    q_at = q_row * a.q_stride + static_cast<long long>(seg.head * a.group + at - q_row * a.group) * D;
+            }
+#pragma unroll 4
+            for (int i = lane; i < 32 * kRowChunks; i += 32) {
+                const int r = warp % 4 * 32 + i / kRowChunks, ch = i % kRowChunks;
+                const long long from = __shfl_sync(0xFFFFFFFFu, q_at, i / kRowChunks);
+                cp_async16_or_zeros(q_to + ch / 8 * S::kQChunkBytes + r * 128 + ((ch ^ r) & 7) * 16,
+                                    a.q + (from < 0 ? 0 : from) + ch * 8, from >= 0);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            if (flip != 0u) {  // a negative scale: its own copies with the signs turned
+                for (int i = lane; i < 32 * kRowChunks; i += 32) {
+                    const int r = warp % 4 * 32 + i / kRowChunks, ch = i % kRowChunks;
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + tile * S::kQBytes + ch / 8 * S::kQChunkBytes + r * 128 +
+                                                         ((ch ^ r) & 7) * 16);
+                    *v = make_uint4(v->x ^ flip, v->y ^ flip, v->z ^ flip, v->w ^ flip);
                 }
             }
             ptx::fence_proxy_async_shared();
@@ -372,24 +378,34 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             }
             if (!ok || !warp_wait(bar_pv + 8 * tile, (count - 1) & 1)) return false;
             ptx::tc_fence_after_sync();
-            // This segment's partial.
-            const int at = tile * kPrefixRows + row;
+            // This segment's partial, 32 values of the warp's 32 rows at a time by way of its own rows
+            // of the queries' first chunk (they are multiplied): a thread's own row would
+            // go out in 16-byte pieces of 32 rows at once, 5700 clocks where this takes 1500.
+            const int row0 = tile * kPrefixRows + warp % 4 * 32;
             float *slot = a.slots + (static_cast<size_t>(range + seg.head) * a.blocks + seg.block) * a.slot_floats;
-            float *to = slot + static_cast<size_t>(at) * D;
-            const bool real = seg.q0 + at < query_rows;
+            uint4 *stage = reinterpret_cast<uint4 *>(smem + tile * S::kQBytes + warp % 4 * 4096);
 #pragma unroll 1
             for (int i = 0; i < D; i += 32) {
-                uint32_t w[32];
-                ptx::tmem_ld_now(o_addr + i, w);
-                if (real)
+                uint32_t o[32];
+                ptx::tmem_ld_now(o_addr + i, o);
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        __stcg(reinterpret_cast<uint4 *>(to + i) + e, make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
+                for (int e = 0; e < 8; ++e)
+                    stage[lane * 8 + (e ^ (lane & 7))] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int r = e * 4 + lane / 8;
+                    if (seg.q0 + row0 + r < query_rows)
+                        __stcg(reinterpret_cast<uint4 *>(slot + static_cast<size_t>(row0 + r) * D + i) + lane % 8,
+                               stage[r * 8 + ((lane ^ r) & 7)]);
+                }
             }
-            if (real) {
-                __stcg(slot + NT * kPrefixRows * D + at, m);
-                __stcg(slot + NT * kPrefixRows * (D + 1) + at, l);
+            if (seg.q0 + row0 + lane < query_rows) {
+                __stcg(slot + NT * kPrefixRows * D + row0 + lane, m);
+                __stcg(slot + NT * kPrefixRows * (D + 1) + row0 + lane, l);
             }
+            __syncwarp();  // the place is read: the next queries may come
             ptx::tc_fence_before_sync();  // O is read: before the next segment's arrival
             return true;
         });
@@ -630,42 +646,49 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const Pref
     const int block = at / per, in_block = at - block * per;
     ptx::pdl_wait();
     const int length = min(max(__ldcg(a.length), 0), a.capacity);
-    const int steps = (length + a.tokens - 1) / a.tokens, total = steps * a.kv_heads;
-    const int ranges = prefix_cut(a.ranges, total);
-    const int first = total > 0 ? prefix_owner(total, ranges, head * steps) : 0;
-    const int parts = total > 0 ? prefix_owner(total, ranges, head * steps + steps - 1) - first + 1 : 0;
+    const int steps = (length + a.tokens - 1) / a.tokens;
+    const PrefixCut cut(steps * a.kv_heads, a.ranges);
+    const int first = steps > 0 ? cut.owner(head * steps) : 0;
+    const int parts = steps > 0 ? cut.owner(head * steps + steps - 1) - first + 1 : 0;
     const float *slots = a.slots + (static_cast<size_t>(first + head) * a.blocks + block) * a.slot_floats;
     const size_t stride = static_cast<size_t>(a.blocks) * a.slot_floats;  // from part to part
     const float *maxima = slots + static_cast<size_t>(per) * D + in_block, *sums = maxima + per;
     const float *values = slots + static_cast<size_t>(in_block) * D + lane;
 
-    // This warp's parts, and the first warp's share in the row's own tokens (sum of weights 2^own).
-    const float own = warp == 0 ? __ldcg(a.own_lse + job) * kLog2e : -INFINITY;
-    float o[kValues], top = fmaxf(own, kNoMaximum), weight = 0.0f;
+    // This warp's parts; the first warp begins with the row's own tokens (sum of weights 2^own).
+    float o[kValues], top = kNoMaximum, weight = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kValues; ++e) o[e] = own != -INFINITY ? __ldcg(a.own_out + static_cast<size_t>(job) * D + lane + e * 32) : 0.0f;
-    for (int s = warp + lane * kJoinWarps; s < parts; s += 32 * kJoinWarps) top = fmaxf(top, __ldcg(maxima + s * stride));
+    for (int e = 0; e < kValues; ++e) o[e] = 0.0f;
+    if (warp == 0) {
+        const float own = __ldcg(a.own_lse + job) * kLog2e;
+        if (own != -INFINITY) {
+            top = fmaxf(own, kNoMaximum);
+            weight = exp2_approx(own - top);
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-    if (own != -INFINITY) {
-        weight = exp2_approx(own - top);
-#pragma unroll
-        for (int e = 0; e < kValues; ++e) o[e] *= weight;
+            for (int e = 0; e < kValues; ++e)
+                o[e] = weight * __ldcg(a.own_out + static_cast<size_t>(job) * D + lane + e * 32);
+        }
     }
     for (int s0 = warp; s0 < parts; s0 += kAhead * kJoinWarps) {
-        float m[kAhead], l[kAhead], v[kAhead][kValues];
+        float m[kAhead], l[kAhead], v[kAhead][kValues], next = top;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const size_t s = s0 + u * kJoinWarps;
-            if (s >= static_cast<size_t>(parts)) break;
-            m[u] = __ldcg(maxima + s * stride);
-            l[u] = __ldcg(sums + s * stride);
+            const bool there = s < static_cast<size_t>(parts);
+            m[u] = there ? __ldcg(maxima + s * stride) : kNoMaximum;
+            l[u] = there ? __ldcg(sums + s * stride) : 0.0f;
 #pragma unroll
-            for (int e = 0; e < kValues; ++e) v[u][e] = __ldcg(values + s * stride + e * 32);
+            for (int e = 0; e < kValues; ++e) v[u][e] = there ? __ldcg(values + s * stride + e * 32) : 0.0f;
         }
 #pragma unroll
+        for (int u = 0; u < kAhead; ++u) next = fmaxf(next, m[u]);
+        const float f = exp2_approx(top - next);
+        top = next;
+        weight *= f;
+#pragma unroll
+        for (int e = 0; e < kValues; ++e) o[e] *= f;
+#pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (s0 + u * kJoinWarps >= parts) break;
             const float w = exp2_approx(m[u] - top);
             weight += w * l[u];
 #pragma unroll

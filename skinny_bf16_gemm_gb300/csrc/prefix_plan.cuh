@@ -57,15 +57,20 @@ __host__ __device__ inline int prefix_lanes(int blocks, int ctas) {
 }
 __host__ __device__ inline int prefix_ranges(int blocks, int ctas) { return ctas / prefix_lanes(blocks, ctas); }
 
-// Ranges of `total` tiles, of `most`.
-__host__ __device__ inline int prefix_cut(int most, int total) { return total < most ? total : most; }
-// First tile of range r, and the range that a tile is in.
-__host__ __device__ inline int prefix_begin(int total, int ranges, int r) {
-    return static_cast<int>(static_cast<long long>(total) * r / ranges);
-}
-__host__ __device__ inline int prefix_owner(int total, int ranges, int x) {
-    return static_cast<int>(((static_cast<long long>(x) + 1) * ranges - 1) / total);
-}
+// An even cut of `total` tiles into ranges, `most` at most: the first `extra` have base + 1.
+struct PrefixCut {
+    int ranges, base, extra;
+    __host__ __device__ PrefixCut(int total, int most) {
+        ranges = total < most ? total : most;
+        base = ranges > 0 ? total / ranges : 0;
+        extra = total - base * ranges;
+    }
+    __host__ __device__ int begin(int r) const { return r * base + (r < extra ? r : extra); }
+    __host__ __device__ int owner(int x) const {
+        const int at = extra * (base + 1);
+        return x < at ? x / (base + 1) : extra + (x - at) / base;
+    }
+};
 
 // A partial: for each query row of the unit head_dim sums, then all maxima, then all sums of
 // weights.
