@@ -175,21 +175,34 @@ int encode_2d(EncodeTiledFn enc, CUtensorMap *map, const void *base, uint64_t ro
 
 }  // namespace
 
-bool encode_cache_map(CUtensorMap *map, const void *base, const skinny_kv_cache *c, int box_rows) {
+bool encode_cache_map(CUtensorMap *map, const void *base, const skinny_kv_cache *c, int box_rows, bool merged) {
     EncodeTiledFn enc;
     if (encoder(&enc) != SKINNY_OK) return false;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
-                                static_cast<cuuint64_t>(c->kv_heads), static_cast<cuuint64_t>(c->num_pages)};
+    using U = cuuint64_t;
+    const U token = static_cast<U>(c->token_stride) * 2, head = static_cast<U>(c->head_stride) * 2,
+            page = static_cast<U>(c->page_stride) * 2;
+    const U D = c->head_dim, tokens = c->page_size, heads = c->kv_heads, pages = c->num_pages;
+    U dims[5] = {D, tokens, heads, pages}, strides[4] = {token, head, page};
+    cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    int rank = 4;
+    if (merged) {
+        if (heads > 1 && head % 128 != 0) return false;  // heads that are no whole chunks apart
+        const U m_dims[5] = {64, 8, (heads - 1) * (head / 128) + D / 64, tokens / 8, pages};
+        const U m_strides[4] = {token, 128, 8 * token, page};
+        const cuuint32_t m_box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(box_rows / 8), 1};
+        std::copy(m_dims, m_dims + 5, dims);
+        std::copy(m_strides, m_strides + 4, strides);
+        std::copy(m_box, m_box + 5, box);
+        rank = 5;
+    }
     // The stride of an axis of one element says nothing, and may be 0; one of 0 elsewhere has
     // no map.
-    const long long given[3] = {c->token_stride, c->head_stride, c->page_stride};
-    cuuint64_t strides[3];
-    for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(given[i]) * 2;
-    for (cuuint64_t st : strides)
-        if (st == 0 || st >= (1ull << 40)) return false;
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
-    const cuuint32_t estride[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estride,
+    for (int i = 0; i + 1 < rank; ++i) {
+        if (dims[i + 1] == 1) strides[i] = 16;
+        if (strides[i] == 0 || strides[i] >= (1ull << 40) || dims[i + 1] >= (1ull << 31)) return false;
+    }
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estride,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -182,7 +182,9 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     alignas(64) CUtensorMap k_map = {}, v_map = {};
     a.box_rows = prefix_box_rows(c->page_size, plan.tokens);
-    if (a.box_rows > 0 && !(encode_cache_map(&k_map, c->k, c, a.box_rows) && encode_cache_map(&v_map, c->v, c, a.box_rows)))
+    a.head_chunks = static_cast<int>(std::min<long long>(c->head_stride / 64, 1ll << 30));
+    if (a.box_rows > 0 && !(encode_cache_map(&k_map, c->k, c, a.box_rows, prefix_merged(D)) &&
+                            encode_cache_map(&v_map, c->v, c, a.box_rows, prefix_merged(D))))
         a.box_rows = 0;
     if (launch_prefix_attention(k_map, v_map, a, D, dev, s, ls.pdl) != cudaSuccess ||
         launch_decode_attention_part(o, D, sms, dev, s) != cudaSuccess ||

@@ -52,9 +52,11 @@ struct LaunchSettings {
 };
 int resolve_settings(const skinny_launch_opts *opts, LaunchSettings *out);
 
-// A tensor map over a cache's keys or values as [pages, heads, tokens, head_dim], boxes of 64
-// values by box_rows tokens with 128-byte swizzle; false if there is none for its strides.
-bool encode_cache_map(CUtensorMap *map, const void *base, const skinny_kv_cache *c, int box_rows);
+// A tensor map over a cache's keys or values with 128-byte swizzle; false if there is none for
+// its strides. merged: [pages, groups of 8 tokens, chunks of 64 values (of all heads), 8, 64],
+// boxes of box_rows tokens with the chunks of one head side by side in every group. Else
+// [pages, heads, tokens, head_dim], boxes of box_rows tokens by 64 values.
+bool encode_cache_map(CUtensorMap *map, const void *base, const skinny_kv_cache *c, int box_rows, bool merged);
 
 // A cache's own rules, and the bytes its keys (or values) span.
 int check_cache(const skinny_kv_cache *c, bool write, size_t *span);

@@ -226,14 +226,15 @@ struct PrefixArgs {
     int lanes, ranges;   // blocks side by side, and the most ranges
     float scale_log2;
     int box_rows;       // tokens of a tensor map's box, or 0: no maps
+    int head_chunks;    // prefix_merged: 128-byte chunks from head to head
     float *slots;       // workspace
     int slot_floats;
     const float *own_out, *own_lse;  // workspace: [rows][q_heads][head_dim] and [rows][q_heads]
     uint16_t *out;
     float *lse;  // or nullptr
 };
-// Tokens of a TMA box of the keys and values: 64 of head_dim by so many tokens of one page, or
-// 0 if boxes will not do (tiles must be whole boxes, and a box whole swizzle atoms).
+// Tokens of a TMA box of the keys and values, all of one page, or 0 if boxes will not do (tiles
+// must be whole boxes, and a box whole swizzle atoms).
 int prefix_box_rows(int page_size, int tokens);
 cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
                                     int head_dim, int device, cudaStream_t stream, bool pdl);

@@ -15,8 +15,9 @@
 //                     boxes of as many tokens as pages and tiles both are multiples of, or,
 //                     for pages of no multiple of 8 and for a tile that the prefix ends in
 //                     (what is behind its end must come out as zeros), by 16-byte cp.async
-//                     with each token's address. Four, because a thread takes some 200 clocks
-//                     to issue a box, of whatever size, and the threads of a warp take turns;
+//                     with each token's address. Two for the keys, two for the values: a
+//                     thread takes some 200 clocks to issue a box, of whatever size, and the
+//                     threads of a warp take turns;
 //   2 MMA warps a tile  the scores, S = Q K^T, from shared memory (both K-major) into tensor
 //                     memory; and O += P V, P in tensor memory and V as it lies, MN-major.
 // Scores, weights and output have places of their own in tensor memory: a softmax thread takes
@@ -96,13 +97,17 @@ struct Shape {
     static constexpr int kTokens = prefix_tokens(D, NT);
     static constexpr int kChunks = (D + 63) / 64;               // 128-byte chunks of a row
     static constexpr int kUnitBytes = kChunks * kTokens * 128;  // a tile's keys, or values
+    static constexpr bool kMerged = prefix_merged(D);
+    static constexpr int kGroupBytes = kMerged ? kChunks * 1024 : 1024;          // from 8 tokens to the next
+    static constexpr int kChunkBytes = kMerged ? 1024 : kTokens * 128;           // from chunk to chunk
     static constexpr int kQChunkBytes = kPrefixRows * 128;
     static constexpr int kQBytes = kChunks * kQChunkBytes;      // one tile of queries
     static constexpr int kMiscBytes = 768;
     static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes);
-    // cp.async: units whose copies are on their way. At most so many that the next keys come
-    // without the last values' place.
-    static constexpr int kLag = kStages / 2;
+    // cp.async: a warp's units (every other one of the ring) whose copies are on their way; at
+    // most so many that the next keys come without the last values' place.
+    static constexpr int kLag = std::max(1, kStages / 4);
+    static_assert(2 * kLag <= kStages - 2, "no unit waits for one behind it");
     static_assert(kStages >= 4, "a key and a value tile in use while others are on their way");
     static constexpr int kRingOffset = NT * kQBytes;
     static constexpr int kMaskWords = (kTokens + 31) / 32;
@@ -113,8 +118,8 @@ struct Shape {
     static constexpr int kBytes = kTailOffset + 16;
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
     static_assert(kDynamicBytes <= 232448, "shared memory of a CTA");
-    static constexpr int kLoaders = 4;  // warps
-    static constexpr int kLoaderWarp = NT * 4, kScoresWarp = kLoaderWarp + kLoaders, kValuesWarp = kScoresWarp + NT;
+    static constexpr int kLoaders = 2;  // warps for the keys, and for the values
+    static constexpr int kLoaderWarp = NT * 4, kScoresWarp = kLoaderWarp + 2 * kLoaders, kValuesWarp = kScoresWarp + NT;
     static constexpr int kThreads = (NT * 4 + 8) * 32;  // groups of four warps, the last not full
     // Registers a thread: a row of scores is kept in them. The groups get 128 each (one tile:
     // 168) at the launch; the softmax takes what the others give.
@@ -412,11 +417,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     } else if (warp < S::kScoresWarp) {
         // ---------------- loaders ----------------
         ptx::give_registers<S::kOtherRegisters>();
-        const int loader = warp - S::kLoaderWarp;
+        const int loader = (warp - S::kLoaderWarp) % S::kLoaders, kv = (warp - S::kLoaderWarp) / S::kLoaders;
+        const uint16_t *from = kv == 0 ? a.k : a.v;
+        const CUtensorMap *map = kv == 0 ? &k_map : &v_map;
         uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::kMaskOffset);
         constexpr int kRowChunks = D / 8, kRows = kTokens / S::kLoaders;  // cp.async: a warp's rows of a tile
-        static_assert(kTokens / 8 <= 32 && kRows <= 32 && kRows * kRowChunks % 32 == 0, "a lane a box, or a row");
-        int unit = 0;  // of the ring, so far
+        constexpr int kMine = (kRows + 31) / 32;                          // .. whose places a lane looks up
+        static_assert(kTokens / 8 <= 32 && kTokens % (2 * S::kLoaders) == 0 && kRows * kRowChunks % 32 == 0, "whole rounds");
+        int unit = kv;  // of the ring, so far
         uint32_t tile_count = 0;
         bool ok = true;
         auto publish = [&](int u) {  // this warp's part of a unit whose copies are complete
@@ -424,13 +432,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_full + 8 * (u % kStages));
         };
-        const int boxes = a.box_rows > 0 ? kTokens / a.box_rows : 0, items = boxes * S::kChunks;
+        const int boxes = a.box_rows > 0 ? kTokens / a.box_rows : 0;
+        const int items = S::kMerged ? boxes : boxes * S::kChunks;  // copies of a unit
         // This warp's bytes of a unit that comes by boxes.
-        const int box_bytes = (items - loader + S::kLoaders - 1) / S::kLoaders * a.box_rows * 128;
+        const int box_bytes = (items - loader + S::kLoaders - 1) / S::kLoaders * a.box_rows * 128 * (S::kMerged ? S::kChunks : 1);
         auto boxed = [&](int tile) { return boxes > 0 && (tile + 1) * kTokens <= length; };
         int head = 0, t = 0;  // of the tile that is looked up
         // Its places: lane's box (page and token within it), or the lane's row of this warp's.
-        long long next = -1;
+        long long next[kMine];
         int next_page = 0, next_token = 0;
         auto look_up = [&]() {
             if (boxed(t)) {
@@ -439,8 +448,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 const int e = a.page_shift >= 0 ? token >> a.page_shift : token / a.page_size;
                 next_page = __ldcg(a.table + e);
                 next_token = token - e * a.page_size;
-            } else if (lane < kRows) {
-                next = place(head, t * kTokens + loader * kRows + lane);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    next[i] = i * 32 + lane < kRows ? place(head, t * kTokens + loader * kRows + i * 32 + lane) : -1;
             }
         };
         if (x_begin < x_end) {
@@ -454,7 +465,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 uint32_t *mask = masks + tile_count % kMaskRing * S::kMaskWords;
                 const bool by_box = boxed(t);
                 const int this_head = head, token = next_token;
-                const long long row_at = next;
+                long long row_at[kMine];
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) row_at[i] = next[i];
                 int page = next_page;
                 if (by_box) {
                     const bool there = lane >= boxes || (page >= 0 && page < a.num_pages);
@@ -463,7 +476,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                         atomicOr(&g_prefix_err, kErrRange);
                         page = a.num_pages;  // past the end: zeros
                     }
-                    if (loader == 0 && lane < S::kMaskWords) {
+                    if (kv == 0 && loader == 0 && lane < S::kMaskWords) {
                         uint32_t bits = whole_mask(lane);
                         if (good != 0xFFFFFFFFu) {
                             bits = 0;
@@ -473,9 +486,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                         mask[lane] = bits;
                     }
                 } else {
-                    if (lane < kRows && row_at < 0 && t * kTokens + loader * kRows + lane < length)
-                        atomicOr(&g_prefix_err, kErrRange);
-                    if (loader == 0) {
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i)
+                        if (i * 32 + lane < kRows && row_at[i] < 0 && t * kTokens + loader * kRows + i * 32 + lane < length)
+                            atomicOr(&g_prefix_err, kErrRange);
+                    if (kv == 0 && loader == 0) {
                         for (int i = 0; i < S::kMaskWords; ++i) {
                             const int at = i * 32 + lane;
                             const uint32_t bits = __ballot_sync(0xFFFFFFFFu, at < kTokens && place(head, t * kTokens + at) >= 0);
@@ -491,47 +506,55 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                     ++head;
                 }
                 if (x + 1 < x_end || block + a.lanes < a.blocks) look_up();
-                for (int kv = 0; kv < 2; ++kv, ++unit) {
-                    const int s = unit % kStages;
-                    const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
-                    // The first round finds the stages free.
-                    if (!(ok = warp_wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1))) break;
-                    if (by_box) {
-                        __syncwarp();  // loader 0: the mask is written
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full + 8 * s, box_bytes);
-                        __syncwarp();
-                        // The lanes' boxes come one after another.
-                        const int item = loader + lane * S::kLoaders, box = item / S::kChunks, ch = item - box * S::kChunks;
-                        const int box_page = __shfl_sync(0xFFFFFFFFu, page, box & 31);
-                        const int box_token = __shfl_sync(0xFFFFFFFFu, token, box & 31);
-                        if (item < items)
-                            ptx::tma_load_4d(to + ch * (kTokens * 128) + box * a.box_rows * 128, kv == 0 ? &k_map : &v_map,
-                                             bar_full + 8 * s, ch * 64, box_token, this_head, box_page);
-                        continue;
+                const int s = unit % kStages;
+                const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
+                // The first round finds the stages free.
+                if (!(ok = warp_wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1))) break;
+                if (by_box) {
+                    __syncwarp();  // the mask is written
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full + 8 * s, box_bytes);
+                    __syncwarp();
+                    // The lanes' boxes come one after another.
+                    const int item = loader + lane * S::kLoaders;
+                    const int box = S::kMerged ? item : item / S::kChunks, ch = S::kMerged ? 0 : item % S::kChunks;
+                    const int box_page = __shfl_sync(0xFFFFFFFFu, page, box & 31);
+                    const int box_token = __shfl_sync(0xFFFFFFFFu, token, box & 31);
+                    if (item < items) {
+                        const uint32_t dst = to + ch * S::kChunkBytes + box * a.box_rows / 8 * S::kGroupBytes;
+                        if constexpr (S::kMerged)
+                            ptx::tma_load_5d(dst, map, bar_full + 8 * s, 0, 0, this_head * a.head_chunks, box_token / 8, box_page);
+                        else
+                            ptx::tma_load_4d(dst, map, bar_full + 8 * s, ch * 64, box_token, this_head, box_page);
                     }
-                    const uint16_t *from = kv == 0 ? a.k : a.v;
-#pragma unroll 4
-                    for (int i = 0; i < kRows * kRowChunks / 32; ++i) {
-                        const int id = i * 32 + lane, own = id / kRowChunks, r = loader * kRows + own, ch = id % kRowChunks;
-                        const long long at = __shfl_sync(0xFFFFFFFFu, row_at, own);
-                        cp_async16_or_zeros(to + ch / 8 * (kTokens * 128) + r * 128 + ((ch ^ r) & 7) * 16,
-                                            from + (at < 0 ? 0 : at) + ch * 8, at >= 0);
-                    }
-                    cp_async_commit();
-                    if (boxes > 0) {  // the tile that the prefix ends in
-                        cp_async_wait<0>();
-                        publish(unit);
-                    } else if (unit >= S::kLag) {
-                        cp_async_wait<S::kLag>();
-                        publish(unit - S::kLag);
-                    }
+                    unit += 2;
+                    continue;
                 }
+#pragma unroll 4
+                for (int i = 0; i < kRows * kRowChunks / 32; ++i) {
+                    const int id = i * 32 + lane, own = id / kRowChunks, r = loader * kRows + own, ch = id % kRowChunks;
+                    long long at = __shfl_sync(0xFFFFFFFFu, row_at[0], own & 31);
+                    if constexpr (kMine > 1) {
+                        const long long second = __shfl_sync(0xFFFFFFFFu, row_at[kMine - 1], own & 31);
+                        if (own >= 32) at = second;
+                    }
+                    cp_async16_or_zeros(to + r / 8 * S::kGroupBytes + ch / 8 * S::kChunkBytes + r % 8 * 128 + ((ch ^ r) & 7) * 16,
+                                        from + (at < 0 ? 0 : at) + ch * 8, at >= 0);
+                }
+                cp_async_commit();
+                if (boxes > 0) {  // the tile that the prefix ends in
+                    cp_async_wait<0>();
+                    publish(unit);
+                } else if (unit >= 2 * S::kLag) {
+                    cp_async_wait<S::kLag>();
+                    publish(unit - 2 * S::kLag);
+                }
+                unit += 2;
             }
         }
         issued = boxes > 0 ? unit : 0;
         cp_async_wait<0>();
         if (ok && boxes == 0)
-            for (int u = max(0, unit - S::kLag); u < unit; ++u) publish(u);
+            for (int u = max(kv, unit - 2 * S::kLag); u < unit; u += 2) publish(u);
     } else {
         ptx::give_registers<S::kOtherRegisters>();
     }
@@ -565,11 +588,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 // The step's before are read, and the keys are there.
                 if (scored > 0 && !wait(bar_free + 8 * tile, (scored - 1) & 1)) return false;
                 if (!full(unit)) return false;
-                const uint64_t k = ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes);
+                const uint64_t k =
+                    ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes, S::kGroupBytes);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)  // addresses in the descriptors are in units of 16 bytes
                     ptx::mma_bf16(tmem + tile * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
-                                  k + s / 4 * (kTokens * 8) + s % 4 * 2, idesc, s > 0);
+                                  k + s / 4 * (S::kChunkBytes / 16) + s % 4 * 2, idesc, s > 0);
                 ptx::mma_commit(bar_s + 8 * tile);
                 ptx::mbar_arrive(bar_s + 8 * tile);  // what the loader wrote before the keys, too
                 release(unit, seg.tiles == 1);
@@ -590,12 +614,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             for (int j = 0; j < seg.n; ++j, unit += 2) {
                 if (!full(unit) || !wait(bar_p + 8 * tile, added++ & 1)) return false;
                 ptx::tc_fence_after_sync();
-                const uint64_t v =
-                    ptx::smem_desc_sw128_mnmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes, kTokens * 128);
+                const uint64_t v = ptx::smem_desc_sw128_mnmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes,
+                                                                S::kChunkBytes, S::kGroupBytes);
 #pragma unroll
                 for (int s = 0; s < kTokens / 16; ++s)
                     ptx::mma_bf16_tmem_a(tmem + S::kOCol + tile * D, tmem + S::kPCol + tile * (kTokens / 2) + s * 8,
-                                         v + s * 128, idesc, s > 0 || j > 0);
+                                         v + s * (S::kGroupBytes / 8), idesc, s > 0 || j > 0);
                 ptx::mma_commit(bar_pv + 8 * tile);
                 release(unit, seg.tiles == 1);
             }
@@ -615,7 +639,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         }
         if (warp >= S::kLoaderWarp && warp < S::kScoresWarp && lane == 0) {
             const uint64_t t0 = ptx::global_timer_ns();
-            for (int u = max(0, issued - kStages); u < issued; ++u)
+            for (int u = max((warp - S::kLoaderWarp) / S::kLoaders, issued - kStages / 2 * 2); u < issued; u += 2)
                 while (!ptx::mbar_try_wait(bar_full + 8 * (u % kStages), (u / kStages) & 1) &&
                        ptx::global_timer_ns() - t0 < kDrainLimitNs) {
                 }

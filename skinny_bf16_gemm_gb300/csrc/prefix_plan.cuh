@@ -72,6 +72,11 @@ struct PrefixCut {
     }
 };
 
+// How a tile's tokens lie in shared memory: rows of 128 bytes (64 values, a chunk) in swizzle
+// atoms of 8 tokens. Where heads are whole chunks the chunks of 8 tokens lie side by side, so that
+// one copy brings them all; else (96) all tokens' first chunks come before their second ones.
+constexpr bool prefix_merged(int head_dim) { return head_dim % 64 == 0; }
+
 // A partial: for each query row of the unit head_dim sums, then all maxima, then all sums of
 // weights.
 __host__ __device__ inline size_t prefix_slot_floats(int head_dim, long long query_rows) {

@@ -82,13 +82,22 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// The same of a 4-D tensor, without a cache hint.
+// The same of a 4-D and of a 5-D tensor, without a cache hint.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0,
                                             int32_t c1, int32_t c2, int32_t c3) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0,
+                                            int32_t c1, int32_t c2, int32_t c3, int32_t c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
         : "memory");
 }
 
@@ -218,14 +227,20 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_kmajor(uint32_t saddr) {
     return d;
 }
 
+// The same for 8-row atoms `group_bytes` apart.
+__device__ __forceinline__ uint64_t smem_desc_sw128_kmajor(uint32_t saddr, uint32_t group_bytes) {
+    return (smem_desc_sw128_kmajor(saddr) & ~(0x3FFFull << 32)) | static_cast<uint64_t>(group_bytes >> 4) << 32;
+}
+
 // The same for an MN-major operand: each K index is a row of 128 bytes (64 BF16 along M/N) of
-// an 8-row swizzle atom; atoms follow along K 1024 bytes apart, and further 64 values
+// an 8-row swizzle atom; atoms follow along K `group_bytes` apart, and further 64 values
 // along M/N `chunk_bytes` on.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mnmajor(uint32_t saddr, uint32_t chunk_bytes) {
+__device__ __forceinline__ uint64_t smem_desc_sw128_mnmajor(uint32_t saddr, uint32_t chunk_bytes,
+                                                            uint32_t group_bytes) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(chunk_bytes >> 4) << 16;  // leading byte offset: along M/N
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;         // stride byte offset: along K
+    d |= static_cast<uint64_t>(group_bytes >> 4) << 32;  // stride byte offset: along K
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
     return d;
