@@ -341,41 +341,38 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                             ptx::tmem_ld_now(o_addr + i, o);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            ptx::tmem_st32(o_addr + i, o);
+                            ptx::tmem_st_columns(o_addr + i, o);
                         }
                     }
                 }
                 float sum[4] = {};
+                uint32_t p[kTokens / 2];
                 auto weights = [&](auto masked) {
 #pragma unroll
-                    for (int i = 0; i < kTokens; i += 16) {
-                        float v[16];
-                        uint32_t p[8];
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            v[e] = __uint_as_float(w[i + e]), v[e + 1] = __uint_as_float(w[i + e + 1]);
-                            fma2(v[e], v[e + 1], c, -m);
-                            v[e] = exp2_approx(v[e]);
-                            v[e + 1] = exp2_approx(v[e + 1]);
-                            if (masked) {
-                                if (!(mask[(i + e) / 32] >> ((i + e) % 32) & 1)) v[e] = 0.0f;
-                                if (!(mask[(i + e) / 32] >> ((i + e) % 32) & 2)) v[e + 1] = 0.0f;
-                            }
-                            add2(sum[e & 2], sum[(e & 2) + 1], v[e], v[e + 1]);
-                            p[e / 2] = pack_bf16(v[e], v[e + 1]);
+                    for (int e = 0; e < kTokens; e += 2) {
+                        float x = __uint_as_float(w[e]), y = __uint_as_float(w[e + 1]);
+                        fma2(x, y, c, -m);
+                        x = exp2_approx(x);
+                        y = exp2_approx(y);
+                        if (masked) {
+                            if (!(mask[e / 32] >> (e % 32) & 1)) x = 0.0f;
+                            if (!(mask[e / 32] >> (e % 32) & 2)) y = 0.0f;
                         }
-                        if (i == 0 && !added) {  // the weights before are multiplied
-                            ok = warp_wait(bar_pv + 8 * tile, (count - 1) & 1);
-                            ptx::tc_fence_after_sync();
-                        }
-                        ptx::tmem_st8(p_addr + i / 2, p);
+                        add2(sum[e & 2], sum[(e & 2) + 1], x, y);
+                        p[e / 2] = pack_bf16(x, y);
                     }
                 };
                 if (all)
                     weights(std::false_type{});
                 else
                     weights(std::true_type{});
-                if (!ok) break;
+                // The weights before are multiplied: waited for no sooner than here, so that the
+                // way from one step's weights through their product to the next's is short.
+                if (!added) {
+                    if (!(ok = warp_wait(bar_pv + 8 * tile, (count - 1) & 1))) break;
+                    ptx::tc_fence_after_sync();
+                }
+                ptx::tmem_st_columns(p_addr, p);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
