@@ -159,10 +159,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             ptx::mbar_init(bar_empty + 8 * s, NT);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(bar_q + 8 * i, 128);
+            ptx::mbar_init(bar_q + 8 * i, 4);  // warps
             ptx::mbar_init(bar_s + 8 * i, 2);  // the products, and the issuer (the mask is there)
-            ptx::mbar_init(bar_free + 8 * i, 128);
-            ptx::mbar_init(bar_p + 8 * i, 128);
+            ptx::mbar_init(bar_free + 8 * i, 4);
+            ptx::mbar_init(bar_p + 8 * i, 4);
             ptx::mbar_init(bar_pv + 8 * i, 1);
         }
         ptx::mbar_init(bar_drain, 2 * NT);
@@ -216,6 +216,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 }
             }
         }
+    };
+    // One arrival for a warp, behind all its lanes.
+    auto warp_arrive = [&](uint32_t bar) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar);
     };
     auto warp_wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
     // The token of a tile and its page: its element offset within the keys, or -1.
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 }
             }
             ptx::fence_proxy_async_shared();
-            ptx::mbar_arrive(bar_q + 8 * tile);
+            warp_arrive(bar_q + 8 * tile);
 
             float m = kNoMaximum, l = 0.0f;  // in units of log2
             for (int j = 0; j < seg.n; ++j, ++count) {
@@ -306,7 +311,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 uint32_t w[kTokens];
                 ptx::tmem_ld_now(s_addr, w);
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bar_free + 8 * tile);
+                warp_arrive(bar_free + 8 * tile);
                 const uint32_t *mask = masks + (first + j) % kMaskRing * S::kMaskWords;
                 bool all = true;
 #pragma unroll
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bar_p + 8 * tile);
+                warp_arrive(bar_p + 8 * tile);
             }
             if (!ok || !warp_wait(bar_pv + 8 * tile, (count - 1) & 1)) return false;
             ptx::tc_fence_after_sync();
