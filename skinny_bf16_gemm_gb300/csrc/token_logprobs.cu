@@ -13,10 +13,11 @@
 //
 // The top list needs no second pass over the row: the `top`-th largest of the threads' own
 // maxima bounds the `top`-th largest value from below (that many threads have a value as
-// large), so only those threads' values, about `top` * values-a-thread, are read again, from
-// L2, and what reaches the bound is listed and ranked by (value, index). Where ties at the
-// bound or few heavy threads overflow the list, the exact bound is found by bisecting the
-// 16-bit values and the ties are taken in the order of their index.
+// large), so only those threads' values are read again, of most of them no more than the
+// kUnroll vectors with their maximum: a thread keeps the largest of its other rounds, too.
+// What reaches the bound is listed and ranked by (value, index).
+// Where ties at the bound or few heavy threads overflow the list, the exact bound is found by
+// bisecting the 16-bit values and the ties are taken in the order of their index.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -87,13 +88,16 @@ __device__ __forceinline__ uint32_t bits_at(const uint4 &v, int e) {
 }
 
 template <int C>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const LogprobArgs a) {
     __shared__ Sums sm_sums[kWarps];
     __shared__ Sums sm_peers[C];
     __shared__ unsigned long long sm_tops[C * kLogprobMaxTop];
     __shared__ unsigned long long sm_list[kList], sm_ties[kList];
     __shared__ int sm_counts[2];
     __shared__ int sm_scan[kWarps];
+    __shared__ uint32_t sm_bound;
+    __shared__ __align__(16) uint16_t sm_maxima[kThreads];
+    __shared__ int sm_again[kWarps][32];  // what a warp reads again: vectors, then lanes
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int rank = C > 1 ? static_cast<int>(blockIdx.x % C) : 0;
     const long long row = blockIdx.x / C;
@@ -116,9 +120,11 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
 
     // ---- one pass: maximum and sums ----
     Sums sums = {kNoMaximum, 0.0f, 0.0f};
-    float best = -INFINITY;  // this thread's largest value
-    auto take = [&](float v) {
-        best = fmaxf(best, v);
+    float best = -INFINITY;    // this thread's largest value
+    float second = -INFINITY;  // the largest of its other rounds
+    int best_at = v_end;       // the first vector of the round with the largest
+    auto take = [&](float v) {  // as another round's
+        second = fmaxf(second, v);
         if (v > sums.m) raise(sums, v);
         const float t = v - sums.m, e = exp2_approx(t * kLog2e);
         sums.s1 += e;
@@ -137,7 +143,13 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
         for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
             for (int e = 0; e < 8; ++e) most = fmaxf(most, logit_of(bits_at(w[u], e)));
-        best = fmaxf(best, most);
+        if (most > best) {
+            second = fmaxf(second, best);
+            best = most;
+            best_at = v;
+        } else {
+            second = fmaxf(second, most);
+        }
         if (most > sums.m) raise(sums, most);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
@@ -158,12 +170,27 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
 
     // ---- this CTA's top list ----
     if (top > 0) {
-        const uint32_t mine = key_of(__float_as_uint(best) >> 16);
-        // The top-th largest of the threads' maxima (0: fewer threads than that).
-        uint32_t bound = 0;
+        const uint32_t mine = key_of(__float_as_uint(fmaxf(best, second)) >> 16);
+        // The top-th largest of the threads' maxima, bit by bit, by one warp with 8 of them a lane
+        // (0: fewer threads than that).
+        sm_maxima[tid] = static_cast<uint16_t>(mine);
+        __syncthreads();
+        if (warp == 0) {
+            const uint4 v = reinterpret_cast<const uint4 *>(sm_maxima)[lane];
+            uint32_t k[8], found = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) k[e] = bits_at(v, e);
 #pragma unroll 1
-        for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1)
-            if (__syncthreads_count(mine >= (bound | bit)) >= top) bound |= bit;
+            for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1) {
+                int n = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) n += k[e] >= (found | bit);
+                if (__reduce_add_sync(0xFFFFFFFFu, n) >= top) found |= bit;
+            }
+            if (lane == 0) sm_bound = found;
+        }
+        __syncthreads();
+        uint32_t bound = sm_bound;
 
         // Every value of this thread in turn.
         auto each = [&](auto &&f) {
@@ -188,20 +215,31 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
                 if (at < kList) sm_ties[at] = entry(key, i);
             }
         };
-        // The values of the threads that reach the bound: a warp reads one thread's vectors
-        // at a time, a vector a lane.
-        unsigned flagged = __ballot_sync(0xFFFFFFFFu, mine >= bound);
-        if (mine >= bound) {
+        // The values of the threads that reach the bound, their vectors dealt to the lanes of their
+        // warp: the round with the largest value, or all if another reaches the bound too.
+        const bool many = key_of(__float_as_uint(second) >> 16) >= bound, one = mine >= bound && !many;
+        if (many) {
             if (lone >= 0) put(key_of(x[lone]), lone);
             if (late >= 0) put(key_of(x[late]), late);
         }
-        for (; flagged != 0; flagged &= flagged - 1) {
-            const int first = v_begin + warp * 32 + __ffs(flagged) - 1;
-            for (int v = first + lane * kThreads; v < v_end; v += 32 * kThreads) {
-                const uint4 w = load_vector(xv + v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) put(key_of(bits_at(w, e)), head + v * 8 + e);
+        const unsigned ones = __ballot_sync(0xFFFFFFFFu, one), all = __ballot_sync(0xFFFFFFFFu, many);
+        const unsigned below = (1u << lane) - 1u;
+        if (one) sm_again[warp][__popc(ones & below)] = best_at;
+        if (many) sm_again[warp][__popc(ones) + __popc(all & below)] = v_begin + tid;
+        __syncwarp();
+        const int each_has = (v_end - v_begin + kThreads - 1) / kThreads, first = __popc(ones) * kUnroll;
+        for (int item = lane; item < first + __popc(all) * each_has; item += 32) {
+            int who = item / kUnroll, i = item % kUnroll;
+            if (item >= first) {
+                who = (item - first) / each_has;
+                i = item - first - who * each_has;
+                who += __popc(ones);
             }
+            const int v = sm_again[warp][who] + i * kThreads;
+            if (v >= v_end) continue;
+            const uint4 w = load_vector(xv + v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) put(key_of(bits_at(w, e)), head + v * 8 + e);
         }
         __syncthreads();
         if (sm_counts[0] > kList) {
@@ -274,14 +312,19 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
         uint32_t to = ptx::smem_addr(sm_tops + rank * kLogprobMaxTop);
         if constexpr (C > 1) to = ptx::map_to_cluster_rank(to, 0);
         auto listed = [&](int i) { return i < above ? sm_list[i] : sm_ties[i - above]; };
+        auto larger = [](const unsigned long long *list, int count, unsigned long long e) {
+            int better = 0;
+#pragma unroll 8
+            for (int j = 0; j < count; ++j) better += list[j] > e;
+            return better;
+        };
         if constexpr (C > 1) {
             __syncthreads();
             ptx::cluster_sync();  // the first CTA runs: its memory may be written
         }
         for (int i = tid; i < n; i += kThreads) {
             const unsigned long long e = listed(i);
-            int better = 0;
-            for (int j = 0; j < n; ++j) better += listed(j) > e;
+            const int better = larger(sm_list, above, e) + larger(sm_ties, n - above, e);
             if (better < top) ptx::st_cluster_u64(to + better * 8, e);
         }
         for (int i = n + tid; i < top; i += kThreads) ptx::st_cluster_u64(to + i * 8, 0ull);
@@ -327,6 +370,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
         int better = C > 1 ? 0 : i;
         if constexpr (C > 1)
             for (int c = 0; c < C; ++c)
+#pragma unroll 8
                 for (int j = 0; j < top; ++j) better += sm_tops[c * kLogprobMaxTop + j] > e;
         if (better >= top) continue;
         const float v = value_of(static_cast<uint32_t>(e >> 32));
