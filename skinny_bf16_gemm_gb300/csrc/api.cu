@@ -338,11 +338,13 @@ int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, vo
         a.lora.rank = lora->rank;
         a.lora.splits = lora_splits(M, K, lora->rank, d->sms);
         a.lora.sums = d->lora_sums;
-        if (launch_lora_shrink(x, a.lora, M, K, s, pdl) != cudaSuccess) {
+        if (launch_lora_shrink(x, a.lora, M, K, d->sms, s, pdl) != cudaSuccess) {
             cudaGetLastError();
             return SKINNY_ERR_LAUNCH;
         }
     }
+    // The shallow ring's room for adapters ends at rank 64.
+    const bool shallow = use_shallow_ring(g, pdl) && !(lora && lora->rank > 64);
     // Split tiles of 64-row accumulators, every CTA within at most two tiles (two
     // scratch slots), plain output: the GEMM only publishes its partials and a
     // small kernel finishes them (same order, same bits). A finisher CTA would
@@ -359,7 +361,7 @@ int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, vo
     if (split && mma_n == 64 && g.ctas >= g.tiles && !logits && !selftest) {
         a.publish_only = 1;
         cudaError_t e = launch_decode_gemm(w_map, x_map, a, mma_n, g.ctas, s, pdl,
-                                           use_shallow_ring(g, pdl), dev);
+                                           shallow, dev);
         if (e == cudaSuccess) {
             SplitKPartials fix = {};
             fix.partials = d->partials;
@@ -377,7 +379,7 @@ int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, vo
         return SKINNY_OK;
     }
     cudaError_t e = launch_decode_gemm(w_map, x_map, a, mma_n, g.ctas, s, pdl,
-                                       use_shallow_ring(g, pdl), dev);
+                                       shallow, dev);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return SKINNY_ERR_LAUNCH;

@@ -101,7 +101,8 @@ cudaError_t launch_decode_gemm(const CUtensorMap &w_map, const CUtensorMap &x_ma
 
 // The adapters' first half (lora_shrink.cu): K slices for a call, and l.sums from x.
 int lora_splits(int M, int K, int rank, int num_sms);
-cudaError_t launch_lora_shrink(const void *x, const LoraArgs &l, int M, int K, cudaStream_t stream, bool pdl);
+cudaError_t launch_lora_shrink(const void *x, const LoraArgs &l, int M, int K, int num_sms, cudaStream_t stream,
+                               bool pdl);
 cudaError_t lora_error_word(int *value, bool clear);
 
 // Split-K scratch held in a static device array (decode_gemm_bf16_noalloc).

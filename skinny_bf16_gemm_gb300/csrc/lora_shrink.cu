@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 #include "plan.cuh"
@@ -29,7 +30,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;     // K values of a warp's step: 16 bytes a lane
 constexpr int kRankTile = 16;
 constexpr int kTokens = 16;   // rows of x at a time
-constexpr int kUnroll = 4;
 __device__ int g_lora_err;  // nonzero: an adapter index was out of range
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -76,14 +76,16 @@ __global__ void __launch_bounds__(kThreads)
     const uint16_t *a_lo = l.A + (static_cast<size_t>(adapter) * l.rank + j0 + (row_lo ? g : 0)) * K;
     const uint16_t *a_hi = l.A + (static_cast<size_t>(adapter) * l.rank + j0 + (row_hi ? g + 8 : 0)) * K;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int c0 = 0; c0 < count; c0 += kTokens) {
-        const bool second = c0 + 8 < count;  // a second block of 8 rows of x
-        const bool in0 = c0 + g < count, in1 = c0 + 8 + g < count;
+    // Up to 16 rows of x at a time. The steps whose loads are on their way together: 8, or 4 with
+    // a second block of 8 rows.
+    auto products = [&](int c0, auto second) {
+        constexpr int kUnroll = second ? 4 : 8;
+        const bool in0 = c0 + g < count, in1 = second && c0 + 8 + g < count;
         const uint16_t *x0 = x + static_cast<size_t>(sm_rows[in0 ? c0 + g : 0]) * K;
         const uint16_t *x1 = x + static_cast<size_t>(sm_rows[in1 ? c0 + 8 + g : 0]) * K;
         float d[2][4] = {};
         for (int k = k_begin + warp * kStep + t8; k - t8 < k_end; k += kWarps * kStep * kUnroll) {
-            uint4 al[kUnroll], ah[kUnroll], b0[kUnroll], b1[kUnroll];
+            uint4 al[kUnroll], ah[kUnroll], b0[kUnroll], b1[second ? kUnroll : 1];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const int at = k + u * kWarps * kStep;
@@ -91,13 +93,13 @@ __global__ void __launch_bounds__(kThreads)
                 al[u] = in && row_lo ? __ldcg(reinterpret_cast<const uint4 *>(a_lo + at)) : zero;
                 ah[u] = in && row_hi ? __ldcg(reinterpret_cast<const uint4 *>(a_hi + at)) : zero;
                 b0[u] = in && in0 ? __ldcg(reinterpret_cast<const uint4 *>(x0 + at)) : zero;
-                b1[u] = in && in1 ? __ldcg(reinterpret_cast<const uint4 *>(x1 + at)) : zero;
+                if constexpr (second) b1[u] = in && in1 ? __ldcg(reinterpret_cast<const uint4 *>(x1 + at)) : zero;
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 mma16816(d[0], al[u].x, ah[u].x, al[u].y, ah[u].y, b0[u].x, b0[u].y);
                 mma16816(d[0], al[u].z, ah[u].z, al[u].w, ah[u].w, b0[u].z, b0[u].w);
-                if (second) {
+                if constexpr (second) {
                     mma16816(d[1], al[u].x, ah[u].x, al[u].y, ah[u].y, b1[u].x, b1[u].y);
                     mma16816(d[1], al[u].z, ah[u].z, al[u].w, ah[u].w, b1[u].z, b1[u].w);
                 }
@@ -107,6 +109,12 @@ __global__ void __launch_bounds__(kThreads)
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sm_sums[warp][b * 8 + (lane & 3) * 2 + (e & 1)][g + (e >> 1) * 8] = d[b][e];
+    };
+    for (int c0 = 0; c0 < count; c0 += kTokens) {
+        if (c0 + 8 < count)
+            products(c0, std::true_type{});
+        else
+            products(c0, std::false_type{});
         __syncthreads();
         for (int i = tid; i < kTokens * kRankTile; i += kThreads) {
             const int token = i / kRankTile, j = i % kRankTile;
@@ -123,19 +131,20 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-// K slices of a call: 256 values or more each, about four CTAs an SM if every row has an
+// K slices of a call: 256 values or more each, about eight CTAs an SM if every row has an
 // adapter of its own, and no more sums than the scratch holds.
 int lora_splits(int M, int K, int rank, int num_sms) {
     const int tiles = (rank + kRankTile - 1) / kRankTile;
     int s = (K + 255) / 256;
-    const int most = 4 * num_sms / (M * tiles), room = kLoraScratchFloats / (M * rank);
+    const int most = 8 * num_sms / (M * tiles), room = kLoraScratchFloats / (M * rank);
     s = s < 32 ? s : 32;
     s = s < most ? s : most;
     s = s < room ? s : room;
     return s > 1 ? s : 1;
 }
 
-cudaError_t launch_lora_shrink(const void *x, const LoraArgs &l, int M, int K, cudaStream_t stream, bool pdl) {
+cudaError_t launch_lora_shrink(const void *x, const LoraArgs &l, int M, int K, int num_sms, cudaStream_t stream,
+                               bool pdl) {
     // Slices of whole steps of 8 values; the last ones may be empty.
     const int slice = ((K + l.splits - 1) / l.splits + 7) / 8 * 8;
     cudaLaunchConfig_t cfg = {};
@@ -146,7 +155,10 @@ cudaError_t launch_lora_shrink(const void *x, const LoraArgs &l, int M, int K, c
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    // Many CTAs that wait for the kernel before take its place: 64 x 7168 x 18432 with 64 adapters
+    // of rank 16 67 us, 61 without; few ones are ready sooner (1 x 2048 x 7168 12.4 us, 13.6).
+    const long long ctas = static_cast<long long>(cfg.gridDim.x) * cfg.gridDim.y * cfg.gridDim.z;
+    cfg.numAttrs = pdl && ctas <= 2 * num_sms ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, lora_shrink_kernel, static_cast<const uint16_t *>(x), l, M, K, slice);
 }
 
