@@ -343,8 +343,7 @@ int gemm_launch(const void *x, const void *W, void *out, int M, int N, int K, vo
             return SKINNY_ERR_LAUNCH;
         }
     }
-    // The shallow ring's room for adapters ends at rank 64.
-    const bool shallow = use_shallow_ring(g, pdl) && !(lora && lora->rank > 64);
+    const bool shallow = use_shallow_ring(g, pdl);
     // Split tiles of 64-row accumulators, every CTA within at most two tiles (two
     // scratch slots), plain output: the GEMM only publishes its partials and a
     // small kernel finishes them (same order, same bits). A finisher CTA would

@@ -61,8 +61,7 @@ constexpr int kL2PrefetchShallow = 8;
 // The longest a producer waits for the previous GEMM's completion signal before
 // it goes on without the prefetch that depends on it (GemmArgs::l2_after_reduce).
 constexpr uint64_t kAfterReduceWaitNs = 50000ull;
-// Shallow rings have 5..6 stages, deep ones 9..11; LORA: 4, and 6..9.
-constexpr int kMaxShallowStages = 6, kLoraShallowStages = 4;
+constexpr int kMaxShallowStages = 6;  // shallow rings have 5..6 stages, deep ones 9..11
 
 // MP: padded row count (MMA N). STAGES: shared-memory ring depth. The deep ring
 // (185-227 KB) keeps the most bytes in flight; the shallow one (~100-112 KB) lets
@@ -72,7 +71,6 @@ constexpr int kMaxShallowStages = 6, kLoraShallowStages = 4;
 template <int MP, int STAGES, bool LORA = false>
 struct Layout {
     static constexpr int kStages = STAGES;
-    static constexpr bool kShallow = STAGES <= (LORA ? kLoraShallowStages : kMaxShallowStages);
     static constexpr int kAccCols = MP == 64 ? 64 : 32;  // TMEM columns per accumulator
     // Two accumulator buffers; LORA: the adapters' part of a tile, in the columns after them
     // (a power of two of columns in all).
@@ -84,12 +82,10 @@ struct Layout {
     static constexpr int kNumBars = 2 * kStages + 7;
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;
-    // LORA: the adapters in use and their rows, scale A x [M][rank], then the epilogue warps' rings
-    // of rows of B in what is left of kLoraBytes (at least 32 rows of rank 64, or 128, a warp).
-    static constexpr int kLoraOffset = kMiscOffset + 24;
-    static constexpr int kLoraAxOffset = kLoraOffset + (8 + 4 + 4) * kMaxM + 16;
-    static constexpr int kLoraBytes = kShallow ? 24576 + MP * 64 * 4 : 49152 + MP * kLoraMaxRank * 4;
-    static constexpr int kBytes = LORA ? kLoraAxOffset + kLoraBytes : kMiscOffset + 16;
+    // LORA: the rows' adapters and their scales, then scale A x [M][rank] (as many bytes as the
+    // call needs).
+    static constexpr int kLoraOffset = kMiscOffset + 24, kLoraAxOffset = kLoraOffset + 2 * kMaxM * 4;
+    static constexpr int kBytes = LORA ? kLoraAxOffset : kMiscOffset + 16;
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
     static_assert(!LORA || kLoraOffset % 16 == 0, "16-byte loads of A x");
     static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment");
@@ -193,13 +189,12 @@ __device__ __forceinline__ void store_tile_staged(const float (&v)[MP], uint16_t
 //
 // LORA: the kernel is launched behind lora_shrink_kernel, which lets it start once x is
 // there, so nothing but the epilogue waits for that kernel. While a tile's weights stream the
-// epilogue's threads, idle otherwise, work its part out: thread = output column n, which takes
-// row n of each B in use from shared memory, where its warp has copied its 32 rows (one stretch
-// of B; cp.async, some adapters ahead, waited for by the warp alone), and multiplies it with A x
-// of the adapter's rows, in FP32; the result waits in tensor memory. A tile's contributors
-// (split K) share the adapters out, or the rows if there are fewer adapters. Each
-// thread reading its own row of B from memory took 79 us where this takes 42 (64 x 20480 x 1024,
-// 64 adapters of rank 32): 32 rows a load are 32 requests.
+// epilogue's threads, idle otherwise, work its part out: thread = output column n, which reads
+// row n of every B in use (each once, but for rows that share an adapter: those find it in
+// L2) and A x from shared memory, in FP32; the result waits in tensor memory. A
+// tile's contributors (split K) share the rows out. Copies of the rows of B through shared memory
+// (cp.async, some adapters ahead, each B once for all its rows) were no faster: 64 x 7168 x 18432
+// with 64 adapters of rank 16 64.7 us, 5 x 4099 x 1000 with 3 of rank 8 13.6 us.
 template <int MP, int STAGES, bool EPI, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_gemm_kernel(const __grid_constant__ CUtensorMap w_map,
@@ -301,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w.next(g.kblocks);
             }
             // The blocks after the ring's worth go to L2 ahead of time.
-            const int lead = L::kShallow ? kL2PrefetchShallow : args.l2_lead;
+            const int lead = STAGES <= kMaxShallowStages ? kL2PrefetchShallow : args.l2_lead;
             const int npf = total - npre < lead ? total - npre : lead;
             BlockCursor pf = w;
             for (int j = 0; j < npf; ++j) {
@@ -413,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ---------------- epilogue (128 threads) ----------------
-        ptx::pdl_wait();  // scratch and out may still be in use by the predecessor
+        if (!LORA) ptx::pdl_wait();  // scratch and out may still be in use by the predecessor
         if (args.clear_gemm_done && blockIdx.x == 0 && threadIdx.x == 64) atomicExch(args.gemm_done, 0u);
         const int quarter = warp & 3;              // TMEM lanes 32*quarter .. +31
         const int row = quarter * 32 + lane;       // weight row within the tile
@@ -425,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool fix_pending = false;
         // Whole tiles of 32 or 64 padded rows, deep ring, 16-byte aligned output
         // rows: the last piece's tile goes out through the ring.
-        constexpr bool kStagedOut = MP >= 32 && !L::kShallow;
+        constexpr bool kStagedOut = MP >= 32 && STAGES > kMaxShallowStages;
         const bool staged = kStagedOut && (reinterpret_cast<uintptr_t>(args.out) & 15) == 0 &&
                             (g.N & 7) == 0;
 
@@ -449,52 +444,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ahead[i] = lo | (hi << 16);
             }
         };
-        // LORA: the adapters in use, each with its rows, and scale A x, the K slices' sums added
-        // in order; and the rows of this piece whose part is in tensor memory.
-        [[maybe_unused]] uint64_t *sm_rows = reinterpret_cast<uint64_t *>(smem + L::kLoraOffset);
-        [[maybe_unused]] int *sm_adapter = reinterpret_cast<int *>(smem + L::kLoraOffset + 8 * kMaxM);
-        [[maybe_unused]] float *sm_scale = reinterpret_cast<float *>(sm_adapter + kMaxM);  // of each row's adapter
-        [[maybe_unused]] int *sm_adapters = sm_adapter + 2 * kMaxM;                         // how many
+        // LORA: the rows' adapters and scale A x, the K slices' sums added in order; and the rows
+        // of this piece whose part is in tensor memory.
+        [[maybe_unused]] int *sm_adapter = reinterpret_cast<int *>(smem + L::kLoraOffset);
+        [[maybe_unused]] float *sm_scale = reinterpret_cast<float *>(sm_adapter + kMaxM);
         [[maybe_unused]] float *sm_ax = reinterpret_cast<float *>(smem + L::kLoraAxOffset);
-        [[maybe_unused]] const int ring_bytes = (L::kLoraBytes - g.M * args.lora.rank * 4) / 64 * 16;  // of a warp
-        [[maybe_unused]] uint8_t *sm_ring = smem + L::kLoraAxOffset + g.M * args.lora.rank * 4 + quarter * ring_bytes;
         [[maybe_unused]] uint64_t lora_rows = 0;
         [[maybe_unused]] const uint32_t lora_taddr =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + L::kLoraCol;
         if constexpr (LORA) {
             const LoraArgs &l = args.lora;
-            if (warp == 2) {
-                // Adapters in the order of their first rows.
-                int id[2];
-                uint64_t rows[2] = {};
-                unsigned first[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int m = h * 32 + lane;
-                    id[h] = m < g.M ? __ldcg(l.adapters + m) : -1;
-                    if (id[h] < 0 || id[h] >= l.count) id[h] = -1;
-                    sm_scale[m] = id[h] >= 0 && l.scales != nullptr ? __ldcg(l.scales + id[h]) : 1.0f;
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) rows[h] = static_cast<uint64_t>(__match_any_sync(0xFFFFFFFFu, id[h])) << 32 * h;
-                if (MP > 32)
-                    for (int i = 0; i < 32; ++i) {
-                        rows[0] |= static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, id[1], i) == id[0]) << (32 + i);
-                        rows[1] |= static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, id[0], i) == id[1]) << i;
-                    }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    first[h] = __ballot_sync(0xFFFFFFFFu, id[h] >= 0 && __ffsll(static_cast<long long>(rows[h])) - 1 == h * 32 + lane);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (first[h] >> lane & 1) {
-                        const int at = (h > 0 ? __popc(first[0]) : 0) + __popc(first[h] & ((1u << lane) - 1u));
-                        sm_rows[at] = rows[h];
-                        sm_adapter[at] = id[h];
-                    }
-                if (lane == 0) *sm_adapters = __popc(first[0]) + __popc(first[1]);
+            // The adapters' numbers are as old as x, and the scales are weights: before the wait.
+            if (etid < kMaxM) {
+                int id = etid < g.M ? __ldcg(l.adapters + etid) : -1;
+                if (id >= l.count) id = -1;
+                sm_adapter[etid] = id;
+                sm_scale[etid] = id >= 0 && l.scales != nullptr ? __ldcg(l.scales + id) : 1.0f;
             }
             ptx::named_barrier_sync(1, kEpilogueThreads);
+            ptx::pdl_wait();  // A x is the kernel's before
             // Sums of rows without an adapter are not there, and what is read of them is not used.
             const int values = g.M * l.rank;
             auto add_slices = [&](auto at_once, auto slices) {  // loads that are on their way together
@@ -529,85 +497,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 add_slices(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
             ptx::named_barrier_sync(1, kEpilogueThreads);
         }
-        // The adapters' part of this thread's column of a tile, for share `share` of `shares`.
-        [[maybe_unused]] auto lora_part = [&](int tile, int share, int shares) {
+        // The adapters' part of column n for the rows m = share (mod shares) of a piece.
+        [[maybe_unused]] auto lora_part = [&](int n, int share, int shares) {
             const LoraArgs &l = args.lora;
-            const int adapters = *sm_adapters;
-            const bool by_rows = adapters < shares;
-            const int step = by_rows ? 1 : shares, begin = by_rows ? 0 : share;
-            uint64_t mine = ~0ull;  // rows of the share
-            if (shares > 1 && by_rows) {
-                mine = 0;
-                for (int m = share; m < kMaxM; m += shares) mine |= 1ull << m;
-            }
-            lora_rows = 0;
-            // A ring entry has the warp's rows of one B, an odd number of 16-byte pieces apart, so that
-            // eight rows' pieces lie in different banks.
-            const int pieces = l.rank / 8, pitch = 16 * (pieces + 1 + pieces % 2), entry = 32 * pitch;
-            const int entries = ring_bytes / entry, ahead = min(entries - 1, ptx::kMostGroupsAhead);
-            const int n0 = tile * kBlockN + quarter * 32, bound = (min(n0 + 32, g.N) - n0) * pieces;  // pieces there are
-            const unsigned inverse = (65535u + pieces) / pieces;  // p / pieces = p * inverse >> 16 for p < 512
-            const uint32_t ring = ptx::smem_addr(sm_ring);
-            int put = 0;  // the entry that is filled next
-            auto copy = [&](int a) {
-                if (a < adapters) {
-                    const uint16_t *from = l.B + (static_cast<size_t>(sm_adapter[a]) * g.N + n0) * l.rank;
-                    for (int p = lane; p < bound; p += 32) {
-                        const int r = static_cast<int>(p * inverse >> 16);
-                        ptx::cp_async16(ring + put * entry + r * pitch + (p - r * pieces) * 16, from + p * 8);
-                    }
-                    put = put + 1 >= entries ? 0 : put + 1;
+            auto wanted = [&](int m) { return m < g.M && sm_adapter[m] >= 0 && m % shares == share; };
+            lora_rows = __ballot_sync(0xFFFFFFFFu, wanted(lane)) |
+                        static_cast<uint64_t>(MP > 32 ? __ballot_sync(0xFFFFFFFFu, wanted(lane + 32)) : 0u) << 32;
+            constexpr int kAtOnce = MP == 16 ? 4 : 8;  // rows whose loads are on their way together
+            const uint16_t *column = l.B + static_cast<size_t>(n < g.N ? n : 0) * l.rank;
+            for (uint64_t rest = lora_rows; rest != 0;) {
+                int m[kAtOnce];
+                const uint4 *b[kAtOnce];
+                float v[kAtOnce];
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    m[u] = rest != 0 ? __ffsll(static_cast<long long>(rest)) - 1 : -1;
+                    rest &= rest - 1;
+                    const size_t id = m[u] < 0 ? 0 : sm_adapter[m[u]];
+                    b[u] = reinterpret_cast<const uint4 *>(column + id * g.N * l.rank);
+                    v[u] = 0.0f;
                 }
-                ptx::cp_async_commit();  // a group an adapter, empty or not
-            };
-            for (int i = 0; i <= ahead; ++i) copy(begin + i * step);
-            int get = 0;
-            for (int a = begin; a < adapters; a += step) {
-                ptx::cp_async_wait_for(ahead);
-                __syncwarp();
-                const uint4 *row = reinterpret_cast<const uint4 *>(sm_ring + get * entry + lane * pitch);
-                uint64_t rest = sm_rows[a] & mine;
-                lora_rows |= rest;
-                // Rows of x, `at_once` of them for a pass over the row of B; four sums each.
-                auto rows = [&](auto at_once) {
-                    constexpr int kAtOnce = decltype(at_once)::value;
-                    int m[kAtOnce];
-                    float v[kAtOnce][4] = {};
-#pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u) {
-                        m[u] = __ffsll(static_cast<long long>(rest)) - 1;
-                        rest &= rest - 1;
-                    }
-#pragma unroll 2
-                    for (int c = 0; c < pieces; ++c) {
-                        const uint4 w = row[c];
-                        const float b[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u),
-                                            __uint_as_float(w.z << 16), __uint_as_float(w.z & 0xFFFF0000u),
-                                            __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xFFFF0000u)};
-#pragma unroll
-                        for (int u = 0; u < kAtOnce; ++u) {
-                            const float4 *ax = reinterpret_cast<const float4 *>(sm_ax + m[u] * l.rank + c * 8);
-                            const float4 t0 = ax[0], t1 = ax[1];
-                            v[u][0] = fmaf(t1.x, b[4], fmaf(t0.x, b[0], v[u][0]));
-                            v[u][1] = fmaf(t1.y, b[5], fmaf(t0.y, b[1], v[u][1]));
-                            v[u][2] = fmaf(t1.z, b[6], fmaf(t0.z, b[2], v[u][2]));
-                            v[u][3] = fmaf(t1.w, b[7], fmaf(t0.w, b[3], v[u][3]));
-                        }
-                    }
+                for (int j = 0; j < l.rank; j += 16) {
+                    uint4 w[kAtOnce][2];
 #pragma unroll
                     for (int u = 0; u < kAtOnce; ++u)
-                        ptx::tmem_st1(lora_taddr + m[u], __float_as_uint((v[u][0] + v[u][1]) + (v[u][2] + v[u][3])));
-                };
-                int left = __popcll(static_cast<long long>(rest));
-                for (; left >= 4; left -= 4) rows(std::integral_constant<int, 4>{});
-                if (left & 2) rows(std::integral_constant<int, 2>{});
-                if (left & 1) rows(std::integral_constant<int, 1>{});
-                get = get + 1 >= entries ? 0 : get + 1;
-                __syncwarp();  // the entry is read
-                copy(a + (ahead + 1) * step);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            w[u][h] = m[u] >= 0 && j + 8 * h < l.rank ? __ldg(b[u] + j / 8 + h) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        if (m[u] < 0) break;
+                        const float4 *ax = reinterpret_cast<const float4 *>(sm_ax + m[u] * l.rank + j);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (j + 8 * h >= l.rank) break;
+                            const float4 t0 = ax[2 * h], t1 = ax[2 * h + 1];
+                            v[u] = fmaf(t0.x, __uint_as_float(w[u][h].x << 16), v[u]);
+                            v[u] = fmaf(t0.y, __uint_as_float(w[u][h].x & 0xFFFF0000u), v[u]);
+                            v[u] = fmaf(t0.z, __uint_as_float(w[u][h].y << 16), v[u]);
+                            v[u] = fmaf(t0.w, __uint_as_float(w[u][h].y & 0xFFFF0000u), v[u]);
+                            v[u] = fmaf(t1.x, __uint_as_float(w[u][h].z << 16), v[u]);
+                            v[u] = fmaf(t1.y, __uint_as_float(w[u][h].z & 0xFFFF0000u), v[u]);
+                            v[u] = fmaf(t1.z, __uint_as_float(w[u][h].w << 16), v[u]);
+                            v[u] = fmaf(t1.w, __uint_as_float(w[u][h].w & 0xFFFF0000u), v[u]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u)
+                    if (m[u] >= 0) ptx::tmem_st1(lora_taddr + m[u], __float_as_uint(v[u]));
             }
-            ptx::cp_async_wait_for(0);  // nothing but empty groups
             ptx::tmem_st_wait();
             __syncwarp();
         };
@@ -746,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (args.epi.bias != nullptr && n < g.N) bias = bf16_value(args.epi.bias[n]);
                 load_residual(n, 0);
             }
-            if constexpr (LORA) lora_part(p.tile, cta - first, last - first + 1);
+            if constexpr (LORA) lora_part(p.tile * kBlockN + row, cta - first, last - first + 1);
             const int b = q & 1;
             const uint32_t aph = (q >> 1) & 1;
             const int r = bounded_wait(bar_acc_full + 8 * b, aph, abort_flag, limit);
@@ -874,19 +813,20 @@ cudaError_t launch_kernel(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            const GemmArgs &args, int ctas, cudaStream_t stream, bool pdl,
                            int device) {
     using L = Layout<MP, STAGES, LORA>;
-    static_assert(L::kDynamicBytes <= 232448, "shared memory of a CTA");
+    constexpr int kMostBytes = L::kDynamicBytes + (LORA ? MP * kLoraMaxRank * 4 : 0);
+    static_assert(kMostBytes <= 232448, "shared memory of a CTA");
     static bool configured[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (!configured[device]) {
         cudaError_t e = cudaFuncSetAttribute(decode_gemm_kernel<MP, STAGES, EPI, LORA>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynamicBytes);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
         if (e != cudaSuccess) return e;
         configured[device] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = L::kDynamicBytes;
+    cfg.dynamicSmemBytes = L::kDynamicBytes + (LORA ? args.M * args.lora.rank * 4 : 0);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -903,9 +843,8 @@ cudaError_t launch_variant(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            const GemmArgs &args, int ctas, cudaStream_t stream, bool pdl,
                            int device) {
     if (args.lora.rank > 0) {
-        // A x and the rings of B take stages' place: up to 80 KB beside the deep ring, 30 beside the
-        // shallow one.
-        constexpr int kLoraStages = STAGES > kMaxShallowStages ? (MP == 64 ? 6 : MP == 32 ? 8 : 9) : kLoraShallowStages;
+        // A x takes one stage of the rings that fill the shared memory (up to 32 KB).
+        constexpr int kLoraStages = STAGES - (MP >= 32 && STAGES > kMaxShallowStages ? 1 : 0);
         return launch_kernel<MP, kLoraStages, true, true>(w_map, x_map, args, ctas, stream, pdl, device);
     }
     if (args.epilogue)
