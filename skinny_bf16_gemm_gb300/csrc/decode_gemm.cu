@@ -68,7 +68,9 @@ constexpr int kMaxShallowStages = 6;  // shallow rings have 5..6 stages, deep on
 // the next kernel's CTAs be resident on the same SM while this one finishes, so
 // with programmatic dependent launch they stream weights across the boundary
 // (plan.cuh use_shallow_ring picks one by the weight bytes per CTA).
-template <int MP, int STAGES, bool LORA = false>
+// LORA: how the adapters' part of a tile is worked out (decode_gemm_bf16_lora), see the kernel.
+enum Lora { kNoLora, kLoraDirect, kLoraCopied };
+template <int MP, int STAGES, int LORA = kNoLora>
 struct Layout {
     static constexpr int kStages = STAGES;
     static constexpr int kAccCols = MP == 64 ? 64 : 32;  // TMEM columns per accumulator
@@ -83,9 +85,13 @@ struct Layout {
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;
     // LORA: the rows' adapters and their scales, then scale A x [M][rank] (as many bytes as the
-    // call needs).
-    static constexpr int kLoraOffset = kMiscOffset + 24, kLoraAxOffset = kLoraOffset + 2 * kMaxM * 4;
-    static constexpr int kBytes = LORA ? kLoraAxOffset : kMiscOffset + 16;
+    // call needs). Copied: before them the adapters in use and their rows, behind them the
+    // epilogue warps' rings of rows of B, in what is left of kLoraBytes (at least 32 rows of rank
+    // 128 a warp).
+    static constexpr int kLoraOffset = kMiscOffset + 24, kLoraListOffset = kLoraOffset + 2 * kMaxM * 4;
+    static constexpr int kLoraAxOffset = kLoraListOffset + (LORA == kLoraCopied ? 12 * kMaxM + 16 : 0);
+    static constexpr int kLoraBytes = LORA == kLoraCopied ? 49152 + MP * kLoraMaxRank * 4 : 0;
+    static constexpr int kBytes = LORA ? kLoraAxOffset + kLoraBytes : kMiscOffset + 16;
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
     static_assert(!LORA || kLoraOffset % 16 == 0, "16-byte loads of A x");
     static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment");
@@ -189,18 +195,26 @@ __device__ __forceinline__ void store_tile_staged(const float (&v)[MP], uint16_t
 //
 // LORA: the kernel is launched behind lora_shrink_kernel, which lets it start once x is
 // there, so nothing but the epilogue waits for that kernel. While a tile's weights stream the
-// epilogue's threads, idle otherwise, work its part out: thread = output column n, which reads
-// row n of every B in use (each once, but for rows that share an adapter: those find it in
-// L2) and A x from shared memory, in FP32; the result waits in tensor memory. A
-// tile's contributors (split K) share the rows out. Copies of the rows of B through shared memory
-// (cp.async, some adapters ahead, each B once for all its rows) were no faster: 64 x 7168 x 18432
-// with 64 adapters of rank 16 64.7 us, 5 x 4099 x 1000 with 3 of rank 8 13.6 us.
-template <int MP, int STAGES, bool EPI, bool LORA>
+// epilogue's threads, idle otherwise, work its part out: thread = output column n, which multiplies
+// row n of every B in use with A x of the adapter's rows, from shared memory, in FP32; the result
+// waits in tensor memory. A tile's contributors (split K) share the work out. Two forms, by
+// the call's rank and rows:
+//   direct  each row of x takes its row of B to registers, eight rows at a time (those that share
+//           an adapter find it in L2). For small ranks, whose 32 rows of a warp are few lines.
+//   copied  each B in use once: the warp copies its 32 rows, one stretch of B, to shared memory
+//           (cp.async, some adapters ahead, waited for by the warp alone), in the place of two or
+//           three stages. From rank 64 on a load of 32 rows' pieces is 32 requests: 64 x 4096 x
+//           4096 with 16 adapters of rank 128 50 us, direct 74; 32 x 18432 x 7168 with 8 of rank 64
+//           54 and 65; but 64 x 7168 x 18432 with 64 of rank 16 65 and 62, 5 x 4099 x 1000 with 3 of
+//           rank 8 13.6 and 11.1.
+template <int MP, int STAGES, bool EPI, int LORA>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_gemm_kernel(const __grid_constant__ CUtensorMap w_map,
                        const __grid_constant__ CUtensorMap x_map, const GemmArgs args) {
     using L = Layout<MP, STAGES, LORA>;
     constexpr int S = L::kStages;
+    constexpr bool kCopied = LORA == kLoraCopied;
+    constexpr bool kShallow = STAGES <= kMaxShallowStages && !kCopied;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -296,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w.next(g.kblocks);
             }
             // The blocks after the ring's worth go to L2 ahead of time.
-            const int lead = STAGES <= kMaxShallowStages ? kL2PrefetchShallow : args.l2_lead;
+            const int lead = kShallow ? kL2PrefetchShallow : args.l2_lead;
             const int npf = total - npre < lead ? total - npre : lead;
             BlockCursor pf = w;
             for (int j = 0; j < npf; ++j) {
@@ -420,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool fix_pending = false;
         // Whole tiles of 32 or 64 padded rows, deep ring, 16-byte aligned output
         // rows: the last piece's tile goes out through the ring.
-        constexpr bool kStagedOut = MP >= 32 && STAGES > kMaxShallowStages;
+        constexpr bool kStagedOut = MP >= 32 && !kShallow;
         const bool staged = kStagedOut && (reinterpret_cast<uintptr_t>(args.out) & 15) == 0 &&
                             (g.N & 7) == 0;
 
@@ -449,6 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         [[maybe_unused]] int *sm_adapter = reinterpret_cast<int *>(smem + L::kLoraOffset);
         [[maybe_unused]] float *sm_scale = reinterpret_cast<float *>(sm_adapter + kMaxM);
         [[maybe_unused]] float *sm_ax = reinterpret_cast<float *>(smem + L::kLoraAxOffset);
+        // Copied: the adapters in use, each with its rows, and how many they are.
+        [[maybe_unused]] uint64_t *sm_rows = reinterpret_cast<uint64_t *>(smem + L::kLoraListOffset);
+        [[maybe_unused]] int *sm_used = reinterpret_cast<int *>(smem + L::kLoraListOffset + 8 * kMaxM);
+        [[maybe_unused]] const int ring_bytes = (L::kLoraBytes - g.M * args.lora.rank * 4) / 64 * 16;  // of a warp
+        [[maybe_unused]] uint8_t *sm_ring = smem + L::kLoraAxOffset + g.M * args.lora.rank * 4 + quarter * ring_bytes;
         [[maybe_unused]] uint64_t lora_rows = 0;
         [[maybe_unused]] const uint32_t lora_taddr =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + L::kLoraCol;
@@ -462,6 +481,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sm_scale[etid] = id >= 0 && l.scales != nullptr ? __ldcg(l.scales + id) : 1.0f;
             }
             ptx::named_barrier_sync(1, kEpilogueThreads);
+            if constexpr (kCopied) {
+                if (warp == 2) {
+                    // Adapters in the order of their first rows.
+                    const int id[2] = {sm_adapter[lane], sm_adapter[32 + lane]};
+                    uint64_t rows[2];
+                    unsigned first[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) rows[h] = static_cast<uint64_t>(__match_any_sync(0xFFFFFFFFu, id[h])) << 32 * h;
+                    for (int i = 0; i < 32; ++i) {
+                        rows[0] |= static_cast<uint64_t>(sm_adapter[32 + i] == id[0]) << (32 + i);
+                        rows[1] |= static_cast<uint64_t>(sm_adapter[i] == id[1]) << i;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        first[h] = __ballot_sync(0xFFFFFFFFu,
+                                                 id[h] >= 0 && __ffsll(static_cast<long long>(rows[h])) - 1 == h * 32 + lane);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (first[h] >> lane & 1) {
+                            const int at = (h > 0 ? __popc(first[0]) : 0) + __popc(first[h] & ((1u << lane) - 1u));
+                            sm_rows[at] = rows[h];
+                            sm_used[at] = id[h];
+                        }
+                    if (lane == 0) sm_used[kMaxM] = __popc(first[0]) + __popc(first[1]);
+                }
+                ptx::named_barrier_sync(1, kEpilogueThreads);
+            }
             ptx::pdl_wait();  // A x is the kernel's before
             // Sums of rows without an adapter are not there, and what is read of them is not used.
             const int values = g.M * l.rank;
@@ -497,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 add_slices(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
             ptx::named_barrier_sync(1, kEpilogueThreads);
         }
-        // The adapters' part of column n for the rows m = share (mod shares) of a piece.
+        // Direct: the adapters' part of column n for the rows m = share (mod shares) of a piece.
         [[maybe_unused]] auto lora_part = [&](int n, int share, int shares) {
             const LoraArgs &l = args.lora;
             auto wanted = [&](int m) { return m < g.M && sm_adapter[m] >= 0 && m % shares == share; };
@@ -547,6 +593,104 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < kAtOnce; ++u)
                     if (m[u] >= 0) ptx::tmem_st1(lora_taddr + m[u], __float_as_uint(v[u]));
             }
+            ptx::tmem_st_wait();
+            __syncwarp();
+        };
+        // Copied: the adapters' part of this thread's column of a tile. A ring entry has the warp's rows of
+        // one B, an odd number of 16-byte pieces apart, so that eight rows' pieces lie in different
+        // banks. lora_begin: share `share` of `shares`, and the first copies on their way.
+        [[maybe_unused]] const int lora_pieces = args.lora.rank / 8;
+        [[maybe_unused]] const int lora_pitch = 16 * (lora_pieces + 1 + lora_pieces % 2), lora_entry = 32 * lora_pitch;
+        [[maybe_unused]] const int lora_entries = kCopied ? ring_bytes / lora_entry : 0;
+        [[maybe_unused]] const int lora_ahead = min(lora_entries - 1, ptx::kMostGroupsAhead);
+        [[maybe_unused]] uint64_t lora_mine = 0, lora_copies = 0, lora_uses = 0;  // rows; adapters to copy, to use
+        [[maybe_unused]] int lora_put = 0, lora_get = 0, lora_n0 = 0, lora_bound = 0;
+        [[maybe_unused]] auto lora_copy = [&]() {
+            if (lora_copies != 0) {
+                const int a = __ffsll(static_cast<long long>(lora_copies)) - 1;
+                lora_copies &= lora_copies - 1;
+                const uint16_t *from = args.lora.B + (static_cast<size_t>(sm_used[a]) * g.N + lora_n0) * args.lora.rank;
+                const unsigned inverse = (65535u + lora_pieces) / lora_pieces;  // p / pieces = p * inverse >> 16, p < 512
+                const uint32_t to = ptx::smem_addr(sm_ring) + lora_put * lora_entry;
+                for (int p = lane; p < lora_bound; p += 32) {
+                    const int r = static_cast<int>(p * inverse >> 16);
+                    ptx::cp_async16(to + r * lora_pitch + (p - r * lora_pieces) * 16, from + p * 8);
+                }
+                lora_put = lora_put + 1 >= lora_entries ? 0 : lora_put + 1;
+            }
+            ptx::cp_async_commit();  // a group an adapter, empty or not
+        };
+        [[maybe_unused]] auto lora_begin = [&](int tile, int share, int shares) {
+            const int adapters = sm_used[kMaxM];
+            lora_mine = ~0ull;
+            lora_uses = adapters == 64 ? ~0ull : (1ull << adapters) - 1;
+            if (shares > 1) {
+                uint64_t every = 0;
+                for (int i = share; i < kMaxM; i += shares) every |= 1ull << i;
+                if (adapters >= shares) {
+                    lora_uses &= every;
+                } else {
+                    lora_mine = every;
+                    for (int a = 0; a < adapters; ++a)
+                        if ((sm_rows[a] & every) == 0) lora_uses &= ~(1ull << a);
+                }
+            }
+            lora_copies = lora_uses;
+            lora_put = lora_get = 0;
+            lora_n0 = tile * kBlockN + quarter * 32;
+            lora_bound = (min(lora_n0 + 32, g.N) - lora_n0) * lora_pieces;
+            for (int i = 0; i <= lora_ahead; ++i) lora_copy();
+        };
+        [[maybe_unused]] auto lora_copied = [&]() {
+            lora_rows = 0;
+            for (; lora_uses != 0; lora_uses &= lora_uses - 1) {
+                ptx::cp_async_wait_for(lora_ahead);
+                __syncwarp();
+                const uint4 *row = reinterpret_cast<const uint4 *>(sm_ring + lora_get * lora_entry + lane * lora_pitch);
+                uint64_t rest = sm_rows[__ffsll(static_cast<long long>(lora_uses)) - 1] & lora_mine;
+                lora_rows |= rest;
+                // Rows of x, `at_once` of them for a pass over the row of B; four sums each.
+                auto rows = [&](auto at_once) {
+                    constexpr int kAtOnce = decltype(at_once)::value;
+                    const float *ax[kAtOnce];
+                    int m[kAtOnce];
+                    float v[kAtOnce][4] = {};
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        m[u] = __ffsll(static_cast<long long>(rest)) - 1;
+                        rest &= rest - 1;
+                        ax[u] = sm_ax + m[u] * args.lora.rank;
+                    }
+#pragma unroll 2
+                    for (int c = 0; c < lora_pieces; ++c) {
+                        const uint4 w = row[c];
+                        const float b[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u),
+                                            __uint_as_float(w.z << 16), __uint_as_float(w.z & 0xFFFF0000u),
+                                            __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xFFFF0000u)};
+#pragma unroll
+                        for (int u = 0; u < kAtOnce; ++u) {
+                            const float4 t0 = reinterpret_cast<const float4 *>(ax[u])[2 * c],
+                                         t1 = reinterpret_cast<const float4 *>(ax[u])[2 * c + 1];
+                            v[u][0] = fmaf(t1.x, b[4], fmaf(t0.x, b[0], v[u][0]));
+                            v[u][1] = fmaf(t1.y, b[5], fmaf(t0.y, b[1], v[u][1]));
+                            v[u][2] = fmaf(t1.z, b[6], fmaf(t0.z, b[2], v[u][2]));
+                            v[u][3] = fmaf(t1.w, b[7], fmaf(t0.w, b[3], v[u][3]));
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        ptx::tmem_st1(lora_taddr + m[u], __float_as_uint((v[u][0] + v[u][1]) + (v[u][2] + v[u][3])));
+                };
+                int left = __popcll(static_cast<long long>(rest));
+                for (; left >= 4; left -= 4) rows(std::integral_constant<int, 4>{});
+                if (left & 2) rows(std::integral_constant<int, 2>{});
+                if (left & 1) rows(std::integral_constant<int, 1>{});
+                lora_get = lora_get + 1 >= lora_entries ? 0 : lora_get + 1;
+                __syncwarp();  // the entry is read
+                lora_copy();
+            }
+            ptx::cp_async_wait_for(0);  // nothing but empty groups
             ptx::tmem_st_wait();
             __syncwarp();
         };
@@ -685,7 +829,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (args.epi.bias != nullptr && n < g.N) bias = bf16_value(args.epi.bias[n]);
                 load_residual(n, 0);
             }
-            if constexpr (LORA) lora_part(p.tile * kBlockN + row, cta - first, last - first + 1);
+            if constexpr (kCopied) {
+                lora_begin(p.tile, cta - first, last - first + 1);
+                lora_copied();
+            } else if constexpr (LORA != kNoLora) {
+                lora_part(p.tile * kBlockN + row, cta - first, last - first + 1);
+            }
             const int b = q & 1;
             const uint32_t aph = (q >> 1) & 1;
             const int r = bounded_wait(bar_acc_full + 8 * b, aph, abort_flag, limit);
@@ -808,12 +957,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int MP, int STAGES, bool EPI, bool LORA>
+template <int MP, int STAGES, bool EPI, int LORA>
 cudaError_t launch_kernel(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            const GemmArgs &args, int ctas, cudaStream_t stream, bool pdl,
                            int device) {
     using L = Layout<MP, STAGES, LORA>;
-    constexpr int kMostBytes = L::kDynamicBytes + (LORA ? MP * kLoraMaxRank * 4 : 0);
+    constexpr int kMostBytes = L::kDynamicBytes + (LORA == kLoraDirect ? MP * kLoraMaxRank * 4 : 0);
     static_assert(kMostBytes <= 232448, "shared memory of a CTA");
     static bool configured[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
@@ -826,7 +975,7 @@ cudaError_t launch_kernel(const CUtensorMap &w_map, const CUtensorMap &x_map,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = L::kDynamicBytes + (LORA ? args.M * args.lora.rank * 4 : 0);
+    cfg.dynamicSmemBytes = L::kDynamicBytes + (LORA == kLoraDirect ? args.M * args.lora.rank * 4 : 0);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -843,13 +992,16 @@ cudaError_t launch_variant(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            const GemmArgs &args, int ctas, cudaStream_t stream, bool pdl,
                            int device) {
     if (args.lora.rank > 0) {
+        if constexpr (MP >= 32 && STAGES > kMaxShallowStages)
+            if (args.lora.rank >= 64)
+                return launch_kernel<MP, MP == 64 ? 6 : 8, true, kLoraCopied>(w_map, x_map, args, ctas, stream, pdl, device);
         // A x takes one stage of the rings that fill the shared memory (up to 32 KB).
         constexpr int kLoraStages = STAGES - (MP >= 32 && STAGES > kMaxShallowStages ? 1 : 0);
-        return launch_kernel<MP, kLoraStages, true, true>(w_map, x_map, args, ctas, stream, pdl, device);
+        return launch_kernel<MP, kLoraStages, true, kLoraDirect>(w_map, x_map, args, ctas, stream, pdl, device);
     }
     if (args.epilogue)
-        return launch_kernel<MP, STAGES, true, false>(w_map, x_map, args, ctas, stream, pdl, device);
-    return launch_kernel<MP, STAGES, false, false>(w_map, x_map, args, ctas, stream, pdl, device);
+        return launch_kernel<MP, STAGES, true, kNoLora>(w_map, x_map, args, ctas, stream, pdl, device);
+    return launch_kernel<MP, STAGES, false, kNoLora>(w_map, x_map, args, ctas, stream, pdl, device);
 }
 
 // Deep rings: about 185 KB for 16 rows, near the 227 KB a CTA may use for 32 and
