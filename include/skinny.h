@@ -522,8 +522,7 @@ SKINNY_API size_t skinny_attention_workspace_bytes(int num_sms);
  *   that all rows share and the row's own tokens after it. The drafter pages have no
  *   counterpart. For a batch behind one long prompt, and for the drafted tokens of one
  *   sequence: decode_attention_bf16 reads shared pages once a row, this reads the prefix
- *   once for up to 256 of a key head's query rows (rows * q_heads / kv_heads), on the tensor
- *   cores.
+ *   once a key head for all its query rows (rows * q_heads / kv_heads), on the tensor cores.
  *
  *   prefix_table   [prefix_width] int32: token j of the prefix is token j % page_size of page
  *                  prefix_table[j / page_size] of the cache.
@@ -535,7 +534,8 @@ SKINNY_API size_t skinny_attention_workspace_bytes(int num_sms);
  *                  aligned, its first SKINNY_ATTENTION_COUNTER_BYTES zero before its first
  *                  use; every call leaves it ready for the next, of any sizes that it is large
  *                  enough for. Calls that may run at the same time need one each.
- *   Three kernels: the prefix, the rows' own tokens while it runs out, and the join. Scores,
+ *   Three kernels: the prefix, the rows' own tokens while it runs out, and the join; for one
+ *   row, or a table of few tokens, one that reads both kinds of tokens row by row. Scores,
  *   maxima, sums and partial outputs are FP32; the prefix's weights are rounded to BF16 (to
  *   nearest) for the product with the values, the own tokens' as in decode_attention_bf16;
  *   the output is rounded once. Deterministic.
@@ -635,7 +635,8 @@ SKINNY_API const char *skinny_status_string(int status);
  *   indices from device memory (decode_gemm_bf16_lora, qk_norm_rope_bf16,
  *   decode_attention_bf16, decode_attention_shared_prefix_bf16, token_logprobs_bf16) met
  *   one out of range, and if that is the only bit the
- *   status is SKINNY_ERR_INDEX) to *word if word is not NULL. Clearing also
+ *   status is SKINNY_ERR_INDEX; 512 if a wait of decode_attention_shared_prefix_bf16 ran
+ *   out) to *word if word is not NULL. Clearing also
  *   re-arms the decode GEMM's scratch flags, so the next call starts clean and
  *   calls stop returning SKINNY_ERR_TIMEOUT. Host pointer: word.
  */

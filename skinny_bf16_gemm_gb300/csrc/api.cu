@@ -1080,17 +1080,19 @@ int skinny_device_error(int device, int *word) {
     if (reduce_word) value |= kErrReduceExchange;
     // The words of the kernels that read indices from device memory.
     int rope_word = 0, attention_word = 0, logprob_word = 0, lora_word = 0,
-        part_word = 0, prefix_word = 0;
+        part_word = 0, joined_word = 0, prefix_word = 0;
     if (st == SKINNY_OK && (rope_error_word(&rope_word, true) != cudaSuccess ||
                             attention_error_word(&attention_word, true) != cudaSuccess ||
                             logprob_error_word(&logprob_word, true) != cudaSuccess ||
                             lora_error_word(&lora_word, true) != cudaSuccess ||
                             attention_part_error_word(&part_word, true) != cudaSuccess ||
+                            attention_joined_error_word(&joined_word, true) != cudaSuccess ||
                             prefix_error_word(&prefix_word, true) != cudaSuccess)) {
         cudaGetLastError();
         st = SKINNY_ERR_DEVICE;
     }
-    if (rope_word || attention_word || logprob_word || lora_word || part_word || (prefix_word & 2)) value |= kErrIndex;
+    if (rope_word || attention_word || logprob_word || lora_word || part_word || joined_word || (prefix_word & 2))
+        value |= kErrIndex;
     if (prefix_word & 1) value |= kErrPrefixWait;
     cudaSetDevice(prev);
     if (word) *word = value;

@@ -32,6 +32,24 @@ bool outputs_clear(const Range (&in)[I], const Range (&outs)[O]) {
     return true;
 }
 
+// Whether the attention reads the prefix with every row's own tokens, in one launch, instead of
+// reading it once and joining: `tokens` is what the prefix's table holds. Every row then reads the
+// whole prefix, from L2 all but once, which is less than the time of two more launches up to about
+// 16 MiB in all for heads of up to 128: 12.4 against 14.7 us for 4 rows x 7 heads behind 509
+// tokens (1 MB), 14.5 against 15.7 for 64 rows behind 500 (16.4 MB), but 20.6 against 15.1 for 64
+// rows behind 2000 (66 MB). A single row's prefix is shared with nobody: 13.6 against 14.2 us for
+// 7 heads behind 8000 tokens, 51.0 against 63.6 for 56 heads over 8 behind 60000. Wider heads run on
+// the tensor cores from the first token on: 17.8 us for 8 rows x 16 heads of 256 behind 2000 tokens,
+// 34.1 in one launch. (Times inside a graph.)
+bool joined_is_faster(int rows, int kv_heads, int head_blocks, int head_dim, long long tokens) {
+    if (head_dim > 128) return false;
+    if (rows == 1 && head_blocks == 1) return true;
+    return tokens * rows * kv_heads * head_blocks * head_dim * 4 <= (16ll << 20);
+}
+long long attention_tiles(int rows, int kv_heads, int head_blocks, long long tokens) {
+    return (tokens + kAttnMinTile - 1) / kAttnMinTile * rows * kv_heads * head_blocks;
+}
+
 template <int N>
 int check_on_device(const Range (&all)[N], int dev) {
     for (const Range &b : all)
@@ -143,8 +161,22 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     if (p->workspace_bytes < ws.bytes) return SKINNY_ERR_SHAPE;
     if ((st = check_on_device(in, dev)) || (st = check_on_device(outs, dev))) return st;
     char *base = static_cast<char *>(p->workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     AttentionArgs o;
     attention_args(&own, pool, &o);
+    // Both kinds of tokens are counted in one int there, and so are the tiles.
+    const long long tokens = o.capacity + capacity;
+    if (joined_is_faster(p->rows, c->kv_heads, o.head_blocks, D, capacity) && tokens < (1ll << 31) - kAttnMinTile &&
+        attention_tiles(p->rows, c->kv_heads, o.head_blocks, tokens) < (1ll << 31)) {
+        o.prefix_table = static_cast<const int *>(p->prefix_table);
+        o.prefix_length = static_cast<const int *>(p->prefix_length);
+        o.prefix_capacity = static_cast<int>(capacity);
+        if (launch_decode_attention_joined(o, D, sms, dev, s, ls.pdl) != cudaSuccess) {
+            cudaGetLastError();
+            return SKINNY_ERR_LAUNCH;
+        }
+        return SKINNY_OK;
+    }
     o.out = nullptr;
     o.part = reinterpret_cast<float *>(base + ws.own_out);
     o.lse = reinterpret_cast<float *>(base + ws.own_lse);
@@ -179,7 +211,6 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     a.own_lse = o.lse;
     a.out = static_cast<uint16_t *>(p->out);
     a.lse = static_cast<float *>(p->lse);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     alignas(64) CUtensorMap k_map = {}, v_map = {};
     a.box_rows = prefix_box_rows(c->page_size, plan.tokens);
     a.head_chunks = static_cast<int>(std::min<long long>(c->head_stride / 64, 1ll << 30));

@@ -5,7 +5,7 @@ namespace skinny {
 
 cudaError_t launch_decode_attention(const AttentionArgs &a, int head_dim, int num_sms, int device,
                                     cudaStream_t stream, bool pdl) {
-    return launch_any_dim<false>(a, head_dim, num_sms, device, stream, pdl);
+    return launch_any_dim<kWhole>(a, head_dim, num_sms, device, stream, pdl);
 }
 
 cudaError_t attention_error_word(int *value, bool clear) { return read_error_word(value, clear); }

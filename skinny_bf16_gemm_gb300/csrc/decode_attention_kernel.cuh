@@ -46,9 +46,11 @@
 // prefetch sizes on the copies, chunks dealt out as CTAs come free (each costs a join),
 // several items of a CTA joined by a warp or two each (3 % slower for one row of one item).
 //
-// PART: the result stays FP32, for the join with the prefix that all rows share
-// (prefix_attention.cu). That kernel's part of the GPU is busy while this one runs: it waits
-// for it only at its end, so that whatever waits for this kernel has waited for both.
+// Two more forms serve decode_attention_shared_prefix_bf16. kPart: the rows' own tokens of a batch
+// behind a shared prefix; the result stays FP32, for the join with the prefix
+// (prefix_attention.cu). That kernel keeps the GPU busy while this one runs: it waits for it only
+// at its end, so that whatever waits for this kernel has waited for both. kJoined: the prefix's
+// tokens come before every row's own, from a table of their own.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -207,9 +209,12 @@ struct Cut {
     }
 };
 
-template <int D, int NB, bool PART>
+enum Form { kWhole, kPart, kJoined };
+
+template <int D, int NB, int FORM>
 __device__ __forceinline__ void decode_attention(const AttentionArgs &a) {
     using S = Shape<D, NB>;
+    constexpr bool PART = FORM == kPart, JOINED = FORM == kJoined;
     constexpr int kSub = S::kSub, kSets = S::kSets, kSlots = S::kSlots;
     constexpr uint32_t kAllSeen = kSub == 32 ? 0xFFFFFFFFu : (1u << (kSub & 31)) - 1u;
     constexpr int kChunks = D / 8;            // 16-byte chunks of a token's row
@@ -237,6 +242,14 @@ __device__ __forceinline__ void decode_attention(const AttentionArgs &a) {
     if (!PART) ptx::pdl_wait();
 
     // ---- the split ----
+    int shared = 0;  // JOINED: tokens of the prefix
+    if constexpr (JOINED) {
+        shared = __ldcg(a.prefix_length);
+        if (shared < 0 || shared > a.prefix_capacity) {
+            if (cta == 0 && tid == 0) atomicOr(&g_attn_err, 1);
+            shared = shared < 0 ? 0 : a.prefix_capacity;
+        }
+    }
     // Prefix sums of the rows' tiles. A length is taken within [0, capacity].
     const int per = (a.rows + kThreads - 1) / kThreads;
     const int r_lo = min(tid * per, a.rows), r_hi = min(r_lo + per, a.rows);
@@ -247,6 +260,7 @@ __device__ __forceinline__ void decode_attention(const AttentionArgs &a) {
             if (cta == 0) atomicOr(&g_attn_err, 1);
             n = n < 0 ? 0 : a.capacity;
         }
+        if constexpr (JOINED) n += shared;
         lengths[r] = n;
         mine += (seen_of(n, a.window, a.sinks).count + kSub - 1) / kSub;
         prefix[r + 1] = mine;
@@ -386,10 +400,17 @@ __device__ __forceinline__ void decode_attention(const AttentionArgs &a) {
         if (ahead_x < x_end) {
             const int t = ahead.tile * kSub + lane;
             if (lane < kSub && t < ahead_seen.count) {
-                const int j = t < ahead_seen.sinks ? t : t + ahead_seen.gap;
+                int j = t < ahead_seen.sinks ? t : t + ahead_seen.gap;
+                const int *table = ahead_table;
+                if constexpr (JOINED) {
+                    if (j < shared)
+                        table = a.prefix_table;
+                    else
+                        j -= shared;
+                }
                 const int e = a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size;
                 in_page = j - e * a.page_size;
-                cp_async4(ptx::smem_addr(&to->y), ahead_table + e);
+                cp_async4(ptx::smem_addr(&to->y), table + e);
             }
             if (lane == 0) look_head[slot] = ahead_head;
             if (++ahead.tile == ahead_tiles && ahead_x + 1 < x_end) {
@@ -965,26 +986,26 @@ __device__ __forceinline__ void decode_attention(const AttentionArgs &a) {
     }
 }
 
-template <int D, int NB, bool PART>
+template <int D, int NB, int FORM>
 __global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_attention_kernel(const AttentionArgs a) {
-    decode_attention<D, NB, PART>(a);
-    if (PART) ptx::pdl_wait();
+    decode_attention<D, NB, FORM>(a);
+    if (FORM == kPart) ptx::pdl_wait();
 }
 
-template <int D, int NB, bool PART>
+template <int D, int NB, int FORM>
 cudaError_t launch(const AttentionArgs &a, int num_sms, int device, cudaStream_t stream, bool pdl) {
     using S = Shape<D, NB>;
     static bool configured[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (!configured[device]) {
-        cudaError_t e = cudaFuncSetAttribute(decode_attention_kernel<D, NB, PART>,
+        cudaError_t e = cudaFuncSetAttribute(decode_attention_kernel<D, NB, FORM>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes(kAttnMaxRows));
         if (e != cudaSuccess) return e;
         configured[device] = true;
     }
     // No more CTAs than the tables could ever hold tiles for their warps.
     const long long tiles = static_cast<long long>(a.rows) * a.kv_heads * a.head_blocks *
-                            ((a.capacity + S::kSub - 1ll) / S::kSub);
+                            ((static_cast<long long>(a.capacity) + a.prefix_capacity + S::kSub - 1) / S::kSub);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(num_sms * attn_ctas_per_sm(D, NB), (tiles + kWarps - 1) / kWarps)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -995,26 +1016,26 @@ cudaError_t launch(const AttentionArgs &a, int num_sms, int device, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_attention_kernel<D, NB, PART>, a);
+    return cudaLaunchKernelEx(&cfg, decode_attention_kernel<D, NB, FORM>, a);
 }
 
-template <int D, bool PART>
+template <int D, int FORM>
 cudaError_t launch_dim(const AttentionArgs &a, int num_sms, int device, cudaStream_t stream, bool pdl) {
-    if (a.block_heads <= 8) return launch<D, 1, PART>(a, num_sms, device, stream, pdl);
-    if (a.block_heads <= 16) return launch<D, 2, PART>(a, num_sms, device, stream, pdl);
-    if constexpr (D <= 128) return launch<D, 4, PART>(a, num_sms, device, stream, pdl);
+    if (a.block_heads <= 8) return launch<D, 1, FORM>(a, num_sms, device, stream, pdl);
+    if (a.block_heads <= 16) return launch<D, 2, FORM>(a, num_sms, device, stream, pdl);
+    if constexpr (D <= 128) return launch<D, 4, FORM>(a, num_sms, device, stream, pdl);
     return cudaErrorInvalidValue;
 }
 
-template <bool PART>
+template <int FORM>
 cudaError_t launch_any_dim(const AttentionArgs &a, int head_dim, int num_sms, int device, cudaStream_t stream,
                            bool pdl) {
     switch (head_dim) {
-        case 64: return launch_dim<64, PART>(a, num_sms, device, stream, pdl);
-        case 96: return launch_dim<96, PART>(a, num_sms, device, stream, pdl);
-        case 128: return launch_dim<128, PART>(a, num_sms, device, stream, pdl);
-        case 192: return launch_dim<192, PART>(a, num_sms, device, stream, pdl);
-        case 256: return launch_dim<256, PART>(a, num_sms, device, stream, pdl);
+        case 64: return launch_dim<64, FORM>(a, num_sms, device, stream, pdl);
+        case 96: return launch_dim<96, FORM>(a, num_sms, device, stream, pdl);
+        case 128: return launch_dim<128, FORM>(a, num_sms, device, stream, pdl);
+        case 192: return launch_dim<192, FORM>(a, num_sms, device, stream, pdl);
+        case 256: return launch_dim<256, FORM>(a, num_sms, device, stream, pdl);
         default: return cudaErrorInvalidValue;
     }
 }

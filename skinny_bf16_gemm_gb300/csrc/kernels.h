@@ -195,6 +195,9 @@ struct AttentionArgs {
     int head_blocks;  // blocks the group is cut into, of block_heads heads at most
     int block_heads;
     int capacity;     // tokens a row's table holds
+    const int *prefix_table;   // the joined form: the prefix's pages,
+    const int *prefix_length;  // its tokens,
+    int prefix_capacity;       // and how many the table holds (0 in the other forms)
     int wide;         // the keys (or values) span more than 2^32 chunks of 16 bytes
     int window, sinks;
     float scale_log2;  // scale * log2(e)
@@ -241,9 +244,12 @@ cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap 
                                     int head_dim, int device, cudaStream_t stream, bool pdl);
 cudaError_t launch_decode_attention_part(const AttentionArgs &a, int head_dim, int num_sms, int device,
                                          cudaStream_t stream);
+cudaError_t launch_decode_attention_joined(const AttentionArgs &a, int head_dim, int num_sms, int device,
+                                           cudaStream_t stream, bool pdl);
 cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, cudaStream_t stream);
 cudaError_t prefix_error_word(int *value, bool clear);
 cudaError_t attention_part_error_word(int *value, bool clear);
+cudaError_t attention_joined_error_word(int *value, bool clear);
 
 // Log probabilities, entropy and top alternatives of rows of logits (token_logprobs_bf16).
 constexpr int kLogprobMaxTop = 32;

@@ -12,6 +12,15 @@ stream after the layer:
     h      = act(x Wup^T + bup)                  decode_gemm_bf16_epilogue
     y      = h Wdown^T + res                     decode_gemm_bf16_epilogue
 
+Two options serve a batch of many requests. ``adapters``: low-rank adapters of any of the
+linears, {"qkv" | "o" | "up" | "down": (A [adapters, rank, K], B [adapters, N, rank])}, with
+``adapter_ids`` [M] naming each row's (-1: none) and ``adapter_scales`` [adapters] or None; such
+a linear goes by decode_gemm_bf16_lora, and the output linear's reduce and norm by
+reduce_residual_rmsnorm. ``prefix_table`` and ``prefix_length``: the pages and the number of
+tokens of a prefix that all rows share, by decode_attention_shared_prefix_bf16;
+``block_table`` and ``lengths`` are then of the rows' own tokens, and ``positions`` count the
+prefix's too.
+
 The attention may be split by heads over tensor-parallel ranks: slots 1.. of ``partials``
 then hold the other ranks' rows of the output linear, as in LayerChain. The feed-forward
 pair is whole on every rank (W_up, W_down [HIDDEN, F] with all of F): y is the stream
@@ -21,15 +30,29 @@ are the caller's tensors, updated in place between steps.
 """
 import torch
 
-from . import (HIDDEN, attention_workspace, decode_attention_bf16, decode_gemm_bf16_epilogue,
-               decode_gemm_bf16_reduce_rmsnorm, qk_norm_rope_bf16, reduce_residual_rmsnorm)
+from . import (HIDDEN, attention_workspace, decode_attention_bf16, decode_attention_shared_prefix_bf16,
+               decode_gemm_bf16_epilogue, decode_gemm_bf16_lora, decode_gemm_bf16_reduce_rmsnorm,
+               qk_norm_rope_bf16, reduce_residual_rmsnorm, shared_prefix_workspace)
+
+LINEARS = ("qkv", "o", "up", "down")
 
 
 class DecoderLayer:
     def __init__(self, M, q_heads, kv_heads, head_dim, W_qkv, W_o, W_up, W_down, gamma_in,
                  gamma_post, q_gamma, k_gamma, rope, k_cache, v_cache, block_table, lengths,
                  positions, slots, b_qkv=None, b_up=None, activation="silu", peers=None, window=0,
-                 sinks=0, interleaved=False, eps=1e-6, pdl=True, device="cuda"):
+                 sinks=0, interleaved=False, eps=1e-6, pdl=True, device="cuda", adapters=None,
+                 adapter_ids=None, adapter_scales=None, prefix_table=None, prefix_length=None):
+        if any(name not in LINEARS for name in adapters or {}):
+            raise ValueError(f"adapters: the linears are {', '.join(LINEARS)}")
+        if adapters and adapter_ids is None:
+            raise ValueError("adapters need adapter_ids")
+        if (prefix_table is None) != (prefix_length is None):
+            raise ValueError("prefix_table and prefix_length come together")
+        if prefix_table is not None and (window or sinks):
+            raise ValueError("a shared prefix has no window")
+        self.adapters, self.adapter_ids, self.adapter_scales = dict(adapters or {}), adapter_ids, adapter_scales
+        self.prefix_table, self.prefix_length = prefix_table, prefix_length
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.W_qkv, self.W_o, self.W_up, self.W_down = W_qkv, W_o, W_up, W_down
         self.gamma_in, self.gamma_post, self.q_gamma, self.k_gamma = gamma_in, gamma_post, q_gamma, k_gamma
@@ -51,27 +74,45 @@ class DecoderLayer:
             self.partials[1:].copy_(peers)
         self.h = torch.empty(M, W_up.shape[0], **bf)
         self.y = torch.empty(M, HIDDEN, **bf)
-        self.workspace = attention_workspace(self.x.device)
+        if prefix_table is None:
+            self.workspace = attention_workspace(self.x.device)
+        else:
+            self.workspace = shared_prefix_workspace(M, q_heads, kv_heads, head_dim, self.x.device)
         self.graph = None
+
+    def _linear(self, name, x, W, out, **opts):
+        if name not in self.adapters:
+            return decode_gemm_bf16_epilogue(x, W, out, **opts)
+        A, B = self.adapters[name]
+        return decode_gemm_bf16_lora(x, W, out, A, B, self.adapter_ids, scales=self.adapter_scales, **opts)
 
     def run(self, stream=None):
         """Enqueue one step reading self.y_in; returns the residual stream after the layer."""
         opts = dict(stream=stream, pdl=self.pdl)
         reduce_residual_rmsnorm(self.y_in, None, self.gamma_in, self.x, self.res, self.eps, **opts)
-        decode_gemm_bf16_epilogue(self.x, self.W_qkv, self.qkv, bias=self.b_qkv, **opts)
+        self._linear("qkv", self.x, self.W_qkv, self.qkv, bias=self.b_qkv, **opts)
         qk_norm_rope_bf16(self.qkv, self.q_heads, self.kv_heads, self.q_gamma, self.k_gamma,
                           self.rope, self.positions, self.q, k_cache=self.k_cache,
                           v_cache=self.v_cache, slots=self.slots, eps=self.eps,
                           interleaved=self.interleaved, **opts)
-        decode_attention_bf16(self.q, self.k_cache, self.v_cache, self.block_table, self.lengths,
-                              self.attn, window=self.window, sinks=self.sinks,
-                              workspace=self.workspace, **opts)
-        decode_gemm_bf16_reduce_rmsnorm(self.attn.view(self.attn.shape[0], -1), self.W_o,
-                                        self.partials, self.res, self.gamma_post, self.x, self.res,
-                                        self.eps, **opts)
-        decode_gemm_bf16_epilogue(self.x, self.W_up, self.h, bias=self.b_up,
-                                  activation=self.activation, **opts)
-        return decode_gemm_bf16_epilogue(self.h, self.W_down, self.y, residual=self.res, **opts)
+        if self.prefix_table is None:
+            decode_attention_bf16(self.q, self.k_cache, self.v_cache, self.block_table, self.lengths,
+                                  self.attn, window=self.window, sinks=self.sinks,
+                                  workspace=self.workspace, **opts)
+        else:
+            decode_attention_shared_prefix_bf16(self.q, self.k_cache, self.v_cache, self.prefix_table,
+                                                self.prefix_length, self.block_table, self.lengths,
+                                                self.attn, workspace=self.workspace, **opts)
+        attn = self.attn.view(self.attn.shape[0], -1)
+        if "o" in self.adapters:
+            self._linear("o", attn, self.W_o, self.partials[0], **opts)
+            reduce_residual_rmsnorm(self.partials, self.res, self.gamma_post, self.x, self.res, self.eps,
+                                    **opts)
+        else:
+            decode_gemm_bf16_reduce_rmsnorm(attn, self.W_o, self.partials, self.res, self.gamma_post,
+                                            self.x, self.res, self.eps, **opts)
+        self._linear("up", self.x, self.W_up, self.h, bias=self.b_up, activation=self.activation, **opts)
+        return self._linear("down", self.h, self.W_down, self.y, residual=self.res, **opts)
 
     def capture(self):
         """Capture one step as a CUDA graph (after at least one eager step)."""

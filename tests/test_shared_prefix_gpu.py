@@ -49,7 +49,7 @@ def reference(q, k_cache, v_cache, prefix_table, prefix, table, lengths, scale):
 class Case:
     """Queries, a pool whose pages are dealt out in any order, tables and lengths."""
 
-    def __init__(self, R, Hq, Hkv, D, page, prefix, lengths, layout="nhd", seed=1, q_pad=0, spare=0):
+    def __init__(self, R, Hq, Hkv, D, page, prefix, lengths, layout="nhd", seed=1, q_pad=0, spare=0, wide=True):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         if isinstance(lengths, int):
@@ -61,6 +61,9 @@ class Case:
         self.k, self.v = make_cache(pages, page, Hkv, D, layout, seed)
         order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
         self.prefix_table = order[:shared].clone()
+        if wide:  # a table of so many tokens that the prefix is read once and joined (but for one row)
+            more = -(-(16 << 20) // (R * Hkv * D * 4 * page)) + 1
+            self.prefix_table = torch.cat([self.prefix_table, torch.full_like(order[:1], -7).expand(more)])
         self.table = order[shared:].view(R, width).clone()
         self.prefix_length = torch.tensor([prefix], dtype=torch.int32, device="cuda")
         wide = torch.randn(R, Hq * D + q_pad, generator=g, device="cuda").mul_(1.3).to(torch.bfloat16)
@@ -86,29 +89,54 @@ class Case:
 
 # One tile of query rows, two, two with the second partly filled, several blocks; every head
 # width; prefixes from one token to many tiles, ending within tiles and pages.
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
 @pytest.mark.parametrize("R,Hq,Hkv,page,prefix,own", [
     (1, 1, 1, 16, 1, 1), (1, 7, 1, 16, 128, 5), (4, 7, 1, 16, 509, 64), (3, 8, 8, 1, 65, 3), (16, 8, 1, 24, 700, 33),
     (17, 8, 1, 64, 1000, 100), (64, 7, 1, 16, 3001, 200), (5, 12, 4, 8, 4096, 9), (33, 32, 2, 32, 2050, 40),
-    (130, 4, 2, 128, 129, 70)])
-def test_shapes(cuda_ok, D, R, Hq, Hkv, page, prefix, own):
-    Case(R, Hq, Hkv, D, page, prefix, own, seed=D + R).check()
+    (130, 4, 2, 128, 129, 70), (1, 96, 2, 16, 700, 20)])
+def test_shapes(cuda_ok, D, R, Hq, Hkv, page, prefix, own, wide):
+    Case(R, Hq, Hkv, D, page, prefix, own, seed=D + R, wide=wide).check()
 
 
+# Pages that no box of 8 tokens fits, of one token and of more than a tile's.
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("page", [1, 4, 12, 100, 1000])
+def test_pages_without_boxes(cuda_ok, D, page):
+    for R, prefix in ((3, 1601), (40, 1919)):
+        Case(R, 8, 1, D, page, prefix, 30, seed=page).check()
+
+
+# More blocks of query rows than there are CTAs: they are gone through in several passes.
+@pytest.mark.parametrize("R,Hq,Hkv,D,page", [(1024, 64, 1, 64, 16), (700, 64, 1, 128, 4), (520, 128, 2, 192, 16)])
+def test_more_blocks_than_ctas(cuda_ok, R, Hq, Hkv, D, page):
+    c = Case(R, Hq, Hkv, D, page, 301, 3, seed=20)
+    c.call()
+    assert sk.device_error() == (0, 0)
+    for r in (0, R // 3, R // 2, R - 130, R - 1):  # a few rows of every pass
+        at = slice(r, r + 1)
+        out, lse, out_tol, lse_tol = reference(c.q[at], c.k, c.v, c.prefix_table, c.prefix, c.table[at], c.lengths[at],
+                                               c.scale)
+        check_close(c.out[at], out, out_tol, "out")
+        check_close(c.lse[at], lse, lse_tol, "lse")
+
+
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("layout", ["nhd", "hnd", "kv", "padded"])
 @pytest.mark.parametrize("R,Hq,Hkv,D", [(6, 14, 2, 128), (48, 16, 2, 64)])
-def test_layouts_and_strides(cuda_ok, layout, R, Hq, Hkv, D):
-    Case(R, Hq, Hkv, D, 16, 1111, 90, layout=layout, seed=5, q_pad=24, spare=2).check()
+def test_layouts_and_strides(cuda_ok, layout, R, Hq, Hkv, D, wide):
+    Case(R, Hq, Hkv, D, 16, 1111, 90, layout=layout, seed=5, q_pad=24, spare=2, wide=wide).check()
 
 
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("R", [2, 40])
 @pytest.mark.parametrize("D", [128, 192])
-def test_lengths_of_zero_and_one(cuda_ok, R, D):
-    Case(R, 7, 1, D, 16, 300, [0, 1] * (R // 2), seed=1).check()  # rows with the prefix alone
-    Case(R, 7, 1, D, 16, 1, [0] * R, seed=2).check()
-    c = Case(R, 7, 1, D, 16, 0, [0, 5] * (R // 2), seed=3).check()  # no prefix
+def test_lengths_of_zero_and_one(cuda_ok, R, D, wide):
+    Case(R, 7, 1, D, 16, 300, [0, 1] * (R // 2), seed=1, wide=wide).check()  # rows with the prefix alone
+    Case(R, 7, 1, D, 16, 1, [0] * R, seed=2, wide=wide).check()
+    c = Case(R, 7, 1, D, 16, 0, [0, 5] * (R // 2), seed=3, wide=wide).check()  # no prefix
     assert (c.out[0] == 0).all() and (c.lse[0] == -math.inf).all()
-    c = Case(R, 7, 1, D, 16, 0, [0] * R, seed=4).check()
+    c = Case(R, 7, 1, D, 16, 0, [0] * R, seed=4, wide=wide).check()
     assert (c.out == 0).all()
 
 
@@ -121,6 +149,8 @@ def test_other_scales(cuda_ok, scale):
     for R in (3, 30):
         c = Case(R, 8, 1, 128, 16, 777, 40, seed=8)
         c.scale = scale
+        c.check()
+        c.prefix_table = c.prefix_table[:49]  # 784 tokens: in one launch
         c.check()
 
 
@@ -135,17 +165,18 @@ def test_growing_scores(cuda_ok):
         c.check()
 
 
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("bad", ["prefix page", "own page", "prefix length", "lengths"])
-def test_bad_indices_are_reported(cuda_ok, bad):
+def test_bad_indices_are_reported(cuda_ok, bad, wide):
     for R in (5, 40):
-        c = Case(R, 8, 1, 128, 16, 640, 64, seed=10)
+        c = Case(R, 8, 1, 128, 16, 640, 64, seed=10, wide=wide)
         c.lengths[:] = 64
         if bad == "prefix page":
             c.prefix_table[3], c.prefix_table[17] = -1, c.k.shape[0]
         elif bad == "own page":
             c.table[2, 1] = 1 << 30
         elif bad == "prefix length":
-            c.prefix_length[0] = 641 + 16
+            c.prefix_length[0] = 16 * c.prefix_table.numel() + 17
         else:
             c.lengths[1] = -1
         c.call()
@@ -154,7 +185,7 @@ def test_bad_indices_are_reported(cuda_ok, bad):
         # As with those tokens left out, or the nearest length.
         got, got_lse = c.out.clone(), c.lse.clone()
         if bad == "prefix page":
-            keep = [i for i in range(40) if i not in (3, 17)]
+            keep = [i for i in range(40) if i not in (3, 17)]  # a table of all the pages that are seen
             c.prefix_table, c.prefix = c.prefix_table[keep].clone(), 640 - 32
         elif bad == "own page":
             c.table[2, 1], c.lengths[2] = c.table[2, 3], 48
@@ -168,9 +199,10 @@ def test_bad_indices_are_reported(cuda_ok, bad):
         check_close(got_lse, lse, lse_tol, bad)
 
 
-def test_infinities_and_nan(cuda_ok):
+@pytest.mark.parametrize("wide", [True, False])
+def test_infinities_and_nan(cuda_ok, wide):
     for R in (3, 40):
-        c = Case(R, 8, 2, 128, 16, 500, 20, seed=11)
+        c = Case(R, 8, 2, 128, 16, 500, 20, seed=11, wide=wide)
         at = c.prefix_table.long()[0]
         c.v[c.prefix_table.long()[2], 3, 0, 5] = math.inf  # value 5 of the first key head's rows
         c.k[at, 1, 1, 0] = math.nan                        # every score of it for the second's
@@ -187,10 +219,11 @@ def test_infinities_and_nan(cuda_ok):
         check_close(c.lse[:, :4], lse[:, :4], lse_tol[:, :4], "lse")
 
 
-def test_places_beyond_the_prefix_are_not_read(cuda_ok):
+@pytest.mark.parametrize("wide", [True, False])
+def test_places_beyond_the_prefix_are_not_read(cuda_ok, wide):
     """NaN in the rest of the last pages, and table entries after them that are no pages."""
     for R in (3, 40):
-        c = Case(R, 7, 1, 128, 16, 500, [37] * R, seed=12, spare=3)
+        c = Case(R, 7, 1, 128, 16, 500, [37] * R, seed=12, spare=3, wide=wide)
         c.prefix_table[32:] = -5
         c.table[:, 3:] = 1 << 29
         for t in (c.k, c.v):
@@ -257,7 +290,45 @@ def test_as_decode_attention_over_the_joined_tables(cuda_ok):
     for R, Hq, Hkv, D in ((5, 14, 2, 128), (64, 32, 8, 64)):
         c = Case(R, Hq, Hkv, D, 16, 1600, 100, seed=19)
         c.check()
-        table = torch.cat([c.prefix_table[None].expand(R, -1), c.table], 1).contiguous()
+        table = torch.cat([c.prefix_table[None, :100].expand(R, -1), c.table], 1).contiguous()
         out, lse = torch.empty_like(c.out), torch.empty_like(c.lse)
         sk.decode_attention_bf16(c.q, c.k, c.v, table, c.lengths + 1600, out, lse=lse)
         assert (out.float() - c.out.float()).abs().max() < 0.02 and (lse - c.lse).abs().max() < 1e-4
+
+
+def test_two_streams_at_once(cuda_ok):
+    """Every stream has a workspace of its own without one being named."""
+    cases = [Case(32, 8, 1, 128, 16, 4000, 500, seed=21), Case(6, 16, 2, 64, 16, 6000, 700, seed=22),
+             Case(5, 8, 1, 128, 16, 200, 700, seed=23, wide=False)]
+    want = []
+    for c in cases:
+        c.check()
+        want.append((c.out.clone(), c.lse.clone()))
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for s, c in zip(streams, cases):
+            c.call(stream=s)
+    torch.cuda.synchronize()
+    assert sk.device_error() == (0, 0)
+    for c, (out, lse) in zip(cases, want):
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+def test_the_last_page_of_a_pool_past_32_bits(cuda_ok):
+    """Element offsets of more than 2^32 (2^33 bytes), by boxes and by single tokens."""
+    for page in (64, 12):
+        D, pages = 128, (1 << 32) // (page * 128) + 70
+        k = torch.empty(pages, page, 1, D, dtype=torch.bfloat16, device="cuda")
+        c = Case(20, 8, 1, D, page, 900, 90, seed=24)
+        used = c.k.shape[0]
+        k[-used:] = c.k  # the keys' pages at the end of a long pool, the values' too
+        v = torch.empty_like(k)
+        v[-used:] = c.v
+        for t in (c.prefix_table, c.table):
+            t[t >= 0] += pages - used
+        c.k, c.v = k, v
+        c.check()
+        del k, v, c
+        torch.cuda.empty_cache()
