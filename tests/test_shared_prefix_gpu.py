@@ -332,3 +332,16 @@ def test_the_last_page_of_a_pool_past_32_bits(cuda_ok):
         c.check()
         del k, v, c
         torch.cuda.empty_cache()
+
+
+def test_a_workspace_too_small_is_refused(cuda_ok):
+    for wide in (True, False):
+        c = Case(6, 8, 1, 128, 16, 200, 20, seed=25, wide=wide)
+        ws = sk.shared_prefix_workspace(6, 8, 1, 128)
+        c.check(workspace=ws)
+        with pytest.raises(sk.SkinnyError) as e:
+            c.call(workspace=ws[:-1])
+        assert sk.STATUS[e.value.status] == "SKINNY_ERR_SHAPE"
+        with pytest.raises(sk.SkinnyError) as e:
+            c.call(workspace=ws.cpu())
+        assert sk.STATUS[e.value.status] == "SKINNY_ERR_DEVICE"
