@@ -13,6 +13,11 @@
 // Programmatic dependent launch: the GEMM behind this kernel may start once every CTA here
 // has seen its own predecessor complete, so x is there for it, and streams its weights and
 // multiplies them while this kernel runs; only its epilogue waits for the sums.
+//
+// Measured (in a graph, both kernels; the GEMM with its epilogue alone in brackets): 13.6 us
+// (12.3) at 1 x 2048 x 7168, rank 16; 56.3 (44.9) at 16 x 18432 x 7168 with 16 adapters of rank
+// 64; 61.8 (49.1) at 64 x 7168 x 18432 with 64 adapters of rank 16 (38 MB of A
+// and 15 MB of B beside the 264 MB of the weight; at the copy rate these take 7.8 us).
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -30,7 +30,7 @@
 // decode_attention_bf16 has where the products are free, would cost half the tensor time
 // again. Maxima, sums and o are FP32.
 //
-// Measured (in a graph, with the own tokens and the join): 156 us for 64 rows x 64 heads over 8
+// Measured (in a graph, with the own tokens and the join): 156 us for 64 rows x 56 heads over 8
 // behind 65521 tokens with 1000 of their own each, of 62 us that the products take at the peak
 // rate (decode_attention_bf16 over joined tables: 2107 us); this kernel alone is 104 us, some 2100
 // clocks a step of 80 tokens of which the tensor cores are busy for 1280: a softmax thread's

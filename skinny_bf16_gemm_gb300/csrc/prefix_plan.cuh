@@ -27,7 +27,6 @@ __host__ __device__ constexpr int prefix_tiles(int head_dim, long long query_row
     return head_dim <= 128 && query_rows > kPrefixRows ? 2 : 1;
 }
 
-
 // Tokens of a step. In tensor memory (512 columns) every tile has a place for its scores (one
 // column a token), one for its weights (half a column) and one for its output (head_dim
 // columns), all apart, so that the next scores are computed while the softmax runs: 80 or 96

@@ -18,6 +18,11 @@
 // What reaches the bound is listed and ranked by (value, index).
 // Where ties at the bound or few heavy threads overflow the list, the exact bound is found by
 // bisecting the 16-bit values and the ties are taken in the order of their index.
+//
+// Measured (in a graph): 2048 rows of 163840 120.7 us, 5.6 TB/s (109.0, 6.2 TB/s, without the
+// list of 8); 64 rows of 163840, on 8 CTAs each, 8.8 us without a list and 16.4 with one of 20:
+// bisecting the bound over one warp's 256 maxima, reading the flagged rounds again and the join
+// of 8 lists are three latencies one after another. 7.1 us for one row of 20480.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
