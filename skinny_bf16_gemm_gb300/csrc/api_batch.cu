@@ -162,7 +162,7 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     if ((st = check_on_device(in, dev)) || (st = check_on_device(outs, dev))) return st;
     char *base = static_cast<char *>(p->workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    AttentionArgs o;
+    SharedAttentionArgs o = {};
     attention_args(&own, pool, &o);
     // Both kinds of tokens are counted in one int there, and so are the tiles.
     const long long tokens = o.capacity + capacity;

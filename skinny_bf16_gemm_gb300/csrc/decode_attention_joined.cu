@@ -4,7 +4,7 @@
 
 namespace skinny {
 
-cudaError_t launch_decode_attention_joined(const AttentionArgs &a, int head_dim, int num_sms, int device,
+cudaError_t launch_decode_attention_joined(const SharedAttentionArgs &a, int head_dim, int num_sms, int device,
                                            cudaStream_t stream, bool pdl) {
     return launch_any_dim<kJoined>(a, head_dim, num_sms, device, stream, pdl);
 }

@@ -57,6 +57,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_plan.cuh"
 #include "kernels.h"
@@ -210,11 +211,20 @@ struct Cut {
 };
 
 enum Form { kWhole, kPart, kJoined };
+template <int FORM>
+using ArgsOf = std::conditional_t<FORM == kWhole, AttentionArgs, SharedAttentionArgs>;
+
+// kPart: what the kernel's end, wherever it is, waits for.
+struct WaitAtTheEnd {
+    __device__ __forceinline__ ~WaitAtTheEnd() { ptx::pdl_wait(); }
+};
+struct NoWait {};
 
 template <int D, int NB, int FORM>
-__device__ __forceinline__ void decode_attention(const AttentionArgs &a) {
+__global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_attention_kernel(const ArgsOf<FORM> a) {
     using S = Shape<D, NB>;
     constexpr bool PART = FORM == kPart, JOINED = FORM == kJoined;
+    [[maybe_unused]] const std::conditional_t<PART, WaitAtTheEnd, NoWait> end;
     constexpr int kSub = S::kSub, kSets = S::kSets, kSlots = S::kSlots;
     constexpr uint32_t kAllSeen = kSub == 32 ? 0xFFFFFFFFu : (1u << (kSub & 31)) - 1u;
     constexpr int kChunks = D / 8;            // 16-byte chunks of a token's row
@@ -401,16 +411,14 @@ __device__ __forceinline__ void decode_attention(const AttentionArgs &a) {
             const int t = ahead.tile * kSub + lane;
             if (lane < kSub && t < ahead_seen.count) {
                 int j = t < ahead_seen.sinks ? t : t + ahead_seen.gap;
-                const int *table = ahead_table;
-                if constexpr (JOINED) {
-                    if (j < shared)
-                        table = a.prefix_table;
-                    else
-                        j -= shared;
-                }
+                const bool own = !JOINED || j >= shared;
+                if constexpr (JOINED) j -= own ? shared : 0;
                 const int e = a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size;
                 in_page = j - e * a.page_size;
-                cp_async4(ptx::smem_addr(&to->y), table + e);
+                if constexpr (JOINED)
+                    cp_async4(ptx::smem_addr(&to->y), (own ? ahead_table : a.prefix_table) + e);
+                else
+                    cp_async4(ptx::smem_addr(&to->y), ahead_table + e);
             }
             if (lane == 0) look_head[slot] = ahead_head;
             if (++ahead.tile == ahead_tiles && ahead_x + 1 < x_end) {
@@ -987,13 +995,7 @@ __device__ __forceinline__ void decode_attention(const AttentionArgs &a) {
 }
 
 template <int D, int NB, int FORM>
-__global__ void __launch_bounds__(kThreads, attn_ctas_per_sm(D, NB)) decode_attention_kernel(const AttentionArgs a) {
-    decode_attention<D, NB, FORM>(a);
-    if (FORM == kPart) ptx::pdl_wait();
-}
-
-template <int D, int NB, int FORM>
-cudaError_t launch(const AttentionArgs &a, int num_sms, int device, cudaStream_t stream, bool pdl) {
+cudaError_t launch(const ArgsOf<FORM> &a, int num_sms, int device, cudaStream_t stream, bool pdl) {
     using S = Shape<D, NB>;
     static bool configured[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
@@ -1004,8 +1006,9 @@ cudaError_t launch(const AttentionArgs &a, int num_sms, int device, cudaStream_t
         configured[device] = true;
     }
     // No more CTAs than the tables could ever hold tiles for their warps.
-    const long long tiles = static_cast<long long>(a.rows) * a.kv_heads * a.head_blocks *
-                            ((static_cast<long long>(a.capacity) + a.prefix_capacity + S::kSub - 1) / S::kSub);
+    long long tokens = a.capacity;
+    if constexpr (FORM == kJoined) tokens += a.prefix_capacity;
+    const long long tiles = static_cast<long long>(a.rows) * a.kv_heads * a.head_blocks * ((tokens + S::kSub - 1) / S::kSub);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(num_sms * attn_ctas_per_sm(D, NB), (tiles + kWarps - 1) / kWarps)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1020,7 +1023,7 @@ cudaError_t launch(const AttentionArgs &a, int num_sms, int device, cudaStream_t
 }
 
 template <int D, int FORM>
-cudaError_t launch_dim(const AttentionArgs &a, int num_sms, int device, cudaStream_t stream, bool pdl) {
+cudaError_t launch_dim(const ArgsOf<FORM> &a, int num_sms, int device, cudaStream_t stream, bool pdl) {
     if (a.block_heads <= 8) return launch<D, 1, FORM>(a, num_sms, device, stream, pdl);
     if (a.block_heads <= 16) return launch<D, 2, FORM>(a, num_sms, device, stream, pdl);
     if constexpr (D <= 128) return launch<D, 4, FORM>(a, num_sms, device, stream, pdl);
@@ -1028,7 +1031,7 @@ cudaError_t launch_dim(const AttentionArgs &a, int num_sms, int device, cudaStre
 }
 
 template <int FORM>
-cudaError_t launch_any_dim(const AttentionArgs &a, int head_dim, int num_sms, int device, cudaStream_t stream,
+cudaError_t launch_any_dim(const ArgsOf<FORM> &a, int head_dim, int num_sms, int device, cudaStream_t stream,
                            bool pdl) {
     switch (head_dim) {
         case 64: return launch_dim<64, FORM>(a, num_sms, device, stream, pdl);

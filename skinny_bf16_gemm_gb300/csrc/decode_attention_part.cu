@@ -4,7 +4,7 @@
 
 namespace skinny {
 
-cudaError_t launch_decode_attention_part(const AttentionArgs &a, int head_dim, int num_sms, int device,
+cudaError_t launch_decode_attention_part(const SharedAttentionArgs &a, int head_dim, int num_sms, int device,
                                          cudaStream_t stream) {
     // Behind the prefix's kernel, which waits for what was before both.
     return launch_any_dim<kPart>(a, head_dim, num_sms, device, stream, true);

@@ -195,17 +195,20 @@ struct AttentionArgs {
     int head_blocks;  // blocks the group is cut into, of block_heads heads at most
     int block_heads;
     int capacity;     // tokens a row's table holds
-    const int *prefix_table;   // the joined form: the prefix's pages,
-    const int *prefix_length;  // its tokens,
-    int prefix_capacity;       // and how many the table holds (0 in the other forms)
     int wide;         // the keys (or values) span more than 2^32 chunks of 16 bytes
     int window, sinks;
     float scale_log2;  // scale * log2(e)
     uint16_t *out;     // [rows][q_heads][head_dim]
-    float *part;       // the FP32 form: [rows][q_heads][head_dim] in place of out
     float *lse;        // [rows][q_heads] or nullptr
     unsigned *counters;  // workspace (attention_plan.cuh): zero between calls
     float *partials;     // workspace: the slots
+};
+// In two forms for decode_attention_shared_prefix_bf16.
+struct SharedAttentionArgs : AttentionArgs {
+    float *part;               // the rows' own tokens alone: [rows][q_heads][head_dim] in place of out
+    const int *prefix_table;   // joined: the prefix's pages,
+    const int *prefix_length;  // its tokens,
+    int prefix_capacity;       // and how many the table holds
 };
 cudaError_t launch_decode_attention(const AttentionArgs &a, int head_dim, int num_sms, int device,
                                     cudaStream_t stream, bool pdl);
@@ -242,9 +245,9 @@ struct PrefixArgs {
 int prefix_box_rows(int page_size, int tokens);
 cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap &v_map, const PrefixArgs &a,
                                     int head_dim, int device, cudaStream_t stream, bool pdl);
-cudaError_t launch_decode_attention_part(const AttentionArgs &a, int head_dim, int num_sms, int device,
+cudaError_t launch_decode_attention_part(const SharedAttentionArgs &a, int head_dim, int num_sms, int device,
                                          cudaStream_t stream);
-cudaError_t launch_decode_attention_joined(const AttentionArgs &a, int head_dim, int num_sms, int device,
+cudaError_t launch_decode_attention_joined(const SharedAttentionArgs &a, int head_dim, int num_sms, int device,
                                            cudaStream_t stream, bool pdl);
 cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, cudaStream_t stream);
 cudaError_t prefix_error_word(int *value, bool clear);
