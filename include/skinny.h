@@ -534,8 +534,8 @@ SKINNY_API size_t skinny_attention_workspace_bytes(int num_sms);
  *                  aligned, its first SKINNY_ATTENTION_COUNTER_BYTES zero before its first
  *                  use; every call leaves it ready for the next, of any sizes that it is large
  *                  enough for. Calls that may run at the same time need one each.
- *   Three kernels: the prefix, the rows' own tokens while it runs out, and the join; for one
- *   row, or a table of few tokens, one that reads both kinds of tokens row by row. Scores,
+ *   Three kernels: the prefix, the rows' own tokens beside it or behind it, and the join; for one
+ *   row, or a prefix that is little work, one that reads both kinds of tokens row by row. Scores,
  *   maxima, sums and partial outputs are FP32; the prefix's weights are rounded to BF16 (to
  *   nearest) for the product with the values, the own tokens' as in decode_attention_bf16;
  *   the output is rounded once. Deterministic.

@@ -34,17 +34,24 @@ bool outputs_clear(const Range (&in)[I], const Range (&outs)[O]) {
 
 // Whether the attention reads the prefix with every row's own tokens, in one launch, instead of
 // reading it once and joining: `tokens` is what the prefix's table holds. Every row then reads the
-// whole prefix, from L2 all but once, which is less than the time of two more launches up to about
-// 16 MiB in all for heads of up to 128: 12.4 against 14.7 us for 4 rows x 7 heads behind 509
-// tokens (1 MB), 14.5 against 15.7 for 64 rows behind 500 (16.4 MB), but 20.6 against 15.1 for 64
-// rows behind 2000 (66 MB). A single row's prefix is shared with nobody: 13.6 against 14.2 us for
-// 7 heads behind 8000 tokens, 51.0 against 63.6 for 56 heads over 8 behind 60000. Wider heads run on
-// the tensor cores from the first token on: 17.8 us for 8 rows x 16 heads of 256 behind 2000 tokens,
-// 34.1 in one launch. (Times inside a graph.)
-bool joined_is_faster(int rows, int kv_heads, int head_blocks, int head_dim, long long tokens) {
-    if (head_dim > 128) return false;
-    if (rows == 1 && head_blocks == 1) return true;
-    return tokens * rows * kv_heads * head_blocks * head_dim * 4 <= (16ll << 20);
+// whole prefix, from L2 all but once, which is less than the time of two more launches and of the
+// partial results of every row and head up to about 12 MiB and 20 KiB a row and head, for heads of
+// up to 128: 12.5 against 14.5 us for 4 rows x 7 heads behind 509 tokens (1 MB), 14.3 against 15.8
+// for 64 x 7 behind 500 (16 MB), 25.9 against 35.1 for 64 x 56 over 8 behind 330 (87 MB); but 17.5
+// against 15.4 for 4 x 7 behind 8000 (16 MB), 20.6 against 15.2 for 64 x 7 behind 2000 (66 MB). With
+// more than 8 heads to a key head that kernel takes longer and the tensor cores do not: 16 x 16 over
+// 1 behind 500 (4 MB) 16.5 and 14.8, 64 x 32 over 2 behind 200 18.1 and 23.3; with more than 16 always (4 x 96 over 2
+// behind 100 21.4 and 14.7).
+// A single row's prefix is shared with nobody: 14.0 against 14.2 us for 7 heads behind 8000 tokens,
+// 50.7 against 63.6 for 56 heads over 8 behind 60000. Wider heads run on the tensor cores from the
+// first token on: 17.8 us for 8 rows x 16 heads of 256 behind 2000 tokens, 34.1 in one launch.
+// (Times inside a graph.)
+bool joined_is_faster(int rows, int q_heads, int kv_heads, int head_dim, long long tokens) {
+    const int group = q_heads / kv_heads;
+    if (head_dim > 128 || group > 16) return false;
+    const long long bytes = tokens * rows * kv_heads * head_dim * 4, joins = rows * q_heads * (20ll << 10);
+    if (group > 8) return bytes * group / 8 <= joins;
+    return rows == 1 || bytes <= (12ll << 20) + joins;
 }
 long long attention_tiles(int rows, int kv_heads, int head_blocks, long long tokens) {
     return (tokens + kAttnMinTile - 1) / kAttnMinTile * rows * kv_heads * head_blocks;
@@ -166,7 +173,7 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     attention_args(&own, pool, &o);
     // Both kinds of tokens are counted in one int there, and so are the tiles.
     const long long tokens = o.capacity + capacity;
-    if (joined_is_faster(p->rows, c->kv_heads, o.head_blocks, D, capacity) && tokens < (1ll << 31) - kAttnMinTile &&
+    if (joined_is_faster(p->rows, p->q_heads, c->kv_heads, D, capacity) && tokens < (1ll << 31) - kAttnMinTile &&
         attention_tiles(p->rows, c->kv_heads, o.head_blocks, tokens) < (1ll << 31)) {
         o.prefix_table = static_cast<const int *>(p->prefix_table);
         o.prefix_length = static_cast<const int *>(p->prefix_length);
@@ -200,9 +207,10 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     a.group = group;
     a.tokens = plan.tokens;
     a.blocks = plan.blocks;
-    a.lanes = prefix_lanes(plan.blocks, sms);
+    const int ctas = prefix_ctas(p->rows, c->kv_heads, D, plan, capacity, o.capacity, sms);
+    a.lanes = prefix_lanes(plan.blocks, ctas);
     // No more ranges than the table could ever hold tiles.
-    a.ranges = static_cast<int>(std::min<long long>(prefix_ranges(plan.blocks, sms),
+    a.ranges = static_cast<int>(std::min<long long>(prefix_ranges(plan.blocks, ctas),
                                                     (capacity + plan.tokens - 1) / plan.tokens * c->kv_heads));
     a.scale_log2 = o.scale_log2;
     a.slots = reinterpret_cast<float *>(base + ws.slots);
@@ -218,7 +226,7 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
                             encode_cache_map(&v_map, c->v, c, a.box_rows, prefix_merged(D))))
         a.box_rows = 0;
     if (launch_prefix_attention(k_map, v_map, a, D, dev, s, ls.pdl) != cudaSuccess ||
-        launch_decode_attention_part(o, D, sms, dev, s) != cudaSuccess ||
+        launch_decode_attention_part(o, D, ctas < sms ? sms - a.ranges * a.lanes : sms, dev, s) != cudaSuccess ||
         launch_prefix_join(a, D, s) != cudaSuccess) {
         cudaGetLastError();
         return SKINNY_ERR_LAUNCH;

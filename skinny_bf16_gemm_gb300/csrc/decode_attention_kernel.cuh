@@ -48,8 +48,8 @@
 //
 // Two more forms serve decode_attention_shared_prefix_bf16. kPart: the rows' own tokens of a batch
 // behind a shared prefix; the result stays FP32, for the join with the prefix
-// (prefix_attention.cu). That kernel keeps the GPU busy while this one runs: it waits for it only
-// at its end, so that whatever waits for this kernel has waited for both. kJoined: the prefix's
+// (prefix_attention.cu). That kernel may run beside this one, which waits for it only at its
+// end, so that whatever waits for this kernel has waited for both. kJoined: the prefix's
 // tokens come before every row's own, from a table of their own.
 #pragma once
 

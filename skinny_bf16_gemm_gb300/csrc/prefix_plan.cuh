@@ -56,6 +56,26 @@ __host__ __device__ inline int prefix_lanes(int blocks, int ctas) {
 }
 __host__ __device__ inline int prefix_ranges(int blocks, int ctas) { return ctas / prefix_lanes(blocks, ctas); }
 
+// CTAs for the prefix where the rows' own tokens have the other SMs at the same time, or `sms`:
+// one after the other on all of them. Side by side hides the shorter kernel's start and end, some
+// 7 us, but the SMs are dealt out by what the tables could hold, the lengths being on the device:
+// the steps of the prefix (0.9 us for one on the tensor cores, 1.2 with wide heads) and half the
+// rows' own tokens (at 6.8 TB/s), each with 1.5 us more for what does not shrink with more SMs. Up
+// to 20 us in all even lengths of 0 or of the whole table cost no more than is hidden; beyond, they
+// might. 64 rows x 7 heads behind 16001 tokens, 1000 of their own: 23.7 us side by side, 30.4 one
+// after the other; 60001 and 1000: 30.6, 38.7; 16001 and 4000: 31.4, 41.6; 32 rows x 32 heads of 64
+// over 8, 32768 and 300: 33.5, 42.8; 16 rows x 7, 16001 and 300: 17.7 either way; 64 x 56 over 8,
+// 65521 and 1000, 100 us in all: 158.9 one after the other, 163.7 side by side at the best.
+inline int prefix_ctas(int rows, int kv_heads, int head_dim, const PrefixPlan &plan, long long prefix_tokens,
+                       long long own_tokens, int sms) {
+    const double steps = static_cast<double>((prefix_tokens + plan.tokens - 1) / plan.tokens) * kv_heads * plan.blocks;
+    const double prefix = steps * (head_dim > 128 ? 1.2 : 0.9) / sms;
+    const double own = static_cast<double>(own_tokens) * rows * kv_heads * head_dim * 2 / 6.8e6;
+    if (prefix + own > 20.0) return sms;
+    const int ctas = static_cast<int>(sms * (prefix + 1.5) / (prefix + own + 3.0));
+    return ctas < 1 ? 1 : ctas;
+}
+
 // An even cut of `total` tiles into ranges, `most` at most: the first `extra` have base + 1.
 struct PrefixCut {
     int ranges, base, extra;

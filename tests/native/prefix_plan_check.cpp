@@ -4,25 +4,27 @@
 #define __host__
 #define __device__
 #include <cstdio>
-#include <set>
+#include <vector>
 
 #include "prefix_plan.cuh"
 
 using namespace skinny;
 
-static int check(int rows, int group, int kv_heads, int head_dim, int sms, long long length, int capacity) {
+static int check(int rows, int group, int kv_heads, int head_dim, int sms, long long length, int capacity, int own) {
     const PrefixPlan plan = prefix_plan(rows, group, head_dim);
-    const int lanes = prefix_lanes(plan.blocks, sms);
+    const int ctas = prefix_ctas(rows, kv_heads, head_dim, plan, capacity, own, sms);
+    if (ctas < 1 || ctas > sms || (sms > 1 && ctas == sms && own < 100 && capacity < 100 && rows < 10)) return 7;
+    const int lanes = prefix_lanes(plan.blocks, ctas);
     const long long tiles_of_table = (capacity + plan.tokens - 1ll) / plan.tokens * kv_heads;
-    long long most = prefix_ranges(plan.blocks, sms);
+    long long most = prefix_ranges(plan.blocks, ctas);
     if (most > tiles_of_table) most = tiles_of_table;
-    if (most < 1 || most * lanes > sms) return 1;
+    if (most < 1 || most * lanes > ctas) return 1;
     const int steps = static_cast<int>((length + plan.tokens - 1) / plan.tokens);
     const PrefixCut cut(steps * kv_heads, static_cast<int>(most));
     const long long q = static_cast<long long>(rows) * group;
     const PrefixWorkspace ws = prefix_workspace(rows, group * kv_heads, kv_heads, head_dim, sms);
     const size_t slots = (ws.bytes - ws.slots) / (prefix_slot_floats(head_dim, q) * sizeof(float));
-    std::set<long long> used;
+    std::vector<char> used(slots);
     int next = 0;
     for (int r = 0; r < cut.ranges; ++r) {
         if (cut.begin(r) != next || cut.begin(r + 1) <= next) return 2;
@@ -34,7 +36,7 @@ static int check(int rows, int group, int kv_heads, int head_dim, int sms, long 
             if (r < first || r > last || cut.owner(x) != r || cut.owner(x + n - 1) != r) return 3;
             for (int b = 0; b < plan.blocks; ++b) {
                 const long long slot = static_cast<long long>(r + head) * plan.blocks + b;
-                if (slot >= static_cast<long long>(slots) || !used.insert(slot).second) return 4;
+                if (slot >= static_cast<long long>(slots) || used[slot]++) return 4;
             }
             x += n;
         }
@@ -42,7 +44,7 @@ static int check(int rows, int group, int kv_heads, int head_dim, int sms, long 
     if (next != steps * kv_heads) return 5;
     for (int head = 0; steps > 0 && head < kv_heads; ++head)
         for (int r = cut.owner(head * steps); r <= cut.owner(head * steps + steps - 1); ++r)
-            if (!used.count(static_cast<long long>(r + head) * plan.blocks)) return 6;
+            if (!used[static_cast<size_t>(r + head) * plan.blocks]) return 6;
     return 0;
 }
 
@@ -56,11 +58,12 @@ int main() {
                     for (int sms : all_sms)
                         for (int length : lengths)
                             for (int capacity : {length > 0 ? length : 1, length + 16, 65536})
-                                if (const int bad = check(rows, group, kv, D, sms, length, capacity)) {
-                                    std::printf("%d: rows %d group %d kv %d D %d sms %d length %d capacity %d\n", bad, rows,
-                                                group, kv, D, sms, length, capacity);
-                                    return 1;
-                                }
+                                for (int own : {1, 1000})
+                                    if (const int bad = check(rows, group, kv, D, sms, length, capacity, own)) {
+                                        std::printf("%d: rows %d group %d kv %d D %d sms %d length %d capacity %d own %d\n", bad,
+                                                    rows, group, kv, D, sms, length, capacity, own);
+                                        return 1;
+                                    }
     std::printf("ok\n");
     return 0;
 }

@@ -62,7 +62,7 @@ class Case:
         order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
         self.prefix_table = order[:shared].clone()
         if wide:  # a table of so many tokens that the prefix is read once and joined (but for one row)
-            more = -(-(16 << 20) // (R * Hkv * D * 4 * page)) + 1
+            more = -(-((16 << 20) + R * Hq * (20 << 10)) // (R * Hkv * D * 4 * page)) + 1
             self.prefix_table = torch.cat([self.prefix_table, torch.full_like(order[:1], -7).expand(more)])
         self.table = order[shared:].view(R, width).clone()
         self.prefix_length = torch.tensor([prefix], dtype=torch.int32, device="cuda")
