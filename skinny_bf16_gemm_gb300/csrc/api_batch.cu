@@ -227,7 +227,7 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
         a.box_rows = 0;
     if (launch_prefix_attention(k_map, v_map, a, D, dev, s, ls.pdl) != cudaSuccess ||
         launch_decode_attention_part(o, D, ctas < sms ? sms - a.ranges * a.lanes : sms, dev, s) != cudaSuccess ||
-        launch_prefix_join(a, D, s) != cudaSuccess) {
+        launch_prefix_join(a, D, sms, s) != cudaSuccess) {
         cudaGetLastError();
         return SKINNY_ERR_LAUNCH;
     }

@@ -249,7 +249,7 @@ cudaError_t launch_decode_attention_part(const SharedAttentionArgs &a, int head_
                                          cudaStream_t stream);
 cudaError_t launch_decode_attention_joined(const SharedAttentionArgs &a, int head_dim, int num_sms, int device,
                                            cudaStream_t stream, bool pdl);
-cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, cudaStream_t stream);
+cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t prefix_error_word(int *value, bool clear);
 cudaError_t attention_part_error_word(int *value, bool clear);
 cudaError_t attention_joined_error_word(int *value, bool clear);

@@ -670,9 +670,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 // and the row's own tokens' result; then the warps' sums in order. All in L2, read once.
 constexpr int kJoinWarps = 4;
 
-template <int D>
+// kAhead: parts whose loads a warp has on their way together.
+template <int D, int kAhead>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const PrefixArgs a) {
-    constexpr int kValues = D / 32, kAhead = D <= 128 ? 8 : 4;
+    constexpr int kValues = D / 32;
     __shared__ float sm_top[kJoinWarps], sm_weight[kJoinWarps], sm_o[kJoinWarps][D];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int job = blockIdx.x;
@@ -785,8 +786,8 @@ cudaError_t launch_prefix(const CUtensorMap &k_map, const CUtensorMap &v_map, co
     return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<D, NT>, k_map, v_map, a);
 }
 
-template <int D>
-cudaError_t launch_join(const PrefixArgs &a, cudaStream_t stream) {
+template <int D, int kAhead>
+cudaError_t launch_join_kernel(const PrefixArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.q_heads, 1, 1);
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
@@ -796,7 +797,18 @@ cudaError_t launch_join(const PrefixArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;  // behind the library's own kernels
-    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<D>, a);
+    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, kAhead>, a);
+}
+
+// 8 parts a warp while all CTAs run at once (four an SM), 4 and more CTAs an SM beyond: 64 rows x 7
+// heads behind 16001 tokens 22.5 us in all with 8, 23.1 with 4; 64 x 56 over 8 behind 8000 52.1 and
+// 45.3, behind 65521 157.5 and 150.8; 64 x 32 over 4 of 64 behind 16001 38.9 and 35.0. Always 4 for
+// wide heads, a part of which is as many registers.
+template <int D>
+cudaError_t launch_join(const PrefixArgs &a, int num_sms, cudaStream_t stream) {
+    if constexpr (D <= 128)
+        if (static_cast<long long>(a.rows) * a.q_heads <= 4ll * num_sms) return launch_join_kernel<D, 8>(a, stream);
+    return launch_join_kernel<D, 4>(a, stream);
 }
 
 }  // namespace
@@ -825,13 +837,13 @@ cudaError_t launch_prefix_attention(const CUtensorMap &k_map, const CUtensorMap 
     }
 }
 
-cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, cudaStream_t stream) {
+cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream) {
     switch (head_dim) {
-        case 64: return launch_join<64>(a, stream);
-        case 96: return launch_join<96>(a, stream);
-        case 128: return launch_join<128>(a, stream);
-        case 192: return launch_join<192>(a, stream);
-        case 256: return launch_join<256>(a, stream);
+        case 64: return launch_join<64>(a, num_sms, stream);
+        case 96: return launch_join<96>(a, num_sms, stream);
+        case 128: return launch_join<128>(a, num_sms, stream);
+        case 192: return launch_join<192>(a, num_sms, stream);
+        case 256: return launch_join<256>(a, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }
