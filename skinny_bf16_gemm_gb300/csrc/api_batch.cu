@@ -36,11 +36,11 @@ bool outputs_clear(const Range (&in)[I], const Range (&outs)[O]) {
 // reading it once and joining: `tokens` is what the prefix's table holds. Every row then reads the
 // whole prefix, from L2 all but once, which is less than the time of two more launches and of the
 // partial results of every row and head up to about 12 MiB and 20 KiB a row and head, for heads of
-// up to 128: 12.5 against 14.5 us for 4 rows x 7 heads behind 509 tokens (1 MB), 14.3 against 15.8
-// for 64 x 7 behind 500 (16 MB), 25.9 against 35.1 for 64 x 56 over 8 behind 330 (87 MB); but 17.5
+// up to 128: 12.2 against 14.7 us for 4 rows x 7 heads behind 509 tokens (1 MB), 14.3 against 15.2
+// for 64 x 7 behind 500 (16 MB), 20.7 against 26.8 for 64 x 56 over 8 behind 200 (52 MB); but 17.5
 // against 15.4 for 4 x 7 behind 8000 (16 MB), 20.6 against 15.2 for 64 x 7 behind 2000 (66 MB). With
 // more than 8 heads to a key head that kernel takes longer and the tensor cores do not: 16 x 16 over
-// 1 behind 500 (4 MB) 16.5 and 14.8, 64 x 32 over 2 behind 200 18.1 and 23.3; with more than 16 always (4 x 96 over 2
+// 1 behind 500 (4 MB) 16.5 and 14.8, 64 x 32 over 2 behind 200 18.2 and 20.0; with more than 16 always (4 x 96 over 2
 // behind 100 21.4 and 14.7).
 // A single row's prefix is shared with nobody: 14.0 against 14.2 us for 7 heads behind 8000 tokens,
 // 50.7 against 63.6 for 56 heads over 8 behind 60000. Wider heads run on the tensor cores from the

@@ -30,14 +30,14 @@
 // decode_attention_bf16 has where the products are free, would cost half the tensor time
 // again. Maxima, sums and o are FP32.
 //
-// Measured (in a graph, with the own tokens and the join): 158 us for 64 rows x 56 heads over 8
+// Measured (in a graph, with the own tokens and the join): 151 us for 64 rows x 56 heads over 8
 // behind 65521 tokens with 1000 of their own each, of 62 us that the products take at the peak
 // rate (decode_attention_bf16 over joined tables: 2107 us); this kernel alone is 104 us, some 2100
 // clocks a step of 80 tokens of which the tensor cores are busy for 1280. Their operands are the
 // closer bound: 144 KB read from shared memory and 40 KB of new tiles written a step are 1440
 // clocks at 128 bytes each, the queries the larger part (64 KB), which tensor memory has no room
-// for. It is not the softmax: two threads a row, half the scores each, took 168 us instead of
-// 158, and 3-4 % less with one tile of query rows. 22.5 us for 64 rows x 7 heads behind 16001
+// for. It is not the softmax: two threads a row, half the scores each, took 10 us more, and
+// 3-4 % less with one tile of query rows. 22.5 us for 64 rows x 7 heads behind 16001
 // tokens with 1000 of their own, side by side (prefix_plan.cuh prefix_ctas).
 //
 // Every wait is bounded; one that runs out is recorded, the CTA waits for its own copies and

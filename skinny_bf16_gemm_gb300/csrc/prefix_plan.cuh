@@ -64,8 +64,8 @@ __host__ __device__ inline int prefix_ranges(int blocks, int ctas) { return ctas
 // to 20 us in all even lengths of 0 or of the whole table cost no more than is hidden; beyond, they
 // might. 64 rows x 7 heads behind 16001 tokens, 1000 of their own: 23.7 us side by side, 30.4 one
 // after the other; 60001 and 1000: 30.6, 38.7; 16001 and 4000: 31.4, 41.6; 32 rows x 32 heads of 64
-// over 8, 32768 and 300: 33.5, 42.8; 16 rows x 7, 16001 and 300: 17.7 either way; 64 x 56 over 8,
-// 65521 and 1000, 100 us in all: 158.9 one after the other, 163.7 side by side at the best.
+// over 8, 32768 and 300: 33.7, 42.8; 16 rows x 7, 16001 and 300: 17.7 either way; 64 x 56 over 8,
+// 65521 and 1000, 100 us in all: 163.7 side by side at the best, 158.9 one after the other.
 inline int prefix_ctas(int rows, int kv_heads, int head_dim, const PrefixPlan &plan, long long prefix_tokens,
                        long long own_tokens, int sms) {
     const double steps = static_cast<double>((prefix_tokens + plan.tokens - 1) / plan.tokens) * kv_heads * plan.blocks;
