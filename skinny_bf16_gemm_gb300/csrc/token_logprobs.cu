@@ -19,10 +19,10 @@
 // Where ties at the bound or few heavy threads overflow the list, the exact bound is found by
 // bisecting the 16-bit values and the ties are taken in the order of their index.
 //
-// Measured (in a graph): 2048 rows of 163840 120.7 us, 5.6 TB/s (109.0, 6.2 TB/s, without the
-// list of 8); 64 rows of 163840, on 8 CTAs each, 8.8 us without a list and 16.4 with one of 20:
+// Measured (in a graph): 2048 rows of 163840 120.4 us, 5.6 TB/s (109.0, 6.2 TB/s, without the
+// list of 8); 64 rows of 163840, on 8 CTAs each, 9.2 us without a list and 15.7 with one of 20:
 // bisecting the bound over one warp's 256 maxima, reading the flagged rounds again and the join
-// of 8 lists are three latencies one after another. 7.1 us for one row of 20480.
+// of 8 lists are three latencies one after another. 6.5 us for one row of 20480.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,8 +34,6 @@
 namespace skinny {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;     // vectors a thread has on their way
 constexpr int kList = 1024;    // candidates (and as many ties) that are ranked at once
 constexpr int kMaxCluster = 8;
@@ -92,8 +90,9 @@ __device__ __forceinline__ uint32_t bits_at(const uint4 &v, int e) {
     return (e & 1) ? w >> 16 : w & 0xFFFFu;
 }
 
-template <int C>
-__global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const LogprobArgs a) {
+template <int C, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1280 / kThreads) token_logprobs_kernel(const LogprobArgs a) {
+    constexpr int kWarps = kThreads / 32;
     __shared__ Sums sm_sums[kWarps];
     __shared__ Sums sm_peers[C];
     __shared__ unsigned long long sm_tops[C * kLogprobMaxTop];
@@ -101,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const Logpr
     __shared__ int sm_counts[2];
     __shared__ int sm_scan[kWarps];
     __shared__ uint32_t sm_bound;
-    __shared__ __align__(16) uint16_t sm_maxima[kThreads];
+    __shared__ uint16_t sm_maxima[kThreads];
     __shared__ int sm_again[kWarps][32];  // what a warp reads again: vectors, then lanes
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int rank = C > 1 ? static_cast<int>(blockIdx.x % C) : 0;
@@ -176,20 +175,19 @@ __global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const Logpr
     // ---- this CTA's top list ----
     if (top > 0) {
         const uint32_t mine = key_of(__float_as_uint(fmaxf(best, second)) >> 16);
-        // The top-th largest of the threads' maxima, bit by bit, by one warp with 8 of them a lane
-        // (0: fewer threads than that).
+        // The top-th largest of the threads' maxima, bit by bit, by one warp with kWarps of them a
+        // lane (0: fewer threads than that).
         sm_maxima[tid] = static_cast<uint16_t>(mine);
         __syncthreads();
         if (warp == 0) {
-            const uint4 v = reinterpret_cast<const uint4 *>(sm_maxima)[lane];
-            uint32_t k[8], found = 0;
+            uint32_t k[kWarps], found = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) k[e] = bits_at(v, e);
+            for (int e = 0; e < kWarps; ++e) k[e] = sm_maxima[e * 32 + lane];
 #pragma unroll 1
             for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1) {
                 int n = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) n += k[e] >= (found | bit);
+                for (int e = 0; e < kWarps; ++e) n += k[e] >= (found | bit);
                 if (__reduce_add_sync(0xFFFFFFFFu, n) >= top) found |= bit;
             }
             if (lane == 0) sm_bound = found;
@@ -385,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const Logpr
     }
 }
 
-template <int C>
-cudaError_t launch(const LogprobArgs &a, cudaStream_t stream, bool pdl) {
+template <int C, int kThreads>
+cudaError_t launch_threads(const LogprobArgs &a, cudaStream_t stream, bool pdl) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.M) * C, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -400,21 +398,34 @@ cudaError_t launch(const LogprobArgs &a, cudaStream_t stream, bool pdl) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<C>, a);
+    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<C, kThreads>, a);
+}
+template <int C>
+cudaError_t launch(const LogprobArgs &a, int threads, cudaStream_t stream, bool pdl) {
+    return threads == 256 ? launch_threads<C, 256>(a, stream, pdl) : launch_threads<C, 128>(a, stream, pdl);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
-    // CTAs a row: as many as keep every SM's threads on a row, but no fewer than a
-    // vector a thread.
+    // CTAs a row: as many as keep every SM's threads on a row, but no fewer than a vector a
+    // thread.
     const int vectors = a.V / 8;
     int c = kMaxCluster;
-    while (c > 1 && (vectors < c * kThreads || static_cast<long long>(a.M) * c > 8ll * num_sms)) c /= 2;
-    if (c == 8) return launch<8>(a, stream, pdl);
-    if (c == 4) return launch<4>(a, stream, pdl);
-    if (c == 2) return launch<2>(a, stream, pdl);
-    return launch<1>(a, stream, pdl);
+    while (c > 1 && (vectors < c * 128 || static_cast<long long>(a.M) * c > 8ll * num_sms)) c /= 2;
+    // 128 threads: twice the rows an SM, so that one's list is made while others are read (512 rows
+    // of 32000, list of 8: 14.7 us, 20.1 with 256; 4096 of 50257: 91.5, 95.0; 128 of 163840, on 8
+    // CTAs: 17.3, 22.2). 256 where a CTA's part is long and all CTAs run at once anyway (64 rows of
+    // 163840: 15.7, 17.1; one: 9.9, 12.6), or where the last CTAs of long rows would run with much
+    // of the GPU idle (2048 of 100000: 84, 88; of 163840: 120, 131).
+    const long long ctas = static_cast<long long>(a.M) * c, at_once = 5ll * num_sms;
+    auto filled = [&](long long places) { return static_cast<double>(ctas) / ((ctas + places - 1) / places * places); };
+    const int threads = ctas <= at_once ? (vectors / c >= 2048 ? 256 : 128)
+                                        : (a.V >= 80000 && filled(at_once) > 1.15 * filled(2 * at_once) ? 256 : 128);
+    if (c == 8) return launch<8>(a, threads, stream, pdl);
+    if (c == 4) return launch<4>(a, threads, stream, pdl);
+    if (c == 2) return launch<2>(a, threads, stream, pdl);
+    return launch<1>(a, threads, stream, pdl);
 }
 
 cudaError_t logprob_error_word(int *value, bool clear) {

@@ -17,7 +17,8 @@ def reference(x, tokens, top):
 
     A weight exp(t), t = x - m <= 0, is off by t's rounding U32 |t|, its product with log2 e
     U32 |t|, and the exponential's 2 ulp, 2^-22; the sum of V weights takes at most n =
-    V / 256 + 80 additions one after another (a thread's own, with rescaling, then joins).
+    V / 256 + 80 additions one after another (a thread's own, with rescaling, then joins; one
+    CTA of 128 threads a row, V / 128 + 15, is for no V here where that is more).
     So S is off by ds = 2^-22 + 2 U32 E|t| + 2 n U32 relative, E the mean over p, and the
     sum of p t by E|t| (2^-22 + 3 U32 + 2 n U32) + 2 U32 E t^2; logarithm, quotient and
     differences by 4 U32 of their results and terms."""
@@ -94,7 +95,8 @@ def some_tokens(M, V, T, seed):
 @pytest.mark.parametrize("M,V,top", [(1, 1, 1), (3, 2, 2), (2, 7, 7), (5, 8, 8), (4, 33, 32), (2, 255, 20),
                                      (3, 2047, 20), (1, 2049, 1), (2, 4096, 32), (1, 8191, 20),
                                      (1, 16384, 32), (1, 16400, 5), (7, 20480, 20), (64, 50257, 5),
-                                     (160, 20000, 8), (400, 10001, 32), (1300, 3000, 4), (2, 163840, 32)])
+                                     (160, 20000, 8), (400, 10001, 32), (1300, 3000, 4), (2, 163840, 32),
+                                     (1600, 80008, 8), (3000, 9, 3), (900, 700, 32)])
 def test_sizes(cuda_ok, M, V, top):
     check(logits(M, V, seed=V), some_tokens(M, V, 3, seed=M), top)
 
