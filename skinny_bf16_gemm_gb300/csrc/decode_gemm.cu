@@ -206,7 +206,10 @@ __device__ __forceinline__ void store_tile_staged(const float (&v)[MP], uint16_t
 //           three stages. From rank 64 on a load of 32 rows' pieces is 32 requests: 64 x 4096 x
 //           4096 with 16 adapters of rank 128 50 us, direct 74; 32 x 18432 x 7168 with 8 of rank 64
 //           54 and 65; but 64 x 7168 x 18432 with 64 of rank 16 65 and 62, 5 x 4099 x 1000 with 3 of
-//           rank 8 13.6 and 11.1.
+//           rank 8 13.6 and 11.1. From rank 24 on where so few adapters serve so many rows that
+//           rank x rows is 96 x adapters or more: 64 x 18432 x 7168 with 32 of rank 48 63, direct 78;
+//           49 x 2173 x 64 with 6 of rank 24 17.5 and 23.0; but 36 x 8521 x 288 with 19 of rank 32
+//           24.5 and 23.4.
 template <int MP, int STAGES, bool EPI, int LORA>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_gemm_kernel(const __grid_constant__ CUtensorMap w_map,
@@ -993,7 +996,7 @@ cudaError_t launch_variant(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            int device) {
     if (args.lora.rank > 0) {
         if constexpr (MP >= 32 && STAGES > kMaxShallowStages)
-            if (args.lora.rank >= 64)
+            if (args.lora.rank >= 64 || (args.lora.rank >= 24 && args.lora.rank * args.M >= 96 * args.lora.count))
                 return launch_kernel<MP, MP == 64 ? 6 : 8, true, kLoraCopied>(w_map, x_map, args, ctas, stream, pdl, device);
         // A x takes one stage of the rings that fill the shared memory (up to 32 KB).
         constexpr int kLoraStages = STAGES - (MP >= 32 && STAGES > kMaxShallowStages ? 1 : 0);
