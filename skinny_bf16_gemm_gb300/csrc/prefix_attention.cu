@@ -114,10 +114,11 @@ struct Shape {
     static constexpr int kQBytes = kChunks * kQChunkBytes;      // one tile of queries
     static constexpr int kMiscBytes = 768;
     static constexpr int kStages = std::min(8, (232448 - 1024 - kMiscBytes - NT * kQBytes) / kUnitBytes);
-    // cp.async: a warp's units (every other one of the ring) whose copies are on their way; at
-    // most so many that the next keys come without the last values' place.
+    using Ring = PrefixRing<kStages>;
+    // cp.async: a warp's units (of its kind) whose copies are on their way; fewer than its kind's
+    // stages, so that the one that is waited for is not among them.
     static constexpr int kLag = std::max(1, kStages / 4);
-    static_assert(2 * kLag <= kStages - 2, "no unit waits for one behind it");
+    static_assert(kLag < Ring::kValues, "no unit waits for one behind it");
     static_assert(kStages >= 4, "a key and a value tile in use while others are on their way");
     static constexpr int kRingOffset = NT * kQBytes;
     static constexpr int kMaskWords = (kTokens + 31) / 32;
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     prefix_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                             const PrefixArgs a) {
     using S = Shape<D, NT>;
+    using Ring = typename S::Ring;
     constexpr int kTokens = S::kTokens, kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         auto publish = [&](int u) {  // this warp's part of a unit whose copies are complete
             ptx::fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar_full + 8 * (u % kStages));
+            if (lane == 0) ptx::mbar_arrive(bar_full + 8 * Ring::stage(u));
         };
         const int boxes = a.box_rows > 0 ? kTokens / a.box_rows : 0;
         const int items = S::kMerged ? boxes : boxes * S::kChunks;  // copies of a unit
@@ -519,10 +521,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                     ++head;
                 }
                 if (x + 1 < x_end || block + a.lanes < a.blocks) look_up();
-                const int s = unit % kStages;
+                const int s = Ring::stage(unit);
                 const uint32_t to = sbase + S::kRingOffset + s * S::kUnitBytes;
                 // The first round finds the stages free.
-                if (!(ok = warp_wait(bar_empty + 8 * s, ((unit / kStages) & 1) ^ 1))) break;
+                if (!(ok = warp_wait(bar_empty + 8 * s, (Ring::round(unit) & 1) ^ 1))) break;
                 if (by_box) {
                     __syncwarp();  // the mask is written
                     if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full + 8 * s, box_bytes);
@@ -572,15 +574,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         ptx::give_registers<S::kOtherRegisters>();
     }
     auto full = [&](int u) {
-        if (!wait(bar_full + 8 * (u % kStages), (u / kStages) & 1)) return false;
+        if (!wait(bar_full + 8 * Ring::stage(u), Ring::round(u) & 1)) return false;
         ptx::tc_fence_after_sync();
         return true;
     };
     // When every tile's products with a unit are complete it is free; a block's only tile speaks
     // for both.
     auto release = [&](int u, bool alone) {
-        ptx::mma_commit(bar_empty + 8 * (u % kStages));
-        if (NT == 2 && alone) ptx::mma_commit(bar_empty + 8 * (u % kStages));
+        ptx::mma_commit(bar_empty + 8 * Ring::stage(u));
+        if (NT == 2 && alone) ptx::mma_commit(bar_empty + 8 * Ring::stage(u));
     };
     // The issuers are one thread each: the waits and commits of one pass while another's products
     // run (a single issuer for all four took twice the time).
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 if (scored > 0 && !wait(bar_free + 8 * tile, (scored - 1) & 1)) return false;
                 if (!full(unit)) return false;
                 const uint64_t k =
-                    ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes, S::kGroupBytes);
+                    ptx::smem_desc_sw128_kmajor(sbase + S::kRingOffset + Ring::stage(unit) * S::kUnitBytes, S::kGroupBytes);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)  // addresses in the descriptors are in units of 16 bytes
                     ptx::mma_bf16(tmem + tile * kTokens, q + s / 4 * (S::kQChunkBytes / 16) + s % 4 * 2,
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             for (int j = 0; j < seg.n; ++j, unit += 2) {
                 if (!full(unit) || !wait(bar_p + 8 * tile, added++ & 1)) return false;
                 ptx::tc_fence_after_sync();
-                const uint64_t v = ptx::smem_desc_sw128_mnmajor(sbase + S::kRingOffset + unit % kStages * S::kUnitBytes,
+                const uint64_t v = ptx::smem_desc_sw128_mnmajor(sbase + S::kRingOffset + Ring::stage(unit) * S::kUnitBytes,
                                                                 S::kChunkBytes, S::kGroupBytes);
 #pragma unroll
                 for (int s = 0; s < kTokens / 16; ++s)
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         if (warp >= S::kLoaderWarp && warp < S::kScoresWarp && lane == 0) {
             const uint64_t t0 = ptx::global_timer_ns();
             for (int u = max((warp - S::kLoaderWarp) / S::kLoaders, issued - kStages / 2 * 2); u < issued; u += 2)
-                while (!ptx::mbar_try_wait(bar_full + 8 * (u % kStages), (u / kStages) & 1) &&
+                while (!ptx::mbar_try_wait(bar_full + 8 * Ring::stage(u), Ring::round(u) & 1) &&
                        ptx::global_timer_ns() - t0 < kDrainLimitNs) {
                 }
         }

@@ -96,6 +96,27 @@ struct PrefixCut {
 // one copy brings them all; else (96) all tokens' first chunks come before their second ones.
 constexpr bool prefix_merged(int head_dim) { return head_dim % 64 == 0; }
 
+// The ring of a CTA's tiles of keys and values. They come in turn, keys first: unit 2 t is tile t's
+// keys, 2 t + 1 its values. Keys and values have stages of their own: a loader waits for the
+// phase in which a stage comes free by its parity, so it must know that the phase before is
+// complete, and it does where it waited for that itself before its last unit there. An even number
+// of stages, gone through in the order of the units, is such a ring. An odd one is not: there the
+// unit before is the other kind's, and of the one before that nothing is known but that it came
+// earlier (the scores of a later tile may be complete sooner than the product with its values), so
+// the odd stage is the keys', which are wanted first.
+template <int kStages>
+struct PrefixRing {
+    static constexpr int kKeys = (kStages + 1) / 2, kValues = kStages / 2;
+    // The stage of a unit, and how many units of the ring it had before.
+    __host__ __device__ static constexpr int stage(int unit) {
+        if (kStages % 2 == 0) return unit % kStages;
+        return unit % 2 ? kKeys + unit / 2 % kValues : unit / 2 % kKeys;
+    }
+    __host__ __device__ static constexpr int round(int unit) {
+        return kStages % 2 == 0 ? unit / kStages : unit / 2 / (unit % 2 ? kValues : kKeys);
+    }
+};
+
 // A partial: for each query row of the unit head_dim sums, then all maxima, then all sums of
 // weights.
 __host__ __device__ inline size_t prefix_slot_floats(int head_dim, long long query_rows) {
