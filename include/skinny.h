@@ -636,7 +636,8 @@ SKINNY_API const char *skinny_status_string(int status);
  *   decode_attention_bf16, decode_attention_shared_prefix_bf16, token_logprobs_bf16) met
  *   one out of range, and if that is the only bit the
  *   status is SKINNY_ERR_INDEX; 512 if a wait of decode_attention_shared_prefix_bf16 ran
- *   out) to *word if word is not NULL. Clearing also
+ *   out, and with it 16 if copies or products of its own did not complete after that, as
+ *   for the decode GEMM) to *word if word is not NULL. Clearing also
  *   re-arms the decode GEMM's scratch flags, so the next call starts clean and
  *   calls stop returning SKINNY_ERR_TIMEOUT. Host pointer: word.
  */

@@ -1094,6 +1094,7 @@ int skinny_device_error(int device, int *word) {
     if (rope_word || attention_word || logprob_word || lora_word || part_word || joined_word || (prefix_word & 2))
         value |= kErrIndex;
     if (prefix_word & 1) value |= kErrPrefixWait;
+    if (prefix_word & 4) value |= kErrDrain;
     cudaSetDevice(prev);
     if (word) *word = value;
     if (st != SKINNY_OK) return st;

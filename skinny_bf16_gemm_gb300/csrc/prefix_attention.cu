@@ -60,8 +60,10 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s for work already issued
-constexpr int kErrWait = 1, kErrRange = 2;
-__device__ int g_prefix_err;  // kErrWait: a wait ran out; kErrRange: a length or page out of range
+constexpr int kErrWait = 1, kErrRange = 2, kErrLeft = 4;
+// kErrWait: a wait ran out; kErrRange: a length or page out of range; kErrLeft: a CTA that gave up
+// ended before its own copies and products were seen to be complete
+__device__ int g_prefix_err;
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -125,8 +127,8 @@ struct Shape {
     static constexpr int kMaskOffset = kRingOffset + kStages * kUnitBytes;  // [kMaskRing][kMaskWords]
     static constexpr int kBarOffset = kMaskOffset + kMaskRing * kMaskWords * 4;
     static constexpr int kBars = 2 * kStages + 2 * 5 + 1;
-    static constexpr int kTailOffset = kBarOffset + kBars * 8;  // tensor memory base, abort flag
-    static constexpr int kBytes = kTailOffset + 16;
+    static constexpr int kTailOffset = kBarOffset + kBars * 8;  // tensor memory base, abort flag, units begun
+    static constexpr int kBytes = kTailOffset + 24;
     static constexpr int kDynamicBytes = kBytes + 1024;  // slack to align the base to 1024
     static_assert(kDynamicBytes <= 232448, "shared memory of a CTA");
     static constexpr int kLoaders = 2;  // warps for the keys, and for the values
@@ -270,7 +272,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 x += s.n;
             }
     };
-    int issued = 0;  // units that the loader has begun
     if (warp < S::kLoaderWarp) {
         // ---------------- softmax: thread = query row ----------------
         ptx::take_registers<S::kSoftmaxRegisters>();
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 unit += 2;
             }
         }
-        issued = boxes > 0 ? unit : 0;
+        if (lane == 0) tail[2 + warp - S::kLoaderWarp] = boxes > 0 ? unit : 0;  // the boxes begun
         cp_async_wait<0>();
         if (ok && boxes == 0)
             for (int u = max(kv, unit - 2 * S::kLag); u < unit; u += 2) publish(u);
@@ -645,19 +646,27 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (*abort_flag) {
-        // Nothing may still read this CTA's shared or tensor memory when it ends.
+        // Nothing may still read or write this CTA's shared or tensor memory when it ends.
+        auto drain = [&](uint32_t bar, uint32_t parity, uint64_t t0) {
+            while (!ptx::mbar_try_wait(bar, parity))
+                if (ptx::global_timer_ns() - t0 > kDrainLimitNs) {
+                    atomicOr(&g_prefix_err, kErrLeft);
+                    break;
+                }
+        };
         if (warp >= S::kScoresWarp && warp < S::kValuesWarp + NT && lane == 0) {
             ptx::mma_commit(bar_drain);
-            const uint64_t t0 = ptx::global_timer_ns();
-            while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::global_timer_ns() - t0 < kDrainLimitNs) {
-            }
+            drain(bar_drain, 0, ptx::global_timer_ns());
         }
         if (warp >= S::kLoaderWarp && warp < S::kScoresWarp && lane == 0) {
+            // Units that the other loader of the kind has begun and this one has not lack this one's
+            // arrival.
+            const int mine = tail[2 + warp - S::kLoaderWarp], other = tail[2 + ((warp - S::kLoaderWarp) ^ 1)];
+            const int end = max(mine, other);
+            for (int u = mine; u < end; u += 2) ptx::mbar_arrive(bar_full + 8 * Ring::stage(u));
             const uint64_t t0 = ptx::global_timer_ns();
-            for (int u = max((warp - S::kLoaderWarp) / S::kLoaders, issued - kStages / 2 * 2); u < issued; u += 2)
-                while (!ptx::mbar_try_wait(bar_full + 8 * Ring::stage(u), Ring::round(u) & 1) &&
-                       ptx::global_timer_ns() - t0 < kDrainLimitNs) {
-                }
+            for (int u = Ring::first_on_its_way(end); u < end; u += 2)
+                drain(bar_full + 8 * Ring::stage(u), Ring::round(u) & 1, t0);
         }
         __syncthreads();
     }

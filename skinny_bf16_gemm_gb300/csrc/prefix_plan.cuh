@@ -115,6 +115,12 @@ struct PrefixRing {
     __host__ __device__ static constexpr int round(int unit) {
         return kStages % 2 == 0 ? unit / kStages : unit / 2 / (unit % 2 ? kValues : kKeys);
     }
+    // The first of a kind's units whose copies may be on their way when `end` is the kind's next
+    // one: before a later one was put into its stage each one before was waited for.
+    __host__ __device__ static constexpr int first_on_its_way(int end) {
+        const int kind = end % 2, first = end - 2 * (kind ? kValues : kKeys);
+        return first > kind ? first : kind;
+    }
 };
 
 // A partial: for each query row of the unit head_dim sums, then all maxima, then all sums of

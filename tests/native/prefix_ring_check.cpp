@@ -1,7 +1,8 @@
 // The ring of the attention over a shared prefix, checked by itself on the host: the loaders, the
 // two issuers and the softmax of a CTA as agents that run in any order, over barriers whose waits
 // see only the parity of a phase. No unit may be put where the one before is still read, none read
-// before it is there, and nobody may wait forever.
+// before it is there, nobody may wait forever, and whenever a CTA would have to give up, the units
+// whose copies it waits for are all that may be on their way.
 #define __host__
 #define __device__
 #include <cstdio>
@@ -18,6 +19,13 @@ struct InTurn {
     static constexpr int kKeys = (kStages + 1) / 2, kValues = kStages / 2;
     static int stage(int unit) { return unit % kStages; }
     static int round(int unit) { return unit / kStages; }
+    static int first_on_its_way(int end) { return end % 2; }
+};
+
+// As many units of a kind waited for as half the stages: one too few of the keys' for an odd number.
+template <int kStages>
+struct HalfDrained : PrefixRing<kStages> {
+    static int first_on_its_way(int end) { return end - kStages / 2 * 2; }
 };
 
 struct Barrier {
@@ -51,6 +59,8 @@ int simulate(unsigned seed, int steps, int lag) {
             if (u >= 2 * steps || !empty[s].complete((Ring::round(u) & 1) ^ 1)) continue;
             if (state[s] != 0) return 1;
             unit_at[s] = u, state[s] = 1, next[who] += 2;
+            for (int t = 0; t < kStages; ++t)
+                if (state[t] == 1 && unit_at[t] % 2 == who && unit_at[t] < Ring::first_on_its_way(next[who])) return 6;
         } else if (who < 4) {  // its copies land
             const int k = who - 2, u = landed[k], s = Ring::stage(u);
             const bool last = next[k] >= 2 * steps;
@@ -110,7 +120,7 @@ int simulate(unsigned seed, int steps, int lag) {
 
 template <int kStages>
 bool check() {
-    bool caught = kStages % 2 == 0;  // in turn they are apart anyway
+    bool caught = kStages % 2 == 0, missed = caught;  // in turn they are apart anyway
     for (unsigned seed = 0; seed < 3000; ++seed)
         for (int lag = 0; lag < PrefixRing<kStages>::kValues; ++lag) {
             const int bad = simulate<PrefixRing<kStages>, kStages>(seed, 40, lag);
@@ -119,9 +129,10 @@ bool check() {
                 return false;
             }
             caught = caught || simulate<InTurn<kStages>, kStages>(seed, 40, lag) != 0;
+            missed = missed || simulate<HalfDrained<kStages>, kStages>(seed, 40, lag) == 6;
         }
-    if (!caught) std::printf("stages %d: nothing found in turn\n", kStages);
-    return caught;
+    if (!caught || !missed) std::printf("stages %d: nothing found in turn, or half drained\n", kStages);
+    return caught && missed;
 }
 
 int main() {

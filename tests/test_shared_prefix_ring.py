@@ -9,7 +9,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 def test_no_unit_of_the_ring_meets_another(tmp_path):
     """tests/native/prefix_ring_check.cpp with the host compiler. It also runs a ring whose stages
-    keys and values take in turn, and must find that an odd number of them is unsafe."""
+    keys and values take in turn and one that waits for half its units at the end, and must find
+    that for an odd number of stages the one is unsafe and the other misses copies."""
     program = str(tmp_path / "ring")
     subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(sk.PKG, "csrc"), "-x", "c++",
                     os.path.join(HERE, "native", "prefix_ring_check.cpp"), "-o", program], check=True, timeout=300)
