@@ -735,6 +735,19 @@ SKINNY_API int skinny_reduce_selftest(const void *partials, int TP, const void *
                                       const void *gamma, void *out, void *residual_out, int M,
                                       float eps, long long timeout_ns, void *stream);
 
+/*
+ * skinny_shared_prefix_selftest -- exercise decode_attention_shared_prefix_bf16's bounded waits.
+ *   Checks its arguments as that call does, then launches its three kernels (whatever the size of
+ *   the prefix) with one role of the prefix's kernel first waiting on a barrier that nothing ever
+ *   completes and timeout_ns nanoseconds (1e3 <= timeout_ns <= 2e9) for every wait of that kernel.
+ *   Each of its CTAs records that, waits for its own copies and products, frees its tensor memory
+ *   and ends; out and lse are left unspecified (a prefix of length 0 leaves nothing to wait for but
+ *   that barrier). skinny_device_error() then reports bit 512 and clears it. The workspace is
+ *   ready for the next call. For tests of the failure path only.
+ */
+SKINNY_API int skinny_shared_prefix_selftest(const skinny_shared_prefix_attention_args *args,
+                                             long long timeout_ns, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -204,6 +204,8 @@ def load_library(path: str = LIBRARY):
     lib.skinny_watchdog_selftest.restype = i32
     lib.skinny_reduce_selftest.argtypes = [vp, i32, vp, vp, vp, vp, i32, f32, ctypes.c_longlong, vp]
     lib.skinny_reduce_selftest.restype = i32
+    lib.skinny_shared_prefix_selftest.argtypes = [vp, ctypes.c_longlong, vp]
+    lib.skinny_shared_prefix_selftest.restype = i32
     _lib = lib
     return lib
 
@@ -894,3 +896,18 @@ def reduce_selftest(partials, residual, gamma, out, residual_out, eps, timeout_n
         gamma.data_ptr(), out.data_ptr(), residual_out.data_ptr(), M, float(eps),
         int(timeout_ns), _stream_handle(stream))
     _check(st, "skinny_reduce_selftest")
+
+
+def shared_prefix_selftest(q, k_cache, v_cache, prefix_table, prefix_length, block_table, lengths, out, lse,
+                           workspace, timeout_ns, stream=None):
+    """Launch the shared-prefix attention with a wait that can never complete (see skinny.h)."""
+    import torch
+    rows, q_heads, D = q.shape
+    st = load_library().skinny_shared_prefix_selftest(
+        _pack_prefix(q.data_ptr(), _rows(q, "q", torch.bfloat16), rows, q_heads,
+                     *_cache_fields(k_cache, v_cache, torch.bfloat16), prefix_table.data_ptr(),
+                     prefix_table.numel(), prefix_length.data_ptr(), block_table.data_ptr(),
+                     block_table.stride(0), block_table.shape[1], lengths.data_ptr(), D ** -0.5,
+                     out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes),
+        int(timeout_ns), _stream_handle(stream))
+    _check(st, "skinny_shared_prefix_selftest")

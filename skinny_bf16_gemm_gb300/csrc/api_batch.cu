@@ -65,6 +65,11 @@ int check_on_device(const Range (&all)[N], int dev) {
     return SKINNY_OK;
 }
 
+constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // 1 s per wait of the prefix's kernel
+
+int shared_prefix(const skinny_shared_prefix_attention_args *p, const skinny_launch_opts *opts, void *stream,
+                  int selftest, unsigned long long limit_ns);
+
 }  // namespace
 
 extern "C" {
@@ -123,6 +128,20 @@ size_t skinny_shared_prefix_workspace_bytes(int rows, int q_heads, int kv_heads,
 
 int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_args *p,
                                         const skinny_launch_opts *opts, void *stream) {
+    return shared_prefix(p, opts, stream, 0, kWaitLimitNs);
+}
+
+int skinny_shared_prefix_selftest(const skinny_shared_prefix_attention_args *p, long long timeout_ns, void *stream) {
+    if (timeout_ns < 1000 || timeout_ns > 2000000000LL) return SKINNY_ERR_ARG;
+    return shared_prefix(p, nullptr, stream, 1, static_cast<unsigned long long>(timeout_ns));
+}
+
+}  // extern "C"
+
+namespace {
+
+int shared_prefix(const skinny_shared_prefix_attention_args *p, const skinny_launch_opts *opts, void *stream,
+                  int selftest, unsigned long long limit_ns) {
     if (!p || !p->prefix_table || !p->prefix_length) return SKINNY_ERR_NULL;
     // The rows' own tokens follow the rules of decode_attention_bf16.
     skinny_decode_attention_args own = {};
@@ -173,7 +192,7 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     attention_args(&own, pool, &o);
     // Both kinds of tokens are counted in one int there, and so are the tiles.
     const long long tokens = o.capacity + capacity;
-    if (joined_is_faster(p->rows, p->q_heads, c->kv_heads, D, capacity) && tokens < (1ll << 31) - kAttnMinTile &&
+    if (!selftest && joined_is_faster(p->rows, p->q_heads, c->kv_heads, D, capacity) && tokens < (1ll << 31) - kAttnMinTile &&
         attention_tiles(p->rows, c->kv_heads, o.head_blocks, tokens) < (1ll << 31)) {
         o.prefix_table = static_cast<const int *>(p->prefix_table);
         o.prefix_length = static_cast<const int *>(p->prefix_length);
@@ -219,6 +238,8 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     a.own_lse = o.lse;
     a.out = static_cast<uint16_t *>(p->out);
     a.lse = static_cast<float *>(p->lse);
+    a.wait_limit_ns = limit_ns;
+    a.selftest = selftest;
     alignas(64) CUtensorMap k_map = {}, v_map = {};
     a.box_rows = prefix_box_rows(c->page_size, plan.tokens);
     a.head_chunks = static_cast<int>(std::min<long long>(c->head_stride / 64, 1ll << 30));
@@ -234,4 +255,4 @@ int decode_attention_shared_prefix_bf16(const skinny_shared_prefix_attention_arg
     return SKINNY_OK;
 }
 
-}  // extern "C"
+}  // namespace

@@ -239,6 +239,8 @@ struct PrefixArgs {
     const float *own_out, *own_lse;  // workspace: [rows][q_heads][head_dim] and [rows][q_heads]
     uint16_t *out;
     float *lse;  // or nullptr
+    unsigned long long wait_limit_ns;
+    int selftest;  // 1: an issuer of products waits on a barrier that nothing completes
 };
 // Tokens of a TMA box of the keys and values, all of one page, or 0 if boxes will not do (tiles
 // must be whole boxes, and a box whole swizzle atoms).
