@@ -216,7 +216,8 @@ SKINNY_API int decode_gemm_bf16_epilogue(const void *x, const void *W, const voi
  *   of A and columns of B); 1 <= num_adapters <= 2^20.
  *   A x is an FP32 sum, scaled and multiplied by B in FP32: no rounding before the one to
  *   BF16. Only adapters in use are read. A row without one gets decode_gemm_bf16_epilogue's
- *   bits. Deterministic. Two kernels; the GEMM streams its weights while the first runs.
+ *   bits. Deterministic: neither dependent launch nor what else the pool holds, or where in it
+ *   the adapters in use are, changes a bit. Two kernels; the GEMM streams its weights while the first runs.
  *   Uses the decode GEMM's per-device scratch (same rules on streams and on the first call).
  *   With programmatic dependent launch A, B, scales, adapters, bias and residual are read
  *   after the wait for the previous kernel.

@@ -70,6 +70,7 @@ constexpr int kMaxShallowStages = 6;  // shallow rings have 5..6 stages, deep on
 // (plan.cuh use_shallow_ring picks one by the weight bytes per CTA).
 // LORA: how the adapters' part of a tile is worked out (decode_gemm_bf16_lora), see the kernel.
 enum Lora { kNoLora, kLoraDirect, kLoraCopied };
+constexpr int kLoraCopiedFrom = 24;  // the smallest rank that may go by kLoraCopied
 template <int MP, int STAGES, int LORA = kNoLora>
 struct Layout {
     static constexpr int kStages = STAGES;
@@ -189,6 +190,19 @@ __device__ __forceinline__ void store_tile_staged(const float (&v)[MP], uint16_t
     }
 }
 
+// Eight products of B and A x added to a row's two sums, of the even and the odd ones: one order for
+// both forms of LORA below, so that a call's bits do not depend on which of them it goes by.
+__device__ __forceinline__ void lora_add(float (&v)[2], const uint4 &b, const float4 &t0, const float4 &t1) {
+    v[0] = fmaf(t0.x, __uint_as_float(b.x << 16), v[0]);
+    v[1] = fmaf(t0.y, __uint_as_float(b.x & 0xFFFF0000u), v[1]);
+    v[0] = fmaf(t0.z, __uint_as_float(b.y << 16), v[0]);
+    v[1] = fmaf(t0.w, __uint_as_float(b.y & 0xFFFF0000u), v[1]);
+    v[0] = fmaf(t1.x, __uint_as_float(b.z << 16), v[0]);
+    v[1] = fmaf(t1.y, __uint_as_float(b.z & 0xFFFF0000u), v[1]);
+    v[0] = fmaf(t1.z, __uint_as_float(b.w << 16), v[0]);
+    v[1] = fmaf(t1.w, __uint_as_float(b.w & 0xFFFF0000u), v[1]);
+}
+
 // EPI: the epilogue of epilogue.cuh. LORA (with EPI): the adapters' second half,
 // scale B_a (A_a x), a the row's adapter. Templates so that the plain kernel keeps its
 // registers.
@@ -206,8 +220,9 @@ __device__ __forceinline__ void store_tile_staged(const float (&v)[MP], uint16_t
 //           three stages. From rank 64 on a load of 32 rows' pieces is 32 requests: 64 x 4096 x
 //           4096 with 16 adapters of rank 128 50 us, direct 74; 32 x 18432 x 7168 with 8 of rank 64
 //           54 and 65; but 64 x 7168 x 18432 with 64 of rank 16 65 and 62, 5 x 4099 x 1000 with 3 of
-//           rank 8 13.6 and 11.1. From rank 24 on where so few adapters serve so many rows that
-//           rank x rows is 96 x adapters or more: 64 x 18432 x 7168 with 32 of rank 48 63, direct 78;
+//           rank 8 13.6 and 11.1. From rank 24 on where a pool of so few adapters (how many of
+//           them are in use only the device knows) serves so many rows that rank x rows is
+//           96 x adapters or more: 64 x 18432 x 7168 with 32 of rank 48 63, direct 78;
 //           49 x 2173 x 64 with 6 of rank 24 17.5 and 23.0; but 36 x 8521 x 288 with 19 of rank 32
 //           24.5 and 23.4.
 template <int MP, int STAGES, bool EPI, int LORA>
@@ -466,7 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         [[maybe_unused]] int *sm_adapter = reinterpret_cast<int *>(smem + L::kLoraOffset);
         [[maybe_unused]] float *sm_scale = reinterpret_cast<float *>(sm_adapter + kMaxM);
         [[maybe_unused]] float *sm_ax = reinterpret_cast<float *>(smem + L::kLoraAxOffset);
-        // Copied: the adapters in use, each with its rows, and how many they are.
+        // How many adapters are in use, and from bit 8 and 16 on which of them (in the order of their
+        // first rows) this lane's rows have: one register. 0: shared out by rows.
+        [[maybe_unused]] int lora_order = 0;
+        [[maybe_unused]] auto lowest = [](uint64_t bits) { return __ffsll(static_cast<long long>(bits)) - 1; };
+        // Copied: the adapters in use, each with its rows.
         [[maybe_unused]] uint64_t *sm_rows = reinterpret_cast<uint64_t *>(smem + L::kLoraListOffset);
         [[maybe_unused]] int *sm_used = reinterpret_cast<int *>(smem + L::kLoraListOffset + 8 * kMaxM);
         [[maybe_unused]] const int ring_bytes = (L::kLoraBytes - g.M * args.lora.rank * 4) / 64 * 16;  // of a warp
@@ -484,32 +503,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sm_scale[etid] = id >= 0 && l.scales != nullptr ? __ldcg(l.scales + id) : 1.0f;
             }
             ptx::named_barrier_sync(1, kEpilogueThreads);
-            if constexpr (kCopied) {
-                if (warp == 2) {
-                    // Adapters in the order of their first rows.
-                    const int id[2] = {sm_adapter[lane], sm_adapter[32 + lane]};
-                    uint64_t rows[2];
-                    unsigned first[2];
+            // Adapters in the order of their first rows, where the call might go by either form: 0.3 us
+            // with 48 rows of rank 32.
+            if (kCopied || (MP >= 32 && l.rank >= kLoraCopiedFrom)) {
+                constexpr int kHalves = MP > 32 ? 2 : 1;
+                int id[kHalves];
+                uint64_t rows[kHalves], firsts = 0;  // rows: those with this lane's adapter
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) rows[h] = static_cast<uint64_t>(__match_any_sync(0xFFFFFFFFu, id[h])) << 32 * h;
-                    for (int i = 0; i < 32; ++i) {
-                        rows[0] |= static_cast<uint64_t>(sm_adapter[32 + i] == id[0]) << (32 + i);
-                        rows[1] |= static_cast<uint64_t>(sm_adapter[i] == id[1]) << i;
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        first[h] = __ballot_sync(0xFFFFFFFFu,
-                                                 id[h] >= 0 && __ffsll(static_cast<long long>(rows[h])) - 1 == h * 32 + lane);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (first[h] >> lane & 1) {
-                            const int at = (h > 0 ? __popc(first[0]) : 0) + __popc(first[h] & ((1u << lane) - 1u));
-                            sm_rows[at] = rows[h];
-                            sm_used[at] = id[h];
-                        }
-                    if (lane == 0) sm_used[kMaxM] = __popc(first[0]) + __popc(first[1]);
+                for (int h = 0; h < kHalves; ++h) {
+                    id[h] = sm_adapter[32 * h + lane];
+                    rows[h] = static_cast<uint64_t>(__match_any_sync(0xFFFFFFFFu, id[h])) << 32 * h;
                 }
-                ptx::named_barrier_sync(1, kEpilogueThreads);
+                if constexpr (kHalves == 2) {
+                    const int4 *ids = reinterpret_cast<const int4 *>(sm_adapter);
+                    auto equal = [](const int4 &at, int to) -> uint32_t {
+                        return (at.x == to) | (at.y == to) << 1 | (at.z == to) << 2 | (at.w == to) << 3;
+                    };
+                    uint32_t upper = 0, lower = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (kCopied) upper |= equal(ids[8 + i], id[0]) << 4 * i;  // direct: only the first is asked for
+                        lower |= equal(ids[i], id[1]) << 4 * i;
+                    }
+                    rows[0] |= static_cast<uint64_t>(upper) << 32;
+                    rows[1] |= lower;
+                }
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+                    firsts |= static_cast<uint64_t>(__ballot_sync(0xFFFFFFFFu, id[h] >= 0 && lowest(rows[h]) == 32 * h + lane)) << 32 * h;
+                lora_order = __popcll(static_cast<long long>(firsts));
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    const int first = lowest(rows[h]);
+                    const int at = __popcll(static_cast<long long>(firsts & ((1ull << first) - 1)));
+                    lora_order |= at << (8 + 8 * h);
+                    if (kCopied && warp == 2 && id[h] >= 0 && first == 32 * h + lane) {
+                        sm_rows[at] = rows[h];
+                        sm_used[at] = id[h];
+                    }
+                }
+                if constexpr (kCopied) ptx::named_barrier_sync(1, kEpilogueThreads);
             }
             ptx::pdl_wait();  // A x is the kernel's before
             // Sums of rows without an adapter are not there, and what is read of them is not used.
@@ -546,25 +579,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 add_slices(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
             ptx::named_barrier_sync(1, kEpilogueThreads);
         }
-        // Direct: the adapters' part of column n for the rows m = share (mod shares) of a piece.
+        // A tile's contributors share its adapters out in turn or, where these are fewer or the call
+        // never goes by the other form, its rows of x: the same rows for a contributor in both forms.
+        // Direct: the part of column n.
         [[maybe_unused]] auto lora_part = [&](int n, int share, int shares) {
             const LoraArgs &l = args.lora;
-            auto wanted = [&](int m) { return m < g.M && sm_adapter[m] >= 0 && m % shares == share; };
-            lora_rows = __ballot_sync(0xFFFFFFFFu, wanted(lane)) |
-                        static_cast<uint64_t>(MP > 32 ? __ballot_sync(0xFFFFFFFFu, wanted(lane + 32)) : 0u) << 32;
+            auto wanted = [&](int h) {
+                const int m = 32 * h + lane;
+                return m < g.M && sm_adapter[m] >= 0 &&
+                       ((lora_order & 0xFF) >= shares ? lora_order >> (8 + 8 * h) & 0xFF : m) % shares == share;
+            };
+            lora_rows = __ballot_sync(0xFFFFFFFFu, wanted(0)) |
+                        static_cast<uint64_t>(MP > 32 ? __ballot_sync(0xFFFFFFFFu, wanted(1)) : 0u) << 32;
             constexpr int kAtOnce = MP == 16 ? 4 : 8;  // rows whose loads are on their way together
             const uint16_t *column = l.B + static_cast<size_t>(n < g.N ? n : 0) * l.rank;
             for (uint64_t rest = lora_rows; rest != 0;) {
-                int m[kAtOnce];
+                uint32_t rows[kAtOnce / 4] = {};  // a byte each
+                int count = 0;
                 const uint4 *b[kAtOnce];
-                float v[kAtOnce];
+                float v[kAtOnce][2] = {};
+                auto row_of = [&](int u) { return static_cast<int>(rows[u / 4] >> 8 * (u % 4) & 0xFFu); };
 #pragma unroll
                 for (int u = 0; u < kAtOnce; ++u) {
-                    m[u] = rest != 0 ? __ffsll(static_cast<long long>(rest)) - 1 : -1;
+                    const int m = rest != 0 ? lowest(rest) : 0;
+                    count += rest != 0;
                     rest &= rest - 1;
-                    const size_t id = m[u] < 0 ? 0 : sm_adapter[m[u]];
+                    rows[u / 4] |= static_cast<uint32_t>(m) << 8 * (u % 4);
+                    const size_t id = u < count ? sm_adapter[m] : 0;
                     b[u] = reinterpret_cast<const uint4 *>(column + id * g.N * l.rank);
-                    v[u] = 0.0f;
                 }
                 for (int j = 0; j < l.rank; j += 16) {
                     uint4 w[kAtOnce][2];
@@ -572,29 +614,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            w[u][h] = m[u] >= 0 && j + 8 * h < l.rank ? __ldg(b[u] + j / 8 + h) : make_uint4(0, 0, 0, 0);
+                            w[u][h] = u < count && j + 8 * h < l.rank ? __ldg(b[u] + j / 8 + h) : make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int u = 0; u < kAtOnce; ++u) {
-                        if (m[u] < 0) break;
-                        const float4 *ax = reinterpret_cast<const float4 *>(sm_ax + m[u] * l.rank + j);
+                        if (u >= count) break;
+                        const float4 *ax = reinterpret_cast<const float4 *>(sm_ax + row_of(u) * l.rank + j);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             if (j + 8 * h >= l.rank) break;
                             const float4 t0 = ax[2 * h], t1 = ax[2 * h + 1];
-                            v[u] = fmaf(t0.x, __uint_as_float(w[u][h].x << 16), v[u]);
-                            v[u] = fmaf(t0.y, __uint_as_float(w[u][h].x & 0xFFFF0000u), v[u]);
-                            v[u] = fmaf(t0.z, __uint_as_float(w[u][h].y << 16), v[u]);
-                            v[u] = fmaf(t0.w, __uint_as_float(w[u][h].y & 0xFFFF0000u), v[u]);
-                            v[u] = fmaf(t1.x, __uint_as_float(w[u][h].z << 16), v[u]);
-                            v[u] = fmaf(t1.y, __uint_as_float(w[u][h].z & 0xFFFF0000u), v[u]);
-                            v[u] = fmaf(t1.z, __uint_as_float(w[u][h].w << 16), v[u]);
-                            v[u] = fmaf(t1.w, __uint_as_float(w[u][h].w & 0xFFFF0000u), v[u]);
+                            lora_add(v[u], w[u][h], t0, t1);
                         }
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < kAtOnce; ++u)
-                    if (m[u] >= 0) ptx::tmem_st1(lora_taddr + m[u], __float_as_uint(v[u]));
+                    if (u < count) ptx::tmem_st1(lora_taddr + row_of(u), __float_as_uint(__fadd_rn(v[u][0], v[u][1])));
             }
             ptx::tmem_st_wait();
             __syncwarp();
@@ -610,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         [[maybe_unused]] int lora_put = 0, lora_get = 0, lora_n0 = 0, lora_bound = 0;
         [[maybe_unused]] auto lora_copy = [&]() {
             if (lora_copies != 0) {
-                const int a = __ffsll(static_cast<long long>(lora_copies)) - 1;
+                const int a = lowest(lora_copies);
                 lora_copies &= lora_copies - 1;
                 const uint16_t *from = args.lora.B + (static_cast<size_t>(sm_used[a]) * g.N + lora_n0) * args.lora.rank;
                 const unsigned inverse = (65535u + lora_pieces) / lora_pieces;  // p / pieces = p * inverse >> 16, p < 512
@@ -624,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::cp_async_commit();  // a group an adapter, empty or not
         };
         [[maybe_unused]] auto lora_begin = [&](int tile, int share, int shares) {
-            const int adapters = sm_used[kMaxM];
+            const int adapters = lora_order & 0xFF;
             lora_mine = ~0ull;
             lora_uses = adapters == 64 ? ~0ull : (1ull << adapters) - 1;
             if (shares > 1) {
@@ -650,40 +685,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::cp_async_wait_for(lora_ahead);
                 __syncwarp();
                 const uint4 *row = reinterpret_cast<const uint4 *>(sm_ring + lora_get * lora_entry + lane * lora_pitch);
-                uint64_t rest = sm_rows[__ffsll(static_cast<long long>(lora_uses)) - 1] & lora_mine;
+                uint64_t rest = sm_rows[lowest(lora_uses)] & lora_mine;
                 lora_rows |= rest;
-                // Rows of x, `at_once` of them for a pass over the row of B; four sums each.
+                // Rows of x, `at_once` of them for a pass over the row of B.
                 auto rows = [&](auto at_once) {
                     constexpr int kAtOnce = decltype(at_once)::value;
                     const float *ax[kAtOnce];
                     int m[kAtOnce];
-                    float v[kAtOnce][4] = {};
+                    float v[kAtOnce][2] = {};
 #pragma unroll
                     for (int u = 0; u < kAtOnce; ++u) {
-                        m[u] = __ffsll(static_cast<long long>(rest)) - 1;
+                        m[u] = lowest(rest);
                         rest &= rest - 1;
                         ax[u] = sm_ax + m[u] * args.lora.rank;
                     }
 #pragma unroll 2
                     for (int c = 0; c < lora_pieces; ++c) {
                         const uint4 w = row[c];
-                        const float b[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u),
-                                            __uint_as_float(w.z << 16), __uint_as_float(w.z & 0xFFFF0000u),
-                                            __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xFFFF0000u)};
 #pragma unroll
                         for (int u = 0; u < kAtOnce; ++u) {
-                            const float4 t0 = reinterpret_cast<const float4 *>(ax[u])[2 * c],
-                                         t1 = reinterpret_cast<const float4 *>(ax[u])[2 * c + 1];
-                            v[u][0] = fmaf(t1.x, b[4], fmaf(t0.x, b[0], v[u][0]));
-                            v[u][1] = fmaf(t1.y, b[5], fmaf(t0.y, b[1], v[u][1]));
-                            v[u][2] = fmaf(t1.z, b[6], fmaf(t0.z, b[2], v[u][2]));
-                            v[u][3] = fmaf(t1.w, b[7], fmaf(t0.w, b[3], v[u][3]));
+                            const float4 *t = reinterpret_cast<const float4 *>(ax[u]) + 2 * c;
+                            lora_add(v[u], w, t[0], t[1]);
                         }
                     }
 #pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u)
-                        ptx::tmem_st1(lora_taddr + m[u], __float_as_uint((v[u][0] + v[u][1]) + (v[u][2] + v[u][3])));
+                    for (int u = 0; u < kAtOnce; ++u) ptx::tmem_st1(lora_taddr + m[u], __float_as_uint(__fadd_rn(v[u][0], v[u][1])));
                 };
                 int left = __popcll(static_cast<long long>(rest));
                 for (; left >= 4; left -= 4) rows(std::integral_constant<int, 4>{});
@@ -996,7 +1022,7 @@ cudaError_t launch_variant(const CUtensorMap &w_map, const CUtensorMap &x_map,
                            int device) {
     if (args.lora.rank > 0) {
         if constexpr (MP >= 32 && STAGES > kMaxShallowStages)
-            if (args.lora.rank >= 64 || (args.lora.rank >= 24 && args.lora.rank * args.M >= 96 * args.lora.count))
+            if (args.lora.rank >= 64 || (args.lora.rank >= kLoraCopiedFrom && args.lora.rank * args.M >= 96 * args.lora.count))
                 return launch_kernel<MP, MP == 64 ? 6 : 8, true, kLoraCopied>(w_map, x_map, args, ctas, stream, pdl, device);
         // A x takes one stage of the rings that fill the shared memory (up to 32 KB).
         constexpr int kLoraStages = STAGES - (MP >= 32 && STAGES > kMaxShallowStages ? 1 : 0);
