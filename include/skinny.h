@@ -535,11 +535,18 @@ SKINNY_API size_t skinny_attention_workspace_bytes(int num_sms);
  *                  aligned, its first SKINNY_ATTENTION_COUNTER_BYTES zero before its first
  *                  use; every call leaves it ready for the next, of any sizes that it is large
  *                  enough for. Calls that may run at the same time need one each.
- *   Three kernels: the prefix, the rows' own tokens beside it or behind it, and the join; for one
- *   row, or a prefix that is little work, one that reads both kinds of tokens row by row. Scores,
- *   maxima, sums and partial outputs are FP32; the prefix's weights are rounded to BF16 (to
- *   nearest) for the product with the values, the own tokens' as in decode_attention_bf16;
- *   the output is rounded once. Deterministic.
+ *   Three kernels: the prefix, the rows' own tokens beside it or behind it, and the join. Or one
+ *   that reads both kinds of tokens row by row: for heads of up to 128, at most 16 to a key head,
+ *   before a prefix that is little work, and for one row of at most 8 heads to a key head before
+ *   any. Scores, maxima, sums and partial outputs are FP32; the output is rounded once. With three
+ *   kernels the prefix's weights are rounded to BF16 (to nearest) for the product with the values;
+ *   the own tokens', and all weights in one kernel, are as in decode_attention_bf16. (A weight of
+ *   the prefix that underflows to 0 is still multiplied with three kernels: an infinite value gives
+ *   NaN there.)
+ *   Deterministic: the same call gives the same bits. Which kernels run, and on how many SMs, goes
+ *   by the sizes and by what the tables could hold, since the lengths are on the device: the
+ *   same tokens in wider tables, or another number of rows, may give other bits within those
+ *   roundings.
  *   prefix_width >= 1; prefix_width * page_size < 2^30; key heads * tiles of the table (of 64
  *   tokens) < 2^31; tables and lengths 4-byte aligned. Every other argument, rule and limit is
  *   decode_attention_bf16's, without a window.

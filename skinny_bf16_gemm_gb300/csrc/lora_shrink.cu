@@ -136,8 +136,9 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-// K slices of a call: 256 values or more each, about eight CTAs an SM if every row has an
-// adapter of its own, and no more sums than the scratch holds.
+// K slices of a call: of 256 values, or more where that would be more than 32 of them, than about
+// eight CTAs an SM if every row had an adapter of its own, or than the scratch has room for (of fewer
+// where K is no multiple: K = 264 two of 136 and 128).
 int lora_splits(int M, int K, int rank, int num_sms) {
     const int tiles = (rank + kRankTile - 1) / kRankTile;
     int s = (K + 255) / 256;

@@ -28,7 +28,8 @@
 // the roundings of different tokens are independent, so they average out in o as the weights
 // do, and add at most as much as the output's own rounding. A second BF16 term, as
 // decode_attention_bf16 has where the products are free, would cost half the tensor time
-// again. Maxima, sums and o are FP32.
+// again with two tiles, and lengthen the softmax and the products, which take turns, with one.
+// Maxima, sums and o are FP32.
 //
 // Measured (in a graph, with the own tokens and the join): 151 us for 64 rows x 56 heads over 8
 // behind 65521 tokens with 1000 of their own each, of 62 us that the products take at the peak

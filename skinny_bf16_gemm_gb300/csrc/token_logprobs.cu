@@ -21,7 +21,7 @@
 //
 // Measured (in a graph): 2048 rows of 163840 120.4 us, 5.6 TB/s (109.0, 6.2 TB/s, without the
 // list of 8); 64 rows of 163840, on 8 CTAs each, 9.2 us without a list and 15.7 with one of 20:
-// bisecting the bound over one warp's 256 maxima, reading the flagged rounds again and the join
+// bisecting the bound over the threads' maxima by one warp, reading the flagged rounds again and the join
 // of 8 lists are three latencies one after another. 6.5 us for one row of 20480.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
