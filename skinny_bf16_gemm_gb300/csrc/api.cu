@@ -563,6 +563,70 @@ int check_cache(const skinny_kv_cache *c, bool write, size_t *span) {
     return SKINNY_OK;
 }
 
+namespace {
+
+// The words of the kernels' files, and what each bit of one is reported as.
+struct ErrorWord {
+    cudaError_t (*find)(int **word);
+    int bits[3];
+};
+constexpr ErrorWord kErrorWords[] = {
+    {reduce_error_word, {kErrReduceExchange, kErrReduceExchange, kErrReduceExchange}},
+    {rope_error_word, {kErrIndex, kErrIndex, kErrIndex}},
+    {attention_error_word, {kErrIndex, kErrIndex, kErrIndex}},
+    {attention_part_error_word, {kErrIndex, kErrIndex, kErrIndex}},
+    {attention_joined_error_word, {kErrIndex, kErrIndex, kErrIndex}},
+    {logprob_error_word, {kErrIndex, kErrIndex, kErrIndex}},
+    {lora_error_word, {kErrIndex, kErrIndex, kErrIndex}},
+    {prefix_error_word, {kErrPrefixWait, kErrIndex, kErrDrain}}};
+constexpr int kNumErrorWords = sizeof(kErrorWords) / sizeof(kErrorWords[0]);
+
+// Reads and clears every error word of the current device, which is idle. The copies go out
+// together and are waited for once.
+int read_error_words(int device, int *value) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    static int *host = nullptr;  // pinned
+    DeviceState &d = g_devices[device];
+    int *words[kNumErrorWords];
+    auto failed = [] {
+        cudaGetLastError();
+        return SKINNY_ERR_DEVICE;
+    };
+    if (!host && cudaHostAlloc(reinterpret_cast<void **>(&host), (kNumErrorWords + 1) * sizeof(int), cudaHostAllocPortable) != cudaSuccess)
+        return host = nullptr, failed();
+    host[kNumErrorWords] = 0;
+    for (int i = 0; i < kNumErrorWords; ++i)
+        if (kErrorWords[i].find(&words[i]) != cudaSuccess ||
+            cudaMemcpyAsync(host + i, words[i], sizeof(int), cudaMemcpyDeviceToHost, nullptr) != cudaSuccess)
+            return failed();
+    if (d.scratch && cudaMemcpyAsync(host + kNumErrorWords, d.err, sizeof(int), cudaMemcpyDeviceToHost, nullptr) != cudaSuccess)
+        return failed();
+    if (cudaStreamSynchronize(nullptr) != cudaSuccess) return failed();
+    int gemm = host[kNumErrorWords], any = gemm;
+    if (d.scratch && (gemm != 0 || *reinterpret_cast<volatile int *>(d.host_err) != 0)) {
+        // A kernel gave up part-way: clear the words and the partial flags, which lets
+        // later calls run again.
+        if (cudaMemset(d.err, 0, sizeof(int)) != cudaSuccess || cudaMemset(d.flags, 0, d.flag_bytes) != cudaSuccess) {
+            *value = gemm;
+            return failed();
+        }
+        if (gemm == 0) gemm = kErrUnknown;
+        any = 1;
+        *reinterpret_cast<volatile int *>(d.host_err) = 0;
+    }
+    *value = gemm;
+    for (int i = 0; i < kNumErrorWords; ++i) {
+        for (int b = 0; b < 3; ++b)
+            if (host[i] >> b & 1) *value |= kErrorWords[i].bits[b];
+        if (host[i] != 0 && cudaMemset(words[i], 0, sizeof(int)) != cudaSuccess) return failed();
+        any |= host[i];
+    }
+    // Cleared before any later launch, on whatever stream.
+    if (any && cudaStreamSynchronize(nullptr) != cudaSuccess) return failed();
+    return SKINNY_OK;
+}
+
+}  // namespace
 }  // namespace skinny
 
 using namespace skinny;
@@ -1049,52 +1113,7 @@ int skinny_device_error(int device, int *word) {
         return SKINNY_ERR_DEVICE;
     }
     int value = 0;
-    int st = SKINNY_OK;
-    {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        DeviceState &d = g_devices[device];
-        if (d.scratch) {
-            if (cudaMemcpy(&value, d.err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) {
-                cudaGetLastError();
-                st = SKINNY_ERR_DEVICE;
-            } else if (value != 0 || *reinterpret_cast<volatile int *>(d.host_err) != 0) {
-                // A kernel gave up part-way: clear the words and the partial flags,
-                // which lets later calls run again.
-                if (cudaMemset(d.err, 0, sizeof(int)) != cudaSuccess ||
-                    cudaMemset(d.flags, 0, d.flag_bytes) != cudaSuccess) {
-                    cudaGetLastError();
-                    st = SKINNY_ERR_DEVICE;
-                } else {
-                    if (value == 0) value = kErrUnknown;
-                    *reinterpret_cast<volatile int *>(d.host_err) = 0;
-                }
-            }
-        }
-    }
-    // The reduce kernel's own word (its cluster exchange waits).
-    int reduce_word = 0;
-    if (st == SKINNY_OK && reduce_error_word(&reduce_word, true) != cudaSuccess) {
-        cudaGetLastError();
-        st = SKINNY_ERR_DEVICE;
-    }
-    if (reduce_word) value |= kErrReduceExchange;
-    // The words of the kernels that read indices from device memory.
-    int rope_word = 0, attention_word = 0, logprob_word = 0, lora_word = 0,
-        part_word = 0, joined_word = 0, prefix_word = 0;
-    if (st == SKINNY_OK && (rope_error_word(&rope_word, true) != cudaSuccess ||
-                            attention_error_word(&attention_word, true) != cudaSuccess ||
-                            logprob_error_word(&logprob_word, true) != cudaSuccess ||
-                            lora_error_word(&lora_word, true) != cudaSuccess ||
-                            attention_part_error_word(&part_word, true) != cudaSuccess ||
-                            attention_joined_error_word(&joined_word, true) != cudaSuccess ||
-                            prefix_error_word(&prefix_word, true) != cudaSuccess)) {
-        cudaGetLastError();
-        st = SKINNY_ERR_DEVICE;
-    }
-    if (rope_word || attention_word || logprob_word || lora_word || part_word || joined_word || (prefix_word & 2))
-        value |= kErrIndex;
-    if (prefix_word & 1) value |= kErrPrefixWait;
-    if (prefix_word & 4) value |= kErrDrain;
+    const int st = read_error_words(device, &value);
     cudaSetDevice(prev);
     if (word) *word = value;
     if (st != SKINNY_OK) return st;

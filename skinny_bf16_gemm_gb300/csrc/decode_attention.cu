@@ -8,6 +8,6 @@ cudaError_t launch_decode_attention(const AttentionArgs &a, int head_dim, int nu
     return launch_any_dim<kWhole>(a, head_dim, num_sms, device, stream, pdl);
 }
 
-cudaError_t attention_error_word(int *value, bool clear) { return read_error_word(value, clear); }
+cudaError_t attention_error_word(int **word) { return error_word(word); }
 
 }  // namespace skinny

@@ -9,6 +9,6 @@ cudaError_t launch_decode_attention_joined(const SharedAttentionArgs &a, int hea
     return launch_any_dim<kJoined>(a, head_dim, num_sms, device, stream, pdl);
 }
 
-cudaError_t attention_joined_error_word(int *value, bool clear) { return read_error_word(value, clear); }
+cudaError_t attention_joined_error_word(int **word) { return error_word(word); }
 
 }  // namespace skinny

@@ -1043,12 +1043,7 @@ cudaError_t launch_any_dim(const ArgsOf<FORM> &a, int head_dim, int num_sms, int
     }
 }
 
-cudaError_t read_error_word(int *value, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_attn_err, sizeof(int));
-    if (e != cudaSuccess || !clear || *value == 0) return e;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_attn_err, &zero, sizeof(int));
-}
+cudaError_t error_word(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_attn_err); }
 
 }  // namespace
 }  // namespace skinny

@@ -10,6 +10,6 @@ cudaError_t launch_decode_attention_part(const SharedAttentionArgs &a, int head_
     return launch_any_dim<kPart>(a, head_dim, num_sms, device, stream, true);
 }
 
-cudaError_t attention_part_error_word(int *value, bool clear) { return read_error_word(value, clear); }
+cudaError_t attention_part_error_word(int **word) { return error_word(word); }
 
 }  // namespace skinny

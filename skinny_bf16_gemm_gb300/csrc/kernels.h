@@ -103,7 +103,7 @@ cudaError_t launch_decode_gemm(const CUtensorMap &w_map, const CUtensorMap &x_ma
 int lora_splits(int M, int K, int rank, int num_sms);
 cudaError_t launch_lora_shrink(const void *x, const LoraArgs &l, int M, int K, int num_sms, cudaStream_t stream,
                                bool pdl);
-cudaError_t lora_error_word(int *value, bool clear);
+cudaError_t lora_error_word(int **word);
 
 // Split-K scratch held in a static device array (decode_gemm_bf16_noalloc).
 constexpr int kStaticScratchCtas = 160;   // CTAs the array holds partial tiles for
@@ -148,9 +148,9 @@ cudaError_t launch_reduce_rmsnorm_selftest(const void *partials, int TP, const v
                                            int M, float eps, unsigned long long limit_ns,
                                            cudaStream_t stream);
 
-// The reduce kernel's own error word on the current device (nonzero: a
-// cluster exchange wait ran out), cleared after reading if `clear`.
-cudaError_t reduce_error_word(int *value, bool clear);
+// Where the reduce keeps its own error word on the current device (nonzero: a cluster
+// exchange wait ran out); the further kernels' below likewise.
+cudaError_t reduce_error_word(int **word);
 
 // Gather TP shards [TP, M, S] into rows [M, TP * S] (S a multiple of 8).
 cudaError_t launch_gather(const void *shards, int TP, int M, int S, void *out,
@@ -177,7 +177,7 @@ struct RopeArgs {
     const long long *slots;
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs &a, int num_sms, cudaStream_t stream, bool pdl);
-cudaError_t rope_error_word(int *value, bool clear);
+cudaError_t rope_error_word(int **word);
 
 // Decode attention over a paged cache (decode_attention_bf16). Strides in elements.
 struct AttentionArgs {
@@ -212,7 +212,7 @@ struct SharedAttentionArgs : AttentionArgs {
 };
 cudaError_t launch_decode_attention(const AttentionArgs &a, int head_dim, int num_sms, int device,
                                     cudaStream_t stream, bool pdl);
-cudaError_t attention_error_word(int *value, bool clear);
+cudaError_t attention_error_word(int **word);
 
 // Attention over a prefix that all rows share (decode_attention_shared_prefix_bf16): the
 // prefix's partials, the rows' own tokens in FP32, and the join (three launches, in this
@@ -252,9 +252,9 @@ cudaError_t launch_decode_attention_part(const SharedAttentionArgs &a, int head_
 cudaError_t launch_decode_attention_joined(const SharedAttentionArgs &a, int head_dim, int num_sms, int device,
                                            cudaStream_t stream, bool pdl);
 cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, cudaStream_t stream);
-cudaError_t prefix_error_word(int *value, bool clear);
-cudaError_t attention_part_error_word(int *value, bool clear);
-cudaError_t attention_joined_error_word(int *value, bool clear);
+cudaError_t prefix_error_word(int **word);
+cudaError_t attention_part_error_word(int **word);
+cudaError_t attention_joined_error_word(int **word);
 
 // Log probabilities, entropy and top alternatives of rows of logits (token_logprobs_bf16).
 constexpr int kLogprobMaxTop = 32;
@@ -271,6 +271,6 @@ struct LogprobArgs {
     long long *top_tokens;  // [M][top] or nullptr
 };
 cudaError_t launch_token_logprobs(const LogprobArgs &a, int num_sms, cudaStream_t stream, bool pdl);
-cudaError_t logprob_error_word(int *value, bool clear);
+cudaError_t logprob_error_word(int **word);
 
 }  // namespace skinny

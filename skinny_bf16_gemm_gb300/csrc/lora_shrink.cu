@@ -168,11 +168,6 @@ cudaError_t launch_lora_shrink(const void *x, const LoraArgs &l, int M, int K, i
     return cudaLaunchKernelEx(&cfg, lora_shrink_kernel, static_cast<const uint16_t *>(x), l, M, K, slice);
 }
 
-cudaError_t lora_error_word(int *value, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_lora_err, sizeof(int));
-    if (e != cudaSuccess || !clear || *value == 0) return e;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_lora_err, &zero, sizeof(int));
-}
+cudaError_t lora_error_word(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_lora_err); }
 
 }  // namespace skinny

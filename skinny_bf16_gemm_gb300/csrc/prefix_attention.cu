@@ -861,12 +861,7 @@ cudaError_t launch_prefix_join(const PrefixArgs &a, int head_dim, int num_sms, c
     }
 }
 
-cudaError_t prefix_error_word(int *value, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_prefix_err, sizeof(int));
-    if (e != cudaSuccess || !clear || *value == 0) return e;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_prefix_err, &zero, sizeof(int));
-}
+cudaError_t prefix_error_word(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_prefix_err); }
 
 }  // namespace skinny
 

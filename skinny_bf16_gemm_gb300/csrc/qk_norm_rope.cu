@@ -278,11 +278,6 @@ cudaError_t launch_qk_norm_rope(const RopeArgs &a, int num_sms, cudaStream_t str
     return launch_lanes<32>(a, num_sms, stream, pdl);
 }
 
-cudaError_t rope_error_word(int *value, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_rope_err, sizeof(int));
-    if (e != cudaSuccess || !clear || *value == 0) return e;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_rope_err, &zero, sizeof(int));
-}
+cudaError_t rope_error_word(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_rope_err); }
 
 }  // namespace skinny

@@ -358,11 +358,6 @@ cudaError_t launch_reduce_rmsnorm_selftest(const void *partials, int TP, const v
                                            eps, stream, false, none, limit_ns);
 }
 
-cudaError_t reduce_error_word(int *value, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_reduce_err, sizeof(int));
-    if (e != cudaSuccess || !clear || *value == 0) return e;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_reduce_err, &zero, sizeof(int));
-}
+cudaError_t reduce_error_word(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_reduce_err); }
 
 }  // namespace skinny

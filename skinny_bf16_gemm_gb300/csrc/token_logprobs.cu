@@ -428,11 +428,6 @@ cudaError_t launch_token_logprobs(const LogprobArgs &a, int num_sms, cudaStream_
     return launch<1>(a, threads, stream, pdl);
 }
 
-cudaError_t logprob_error_word(int *value, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_logprob_err, sizeof(int));
-    if (e != cudaSuccess || !clear || *value == 0) return e;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_logprob_err, &zero, sizeof(int));
-}
+cudaError_t logprob_error_word(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_logprob_err); }
 
 }  // namespace skinny
