@@ -44,7 +44,7 @@ bool outputs_clear(const Range (&in)[I], const Range (&outs)[O]) {
 // behind 100 21.4 and 14.7).
 // A single row's prefix is shared with nobody: 14.0 against 14.2 us for 7 heads behind 8000 tokens,
 // 50.7 against 63.6 for 56 heads over 8 behind 60000. Wider heads run on the tensor cores from the
-// first token on: 17.8 us for 8 rows x 16 heads of 256 behind 2000 tokens, 34.1 in one launch.
+// first token on: 16.9 us for 8 rows x 16 heads of 256 behind 2000 tokens, 34.1 in one launch.
 // (Times inside a graph.)
 bool joined_is_faster(int rows, int q_heads, int kv_heads, int head_dim, long long tokens) {
     const int group = q_heads / kv_heads;
